@@ -362,6 +362,67 @@ int gemm_rs_ex(const void *A, size_t a_stride, const void *B, size_t b_stride, v
  * arguments. */
 size_t gemm_rs_workspace_bytes(int P, int M, int N, int K);
 
+/* Attention heads of P logical ranks: element (rank r, token t, head h, i) at
+ * base + r*slot + t*token + h*head + 2*i bytes (bf16; the D elements of a
+ * head are contiguous).  base is 16-byte aligned and every stride of an
+ * extent above 1 is a multiple of 16 bytes and at least 2*D, so heads inside
+ * a fused Q/K/V activation (the C of ag_gemm) are taken in place, and an
+ * output may be the A operand of gemm_rs. */
+typedef struct {
+    void *base;
+    size_t slot, token, head;
+} rc_heads;
+
+/*
+ * Arguments of attn_fwd and attn_bwd.  q, out, dout, dq: [P][Tq][Hq][D];
+ * k, v, dk, dv: [P][Tk][Hkv][D]; lse: f32 [P][Tq][Hq], contiguous.  Query
+ * head h of a rank uses key head h / (Hq / Hkv).
+ * Sequences (DEVICE int32): queries of sequence b are tokens
+ * [cu_q[b], cu_q[b+1]), its keys tokens [cu_k[b], cu_k[b+1]) -- or only the
+ * first used_k[b] of them where used_k is not null (a key/value cache with
+ * room left).  b < B.  Offsets must not decrease; values outside a tensor are
+ * clamped to it.  causal: query i of n sees key j of m when j <= i + m - n
+ * (the last query sees every key; with more queries than keys the first ones
+ * see none).  scale > 0 multiplies the scores.
+ * workspace: null for the library's own, else DEVICE memory of ws_bytes bytes
+ * (256-byte aligned, zeroed once before first use; at least the call's
+ * *_workspace_bytes), under the rules of ring_all_gather_ex.
+ */
+typedef struct {
+    rc_heads q, k, v, out;
+    rc_heads dout, dq, dk, dv; /* attn_bwd only */
+    float *lse;
+    const int32_t *cu_q, *cu_k, *used_k;
+    void *workspace;
+    size_t ws_bytes;
+    int P, B, Tq, Tk, Hq, Hkv, D, causal;
+    float scale;
+    int reserved; /* 0 */
+} rc_attn_args;
+
+/*
+ * attn_fwd -- attention of every rank's heads over packed sequences:
+ *     out = softmax(scale q k^T over the visible keys) v,
+ *     lse = ln sum exp(scale q k^T)   (natural logarithm; lse may be null).
+ * Scores, maxima, sums and the accumulator are binary32; the weights are
+ * rounded to bf16 for their product with v and out is rounded once.  A row
+ * that sees no key gives out = 0, lse = -inf.  Keys and values that a row does
+ * not see never reach it, whatever they hold (NaN and infinities included).
+ * Rows of q outside every sequence leave out and lse untouched.  The result
+ * does not depend on timing: splits of long key ranges are joined in order.
+ * A sequence may have any number of queries: a whole prompt, a later piece of
+ * one (keys in a cache), or one token.  Where queries fill few rows (mean
+ * Tq/B times Hq/Hkv at most 128) key ranges are divided over the GPU.
+ * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, B >= 1, Hq a
+ * multiple of Hkv with Hq/Hkv <= 128, D a multiple of 8 up to 128,
+ * 0 < scale < inf, layouts as for rc_heads, reserved 0.  Tq = 0 does nothing.
+ */
+int attn_fwd(const rc_attn_args *args, void *stream);
+
+/* Workspace bytes attn_fwd needs for these sizes (pointers and strides are
+ * not read); 0 for invalid sizes or when no sm_103 device is current. */
+size_t attn_fwd_workspace_bytes(const rc_attn_args *args);
+
 /*
  * ring_status -- waits for `stream`, then returns and clears the device
  * status of the library's own signal areas on the calling device: the

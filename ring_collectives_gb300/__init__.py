@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -31,6 +32,7 @@ __all__ = [
     "ag_gemm_ex", "ag_gemm_kn", "ag_gemm_workspace_bytes", "RC_B_NK", "RC_B_KN", "gemm_rs_ex", "gemm_rs_workspace_bytes",
     "ring_last_error", "ring_set_timeout_ms", "ring_set_slices", "ring_debug_skip_notify", "ag_gemm_debug_skip_piece",
     "ring_debug_set_trace", "ring_debug_l2_rate", "ring_finalize", "library_path", "load",
+    "attn_fwd", "attn_fwd_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -77,6 +79,8 @@ _SIGNATURES = {
     "ring_debug_set_trace": ([_vp, _sz], _i),
     "ring_debug_l2_rate": ([_vp, _vp, _vp, _sz, _i, _i, _vp], _i),
     "ring_finalize": ([], _i),
+    "attn_fwd": ([ctypes.c_char_p, _vp], _i),
+    "attn_fwd_workspace_bytes": ([ctypes.c_char_p], _sz),
 }
 
 _lib = None
@@ -485,3 +489,65 @@ def ring_allreduce_noalloc(bufs: torch.Tensor, N: int | None = None, stream=None
     with torch.cuda.device(bufs.device):
         _check(fn(bp, bs, bufs.size(0), N, dt, _stream(stream, bufs.device)))
     return bufs
+
+
+# rc_attn_args of include/ringcoll.h: eight rc_heads, six pointers and sizes, eight ints, scale, reserved
+_ATTN_ARGS = struct.Struct("@32Q6Q8ifi")
+_NO_HEADS = (0, 0, 0, 0)
+
+
+def _heads(t: torch.Tensor, name: str, shape=None):
+    if not t.is_cuda or t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bf16 CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    st = t.stride()
+    if len(st) != 4 or (st[3] != 1 and t.size(3) > 1):
+        raise ValueError(f"{name} must be [P, T, H, D] with contiguous heads")
+    return t.data_ptr(), 2 * st[0], 2 * st[1], 2 * st[2]
+
+
+def _index(t, name: str, n: int) -> int:
+    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or t.size(0) != n or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, causal, scale):
+    return P, B, Tq, Tk, Hq, Hkv, D, int(bool(causal)), D ** -0.5 if scale is None else scale, 0
+
+
+def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor | None,
+             cu_q: torch.Tensor, cu_k: torch.Tensor, used_k: torch.Tensor | None = None, causal: bool = True,
+             scale: float | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of P ranks' heads over packed sequences, bf16.
+
+    q, out [P, Tq, Hq, D]; k, v [P, Tk, Hkv, D]; lse float32 [P, Tq, Hq] or None.  Any
+    strides with contiguous heads and 16-byte multiples, so q, k, v may be views of the
+    fused activations that ag_gemm writes.  Sequence b holds queries cu_q[b]:cu_q[b+1]
+    and keys cu_k[b]:cu_k[b+1], or the first used_k[b] of them (a cache); int32 on the
+    device.  causal: the last query of a sequence sees all its keys, each earlier one a
+    key less.  scale defaults to D ** -0.5.  workspace: as for the ``_ex`` calls."""
+    P, Tq, Hq, D = q.shape
+    kshape = (P, k.size(1), k.size(2), D)
+    B = cu_q.numel() - 1
+    args = _ATTN_ARGS.pack(
+        *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(v, "v", kshape), *_heads(out, "out", q.shape),
+        *_NO_HEADS * 4, 0 if lse is None else _lse(lse, P, Tq, Hq), _index(cu_q, "cu_q", B + 1),
+        _index(cu_k, "cu_k", B + 1), 0 if used_k is None else _index(used_k, "used_k", B),
+        *((0, 0) if workspace is None else _ws(workspace)),
+        *_attn_sizes(P, B, Tq, kshape[1], Hq, kshape[2], D, causal, scale))
+    with torch.cuda.device(q.device):
+        _check(load().attn_fwd(args, _stream(stream, q.device)))
+    return out
+
+
+def _lse(lse, P, Tq, Hq):
+    if not lse.is_cuda or lse.dtype != torch.float32 or lse.shape != (P, Tq, Hq) or not lse.is_contiguous():
+        raise TypeError(f"lse must be a contiguous float32 CUDA tensor of shape {[P, Tq, Hq]}")
+    return lse.data_ptr()
+
+
+def attn_fwd_workspace_bytes(P: int, B: int, Tq: int, Tk: int, Hq: int, Hkv: int, D: int) -> int:
+    args = _ATTN_ARGS.pack(*(0,) * 38, *_attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, True, None))
+    return int(load().attn_fwd_workspace_bytes(args))

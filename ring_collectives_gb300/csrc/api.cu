@@ -167,6 +167,8 @@ struct DeviceState {
     void *ws = nullptr;  // WsHeader followed by the signal words
     size_t ws_bytes = 0;
     uint64_t launches = 0;
+    void *scratch = nullptr; // prepare_scratch
+    size_t scratch_bytes = 0;
 };
 DeviceState g_dev[kMaxDevices];
 
@@ -485,6 +487,44 @@ int prepare_workspace_ext(void *ext, size_t ext_bytes, size_t sig_words, WsHeade
     *sig = (uint32_t *)((char *)ext + sizeof(WsHeader));
     *sm_count = st->sm_count;
     *timeout_ns = (unsigned long long)g_timeout_ms.load() * 1000000ull;
+    return RC_OK;
+}
+
+int device_sms(int *sms)
+{
+    int dev;
+    DeviceState *st = nullptr;
+    const int rc_ = current_device(&dev, &st);
+    if (!rc_) *sms = st->sm_count;
+    return rc_;
+}
+
+int prepare_scratch(size_t bytes, void **out)
+{
+    int dev;
+    DeviceState *st = nullptr;
+    int rc_ = current_device(&dev, &st);
+    if (rc_) return rc_;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (st->scratch_bytes < bytes) {
+        cudaError_t e;
+        if (st->scratch) {
+            e = cudaDeviceSynchronize();   // earlier calls may still use the old block
+            if (e != cudaSuccess) return cuda_fail(e, "synchronise before scratch resize");
+            cudaFree(st->scratch);
+            st->scratch = nullptr;
+            st->scratch_bytes = 0;
+        }
+        const size_t want = (bytes + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
+        e = cudaMalloc(&st->scratch, want);
+        if (e != cudaSuccess) {
+            st->scratch = nullptr;
+            (void)cudaGetLastError();
+            return fail(RC_ERR_NOMEM, "scratch of %zu bytes: %s", want, cudaGetErrorString(e));
+        }
+        st->scratch_bytes = want;
+    }
+    *out = st->scratch;
     return RC_OK;
 }
 
@@ -1114,6 +1154,13 @@ int ring_finalize(void)
             g_dev[d].ws = nullptr;
             g_dev[d].ws_bytes = 0;
             g_dev[d].launches = 0;
+        }
+        if (g_dev[d].scratch) {
+            cudaSetDevice(d);
+            cudaDeviceSynchronize();
+            cudaFree(g_dev[d].scratch);
+            g_dev[d].scratch = nullptr;
+            g_dev[d].scratch_bytes = 0;
         }
         if (g_pipe[d].in) {
             cudaSetDevice(d);

@@ -1,0 +1,198 @@
+// attn.cuh -- what the attention kernels share: the arguments of a launch,
+// the mapping of work units to packed sequences, TMEM stores, the MMA whose
+// A operand lies in TMEM, and the tensor maps of head-strided operands.
+//
+// Rows.  The G = Hq / Hkv query heads that share a key head are packed with
+// the tokens: row r of a 128-row tile is token r / G, head r % G of the
+// group.  A tile holds TT = 128 / G whole tokens (G * TT rows; the other rows
+// stay masked), so one key tile serves all heads of the group, a single token
+// fills G rows, and the gradients of a shared key head sum inside one tile.
+#pragma once
+#include <cuda.h>
+#include <stdint.h>
+
+#include "internal.h"
+#include "ringcoll.h"
+#include "tc.cuh"
+
+namespace rc {
+namespace attn {
+
+using namespace tc;
+
+constexpr int KT = 128;                    // keys per tile, and rows per query tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Strided {
+    char *base;
+    size_t slot, token, head;              // bytes
+};
+
+struct Params {
+    Strided q, out, dout, dq, dk, dv;      // operands that are also accessed without TMA
+    const char *v;                         // values, for the non-finite path of the forward pass
+    size_t v_slot, v_token, v_head;
+    const char *o;                         // forward output (backward)
+    size_t o_slot, o_token, o_head;
+    float *lse;                            // [P][Tq][Hq], or null (forward)
+    float *delta;                          // [P][Tq][Hq] rowsum(dO * O) (backward)
+    float *part_o, *part_lse;              // partial results of split sequences
+    const int32_t *cu_q, *cu_k, *used_k;
+    WsHeader *hdr;
+    int P, B, Tq, Tk, Hq, Hkv, G, D, causal;
+    int TT;                                // tokens per 128-row tile
+    int TPU;                               // query tokens per work unit
+    int sms, part_rows;
+    int may_split;                         // 1: key ranges may be split (part_o / part_lse are there)
+    float scale;
+    unsigned long long timeout_ns;
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                                            uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, int u,
+                                            uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+                 ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(u), "r"(bar)
+                 : "memory");
+}
+
+// D[tmem] (+)= A[tmem, bf16 pairs] . B[smem desc]
+__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+
+// Stores 16 / 32 columns of this thread's TMEM lane; tmem_wait_st() ends them.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                 "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+                 "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+                 "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+                 "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+{
+    return pack_bf16x2(__float_as_uint(lo), __float_as_uint(hi));
+}
+
+// 128 threads of a warpgroup (named barrier 1 + wg).
+__device__ __forceinline__ void wg_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+// ------------------------------------------------------------ sequences
+// Offsets and lengths come from device memory and are clamped to the
+// tensors, so no value of theirs reaches outside an operand.
+struct Seq {
+    int q0, ql, k0, kl;
+};
+
+__device__ __forceinline__ Seq seq_of(const Params &p, int b)
+{
+    Seq s;
+    const int qa = min(max(__ldg(p.cu_q + b), 0), p.Tq), qb = min(max(__ldg(p.cu_q + b + 1), qa), p.Tq);
+    const int ka = min(max(__ldg(p.cu_k + b), 0), p.Tk), kb = min(max(__ldg(p.cu_k + b + 1), ka), p.Tk);
+    s.q0 = qa;
+    s.ql = qb - qa;
+    s.k0 = ka;
+    s.kl = kb - ka;
+    if (p.used_k) s.kl = min(max(__ldg(p.used_k + b), 0), s.kl);
+    return s;
+}
+
+// Keys that query token i of the sequence sees (possibly none).  The causal
+// mask is aligned to the end: the last query sees every key.
+__device__ __forceinline__ int seen(const Params &p, const Seq &s, int i)
+{
+    if (!p.causal) return s.kl;
+    return min(max(i + 1 + s.kl - s.ql, 0), s.kl);
+}
+
+__device__ __forceinline__ int warp_incl_scan(int v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// Finds the sequence that holds item x when sequence b holds count(b) items;
+// every lane of the warp gets (b, x - items before b).
+template <class F>
+__device__ __forceinline__ void locate(int B, int x, int lane, F count, int &b_out, int &local)
+{
+    int before = 0;
+    b_out = B - 1;
+    local = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int b = b0 + lane;
+        const int n = b < B ? count(b) : 0;
+        const int inc = warp_incl_scan(n, lane);
+        const int total = __shfl_sync(0xFFFFFFFFu, inc, 31);
+        if (x < before + total) {
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, x < before + inc);
+            const int l = __ffs(hit) - 1;
+            b_out = b0 + l;
+            local = x - before - __shfl_sync(0xFFFFFFFFu, inc - n, l);
+            return;
+        }
+        before += total;
+    }
+}
+
+__device__ __forceinline__ long long warp_sum(long long v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+constexpr int kNoSplit = 1 << 28;          // key tiles of a part when keys are not split
+
+// Parts (SPLIT) or units (PAIR) that a split launch aims at.
+__host__ __device__ constexpr long long split_target(bool split, int sms) { return (split ? 8ll : 3ll) * sms; }
+
+// Host helpers (attn_api.cu).
+int head_map5(CUtensorMap *map, const rc_heads &h, int P, int T, int Hkv, int G, int D, int box_tokens);
+int head_map4(CUtensorMap *map, const rc_heads &h, int P, int T, int Hkv, int D);
+cudaError_t launch_attn_fwd(const Params &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                            bool split, cudaStream_t st);
+
+} // namespace attn
+} // namespace rc

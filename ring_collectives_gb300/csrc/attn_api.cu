@@ -1,0 +1,213 @@
+// attn_api.cu -- the C entry points of the attention operators: argument
+// checks, tensor maps, the form and split of a launch, partial-result space.
+#include <cudaTypedefs.h>
+
+#include <cmath>
+#include <mutex>
+
+#include "attn.cuh"
+
+namespace rc {
+namespace attn {
+
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) ==
+                cudaSuccess &&
+            qr == cudaDriverEntryPointSuccess)
+            fn = (PFN_cuTensorMapEncodeTiled_v12000)f;
+    });
+    return fn;
+}
+
+static int encode(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                  const cuuint32_t *box)
+{
+    auto fn = encode_fn();
+    if (!fn) return set_error(RC_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available from the driver");
+    cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), dims,
+                          strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return set_error(RC_ERR_INVALID, "tensor map encoding failed (CUresult %d)", (int)r);
+    return RC_OK;
+}
+
+// Query-side heads as [P][Hkv][T][G][D], a box of box_tokens tokens of one
+// group.  Columns past D and tokens past T read as zero.
+int head_map5(CUtensorMap *map, const rc_heads &h, int P, int T, int Hkv, int G, int D, int box_tokens)
+{
+    const cuuint64_t dims[5] = {(cuuint64_t)D, (cuuint64_t)G, (cuuint64_t)T, (cuuint64_t)Hkv, (cuuint64_t)P};
+    const cuuint64_t strides[4] = {h.head, h.token, (cuuint64_t)G * h.head, h.slot};
+    const cuuint32_t box[5] = {64, (cuuint32_t)G, (cuuint32_t)box_tokens, 1, 1};
+    return encode(map, h.base, 5, dims, strides, box);
+}
+
+// Key-side heads as [P][Hkv][T][D], a box of 128 tokens.
+int head_map4(CUtensorMap *map, const rc_heads &h, int P, int T, int Hkv, int D)
+{
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)T, (cuuint64_t)Hkv, (cuuint64_t)P};
+    const cuuint64_t strides[3] = {h.token, h.head, h.slot};
+    const cuuint32_t box[4] = {64, KT, 1, 1};
+    return encode(map, h.base, 4, dims, strides, box);
+}
+
+// Checks one operand and gives the strides of extents of 1 a valid value.
+static int check_heads(rc_heads &h, const char *name, int P, int T, int H, int D)
+{
+    if (!h.base) return set_error(RC_ERR_INVALID, "%s is null", name);
+    const size_t least = (size_t)D * 2;
+    if (H == 1) h.head = least;
+    if (T == 1) h.token = least;
+    if (P == 1) h.slot = least;
+    if (((uintptr_t)h.base | h.slot | h.token | h.head) & 15u)
+        return set_error(RC_ERR_INVALID, "%s: base and strides must be multiples of 16 bytes", name);
+    if (h.head < least || h.token < least || h.slot < least)
+        return set_error(RC_ERR_INVALID, "%s: a stride is below the %zu bytes of a head", name, least);
+    if (h.slot >> 40 || h.token >> 40 || h.head >> 32)
+        return set_error(RC_ERR_INVALID, "%s: a stride is too large", name);
+    return RC_OK;
+}
+
+static int check_sizes(const rc_attn_args &a)
+{
+    if (a.P < 1 || a.P > RC_MAX_P) return set_error(RC_ERR_INVALID, "P=%d outside 1..%d", a.P, RC_MAX_P);
+    if (a.B < 1 || a.Tq < 0 || a.Tk < 0) return set_error(RC_ERR_INVALID, "need B >= 1, Tq >= 0 and Tk >= 0 (got %d, %d, %d)", a.B, a.Tq, a.Tk);
+    if (a.Hq < 1 || a.Hkv < 1 || a.Hq % a.Hkv || a.Hq / a.Hkv > KT || a.Hq > 65536)
+        return set_error(RC_ERR_INVALID, "need Hq a multiple of Hkv and Hq/Hkv <= %d (got %d, %d)", KT, a.Hq, a.Hkv);
+    if (a.D < 8 || a.D > 128 || a.D % 8) return set_error(RC_ERR_INVALID, "D=%d is not a multiple of 8 up to 128", a.D);
+    if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return set_error(RC_ERR_INVALID, "scale must be positive and finite");
+    if (a.causal != 0 && a.causal != 1) return set_error(RC_ERR_INVALID, "causal must be 0 or 1");
+    if (a.reserved) return set_error(RC_ERR_INVALID, "reserved must be 0");
+    return RC_OK;
+}
+
+static Strided strided(const rc_heads &h) { return Strided{(char *)h.base, h.slot, h.token, h.head}; }
+
+static void fill(Params &p, const rc_attn_args &a)
+{
+    p.lse = a.lse;
+    p.cu_q = a.cu_q;
+    p.cu_k = a.cu_k;
+    p.used_k = a.used_k;
+    p.P = a.P;
+    p.B = a.B;
+    p.Tq = a.Tq;
+    p.Tk = a.Tk;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = a.Hq / a.Hkv;
+    p.D = a.D;
+    p.causal = a.causal;
+    p.scale = a.scale;
+    p.TT = KT / p.G;
+}
+
+// The form of a forward launch and the bytes of its partial results.
+struct FwdPlan {
+    bool split;
+    size_t units, bytes;
+};
+
+// SPLIT when the queries of a sequence fill at most one row tile on average.
+// Measured on GB300: see the table in attn_fwd.cu.
+static FwdPlan plan_fwd(Params &p, int sms)
+{
+    FwdPlan f{};
+    f.split = (long long)p.Tq * p.G <= (long long)KT * p.B;
+    p.sms = sms;
+    p.TPU = f.split ? p.TT : 2 * p.TT;
+    const long long HP = (long long)p.P * p.Hkv, tiles = (p.Tq + p.TPU - 1) / p.TPU;
+    p.may_split = f.split ? (tiles > p.B ? tiles : p.B) * HP < 4ll * sms : tiles * HP < 2ll * sms;
+    p.part_rows = p.G * (p.TT < p.Tq ? p.TT : p.Tq);
+    if (p.may_split) {
+        long long n0 = p.Tq / p.TPU + p.B;     // row tiles (pairs), at most
+        if (n0 > p.Tq) n0 = p.Tq;
+        f.units = (size_t)(n0 * HP + split_target(f.split, sms));
+        const size_t DP = p.D <= 64 ? 64 : 128;
+        f.bytes = 2 * f.units * (size_t)p.part_rows * (DP + 1) * 4;
+    }
+    return f;
+}
+
+constexpr size_t kWsHead = 256;   // the status header of a caller's workspace, padded
+
+static int take_workspace(const rc_attn_args &a, size_t bytes, Params &p, char **scratch)
+{
+    uint32_t *unused = nullptr;
+    int sms = 0;
+    if (a.workspace && ((uintptr_t)a.workspace & 255u))
+        return set_error(RC_ERR_INVALID, "workspace must be 256-byte aligned");
+    int rc_ = prepare_workspace_ext(a.workspace, a.ws_bytes, a.workspace ? (kWsHead - sizeof(WsHeader) + bytes + 3) / 4 : 0,
+                                    &p.hdr, &unused, &sms, &p.timeout_ns);
+    if (rc_) return rc_;
+    if (a.workspace) {
+        *scratch = (char *)a.workspace + kWsHead;
+        return RC_OK;
+    }
+    void *s = nullptr;
+    if (bytes && (rc_ = prepare_scratch(bytes, &s))) return rc_;
+    *scratch = (char *)s;
+    return RC_OK;
+}
+
+static int run_fwd(const rc_attn_args *args, void *stream)
+{
+    if (!args) return set_error(RC_ERR_INVALID, "null args");
+    rc_attn_args a = *args;
+    int rc_ = check_sizes(a);
+    if (rc_) return rc_;
+    if (a.Tq == 0) return RC_OK;
+    if ((rc_ = check_heads(a.q, "q", a.P, a.Tq, a.Hq, a.D)) || (rc_ = check_heads(a.out, "out", a.P, a.Tq, a.Hq, a.D)))
+        return rc_;
+    if (a.Tk && ((rc_ = check_heads(a.k, "k", a.P, a.Tk, a.Hkv, a.D)) || (rc_ = check_heads(a.v, "v", a.P, a.Tk, a.Hkv, a.D))))
+        return rc_;
+    if (!a.cu_q || !a.cu_k) return set_error(RC_ERR_INVALID, "cu_q or cu_k is null");
+    if (a.out.base == a.q.base || (a.Tk && (a.out.base == a.k.base || a.out.base == a.v.base)))
+        return set_error(RC_ERR_INVALID, "out overlaps an input");
+    int sms = 0;
+    if ((rc_ = device_sms(&sms))) return rc_;
+    Params p{};
+    fill(p, a);
+    const FwdPlan f = plan_fwd(p, sms);
+    char *scratch = nullptr;
+    if ((rc_ = take_workspace(a, f.bytes, p, &scratch))) return rc_;
+    p.part_o = (float *)scratch;
+    p.part_lse = (float *)(scratch + 2 * f.units * (size_t)p.part_rows * (p.D <= 64 ? 64 : 128) * 4);
+    p.out = strided(a.out);
+    p.v = (const char *)a.v.base;
+    p.v_slot = a.v.slot;
+    p.v_token = a.v.token;
+    p.v_head = a.v.head;
+    CUtensorMap mq, mk, mv;
+    if ((rc_ = head_map5(&mq, a.q, a.P, a.Tq, a.Hkv, p.G, a.D, p.TT))) return rc_;
+    if (a.Tk) {
+        if ((rc_ = head_map4(&mk, a.k, a.P, a.Tk, a.Hkv, a.D)) || (rc_ = head_map4(&mv, a.v, a.P, a.Tk, a.Hkv, a.D)))
+            return rc_;
+    } else {
+        mk = mv = mq;   // no key exists, so neither is read
+    }
+    const cudaError_t e = launch_attn_fwd(p, mq, mk, mv, f.split, (cudaStream_t)stream);
+    if (e != cudaSuccess) return set_error(RC_ERR_CUDA, "attn_fwd launch: %s", cudaGetErrorString(e));
+    return RC_OK;
+}
+
+} // namespace attn
+} // namespace rc
+
+extern "C" int attn_fwd(const rc_attn_args *args, void *stream) { return rc::attn::run_fwd(args, stream); }
+
+extern "C" size_t attn_fwd_workspace_bytes(const rc_attn_args *args)
+{
+    using namespace rc::attn;
+    int sms = 0;
+    if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
+    Params p{};
+    fill(p, *args);
+    return kWsHead + plan_fwd(p, sms).bytes;
+}

@@ -1,0 +1,743 @@
+// attn_fwd.cu -- attention over packed sequences on the 5th-generation tensor
+// cores, forward.
+//
+//   s_ij = scale q_i . k_j over the keys j that token i sees,
+//   o_i = sum_j exp(s_ij - m_i) v_j / l_i,  l_i = sum_j exp(s_ij - m_i),
+//   lse_i = m_i + ln l_i
+// in one pass over the keys: a running maximum m and sum l for each row, both
+// in binary32, and an accumulator O that is rescaled when m moves.  m is only
+// moved when it would grow by more than 2^8 (any m gives the same quotient;
+// the sums stay far inside binary32), which almost never happens after the
+// first tile, so the accumulator stays in TMEM.  The weights exp(s - m) are
+// rounded to bf16 for the second product -- the tensor cores' input type --
+// while l sums them unrounded.
+//
+// One persistent block per SM, 12 warps:
+//   warps 0-3, 4-7  softmax of row tile 0 / 1: one thread a row, so maxima and
+//                   sums need no shuffles; S arrives in TMEM, P goes back to
+//                   TMEM over S and is the A operand of the second product
+//   warp 8          TMA loads: query tiles, then key and value tiles through
+//                   one ring of stages in the order the MMAs consume them
+//   warp 9          MMA issue: S_t = Q_t K^T, O_t += P_t V for the two tiles in
+//                   turn, so one tile's softmax runs under the other's MMAs
+//   warps 10-11     guard: in tiles that some row does not see whole, clears
+//                   value rows past the end and non-finite values, because
+//                   0 x inf would reach rows that must not see them; rows that
+//                   do see one add it in the epilogue
+// Two forms.  PAIR: the two row tiles are 256 consecutive rows and share every
+// key tile.  SPLIT (few rows per sequence, single tokens above all): both are
+// the same rows, over two halves of a key range, so the loads of one hide the
+// latency of the other and the kernel runs at the rate of the key cache.
+// When there are too few units to fill the GPU, key ranges are split further
+// and k_attn_join adds the partial results in a fixed order.
+#include <mutex>
+
+#include "attn.cuh"
+
+namespace rc {
+namespace attn {
+
+constexpr int FWD_THREADS = 384;
+
+template <int DP, bool SPLIT>
+struct FwdCfg {
+    static constexpr int KV_STAGE = KT * DP * 2;
+    static constexpr int NQ = SPLIT ? 1 : 2;
+    static constexpr int STAGES = DP == 128 ? (SPLIT ? 6 : 5) : 8;
+    static constexpr int SMEM = (NQ + STAGES) * KV_STAGE + 1024 + 1024;
+};
+
+// The split of this launch's keys, the same in every warp and kernel of it.
+struct Plan {
+    int cs;        // key tiles per part (a huge number: no split)
+    int units;     // units of one key head
+};
+
+__device__ __forceinline__ int parts_of(int kt, int cs)
+{
+    return max(1, (kt + cs - 1) / cs);
+}
+
+template <bool SPLIT>
+__device__ __forceinline__ int units_per_tile(int kt, int cs)
+{
+    const int np = parts_of(kt, cs);
+    return SPLIT ? (np + 1) / 2 : np;
+}
+
+// Splitting rule (p.may_split: decided on the host, which sizes the partial
+// results by it).  PAIR: when unsplit units would not give two waves of
+// blocks, parts of at least 4 key tiles, about 3 units per SM.  SPLIT: below 4
+// units per SM, parts of at least 2 tiles, about 8 parts per SM (two to a unit).
+template <bool SPLIT>
+__device__ Plan make_plan(const Params &p, int lane)
+{
+    const int HP = p.P * p.Hkv;
+    Plan pl;
+    pl.cs = kNoSplit;
+    if (p.may_split) {
+        long long work = 0;
+        for (int b = lane; b < p.B; b += 32) {
+            const Seq s = seq_of(p, b);
+            work += (long long)((s.ql + p.TPU - 1) / p.TPU) * ((s.kl + KT - 1) / KT);
+        }
+        work = warp_sum(work) * HP;
+        const long long target = split_target(SPLIT, p.sms), c = (work + target - 1) / target;
+        pl.cs = (int)max(c, SPLIT ? 2ll : 4ll);
+    }
+    long long u = 0;
+    for (int b = lane; b < p.B; b += 32) {
+        const Seq s = seq_of(p, b);
+        u += (long long)((s.ql + p.TPU - 1) / p.TPU) * units_per_tile<SPLIT>((s.kl + KT - 1) / KT, pl.cs);
+    }
+    pl.units = (int)warp_sum(u);
+    return pl;
+}
+
+struct Unit {
+    Seq s;
+    int hk, slot;
+    int tok;         // first query token of row tile 0, within the sequence
+    int ntok[2];     // valid tokens of the row tiles
+    int jb[2], n[2]; // first key tile and number of key tiles of each row tile
+    int guard;       // key tiles from here on are not seen whole by every row
+    int nparts;      // parts of this unit's rows (1: results are final)
+    int index;       // unit number (partial results); -1: no more units
+    int poison;      // set by the guard when it cleared a value of this unit
+};
+constexpr int UNITS = 4;            // units in the block's ring
+constexpr int UNIT_READERS = 11;    // warps that release one: MMA, guard, softmax
+
+template <bool SPLIT>
+__device__ Unit unit_of(const Params &p, const Plan &pl, int u, int lane)
+{
+    Unit w;
+    const int HP = p.P * p.Hkv;
+    const int x = u / HP, hp = u % HP;
+    w.index = u;
+    w.hk = hp % p.Hkv;
+    w.slot = hp / p.Hkv;
+    int b, local;
+    locate(p.B, x, lane,
+           [&](int bb) {
+               const Seq s = seq_of(p, bb);
+               return ((s.ql + p.TPU - 1) / p.TPU) * units_per_tile<SPLIT>((s.kl + KT - 1) / KT, pl.cs);
+           },
+           b, local);
+    w.s = seq_of(p, b);
+    const int kt = (w.s.kl + KT - 1) / KT, cs = pl.cs;
+    const int upt = units_per_tile<SPLIT>(kt, cs), nt = (w.s.ql + p.TPU - 1) / p.TPU;
+    const int tile = nt - 1 - local / upt, c = local % upt;   // the tiles that see most keys first
+    w.nparts = parts_of(kt, cs);
+    w.tok = tile * p.TPU;
+    const int left = w.s.ql - w.tok;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int first = SPLIT ? w.tok : w.tok + t * p.TT;
+        w.ntok[t] = SPLIT ? min(left, p.TT) : min(max(left - t * p.TT, 0), p.TT);
+        const int part = SPLIT ? 2 * c + t : c;
+        const int see = w.ntok[t] > 0 ? seen(p, w.s, first + w.ntok[t] - 1) : 0;
+        const int je = min((see + KT - 1) / KT, cs >= kNoSplit ? kNoSplit : (part + 1) * cs);
+        w.jb[t] = part * (cs >= kNoSplit ? 0 : cs);
+        w.n[t] = part < w.nparts ? max(0, je - w.jb[t]) : 0;
+    }
+    w.guard = seen(p, w.s, w.tok) / KT;
+    w.poison = 0;
+    return w;
+}
+
+// Ring entries in the order the MMAs consume them.  PAIR: K_0, V_0, K_1, V_1,
+// ... (each serves both row tiles).  SPLIT: K0_0 K1_0 | V0_0 K0_1 | V1_0 K1_1 |
+// V0_1 ... with the entries of finished halves left out.  f(is_v, t, j).
+template <bool SPLIT, class F>
+__device__ __forceinline__ void for_entries(const Unit &w, F f)
+{
+    if (!SPLIT) {
+        const int n = max(w.n[0], w.n[1]);
+        if (n > 0 && !f(false, 0, 0)) return;
+        for (int j = 0; j < n; ++j) {
+            if (!f(true, 0, j)) return;
+            if (j + 1 < n && !f(false, 0, j + 1)) return;
+        }
+    } else {
+        const int n = max(w.n[0], w.n[1]);
+        for (int t = 0; t < 2; ++t)
+            if (w.n[t] > 0 && !f(false, t, 0)) return;
+        for (int j = 0; j < n; ++j)
+            for (int t = 0; t < 2; ++t) {
+                if (j < w.n[t] && !f(true, t, j)) return;
+                if (j + 1 < w.n[t] && !f(false, t, j + 1)) return;
+            }
+    }
+}
+
+__device__ __forceinline__ bool nonfinite_bf16(uint32_t bits16) { return (bits16 & 0x7F80u) == 0x7F80u; }
+
+template <int DP, bool SPLIT>
+__global__ void __launch_bounds__(FWD_THREADS, 1)
+    k_attn_fwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+               const __grid_constant__ CUtensorMap map_v, const Params p)
+{
+    using C = FwdCfg<DP, SPLIT>;
+    constexpr int NST = C::STAGES, STAGE = C::KV_STAGE, BLK = KT * 128;   // 64-column blocks of 16 KiB
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    uint8_t *const gbase = smem_raw + (base - raw);
+    const uint32_t sQ = base, sKV = base + C::NQ * STAGE;
+    uint8_t *const gKV = gbase + C::NQ * STAGE;
+    uint8_t *const ctl = gKV + NST * STAGE;
+    const uint32_t bars = smem_u32(ctl);
+    const uint32_t full_bar = bars, empty_bar = bars + 8 * NST, guard_bar = bars + 16 * NST;
+    const uint32_t q_full = bars + 24 * NST, q_empty = q_full + 8;
+    const uint32_t s_full = q_full + 16, p_ready = q_full + 32, o_full = q_full + 48, drain_bar = q_full + 64;
+    uint32_t *const tmem_slot = (uint32_t *)(ctl + 24 * NST + 72);
+    int *const abort_flag = (int *)(ctl + 24 * NST + 76);
+    const uint32_t u_full = q_full + 80, u_empty = u_full + 8 * UNITS;
+    Unit *const units = (Unit *)(ctl + 24 * NST + 80 + 16 * UNITS);
+    static_assert(24 * NST + 80 + 16 * UNITS + UNITS * sizeof(Unit) <= 1024, "control area");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(full_bar + 8 * s, 1);
+            mbar_init(empty_bar + 8 * s, 3);     // the MMAs' commit and the two guard warps
+            mbar_init(guard_bar + 8 * s, 2);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(s_full + 8 * t, 1);
+            mbar_init(p_ready + 8 * t, 4);
+            mbar_init(o_full + 8 * t, 1);
+        }
+        mbar_init(drain_bar, 1);
+        for (int i = 0; i < UNITS; ++i) {
+            mbar_init(u_full + 8 * i, 1);
+            mbar_init(u_empty + 8 * i, UNIT_READERS);
+        }
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_q) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_v) : "memory");
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;        // S/P tiles at columns 0 and 128, O tiles at 256 and 384
+    const Abort ab{abort_flag, p.hdr, p.timeout_ns, 0xB1u, 0};
+
+    // The next unit of the block's ring; null when there is none or the block gave up.
+    auto next_unit = [&](uint32_t it) -> const Unit * {
+        const int got = lane == 0 ? (int)wait_bar(u_full + 8 * (it % UNITS), (it / UNITS) & 1, ab, 12) : 0;
+        if (!__shfl_sync(0xFFFFFFFFu, got, 0)) return nullptr;
+        __syncwarp();
+        const Unit *w = units + it % UNITS;
+        return w->index < 0 ? nullptr : w;
+    };
+    auto release_unit = [&](uint32_t it) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_empty + 8 * (it % UNITS));
+    };
+
+    // 384 x 168 registers at launch = 256 x 216 + 128 x 72.  Set inside
+    // the branches: ptxas allocates the code that a setmaxnreg dominates by it.
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8) {
+            // ---------------- units, one ahead of the loads, and the TMA loads
+            const Plan pl = make_plan<SPLIT>(p, lane);
+            const int total = pl.units * p.P * p.Hkv;
+            auto publish = [&](uint32_t it, const Unit &w) {
+                bool ok = true;
+                if (lane == 0) {
+                    ok = wait_bar(u_empty + 8 * (it % UNITS), ((it / UNITS) & 1) ^ 1u, ab, 13);
+                    if (ok) {
+                        units[it % UNITS] = w;
+                        mbar_arrive(u_full + 8 * (it % UNITS));
+                    }
+                }
+                return __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+            };
+            uint32_t e = 0, nq = 0, it = 0;
+            int u = blockIdx.x;
+            Unit next;
+            if (u < total) next = unit_of<SPLIT>(p, pl, u, lane);
+            else next.index = -1;
+            bool ok = publish(0, next);
+            while (ok && next.index >= 0) {
+                const Unit w = next;
+                u += gridDim.x;
+                if (u < total) next = unit_of<SPLIT>(p, pl, u, lane);
+                else next.index = -1;
+                ok = publish(++it, next);
+                if (!ok || max(w.n[0], w.n[1]) == 0) continue;
+                if (lane == 0) {
+                    ok = wait_bar(q_empty, (nq & 1) ^ 1u, ab, 1);
+                    if (ok) {
+                        const uint32_t box = (uint32_t)(p.G * p.TT) * 128u;
+                        const int tiles = !SPLIT && w.ntok[1] > 0 ? 2 : 1;
+                        mbar_expect_tx(q_full, box * (DP / 64) * tiles);
+                        for (int t = 0; t < tiles; ++t)
+                            for (int d = 0; d < DP / 64; ++d)
+                                tma_load_5d(sQ + t * STAGE + d * BLK, &map_q, d * 64, 0, w.s.q0 + w.tok + t * p.TT, w.hk,
+                                            w.slot, q_full);
+                        ++nq;
+                        for_entries<SPLIT>(w, [&](bool is_v, int t, int j) {
+                            const uint32_t st = e % NST;
+                            if (!wait_bar(empty_bar + 8 * st, ((e / NST) & 1) ^ 1u, ab, 2)) {
+                                ok = false;
+                                return false;
+                            }
+                            mbar_expect_tx(full_bar + 8 * st, STAGE);
+                            for (int d = 0; d < DP / 64; ++d)
+                                tma_load_4d(sKV + st * STAGE + d * BLK, is_v ? &map_v : &map_k, d * 64,
+                                            w.s.k0 + (w.jb[t] + j) * KT, w.hk, w.slot, full_bar + 8 * st);
+                            ++e;
+                            return true;
+                        });
+                    }
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+            }
+            if (lane == 0 && *(volatile int *)abort_flag) {
+                // let the copies in flight land before the block gives up its shared memory
+                for (uint32_t s = 0; s < NST; ++s)
+                    if (e > s) wait_bar(full_bar + 8 * s, ((e - 1 - s) / NST) & 1, ab, 9, true);
+                if (nq) wait_bar(q_full, (nq - 1) & 1, ab, 9, true);
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ---------------- MMA issuer
+            constexpr uint32_t kIdS = idesc_bf16_f32(KT, KT);
+            constexpr uint32_t kIdO = idesc_bf16_f32(KT, DP) | kIdescBMnMajor;
+            uint32_t e = 0, nq = 0, guard_phase = 0, np[2] = {0, 0};
+            bool ok = true;
+            const Unit *wp;
+            for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
+                const Unit &w = *wp;
+                const int n = max(w.n[0], w.n[1]);
+                if (n == 0) continue;
+                if (lane == 0) {
+                    ok = wait_bar(q_full, nq & 1, ab, 3);
+                    // S_t = Q_t K^T with the keys of ring stage st
+                    auto score = [&](int t, uint32_t st) {
+    #pragma unroll
+                        for (int kk = 0; kk < DP / 16; ++kk)
+                            tc_mma(tmem + t * KT, smem_desc_sw128(sQ + (SPLIT ? 0 : t * STAGE) + (kk >> 2) * BLK) + 2 * (kk & 3),
+                                   smem_desc_sw128(sKV + st * STAGE + (kk >> 2) * BLK) + 2 * (kk & 3), kIdS, kk != 0);
+                        tc_commit(s_full + 8 * t);
+                    };
+                    // O_t += P_t V with the values of ring stage st
+                    auto weigh = [&](int t, uint32_t st, bool first) {
+                        const uint64_t vd = smem_desc_mn_sw128(sKV + st * STAGE, BLK);
+    #pragma unroll
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            tc_mma_ta(tmem + 256 + t * KT, tmem + t * KT + kk * 8, vd + 128 * kk, kIdO, !first || kk);
+                    };
+                    auto take = [&](uint32_t en, bool guarded) {
+                        const uint32_t st = en % NST;
+                        if (guarded) {
+                            if (!wait_bar(guard_bar + 8 * st, (guard_phase >> st) & 1, ab, 5)) return false;
+                            guard_phase ^= 1u << st;
+                            return true;
+                        }
+                        return wait_bar(full_bar + 8 * st, (en / NST) & 1, ab, 4);
+                    };
+                    auto weights = [&](int t) { return wait_bar(p_ready + 8 * t, np[t]++ & 1, ab, 6); };
+                    bool last_s = false;
+                    auto q_done = [&](int left) {
+                        if (left == 0 && !last_s) {
+                            tc_commit(q_empty);
+                            last_s = true;
+                        }
+                    };
+                    int left = w.n[0] + w.n[1];
+                    if (!SPLIT) {
+                        if (ok) ok = take(e, false);
+                        if (ok) {
+                            tc_fence_after();
+                            for (int t = 0; t < 2; ++t)
+                                if (w.n[t] > 0) score(t, e % NST), --left;
+                            tc_commit(empty_bar + 8 * (e % NST));
+                            q_done(left);
+                            ++e;
+                        }
+                        for (int j = 0; j < n && ok; ++j) {
+                            const uint32_t ev = e, ek = e + 1;
+                            const bool more = j + 1 < n;
+                            ok = take(ev, w.jb[0] + j >= w.guard);
+                            bool have_k = false;
+                            for (int t = 0; t < 2 && ok; ++t) {
+                                if (j >= w.n[t]) continue;
+                                if (!(ok = weights(t))) break;
+                                tc_fence_after();
+                                weigh(t, ev % NST, j == 0);
+                                if (j + 1 == w.n[t]) tc_commit(o_full + 8 * t);
+                                if (t == 1 || j >= w.n[1]) tc_commit(empty_bar + 8 * (ev % NST));
+                                if (j + 1 < w.n[t]) {
+                                    if (!have_k && !(ok = take(ek, false))) break;
+                                    have_k = true;
+                                    tc_fence_after();
+                                    score(t, ek % NST);
+                                    --left;
+                                }
+                            }
+                            if (more && ok) tc_commit(empty_bar + 8 * (ek % NST));
+                            q_done(left);
+                            e += more ? 2 : 1;
+                        }
+                    } else {
+                        for (int t = 0; t < 2 && ok; ++t)
+                            if (w.n[t] > 0) {
+                                if (!(ok = take(e, false))) break;
+                                tc_fence_after();
+                                score(t, e % NST);
+                                tc_commit(empty_bar + 8 * (e % NST));
+                                --left;
+                                ++e;
+                            }
+                        q_done(left);
+                        for (int j = 0; j < n && ok; ++j)
+                            for (int t = 0; t < 2 && ok; ++t) {
+                                if (j >= w.n[t]) continue;
+                                if (!(ok = take(e, w.jb[t] + j >= w.guard)) || !(ok = weights(t))) break;
+                                tc_fence_after();
+                                weigh(t, e % NST, j == 0);
+                                tc_commit(empty_bar + 8 * (e % NST));
+                                if (j + 1 == w.n[t]) tc_commit(o_full + 8 * t);
+                                ++e;
+                                if (j + 1 < w.n[t]) {
+                                    if (!(ok = take(e, false))) break;
+                                    tc_fence_after();
+                                    score(t, e % NST);
+                                    tc_commit(empty_bar + 8 * (e % NST));
+                                    --left;
+                                    ++e;
+                                }
+                                q_done(left);
+                            }
+                    }
+                    ++nq;
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+            }
+            if (lane == 0) {
+                tc_commit(drain_bar);
+                wait_bar(drain_bar, 0, ab, 10, true);
+            }
+            __syncwarp();
+        } else {
+            // ---------------- guard: rows [64 g, 64 g + 64) of a value tile
+            const int g = warp - 10;
+            uint32_t e = 0;
+            bool ok = true;
+            const Unit *wp;
+            for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
+                const Unit &w = *wp;
+                for_entries<SPLIT>(w, [&](bool is_v, int t, int j) {
+                    // Every entry is waited for and released, in order: a guard that
+                    // only looked at its own entries could meet a stage's barrier one
+                    // whole round early or late, where the phase parity says nothing.
+                    const uint32_t en = e++, st = en % NST;
+                    const int jt = w.jb[t] + j;
+                    int got = lane == 0 ? (int)wait_bar(full_bar + 8 * st, (en / NST) & 1, ab, 7) : 0;
+                    got = __shfl_sync(0xFFFFFFFFu, got, 0);
+                    if (!got) {
+                        ok = false;
+                        return false;
+                    }
+                    __syncwarp();
+                    if (!is_v || jt < w.guard) {
+                        if (lane == 0) mbar_arrive(empty_bar + 8 * st);
+                        return true;
+                    }
+                    const int valid = w.s.kl - jt * KT;    // rows from here on are past the end
+                    bool found = false;
+    #pragma unroll 4
+                    for (int i = lane; i < 64 * 8 * (DP / 64); i += 32) {
+                        const int row = g * 64 + ((i >> 3) & 63), blk = i >> 9;
+                        uint4 *const a = (uint4 *)(gKV + st * STAGE + blk * BLK + row * 128 + (i & 7) * 16);
+                        if (row >= valid) {
+                            *a = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        uint32_t x[4] = {a->x, a->y, a->z, a->w};
+                        bool bad = false;
+    #pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            if (nonfinite_bf16(x[h])) x[h] &= 0xFFFF0000u, bad = true;
+                            if (nonfinite_bf16(x[h] >> 16)) x[h] &= 0x0000FFFFu, bad = true;
+                        }
+                        if (bad) {
+                            *a = make_uint4(x[0], x[1], x[2], x[3]);
+                            found = true;
+                        }
+                    }
+                    if (found) *(volatile int *)&units[it % UNITS].poison = 1;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(guard_bar + 8 * st);
+                        mbar_arrive(empty_bar + 8 * st);
+                    }
+                    return true;
+                });
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // ---------------- softmax and epilogue of row tile t
+        const int t = warp >> 2;
+        const int r = threadIdx.x & 127;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_off + t * KT, tO = tmem + lane_off + 256 + t * KT;
+        const float c = p.scale * kLog2e;
+        uint32_t ns = 0, no = 0;
+        bool ok = true;
+        const Unit *wp;
+        for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
+            const Unit &w = *wp;
+            const int n = w.n[t];
+            const int ti = r / p.G;                                    // token of this row within the tile
+            const int tok = (SPLIT ? w.tok : w.tok + t * p.TT) + ti;   // and within the sequence
+            const bool valid = ti < w.ntok[t];
+            const int lim = valid ? seen(p, w.s, tok) : 0;             // keys this row sees
+            int here = lim - w.jb[t] * KT;                             // and from this key tile on
+            float m = -INFINITY, mc = 0.f, l = 0.f;                    // mc = c * m, 0 while nothing was seen
+            for (int j = 0; j < n; ++j, here -= KT) {
+                if (!(ok = __all_sync(0xFFFFFFFFu, wait_bar(s_full + 8 * t, ns & 1, ab, 8)))) break;
+                ++ns;
+                tc_fence_after();
+                uint32_t v[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + q * 32, v[q]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_wait_ld32(v[q]);
+                if (__any_sync(0xFFFFFFFFu, here < KT)) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (q * 32 + i >= here) v[q][i] = 0xFF800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(v[q][i]), __uint_as_float(v[q][i + 1])));
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                // Move m when it would grow by more than 8 / c, or off -inf.
+                const bool move = mt > m && (m == -INFINITY || (mt - m) * c > 8.f);
+                if (__any_sync(0xFFFFFFFFu, move)) {
+                    const float f = !move ? 1.f : (m == -INFINITY ? 0.f : ex2((m - mt) * c));
+                    if (move) {
+                        m = mt;
+                        mc = mt * c;
+                    }
+                    l *= f;
+                    if (j > 0) {
+                        uint32_t o[32];
+#pragma unroll
+                        for (int q = 0; q < DP / 32; ++q) {
+                            tmem_ld32(tO + q * 32, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32(tO + q * 32, o);
+                        }
+                    }
+                }
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float a = ex2(fmaf(__uint_as_float(v[q][2 * i]), c, -mc));
+                        const float b = ex2(fmaf(__uint_as_float(v[q][2 * i + 1]), c, -mc));
+                        sum[i & 3] += a + b;
+                        pk[i] = pack2(a, b);
+                    }
+                    tmem_st16(tS + q * 16, pk);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + 8 * t);
+            }
+            if (!ok) break;
+            if (n > 0) {
+                if (!(ok = __all_sync(0xFFFFFFFFu, wait_bar(o_full + 8 * t, no & 1, ab, 11)))) break;
+                ++no;
+                tc_fence_after();
+            }
+            const int head = w.hk * p.G + r % p.G;
+            const bool final_ = w.nparts == 1;
+            if (SPLIT && final_ && t == 1) continue;                  // one part: row tile 0 has it
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const size_t qi = (size_t)w.s.q0 + tok;
+            const bool add_back = *(volatile const int *)&w.poison != 0;
+            char *const dst = p.out.base + w.slot * p.out.slot + qi * p.out.token + head * p.out.head;
+            float *const part = p.part_o + ((size_t)(2 * w.index + t) * p.part_rows + r) * DP;
+#pragma unroll
+            for (int q = 0; q < DP / 32; ++q) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(tO + q * 32, o);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0u;
+                }
+                if (!valid) continue;
+                float f[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
+                if (add_back) {
+                    // non-finite values that this row does see, taken out by the guard
+                    const int k1 = min(lim, (w.jb[t] + n) * KT);
+                    for (int k = max(w.guard, w.jb[t]) * KT; k < k1; ++k) {
+                        const uint16_t *vr = (const uint16_t *)(p.v + w.slot * p.v_slot +
+                                                                ((size_t)w.s.k0 + k) * p.v_token + w.hk * p.v_head);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (q * 32 + i < p.D) {
+                                const uint32_t x = vr[q * 32 + i];
+                                if (nonfinite_bf16(x)) f[i] += __uint_as_float(x << 16);
+                            }
+                    }
+                }
+                if (final_) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8)
+                        if (q * 32 + i < p.D)
+                            st_v4(dst + (q * 32 + i) * 2, make_uint4(pack2(f[i], f[i + 1]), pack2(f[i + 2], f[i + 3]),
+                                                                     pack2(f[i + 4], f[i + 5]), pack2(f[i + 6], f[i + 7])));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        *(float4 *)(part + q * 32 + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+                }
+            }
+            if (valid) {
+                const float lse = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
+                if (!final_)
+                    p.part_lse[(size_t)(2 * w.index + t) * p.part_rows + r] = lse;
+                else if (p.lse)
+                    p.lse[((size_t)w.slot * p.Tq + qi) * p.Hq + head] = lse;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Joins the parts of split rows in part order: one warp a row,
+//   lse = m + ln sum_c exp(lse_c - m),  o = sum_c exp(lse_c - lse) o_c.
+template <int DP, bool SPLIT>
+__global__ void __launch_bounds__(256) k_attn_join(const Params p)
+{
+    const int lane = threadIdx.x & 31;
+    const Plan pl = make_plan<SPLIT>(p, lane);
+    const long long rows = (long long)p.P * p.Tq * p.Hq;
+    const int HP = p.P * p.Hkv;
+    for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
+        const int head = (int)(row % p.Hq);
+        const int qi = (int)(row / p.Hq % p.Tq), slot = (int)(row / p.Hq / p.Tq);
+        // the sequence of token qi, and the units before it
+        int units = 0, b_hit = -1;
+        Seq s{};
+        for (int b0 = 0; b0 < p.B && b_hit < 0; b0 += 32) {
+            const int b = b0 + lane;
+            Seq sb{};
+            int n = 0;
+            if (b < p.B) {
+                sb = seq_of(p, b);
+                const int kt = (sb.kl + KT - 1) / KT;
+                n = ((sb.ql + p.TPU - 1) / p.TPU) * units_per_tile<SPLIT>(kt, pl.cs);
+            }
+            const int inc = warp_incl_scan(n, lane);
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, b < p.B && qi >= sb.q0 && qi < sb.q0 + sb.ql);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                b_hit = b0 + src;
+                units += __shfl_sync(0xFFFFFFFFu, inc - n, src);
+            } else {
+                units += __shfl_sync(0xFFFFFFFFu, inc, 31);
+            }
+        }
+        if (b_hit < 0) continue;
+        s = seq_of(p, b_hit);
+        const int kt = (s.kl + KT - 1) / KT, cs = pl.cs;
+        const int np = parts_of(kt, cs), upt = units_per_tile<SPLIT>(kt, cs);
+        if (np == 1) continue;
+        const int i = qi - s.q0, tile = i / p.TPU, nt = (s.ql + p.TPU - 1) / p.TPU;
+        const int in_tile = i - tile * p.TPU, t_pair = in_tile / p.TT;
+        const int r = (in_tile % p.TT) * p.G + head % p.G;
+        const int x0 = units + (nt - 1 - tile) * upt, hp = slot * p.Hkv + head / p.G;
+        auto slot_of = [&](int c) {
+            const size_t u = (size_t)(x0 + (SPLIT ? c >> 1 : c)) * HP + hp;
+            return (2 * u + (SPLIT ? c & 1 : t_pair)) * p.part_rows + r;
+        };
+        float m = -INFINITY;
+        for (int c = lane; c < np; c += 32) m = fmaxf(m, p.part_lse[slot_of(c)]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float base = m == -INFINITY ? 0.f : m;
+        float acc[DP / 32] = {}, sum = 0.f;
+        for (int c = 0; c < np; ++c) {
+            const size_t sl = slot_of(c);
+            const float wgt = expf(p.part_lse[sl] - base);
+            sum += wgt;
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d) acc[d] += wgt * p.part_o[sl * DP + d * 32 + lane];
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        char *const dst = p.out.base + slot * p.out.slot + (size_t)qi * p.out.token + head * p.out.head;
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+            if (d * 32 + lane < p.D) st_u16(dst + (d * 32 + lane) * 2, (uint16_t)pack2(acc[d] * inv, 0.f));
+        if (lane == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
+    }
+}
+
+template <int DP, bool SPLIT>
+static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                          cudaStream_t st)
+{
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+        attr = cudaFuncSetAttribute(k_attn_fwd<DP, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    FwdCfg<DP, SPLIT>::SMEM);
+    });
+    if (attr != cudaSuccess) return attr;
+    k_attn_fwd<DP, SPLIT><<<p.sms, FWD_THREADS, FwdCfg<DP, SPLIT>::SMEM, st>>>(mq, mk, mv, p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !p.may_split) return e;
+    const long long rows = (long long)p.P * p.Tq * p.Hq;
+    const long long blocks = (rows + 7) / 8;
+    k_attn_join<DP, SPLIT><<<(unsigned)(blocks < 8ll * p.sms ? blocks : 8ll * p.sms), 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attn_fwd(const Params &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                            bool split, cudaStream_t st)
+{
+    if (p.D <= 64)
+        return split ? launch<64, true>(p, mq, mk, mv, st) : launch<64, false>(p, mq, mk, mv, st);
+    return split ? launch<128, true>(p, mq, mk, mv, st) : launch<128, false>(p, mq, mk, mv, st);
+}
+
+} // namespace attn
+} // namespace rc

@@ -79,6 +79,14 @@ int prepare_workspace(size_t sig_words, WsHeader **hdr, uint32_t **sig, int *sm_
 int prepare_workspace_ext(void *ext, size_t ext_bytes, size_t sig_words, WsHeader **hdr, uint32_t **sig,
                           int *sm_count, unsigned long long *timeout_ns);
 
+// prepare_scratch: at least `bytes` of plain device memory of the current
+// device (256-byte aligned, contents arbitrary), grown on demand and released
+// by ring_finalize.  Kept apart from the signal words, whose old values must
+// survive between launches.
+int prepare_scratch(size_t bytes, void **out);
+// The current device must be an sm_103 GPU; gives its SM count.
+int device_sms(int *sms);
+
 // Threads per block of the ring kernel, and the blocks per SM its register
 // budget is sized for (build-time tuning knobs).
 // Small blocks, many per SM: while some blocks wait on their left neighbour
