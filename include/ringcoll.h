@@ -424,6 +424,24 @@ int attn_fwd(const rc_attn_args *args, void *stream);
 size_t attn_fwd_workspace_bytes(const rc_attn_args *args);
 
 /*
+ * attn_bwd -- gradients of attn_fwd.  Reads q, k, v, out, lse (as attn_fwd
+ * left them) and dout; writes dq, dk, dv, each rounded once from binary32
+ * sums (the weights and score gradients are rounded to bf16 for their
+ * products).  dk and dv sum over the query heads that share a key head.  No
+ * sum crosses thread blocks: results do not depend on timing.  Tokens outside
+ * every sequence, and keys from used_k[b] on, are neither read nor written;
+ * keys that no query sees, and queries that see no key, get 0.  Sequences do
+ * not reach one another, whatever they hold; a non-finite value makes
+ * gradients of its own sequence and head group non-finite, also where the
+ * mask hides it.  Arguments and requirements as attn_fwd, lse not null;
+ * the gradients may be views of one fused buffer and must not overlap inputs.
+ */
+int attn_bwd(const rc_attn_args *args, void *stream);
+
+/* Workspace bytes attn_bwd needs; 0 as for attn_fwd_workspace_bytes. */
+size_t attn_bwd_workspace_bytes(const rc_attn_args *args);
+
+/*
  * ring_status -- waits for `stream`, then returns and clears the device
  * status of the library's own signal areas on the calling device: the
  * workspace of the regular entry points and the fixed array of

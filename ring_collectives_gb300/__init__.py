@@ -32,7 +32,7 @@ __all__ = [
     "ag_gemm_ex", "ag_gemm_kn", "ag_gemm_workspace_bytes", "RC_B_NK", "RC_B_KN", "gemm_rs_ex", "gemm_rs_workspace_bytes",
     "ring_last_error", "ring_set_timeout_ms", "ring_set_slices", "ring_debug_skip_notify", "ag_gemm_debug_skip_piece",
     "ring_debug_set_trace", "ring_debug_l2_rate", "ring_finalize", "library_path", "load",
-    "attn_fwd", "attn_fwd_workspace_bytes",
+    "attn_fwd", "attn_fwd_workspace_bytes", "attn_bwd", "attn_bwd_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -81,6 +81,8 @@ _SIGNATURES = {
     "ring_finalize": ([], _i),
     "attn_fwd": ([ctypes.c_char_p, _vp], _i),
     "attn_fwd_workspace_bytes": ([ctypes.c_char_p], _sz),
+    "attn_bwd": ([ctypes.c_char_p, _vp], _i),
+    "attn_bwd_workspace_bytes": ([ctypes.c_char_p], _sz),
 }
 
 _lib = None
@@ -551,3 +553,30 @@ def _lse(lse, P, Tq, Hq):
 def attn_fwd_workspace_bytes(P: int, B: int, Tq: int, Tk: int, Hq: int, Hkv: int, D: int) -> int:
     args = _ATTN_ARGS.pack(*(0,) * 38, *_attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, True, None))
     return int(load().attn_fwd_workspace_bytes(args))
+
+
+def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+             dout: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, cu_q: torch.Tensor,
+             cu_k: torch.Tensor, used_k: torch.Tensor | None = None, causal: bool = True, scale: float | None = None,
+             workspace: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of :func:`attn_fwd` (``out`` and ``lse`` are its results): writes dq
+    [P, Tq, Hq, D] and dk, dv [P, Tk, Hkv, D], which may be views of one fused gradient
+    buffer.  The other arguments are those of the forward call."""
+    P, Tq, Hq, D = q.shape
+    qshape, kshape = q.shape, (P, k.size(1), k.size(2), D)
+    B = cu_q.numel() - 1
+    args = _ATTN_ARGS.pack(
+        *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(v, "v", kshape), *_heads(out, "out", qshape),
+        *_heads(dout, "dout", qshape), *_heads(dq, "dq", qshape), *_heads(dk, "dk", kshape),
+        *_heads(dv, "dv", kshape), _lse(lse, P, Tq, Hq), _index(cu_q, "cu_q", B + 1),
+        _index(cu_k, "cu_k", B + 1), 0 if used_k is None else _index(used_k, "used_k", B),
+        *((0, 0) if workspace is None else _ws(workspace)),
+        *_attn_sizes(P, B, Tq, kshape[1], Hq, kshape[2], D, causal, scale))
+    with torch.cuda.device(q.device):
+        _check(load().attn_bwd(args, _stream(stream, q.device)))
+    return dq, dk, dv
+
+
+def attn_bwd_workspace_bytes(P: int, B: int, Tq: int, Tk: int, Hq: int, Hkv: int, D: int) -> int:
+    args = _ATTN_ARGS.pack(*(0,) * 38, *_attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, True, None))
+    return int(load().attn_bwd_workspace_bytes(args))

@@ -193,6 +193,8 @@ int head_map5(CUtensorMap *map, const rc_heads &h, int P, int T, int Hkv, int G,
 int head_map4(CUtensorMap *map, const rc_heads &h, int P, int T, int Hkv, int D);
 cudaError_t launch_attn_fwd(const Params &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                             bool split, cudaStream_t st);
+cudaError_t launch_attn_bwd(const Params &p, const CUtensorMap &mq, const CUtensorMap &mdo, const CUtensorMap &mk,
+                            const CUtensorMap &mv, cudaStream_t st);
 
 } // namespace attn
 } // namespace rc

@@ -197,8 +197,74 @@ static int run_fwd(const rc_attn_args *args, void *stream)
     return RC_OK;
 }
 
+static size_t delta_bytes(const rc_attn_args &a) { return (size_t)a.P * a.Tq * a.Hq * 4; }
+
+static int run_bwd(const rc_attn_args *args, void *stream)
+{
+    if (!args) return set_error(RC_ERR_INVALID, "null args");
+    rc_attn_args a = *args;
+    int rc_ = check_sizes(a);
+    if (rc_) return rc_;
+    if (a.Tq == 0 && a.Tk == 0) return RC_OK;
+    if (a.Tq && ((rc_ = check_heads(a.q, "q", a.P, a.Tq, a.Hq, a.D)) ||
+                 (rc_ = check_heads(a.out, "out", a.P, a.Tq, a.Hq, a.D)) ||
+                 (rc_ = check_heads(a.dout, "dout", a.P, a.Tq, a.Hq, a.D)) ||
+                 (rc_ = check_heads(a.dq, "dq", a.P, a.Tq, a.Hq, a.D))))
+        return rc_;
+    if (a.Tk && ((rc_ = check_heads(a.k, "k", a.P, a.Tk, a.Hkv, a.D)) ||
+                 (rc_ = check_heads(a.v, "v", a.P, a.Tk, a.Hkv, a.D)) ||
+                 (rc_ = check_heads(a.dk, "dk", a.P, a.Tk, a.Hkv, a.D)) ||
+                 (rc_ = check_heads(a.dv, "dv", a.P, a.Tk, a.Hkv, a.D))))
+        return rc_;
+    if (!a.cu_q || !a.cu_k) return set_error(RC_ERR_INVALID, "cu_q or cu_k is null");
+    if (a.Tq && !a.lse) return set_error(RC_ERR_INVALID, "lse is null");
+    const void *const in[] = {a.Tk ? a.k.base : nullptr, a.Tk ? a.v.base : nullptr, a.Tq ? a.q.base : nullptr,
+                              a.Tq ? a.out.base : nullptr, a.Tq ? a.dout.base : nullptr};
+    const void *const res[] = {a.Tq ? a.dq.base : nullptr, a.Tk ? a.dk.base : nullptr, a.Tk ? a.dv.base : nullptr};
+    for (int i = 0; i < 3; ++i) {
+        for (const void *x : in)
+            if (x && x == res[i]) return set_error(RC_ERR_INVALID, "a gradient overlaps an input");
+        if (res[i] && res[i] == res[(i + 1) % 3]) return set_error(RC_ERR_INVALID, "two gradients overlap");
+    }
+    Params p{};
+    fill(p, a);
+    if ((rc_ = device_sms(&p.sms))) return rc_;
+    char *scratch = nullptr;
+    if ((rc_ = take_workspace(a, delta_bytes(a), p, &scratch))) return rc_;
+    p.delta = (float *)scratch;
+    p.o = (const char *)a.out.base;
+    p.o_slot = a.out.slot;
+    p.o_token = a.out.token;
+    p.o_head = a.out.head;
+    p.dout = strided(a.dout);
+    p.dq = strided(a.dq);
+    p.dk = strided(a.dk);
+    p.dv = strided(a.dv);
+    CUtensorMap mq{}, mdo{}, mk{}, mv{};
+    if (a.Tq && ((rc_ = head_map5(&mq, a.q, a.P, a.Tq, a.Hkv, p.G, a.D, p.TT)) ||
+                 (rc_ = head_map5(&mdo, a.dout, a.P, a.Tq, a.Hkv, p.G, a.D, p.TT))))
+        return rc_;
+    if (a.Tk && ((rc_ = head_map4(&mk, a.k, a.P, a.Tk, a.Hkv, a.D)) || (rc_ = head_map4(&mv, a.v, a.P, a.Tk, a.Hkv, a.D))))
+        return rc_;
+    if (!a.Tq) mq = mdo = mk;   // without queries (or keys) no tile of theirs is read
+    if (!a.Tk) mk = mv = mq;
+    const cudaError_t e = launch_attn_bwd(p, mq, mdo, mk, mv, (cudaStream_t)stream);
+    if (e != cudaSuccess) return set_error(RC_ERR_CUDA, "attn_bwd launch: %s", cudaGetErrorString(e));
+    return RC_OK;
+}
+
 } // namespace attn
 } // namespace rc
+
+extern "C" int attn_bwd(const rc_attn_args *args, void *stream) { return rc::attn::run_bwd(args, stream); }
+
+extern "C" size_t attn_bwd_workspace_bytes(const rc_attn_args *args)
+{
+    using namespace rc::attn;
+    int sms = 0;
+    if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
+    return kWsHead + delta_bytes(*args);
+}
 
 extern "C" int attn_fwd(const rc_attn_args *args, void *stream) { return rc::attn::run_fwd(args, stream); }
 

@@ -1,0 +1,705 @@
+// attn_bwd.cu -- gradients of attention over packed sequences, on the
+// 5th-generation tensor cores.  With p_ij = exp(s_ij - lse_i) recomputed from
+// the forward pass's log-sums and delta_i = dO_i . O_i:
+//   dV_j = sum_i p_ij dO_i,   dS_ij = p_ij (dO_i . V_j - delta_i),
+//   dQ_i = scale sum_j dS_ij K_j,   dK_j = scale sum_i dS_ij Q_i.
+//
+// Two kernels, each owning its outputs: k_attn_dq keeps 128 query rows and
+// runs over the key tiles; k_attn_dkv keeps 128 keys and runs over the query
+// row tiles of all heads of the group, so the gradients of a shared key head
+// add up in one accumulator.  Recomputing S and dO V^T in both costs 7 instead
+// of 5 products per tile pair; in exchange no sum crosses blocks: no atomics,
+// no binary32 dQ in memory, and results that do not depend on timing.
+//
+// Blocks of 12 warps, one per SM: warps 0-7 do the elementwise work (two
+// warpgroups, 64 columns of a 128x128 tile each, a thread a row), warp 8 the
+// units and TMA loads, warp 9 the MMAs, and in k_attn_dkv warps 10-11 bring
+// the row statistics.  P and dS are rounded to bf16 -- the tensor cores'
+// input type -- and written to TMEM over the scores they came from, where they
+// are the A operands of the second products; all sums are binary32.
+#include <mutex>
+
+#include "attn.cuh"
+
+namespace rc {
+namespace attn {
+
+constexpr int BWD_THREADS = 384;
+constexpr int BLK = KT * 128;              // a 64-column block of a 128-row tile: 16 KiB
+constexpr int BUNITS = 4;
+
+struct BUnit {
+    Seq s;
+    int hk, slot;
+    int first;      // dq: first query token of the tile; dkv: first key
+    int count;      // dq: valid tokens; dkv: valid keys
+    int from, n;    // first inner tile and their number
+    int index;      // -1: no more units
+};
+
+// dq: one unit per 128-row query tile, the ones that see most keys first.
+// dkv: one unit per key tile in order, so those seen by most queries first.
+template <bool DKV>
+__device__ __forceinline__ int bunits(const Params &p, const Seq &s)
+{
+    return DKV ? (s.kl + KT - 1) / KT : (s.ql + p.TT - 1) / p.TT;
+}
+
+template <bool DKV>
+__device__ int bunits_total(const Params &p, int lane)
+{
+    long long n = 0;
+    for (int b = lane; b < p.B; b += 32) n += bunits<DKV>(p, seq_of(p, b));
+    return (int)warp_sum(n);
+}
+
+template <bool DKV>
+__device__ BUnit bunit_of(const Params &p, int u, int lane)
+{
+    BUnit w;
+    const int HP = p.P * p.Hkv, hp = u % HP;
+    w.index = u;
+    w.hk = hp % p.Hkv;
+    w.slot = hp / p.Hkv;
+    int b, local;
+    locate(p.B, u / HP, lane, [&](int bb) { return bunits<DKV>(p, seq_of(p, bb)); }, b, local);
+    w.s = seq_of(p, b);
+    if (DKV) {
+        w.first = local * KT;
+        w.count = min(KT, w.s.kl - w.first);
+        // the first query token that sees key `first`
+        const int i0 = p.causal ? max(0, w.first - (w.s.kl - w.s.ql)) : 0;
+        w.from = min(i0, w.s.ql) / p.TT;
+        w.n = i0 < w.s.ql ? (w.s.ql + p.TT - 1) / p.TT - w.from : 0;
+    } else {
+        w.first = (bunits<false>(p, w.s) - 1 - local) * p.TT;
+        w.count = min(p.TT, w.s.ql - w.first);
+        w.from = 0;
+        w.n = (seen(p, w.s, w.first + w.count - 1) + KT - 1) / KT;
+    }
+    return w;
+}
+
+// One 64-column block after another of a 128-row tile.
+template <int DP>
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap *map, int token, int hk, int slot, uint32_t bar)
+{
+    for (int d = 0; d < DP / 64; ++d) tma_load_5d(dst + d * BLK, map, d * 64, 0, token, hk, slot, bar);
+}
+
+template <int DP>
+__device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap *map, int token, int hk, int slot, uint32_t bar)
+{
+    for (int d = 0; d < DP / 64; ++d) tma_load_4d(dst + d * BLK, map, d * 64, token, hk, slot, bar);
+}
+
+// D = A B^T over DP columns, both K-major in shared memory.
+template <int DP>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b)
+{
+    constexpr uint32_t id = idesc_bf16_f32(KT, KT);
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk)
+        tc_mma(d, smem_desc_sw128(a + (kk >> 2) * BLK) + 2 * (kk & 3), smem_desc_sw128(b + (kk >> 2) * BLK) + 2 * (kk & 3),
+               id, kk != 0);
+}
+
+// D (+)= A B over 128 rows of B; A in TMEM as bf16, its two 64-row halves 64 columns apart.
+template <int DP>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool first)
+{
+    constexpr uint32_t id = idesc_bf16_f32(KT, DP) | kIdescBMnMajor;
+    const uint64_t bd = smem_desc_mn_sw128(b, BLK);
+#pragma unroll
+    for (int kk = 0; kk < KT / 16; ++kk)
+        tc_mma_ta(d, a + (kk >> 2) * 64 + (kk & 3) * 8, bd + 128 * kk, id, !first || kk);
+}
+
+// Clears rows [r0, 128) of a tile of DP columns; `tid` of `n` threads.
+template <int DP>
+__device__ __forceinline__ void clear_rows(uint8_t *tile, int r0, int tid, int n)
+{
+    for (int i = tid; i < (KT - r0) * 8 * (DP / 64); i += n) {
+        const int blk = i / ((KT - r0) * 8), k = i % ((KT - r0) * 8);
+        *(uint4 *)(tile + blk * BLK + r0 * 128 + k * 16) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+__device__ __forceinline__ void fence_smem_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Abort &ab, int where)
+{
+    return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, ab, where));
+}
+
+// 64 accumulator columns of this thread's row, times f, as bf16 at dst (columns
+// [c0, c0 + 64) of a head of D).
+__device__ __forceinline__ void store_acc(uint32_t t, char *dst, int c0, int D, float f, bool valid, bool zero)
+{
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t o[32];
+        if (!zero) {
+            tmem_ld32(t + q * 32, o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (!valid) continue;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+            const int c = c0 + q * 32 + i;
+            if (c < D)
+                st_v4(dst + c * 2, make_uint4(pack2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f),
+                                              pack2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f),
+                                              pack2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f),
+                                              pack2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f)));
+        }
+    }
+}
+
+// Shared-memory plan.  Two resident tiles (dq: Q, dO; dkv: K, V), a ring of
+// NA tiles (dq: K; dkv: Q) and one of NB tiles (dq: V; dkv: dO).  The first
+// ring is deeper because its tiles serve two products an iteration apart.
+template <int DP>
+struct BwdCfg {
+    static constexpr int TILE = KT * DP * 2;
+    static constexpr int NA = 3, NB = 2;
+    static constexpr int CTL = 3072;      // with 32 KiB tiles exactly the 227 KiB of a block
+    static constexpr int SMEM = (2 + NA + NB) * TILE + CTL;
+};
+
+// Barriers of both kernels, in the control area.
+struct Bars {
+    uint32_t res_full, res_empty, a_full, a_empty, b_full, b_empty, s_full, dp_full, p_ready, ds_ready, acc_full,
+        stat_full, stat_empty, u_full, u_empty, drain;
+};
+
+template <int NA, int NB>
+__device__ __forceinline__ Bars bars_at(uint32_t x)
+{
+    Bars b;
+    b.res_full = x;
+    b.res_empty = x + 8;
+    b.a_full = x + 16;
+    b.a_empty = b.a_full + 8 * NA;
+    b.b_full = b.a_empty + 8 * NA;
+    b.b_empty = b.b_full + 8 * NB;
+    b.s_full = b.b_empty + 8 * NB;      // two
+    b.dp_full = b.s_full + 16;
+    b.p_ready = b.dp_full + 8;
+    b.ds_ready = b.p_ready + 8;
+    b.acc_full = b.ds_ready + 8;
+    b.stat_full = b.acc_full + 8;       // two
+    b.stat_empty = b.stat_full + 16;    // two
+    b.u_full = b.stat_empty + 16;
+    b.u_empty = b.u_full + 8 * BUNITS;
+    b.drain = b.u_empty + 8 * BUNITS;
+    return b;
+}
+
+template <int DP, bool DKV>
+__global__ void __launch_bounds__(BWD_THREADS, 1)
+    k_attn_bwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params p)
+{
+    using C = BwdCfg<DP>;
+    constexpr int TILE = C::TILE, NA = C::NA, NB = C::NB;
+    constexpr int READERS = DKV ? 11 : 9;     // warps that release a unit
+    extern __shared__ __align__(1024) uint8_t gbase[];   // swizzled tiles start on 1024 bytes
+    const uint32_t base = smem_u32(gbase);
+    const uint32_t sR0 = base, sR1 = base + TILE, sA = base + 2 * TILE, sB = sA + NA * TILE;
+    uint8_t *const gA = gbase + 2 * TILE, *const gB = gA + NA * TILE;
+    uint8_t *const ctl = gB + NB * TILE;
+    const Bars bar = bars_at<NA, NB>(smem_u32(ctl));
+    BUnit *const units = (BUnit *)(ctl + 512);
+    uint32_t *const tmem_slot = (uint32_t *)(ctl + 1000);
+    int *const abort_flag = (int *)(ctl + 1004);
+    float *const stats = (float *)(ctl + 1024);       // dkv: [2 stages][lse, delta][128 rows]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(bar.res_full, 1);
+        mbar_init(bar.res_empty, 1);
+        for (int s = 0; s < NA; ++s) mbar_init(bar.a_full + 8 * s, 1), mbar_init(bar.a_empty + 8 * s, 1);
+        for (int s = 0; s < NB; ++s) mbar_init(bar.b_full + 8 * s, 1), mbar_init(bar.b_empty + 8 * s, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar.s_full + 8 * s, 1);
+            mbar_init(bar.stat_full + 8 * s, 2);
+            mbar_init(bar.stat_empty + 8 * s, 8);
+        }
+        mbar_init(bar.dp_full, 1);
+        mbar_init(bar.p_ready, 8);
+        mbar_init(bar.ds_ready, 8);
+        mbar_init(bar.acc_full, 1);
+        for (int i = 0; i < BUNITS; ++i) mbar_init(bar.u_full + 8 * i, 1), mbar_init(bar.u_empty + 8 * i, READERS);
+        mbar_init(bar.drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_q) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_do) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_v) : "memory");
+    }
+    // Rows past G * TT are never loaded; as rows of a B operand they must be finite.
+    if (DKV && p.G * p.TT < KT)
+        for (int s = 0; s < NA + NB; ++s) clear_rows<DP>(gA + s * TILE, p.G * p.TT, threadIdx.x, BWD_THREADS);
+    fence_smem_async();
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // dq:  S buffers 0 and 128, dP 256, dQ 384.  dkv: dV 0, dK 128, S 256, dP 384.
+    const Abort ab{abort_flag, p.hdr, p.timeout_ns, DKV ? 0xB3u : 0xB2u, 0};
+
+    auto next_unit = [&](uint32_t it) -> const BUnit * {
+        const int got = lane == 0 ? (int)wait_bar(bar.u_full + 8 * (it % BUNITS), (it / BUNITS) & 1, ab, 12) : 0;
+        if (!__shfl_sync(0xFFFFFFFFu, got, 0)) return nullptr;
+        __syncwarp();
+        const BUnit *w = units + it % BUNITS;
+        return w->index < 0 ? nullptr : w;
+    };
+    auto release_unit = [&](uint32_t it) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.u_empty + 8 * (it % BUNITS));
+    };
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 8) {
+            // ---------------- units, one ahead of the loads, and the TMA loads
+            const int total = bunits_total<DKV>(p, lane) * p.P * p.Hkv;
+            const uint32_t rows = (uint32_t)(p.G * p.TT) * 128u * (DP / 64);
+            auto publish = [&](uint32_t it, const BUnit &w) {
+                bool ok = true;
+                if (lane == 0) {
+                    ok = wait_bar(bar.u_empty + 8 * (it % BUNITS), ((it / BUNITS) & 1) ^ 1u, ab, 13);
+                    if (ok) {
+                        units[it % BUNITS] = w;
+                        mbar_arrive(bar.u_full + 8 * (it % BUNITS));
+                    }
+                }
+                return __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
+            };
+            uint32_t ea = 0, eb = 0, nr = 0, it = 0;
+            int u = blockIdx.x;
+            BUnit next;
+            if (u < total) next = bunit_of<DKV>(p, u, lane);
+            else next.index = -1;
+            bool ok = publish(0, next);
+            while (ok && next.index >= 0) {
+                const BUnit w = next;
+                u += gridDim.x;
+                if (u < total) next = bunit_of<DKV>(p, u, lane);
+                else next.index = -1;
+                ok = publish(++it, next);
+                if (!ok || w.n == 0) continue;
+                if (lane == 0 && (ok = wait_bar(bar.res_empty, (nr & 1) ^ 1u, ab, 1))) {
+                    if (DKV) {
+                        mbar_expect_tx(bar.res_full, 2 * TILE);
+                        load_keys<DP>(sR0, &map_k, w.s.k0 + w.first, w.hk, w.slot, bar.res_full);
+                        load_keys<DP>(sR1, &map_v, w.s.k0 + w.first, w.hk, w.slot, bar.res_full);
+                    } else {
+                        mbar_expect_tx(bar.res_full, 2 * rows);
+                        load_rows<DP>(sR0, &map_q, w.s.q0 + w.first, w.hk, w.slot, bar.res_full);
+                        load_rows<DP>(sR1, &map_do, w.s.q0 + w.first, w.hk, w.slot, bar.res_full);
+                    }
+                    ++nr;
+                    for (int j = 0; j < w.n && ok; ++j) {
+                        const uint32_t st = ea % NA, su = eb % NB;
+                        const int at = DKV ? w.s.q0 + (w.from + j) * p.TT : w.s.k0 + j * KT;
+                        if (!(ok = wait_bar(bar.a_empty + 8 * st, ((ea / NA) & 1) ^ 1u, ab, 2))) break;
+                        mbar_expect_tx(bar.a_full + 8 * st, DKV ? rows : TILE);
+                        if (DKV) load_rows<DP>(sA + st * TILE, &map_q, at, w.hk, w.slot, bar.a_full + 8 * st);
+                        else load_keys<DP>(sA + st * TILE, &map_k, at, w.hk, w.slot, bar.a_full + 8 * st);
+                        ++ea;
+                        if (!(ok = wait_bar(bar.b_empty + 8 * su, ((eb / NB) & 1) ^ 1u, ab, 2))) break;
+                        mbar_expect_tx(bar.b_full + 8 * su, DKV ? rows : TILE);
+                        if (DKV) load_rows<DP>(sB + su * TILE, &map_do, at, w.hk, w.slot, bar.b_full + 8 * su);
+                        else load_keys<DP>(sB + su * TILE, &map_v, at, w.hk, w.slot, bar.b_full + 8 * su);
+                        ++eb;
+                    }
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+            }
+            if (lane == 0 && *(volatile int *)abort_flag) {
+                // let the copies in flight land before the block gives up its shared memory
+                for (uint32_t s = 0; s < NA; ++s)
+                    if (ea > s) wait_bar(bar.a_full + 8 * s, ((ea - 1 - s) / NA) & 1, ab, 9, true);
+                for (uint32_t s = 0; s < NB; ++s)
+                    if (eb > s) wait_bar(bar.b_full + 8 * s, ((eb - 1 - s) / NB) & 1, ab, 9, true);
+                if (nr) wait_bar(bar.res_full, (nr - 1) & 1, ab, 9, true);
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ---------------- MMA issuer
+            uint32_t ea = 0, eb = 0, nr = 0, nt = 0;     // nt: tiles done, the phase of p_ready and ds_ready
+            bool ok = true;
+            const BUnit *wp;
+            for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
+                const int n = wp->n;
+                if (n == 0) continue;
+                if (lane == 0) {
+                    auto a_wait = [&](uint32_t e) { return wait_bar(bar.a_full + 8 * (e % NA), (e / NA) & 1, ab, 4); };
+                    auto b_wait = [&](uint32_t e) { return wait_bar(bar.b_full + 8 * (e % NB), (e / NB) & 1, ab, 5); };
+                    ok = wait_bar(bar.res_full, nr & 1, ab, 3);
+                    if (DKV) {
+                        // S^T = K Q^T, dP^T = V dO^T; dV += P^T dO, dK += dS^T Q.  S of the next
+                        // tile is issued behind dV (it takes P's place), dP behind dK.
+                        auto scores = [&](uint32_t e) {
+                            if (!a_wait(e)) return false;
+                            tc_fence_after();
+                            mma_scores<DP>(tmem + 256, sR0, sA + (e % NA) * TILE);
+                            tc_commit(bar.s_full);
+                            return true;
+                        };
+                        auto dps = [&](uint32_t e) {
+                            if (!b_wait(e)) return false;
+                            tc_fence_after();
+                            mma_scores<DP>(tmem + 384, sR1, sB + (e % NB) * TILE);
+                            tc_commit(bar.dp_full);
+                            return true;
+                        };
+                        ok = ok && scores(ea) && dps(eb);
+                        for (int j = 0; j < n && ok; ++j) {
+                            if (!(ok = wait_bar(bar.p_ready, nt & 1, ab, 6))) break;
+                            tc_fence_after();
+                            mma_rows<DP>(tmem, tmem + 256, sB + (eb % NB) * TILE, j == 0);
+                            tc_commit(bar.b_empty + 8 * (eb % NB));
+                            if (j + 1 < n && !(ok = scores(ea + 1))) break;
+                            if (!(ok = wait_bar(bar.ds_ready, nt & 1, ab, 7))) break;
+                            tc_fence_after();
+                            mma_rows<DP>(tmem + 128, tmem + 384, sA + (ea % NA) * TILE, j == 0);
+                            tc_commit(bar.a_empty + 8 * (ea % NA));
+                            if (j + 1 < n && !(ok = dps(eb + 1))) break;
+                            ++ea, ++eb, ++nt;
+                        }
+                    } else {
+                        // S = Q K^T, dP = dO V^T; dQ += dS K.  Scores run two tiles ahead in two
+                        // buffers; dP of the next tile goes first once dS of this one is out.
+                        auto scores = [&](uint32_t e, int j) {
+                            if (!a_wait(e)) return false;
+                            tc_fence_after();
+                            mma_scores<DP>(tmem + (j & 1) * 128, sR0, sA + (e % NA) * TILE);
+                            tc_commit(bar.s_full + 8 * (j & 1));
+                            return true;
+                        };
+                        auto dps = [&]() {
+                            if (!b_wait(eb)) return false;
+                            tc_fence_after();
+                            mma_scores<DP>(tmem + 256, sR1, sB + (eb % NB) * TILE);
+                            tc_commit(bar.dp_full);
+                            tc_commit(bar.b_empty + 8 * (eb % NB));
+                            ++eb;
+                            return true;
+                        };
+                        ok = ok && scores(ea, 0) && dps();
+                        if (ok && n > 1) ok = scores(ea + 1, 1);
+                        for (int j = 0; j < n && ok; ++j) {
+                            if (!(ok = wait_bar(bar.ds_ready, nt & 1, ab, 7))) break;
+                            tc_fence_after();
+                            if (j + 1 < n && !(ok = dps())) break;
+                            mma_rows<DP>(tmem + 384, tmem + (j & 1) * 128, sA + (ea % NA) * TILE, j == 0);
+                            tc_commit(bar.a_empty + 8 * (ea % NA));
+                            if (j + 2 < n && !(ok = scores(ea + 2, j))) break;
+                            ++ea, ++nt;
+                        }
+                    }
+                    tc_commit(bar.acc_full);
+                    tc_commit(bar.res_empty);
+                    ++nr;
+                }
+                ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+            }
+            if (lane == 0) {
+                tc_commit(bar.drain);
+                wait_bar(bar.drain, 0, ab, 10, true);
+            }
+            __syncwarp();
+        } else if (DKV) {
+            // ---------------- row statistics: 64 rows of a tile per warp
+            uint32_t e = 0;
+            bool ok = true;
+            const BUnit *wp;
+            for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
+                const BUnit &w = *wp;
+                for (int j = 0; j < w.n && ok; ++j, ++e) {
+                    const uint32_t st = e & 1;
+                    float l2[2], dl[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = (warp - 10) * 64 + h * 32 + lane;
+                        const int tok = (w.from + j) * p.TT + r / p.G;
+                        l2[h] = INFINITY;      // exp2(s - inf) = 0: rows that do not exist or see nothing
+                        dl[h] = 0.f;
+                        if (r < p.G * p.TT && tok < w.s.ql) {
+                            const size_t at = ((size_t)w.slot * p.Tq + w.s.q0 + tok) * p.Hq + w.hk * p.G + r % p.G;
+                            const float x = p.lse[at];
+                            if (x != -INFINITY) l2[h] = x * kLog2e;
+                            dl[h] = p.delta[at];
+                        }
+                    }
+                    int got = lane == 0 ? (int)wait_bar(bar.stat_empty + 8 * st, ((e >> 1) & 1) ^ 1u, ab, 14) : 0;
+                    ok = __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
+                    if (!ok) break;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = (warp - 10) * 64 + h * 32 + lane;
+                        stats[st * 256 + r] = l2[h];
+                        stats[st * 256 + 128 + r] = dl[h];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar.stat_full + 8 * st);
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int wg = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tm = tmem + lane_off;
+        const float c = p.scale * kLog2e;
+        uint32_t ns = 0, nu = 0, nsb[2] = {0, 0};
+        bool ok = true;
+        const BUnit *wp;
+        for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
+            const BUnit &w = *wp;
+            const int n = w.n;
+            if (DKV) {
+                // ---------------- thread: key first + r, query rows [64 wg, 64 wg + 64) of each tile
+                const int key = w.first + r;
+                const bool valid = r < w.count;
+                for (int j = 0; j < n; ++j, ++ns) {
+                    const uint32_t st = ns & 1;
+                    const int tok0 = (w.from + j) * p.TT;
+                    const int rows = p.G * min(p.TT, w.s.ql - tok0);
+                    if (!(ok = wait_all(bar.s_full, ns & 1, ab, 8))) break;
+                    tc_fence_after();
+                    uint32_t s[2][32];
+                    tmem_ld32_async(tm + 256 + wg * 64, s[0]);
+                    tmem_ld32_async(tm + 256 + wg * 64 + 32, s[1]);
+                    if (!(ok = wait_all(bar.stat_full + 8 * st, (ns >> 1) & 1, ab, 15))) break;
+                    tmem_wait_ld32(s[0]);
+                    tmem_wait_ld32(s[1]);
+                    const float *const sl = stats + st * 256 + wg * 64, *const sd = sl + 128;
+                    // rows [lo, hi) of the tile see this key
+                    int lo = p.causal ? (key - (w.s.kl - w.s.ql) - tok0) * p.G : 0;
+                    int hi = rows;
+                    if (!valid) lo = KT;
+                    lo -= wg * 64;
+                    hi -= wg * 64;
+                    const bool mask = __any_sync(0xFFFFFFFFu, lo > 0 || hi < 64);
+                    float pr[64];
+                    uint32_t pk[2][16];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 l4 = *(const float4 *)(sl + q * 32 + i);
+                            pr[q * 32 + i] = ex2(fmaf(__uint_as_float(s[q][i]), c, -l4.x));
+                            pr[q * 32 + i + 1] = ex2(fmaf(__uint_as_float(s[q][i + 1]), c, -l4.y));
+                            pr[q * 32 + i + 2] = ex2(fmaf(__uint_as_float(s[q][i + 2]), c, -l4.z));
+                            pr[q * 32 + i + 3] = ex2(fmaf(__uint_as_float(s[q][i + 3]), c, -l4.w));
+                        }
+                    if (mask) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i < lo || i >= hi) pr[i] = 0.f;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) pk[q][i] = pack2(pr[q * 32 + 2 * i], pr[q * 32 + 2 * i + 1]);
+                        tmem_st16(tm + 256 + wg * 64 + q * 16, pk[q]);
+                    }
+                    tmem_wait_st();
+                    const bool tail = rows < p.G * p.TT;
+                    if (tail) {
+                        // rows of the next sequence in this tile: cleared in both operands, which have landed
+                        // once S and dP are complete
+                        if (!(ok = wait_all(bar.dp_full, ns & 1, ab, 16))) break;
+                        // ring entry ns holds this tile in both rings
+                        clear_rows<DP>(gA + (ns % NA) * TILE, rows, threadIdx.x, 256);
+                        clear_rows<DP>(gB + (ns % NB) * TILE, rows, threadIdx.x, 256);
+                        fence_smem_async();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar.p_ready);
+                    if (!(ok = wait_all(bar.dp_full, ns & 1, ab, 16))) break;
+                    tc_fence_after();
+                    tmem_ld32_async(tm + 384 + wg * 64, s[0]);
+                    tmem_ld32_async(tm + 384 + wg * 64 + 32, s[1]);
+                    tmem_wait_ld32(s[0]);
+                    tmem_wait_ld32(s[1]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 d4 = *(const float4 *)(sd + q * 32 + i);
+                            pr[q * 32 + i] *= __uint_as_float(s[q][i]) - d4.x;
+                            pr[q * 32 + i + 1] *= __uint_as_float(s[q][i + 1]) - d4.y;
+                            pr[q * 32 + i + 2] *= __uint_as_float(s[q][i + 2]) - d4.z;
+                            pr[q * 32 + i + 3] *= __uint_as_float(s[q][i + 3]) - d4.w;
+                        }
+                    if (mask) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i < lo || i >= hi) pr[i] = 0.f;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar.stat_empty + 8 * st);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) pk[q][i] = pack2(pr[q * 32 + 2 * i], pr[q * 32 + 2 * i + 1]);
+                        tmem_st16(tm + 384 + wg * 64 + q * 16, pk[q]);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar.ds_ready);
+                }
+                if (!ok) break;
+                if (n > 0) {
+                    if (!(ok = wait_all(bar.acc_full, nu & 1, ab, 11))) break;
+                    ++nu;
+                    tc_fence_after();
+                }
+                if (wg * 64 < DP) {
+                    const size_t at = (size_t)w.s.k0 + key;
+                    store_acc(tm + wg * 64, p.dv.base + w.slot * p.dv.slot + at * p.dv.token + w.hk * p.dv.head, wg * 64,
+                              p.D, 1.f, valid, n == 0);
+                    store_acc(tm + 128 + wg * 64, p.dk.base + w.slot * p.dk.slot + at * p.dk.token + w.hk * p.dk.head,
+                              wg * 64, p.D, p.scale, valid, n == 0);
+                }
+            } else {
+                // ---------------- thread: query row r of the tile, keys [64 wg, 64 wg + 64) of each tile
+                const int ti = r / p.G, head = w.hk * p.G + r % p.G;
+                const bool valid = ti < w.count;
+                const size_t qi = (size_t)w.s.q0 + w.first + ti;
+                const size_t at = ((size_t)w.slot * p.Tq + qi) * p.Hq + head;
+                int here = (valid ? seen(p, w.s, w.first + ti) : 0) - wg * 64;   // keys seen from this tile's half on
+                float l2 = INFINITY, delta = 0.f;
+                if (valid) {
+                    // both warpgroups sum the whole row: cheaper than a barrier between them
+                    const float x = p.lse[at];
+                    if (x != -INFINITY) l2 = x * kLog2e;
+                    const char *o = p.o + w.slot * p.o_slot + qi * p.o_token + head * p.o_head;
+                    const char *g = p.dout.base + w.slot * p.dout.slot + qi * p.dout.token + head * p.dout.head;
+#pragma unroll 4
+                    for (int i = 0; i < p.D; i += 8) {
+                        const uint4 a = *(const uint4 *)(o + i * 2), b = *(const uint4 *)(g + i * 2);
+                        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            delta = fmaf(__uint_as_float(av[h] << 16), __uint_as_float(bv[h] << 16), delta);
+                            delta = fmaf(__uint_as_float(av[h] & 0xFFFF0000u), __uint_as_float(bv[h] & 0xFFFF0000u), delta);
+                        }
+                    }
+                    if (wg == 0) p.delta[at] = delta;
+                }
+                for (int j = 0; j < n; ++j, ++ns, here -= KT) {
+                    const int sb = j & 1;
+                    if (!(ok = wait_all(bar.s_full + 8 * sb, nsb[sb] & 1, ab, 8))) break;
+                    ++nsb[sb];
+                    tc_fence_after();
+                    uint32_t s[2][32];
+                    float pr[64];
+                    tmem_ld32_async(tm + sb * 128 + wg * 64, s[0]);
+                    tmem_ld32_async(tm + sb * 128 + wg * 64 + 32, s[1]);
+                    tmem_wait_ld32(s[0]);
+                    tmem_wait_ld32(s[1]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) pr[q * 32 + i] = ex2(fmaf(__uint_as_float(s[q][i]), c, -l2));
+                    if (!(ok = wait_all(bar.dp_full, ns & 1, ab, 16))) break;
+                    tc_fence_after();
+                    tmem_ld32_async(tm + 256 + wg * 64, s[0]);
+                    tmem_ld32_async(tm + 256 + wg * 64 + 32, s[1]);
+                    tmem_wait_ld32(s[0]);
+                    tmem_wait_ld32(s[1]);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) pr[q * 32 + i] *= __uint_as_float(s[q][i]) - delta;
+                    if (__any_sync(0xFFFFFFFFu, here < 64)) {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i)
+                            if (i >= here) pr[i] = 0.f;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) pk[i] = pack2(pr[q * 32 + 2 * i], pr[q * 32 + 2 * i + 1]);
+                        tmem_st16(tm + sb * 128 + wg * 64 + q * 16, pk);
+                    }
+                    tmem_wait_st();
+                    const int left = w.s.kl - j * KT;
+                    if (left < KT) {     // keys past the end, as rows of dQ's B operand
+                        clear_rows<DP>(gA + (ns % NA) * TILE, left, threadIdx.x, 256);
+                        fence_smem_async();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar.ds_ready);
+                }
+                if (!ok) break;
+                if (n > 0) {
+                    if (!(ok = wait_all(bar.acc_full, nu & 1, ab, 11))) break;
+                    ++nu;
+                    tc_fence_after();
+                }
+                if (wg * 64 < DP)
+                    store_acc(tm + 384 + wg * 64, p.dq.base + w.slot * p.dq.slot + qi * p.dq.token + head * p.dq.head,
+                              wg * 64, p.D, p.scale, valid, n == 0);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+template <int DP>
+static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensorMap &mdo, const CUtensorMap &mk,
+                          const CUtensorMap &mv, cudaStream_t st)
+{
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+        attr = cudaFuncSetAttribute(k_attn_bwd<DP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdCfg<DP>::SMEM);
+        if (attr == cudaSuccess)
+            attr = cudaFuncSetAttribute(k_attn_bwd<DP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        BwdCfg<DP>::SMEM);
+    });
+    if (attr != cudaSuccess) return attr;
+    cudaError_t e = cudaSuccess;
+    if (p.Tq) {
+        k_attn_bwd<DP, false><<<p.sms, BWD_THREADS, BwdCfg<DP>::SMEM, st>>>(mq, mdo, mk, mv, p);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && p.Tk) {
+        k_attn_bwd<DP, true><<<p.sms, BWD_THREADS, BwdCfg<DP>::SMEM, st>>>(mq, mdo, mk, mv, p);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+cudaError_t launch_attn_bwd(const Params &p, const CUtensorMap &mq, const CUtensorMap &mdo, const CUtensorMap &mk,
+                            const CUtensorMap &mv, cudaStream_t st)
+{
+    return p.D <= 64 ? launch<64>(p, mq, mdo, mk, mv, st) : launch<128>(p, mq, mdo, mk, mv, st);
+}
+
+} // namespace attn
+} // namespace rc
