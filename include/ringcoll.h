@@ -441,6 +441,57 @@ int attn_bwd(const rc_attn_args *args, void *stream);
 /* Workspace bytes attn_bwd needs; 0 as for attn_fwd_workspace_bytes. */
 size_t attn_bwd_workspace_bytes(const rc_attn_args *args);
 
+/* Which elements of a head rotate together: (i, i + D/2) or (2i, 2i + 1). */
+typedef enum { RC_ROPE_HALF = 0, RC_ROPE_PAIRS = 1 } rc_rope_layout;
+
+/*
+ * Arguments of qk_norm_rope and qk_norm_rope_bwd.  q, q_out, dq: [P][T][Hq][D];
+ * k, k_out, dk: [P][T][Hkv][D] (rc_heads).  gamma_q, gamma_k: f32 [D], shared by
+ * every head and rank.  cos, sin: f32 [npos][D/2], row pos holding the cosine
+ * and sine of every pair's angle at position pos.  pos: int32 [T], the
+ * position of each token (DEVICE; one outside [0, npos) gives NaN).
+ * dgamma_q, dgamma_k: f32 [P][D] (written): rank r's own sums, which a
+ * ring_allreduce of the slots turns into the gradient of the shared weights.
+ * workspace (qk_norm_rope_bwd): null for the library's own, else DEVICE memory
+ * of ws_bytes bytes, 256-byte aligned, contents arbitrary.
+ */
+typedef struct {
+    rc_heads q, k, q_out, k_out;
+    rc_heads dq, dk; /* qk_norm_rope_bwd only */
+    const float *gamma_q, *gamma_k, *cos, *sin;
+    const int32_t *pos;
+    float *dgamma_q, *dgamma_k; /* qk_norm_rope_bwd only */
+    void *workspace;
+    size_t ws_bytes;
+    int P, T, Hq, Hkv, D, npos, layout;
+    float eps;
+} rc_qk_norm_args;
+
+/*
+ * qk_norm_rope -- RMS norm of every query and key head, then the rotary
+ * position rotation, in one pass:
+ *     y = x (mean x^2 + eps)^(-1/2) gamma,
+ *     (z_a, z_b) = (y_a cos - y_b sin, y_a sin + y_b cos) for each pair (a, b),
+ * in binary32, rounded once to bf16.  q_out and k_out may be q and k (in
+ * place) and must not overlap them otherwise.
+ * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, D a multiple of 8
+ * up to 256, layouts as for rc_heads, gamma, cos and sin 16-byte aligned,
+ * eps >= 0.  T = 0 does nothing.
+ */
+int qk_norm_rope(const rc_qk_norm_args *args, void *stream);
+
+/*
+ * qk_norm_rope_bwd -- its gradient: q, k are the forward inputs, q_out and
+ * k_out the gradients of the outputs (read); writes dq, dk (which may be
+ * q_out and k_out) and dgamma_q, dgamma_k, summed in binary32 in an order
+ * that does not depend on timing.  T = 0 gives dgamma = 0.
+ */
+int qk_norm_rope_bwd(const rc_qk_norm_args *args, void *stream);
+
+/* Workspace bytes qk_norm_rope_bwd needs (pointers and strides are not read);
+ * 0 for invalid sizes or when no sm_103 device is current. */
+size_t qk_norm_rope_bwd_workspace_bytes(const rc_qk_norm_args *args);
+
 /*
  * ring_status -- waits for `stream`, then returns and clears the device
  * status of the library's own signal areas on the calling device: the

@@ -33,12 +33,14 @@ __all__ = [
     "ring_last_error", "ring_set_timeout_ms", "ring_set_slices", "ring_debug_skip_notify", "ag_gemm_debug_skip_piece",
     "ring_debug_set_trace", "ring_debug_l2_rate", "ring_finalize", "library_path", "load",
     "attn_fwd", "attn_fwd_workspace_bytes", "attn_bwd", "attn_bwd_workspace_bytes",
+    "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes", "RC_ROPE_HALF", "RC_ROPE_PAIRS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libringcoll.so")
 
 RC_OK, RC_ERR_INVALID, RC_ERR_CUDA, RC_ERR_TIMEOUT, RC_ERR_UNSUPPORTED, RC_ERR_NOMEM = range(6)
+RC_ROPE_HALF, RC_ROPE_PAIRS = 0, 1   # rotated pairs (i, i + D/2) or (2i, 2i + 1)
 RC_B_NK, RC_B_KN = 0, 1   # ag_gemm weight layouts: [N][K] (nn.Linear) or [K][N] (x @ W)
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.int32: 2}
 
@@ -83,6 +85,9 @@ _SIGNATURES = {
     "attn_fwd_workspace_bytes": ([ctypes.c_char_p], _sz),
     "attn_bwd": ([ctypes.c_char_p, _vp], _i),
     "attn_bwd_workspace_bytes": ([ctypes.c_char_p], _sz),
+    "qk_norm_rope": ([ctypes.c_char_p, _vp], _i),
+    "qk_norm_rope_bwd": ([ctypes.c_char_p, _vp], _i),
+    "qk_norm_rope_bwd_workspace_bytes": ([ctypes.c_char_p], _sz),
 }
 
 _lib = None
@@ -580,3 +585,60 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
 def attn_bwd_workspace_bytes(P: int, B: int, Tq: int, Tk: int, Hq: int, Hkv: int, D: int) -> int:
     args = _ATTN_ARGS.pack(*(0,) * 38, *_attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, True, None))
     return int(load().attn_bwd_workspace_bytes(args))
+
+
+# rc_qk_norm_args of include/ringcoll.h: six rc_heads, nine pointers and sizes, seven ints, eps
+_QK_NORM_ARGS = struct.Struct("@24Q9Q7if")
+
+
+def _f32(t, name: str, shape) -> int:
+    if not t.is_cuda or t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _qk_norm(q, k, gamma_q, gamma_k, cos, sin, pos, layout, eps, q_out, k_out, grads, workspace):
+    P, T, Hq, D = q.shape
+    kshape = (P, T, k.size(2), D)
+    table = (cos.size(0), D // 2)
+    heads = _NO_HEADS * 2 if grads is None else _heads(grads[0], "dq", q.shape) + _heads(grads[1], "dk", kshape)
+    dg = (0, 0) if grads is None else (_f32(grads[2], "dgamma_q", (P, D)), _f32(grads[3], "dgamma_k", (P, D)))
+    names = ("q_out", "k_out") if grads is None else ("dq_out", "dk_out")
+    return _QK_NORM_ARGS.pack(
+        *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(q_out, names[0], q.shape), *_heads(k_out, names[1], kshape),
+        *heads, _f32(gamma_q, "gamma_q", (D,)), _f32(gamma_k, "gamma_k", (D,)), _f32(cos, "cos", table),
+        _f32(sin, "sin", table), _index(pos, "pos", T), *dg, *((0, 0) if workspace is None else _ws(workspace)),
+        P, T, Hq, kshape[2], D, table[0], layout, eps)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, gamma_q: torch.Tensor, gamma_k: torch.Tensor, cos: torch.Tensor,
+                 sin: torch.Tensor, pos: torch.Tensor, q_out: torch.Tensor, k_out: torch.Tensor,
+                 layout: int = RC_ROPE_HALF, eps: float = 1e-6, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of every query and key head with weights gamma [D], then the rotation by
+    the angles whose cosines and sines are rows pos[t] of cos, sin (float32 [npos, D/2]).
+    q, q_out [P, T, Hq, D], k, k_out [P, T, Hkv, D] bf16, any strides as for attn_fwd; in
+    place when q_out is q and k_out is k."""
+    args = _qk_norm(q, k, gamma_q, gamma_k, cos, sin, pos, layout, eps, q_out, k_out, None, None)
+    with torch.cuda.device(q.device):
+        _check(load().qk_norm_rope(args, _stream(stream, q.device)))
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, gamma_q: torch.Tensor, gamma_k: torch.Tensor,
+                     cos: torch.Tensor, sin: torch.Tensor, pos: torch.Tensor, dq_out: torch.Tensor,
+                     dk_out: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dgamma_q: torch.Tensor,
+                     dgamma_k: torch.Tensor, layout: int = RC_ROPE_HALF, eps: float = 1e-6,
+                     workspace: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradient of :func:`qk_norm_rope` from its inputs and the gradients dq_out, dk_out of
+    its outputs: writes dq, dk (bf16; may be dq_out, dk_out) and each rank's own sums of
+    the weight gradients, dgamma_q and dgamma_k (float32 [P, D])."""
+    args = _qk_norm(q, k, gamma_q, gamma_k, cos, sin, pos, layout, eps, dq_out, dk_out, (dq, dk, dgamma_q, dgamma_k),
+                    workspace)
+    with torch.cuda.device(q.device):
+        _check(load().qk_norm_rope_bwd(args, _stream(stream, q.device)))
+    return dq, dk
+
+
+def qk_norm_rope_bwd_workspace_bytes(P: int, T: int, Hq: int, Hkv: int, D: int) -> int:
+    args = _QK_NORM_ARGS.pack(*(0,) * 33, P, T, Hq, Hkv, D, 1, RC_ROPE_HALF, 0.0)
+    return int(load().qk_norm_rope_bwd_workspace_bytes(args))
