@@ -65,14 +65,77 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
                  : "memory");
 }
 
-// D[tmem] (+)= A[tmem, bf16 pairs] . B[smem desc]
-__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate)
+// ------------------------------------------------------------ MMA issue
+// An MMA of these shapes runs for 64 clocks, so its issue has to be cheap.  The
+// whole MMA warp walks the loops with warp-uniform values (uniform()) and one
+// elected lane issues: descriptors then stay in uniform registers.  With all of
+// it under one lane's branch, issuing took longer than executing: at 4096
+// tokens x 32 heads of 128 the forward pass spent 2300 clocks of issue on each
+// tile's 1024 clocks of MMA.
+__device__ __forceinline__ bool elect_one()
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+// A value that is the same in every lane, in a form the compiler knows to be so.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+// Descriptors (smem_desc_sw128, smem_desc_mn_sw128) as a varying low word -- the
+// address in 16-byte units, and the block step of an MN-major tile -- and this high word.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr int BLK = KT * 128;              // a 64-column block of a 128-row tile: 16 KiB
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return addr >> 4; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) { return (addr >> 4) | ((uint32_t)(BLK >> 4) << 16); }
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
                  : "memory");
+}
+
+// A in TMEM as packed bf16
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
+                 : "memory");
+}
+
+// D = A B^T over DP columns, both tiles K-major in shared memory.
+template <int DP>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b)
+{
+    constexpr uint32_t id = idesc_bf16_f32(KT, KT);
+    const uint32_t ad = desc_k(a), bd = desc_k(b);
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * (BLK >> 4) + 2 * (kk & 3);
+        mma_ss(d, ad + off, bd + off, id, kk != 0);
+    }
+}
+
+// D (+)= A B over the 128 rows of B, a tile of DP columns; A in TMEM, the
+// second 64 of its columns (of bf16) `half` TMEM columns from the first.
+template <int DP>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool first, int half)
+{
+    constexpr uint32_t id = idesc_bf16_f32(KT, DP) | kIdescBMnMajor;
+    const uint32_t bd = desc_mn(b);
+#pragma unroll
+    for (int kk = 0; kk < KT / 16; ++kk)
+        mma_ts(d, a + (kk >> 2) * half + (kk & 3) * 8, bd + 128 * kk, id, kk ? 1u : (first ? 0u : 1u));
+}
+
+// Every lane waits; the same answer in all.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Abort &ab, int where)
+{
+    return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, ab, where));
 }
 
 // Stores 16 / 32 columns of this thread's TMEM lane; tmem_wait_st() ends them.

@@ -25,7 +25,6 @@ namespace rc {
 namespace attn {
 
 constexpr int BWD_THREADS = 384;
-constexpr int BLK = KT * 128;              // a 64-column block of a 128-row tile: 16 KiB
 constexpr int BUNITS = 4;
 
 struct BUnit {
@@ -93,28 +92,6 @@ __device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap *map, 
     for (int d = 0; d < DP / 64; ++d) tma_load_4d(dst + d * BLK, map, d * 64, token, hk, slot, bar);
 }
 
-// D = A B^T over DP columns, both K-major in shared memory.
-template <int DP>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b)
-{
-    constexpr uint32_t id = idesc_bf16_f32(KT, KT);
-#pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk)
-        tc_mma(d, smem_desc_sw128(a + (kk >> 2) * BLK) + 2 * (kk & 3), smem_desc_sw128(b + (kk >> 2) * BLK) + 2 * (kk & 3),
-               id, kk != 0);
-}
-
-// D (+)= A B over 128 rows of B; A in TMEM as bf16, its two 64-row halves 64 columns apart.
-template <int DP>
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool first)
-{
-    constexpr uint32_t id = idesc_bf16_f32(KT, DP) | kIdescBMnMajor;
-    const uint64_t bd = smem_desc_mn_sw128(b, BLK);
-#pragma unroll
-    for (int kk = 0; kk < KT / 16; ++kk)
-        tc_mma_ta(d, a + (kk >> 2) * 64 + (kk & 3) * 8, bd + 128 * kk, id, !first || kk);
-}
-
 // Clears rows [r0, 128) of a tile of DP columns; `tid` of `n` threads.
 template <int DP>
 __device__ __forceinline__ void clear_rows(uint8_t *tile, int r0, int tid, int n)
@@ -126,11 +103,6 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int r0, int tid, int n
 }
 
 __device__ __forceinline__ void fence_smem_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Abort &ab, int where)
-{
-    return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, ab, where));
-}
 
 // 64 accumulator columns of this thread's row, times f, as bf16 at dst (columns
 // [c0, c0 + 64) of a head of D).
@@ -337,89 +309,86 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             }
             __syncwarp();
         } else if (warp == 9) {
-            // ---------------- MMA issuer
-            uint32_t ea = 0, eb = 0, nr = 0, nt = 0;     // nt: tiles done, the phase of p_ready and ds_ready
+            // ---------------- MMA issuer (the whole warp, one elected lane issues)
+            uint32_t sa = 0, pa = 0, sb = 0, pb = 0;     // ring positions: stage and phase
+            uint32_t nr = 0, nt = 0;                     // nt: tiles done, the phase of p_ready and ds_ready
             bool ok = true;
+            const uint32_t tm = (uint32_t)uniform((int)tmem);
             const BUnit *wp;
-            for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
-                const int n = wp->n;
-                if (n == 0) continue;
-                if (lane == 0) {
-                    auto a_wait = [&](uint32_t e) { return wait_bar(bar.a_full + 8 * (e % NA), (e / NA) & 1, ab, 4); };
-                    auto b_wait = [&](uint32_t e) { return wait_bar(bar.b_full + 8 * (e % NB), (e / NB) & 1, ab, 5); };
-                    ok = wait_bar(bar.res_full, nr & 1, ab, 3);
-                    if (DKV) {
-                        // S^T = K Q^T, dP^T = V dO^T; dV += P^T dO, dK += dS^T Q.  S of the next
-                        // tile is issued behind dV (it takes P's place), dP behind dK.
-                        auto scores = [&](uint32_t e) {
-                            if (!a_wait(e)) return false;
-                            tc_fence_after();
-                            mma_scores<DP>(tmem + 256, sR0, sA + (e % NA) * TILE);
-                            tc_commit(bar.s_full);
-                            return true;
-                        };
-                        auto dps = [&](uint32_t e) {
-                            if (!b_wait(e)) return false;
-                            tc_fence_after();
-                            mma_scores<DP>(tmem + 384, sR1, sB + (e % NB) * TILE);
-                            tc_commit(bar.dp_full);
-                            return true;
-                        };
-                        ok = ok && scores(ea) && dps(eb);
-                        for (int j = 0; j < n && ok; ++j) {
-                            if (!(ok = wait_bar(bar.p_ready, nt & 1, ab, 6))) break;
-                            tc_fence_after();
-                            mma_rows<DP>(tmem, tmem + 256, sB + (eb % NB) * TILE, j == 0);
-                            tc_commit(bar.b_empty + 8 * (eb % NB));
-                            if (j + 1 < n && !(ok = scores(ea + 1))) break;
-                            if (!(ok = wait_bar(bar.ds_ready, nt & 1, ab, 7))) break;
-                            tc_fence_after();
-                            mma_rows<DP>(tmem + 128, tmem + 384, sA + (ea % NA) * TILE, j == 0);
-                            tc_commit(bar.a_empty + 8 * (ea % NA));
-                            if (j + 1 < n && !(ok = dps(eb + 1))) break;
-                            ++ea, ++eb, ++nt;
-                        }
-                    } else {
-                        // S = Q K^T, dP = dO V^T; dQ += dS K.  Scores run two tiles ahead in two
-                        // buffers; dP of the next tile goes first once dS of this one is out.
-                        auto scores = [&](uint32_t e, int j) {
-                            if (!a_wait(e)) return false;
-                            tc_fence_after();
-                            mma_scores<DP>(tmem + (j & 1) * 128, sR0, sA + (e % NA) * TILE);
-                            tc_commit(bar.s_full + 8 * (j & 1));
-                            return true;
-                        };
-                        auto dps = [&]() {
-                            if (!b_wait(eb)) return false;
-                            tc_fence_after();
-                            mma_scores<DP>(tmem + 256, sR1, sB + (eb % NB) * TILE);
-                            tc_commit(bar.dp_full);
-                            tc_commit(bar.b_empty + 8 * (eb % NB));
-                            ++eb;
-                            return true;
-                        };
-                        ok = ok && scores(ea, 0) && dps();
-                        if (ok && n > 1) ok = scores(ea + 1, 1);
-                        for (int j = 0; j < n && ok; ++j) {
-                            if (!(ok = wait_bar(bar.ds_ready, nt & 1, ab, 7))) break;
-                            tc_fence_after();
-                            if (j + 1 < n && !(ok = dps())) break;
-                            mma_rows<DP>(tmem + 384, tmem + (j & 1) * 128, sA + (ea % NA) * TILE, j == 0);
-                            tc_commit(bar.a_empty + 8 * (ea % NA));
-                            if (j + 2 < n && !(ok = scores(ea + 2, j))) break;
-                            ++ea, ++nt;
-                        }
-                    }
-                    tc_commit(bar.acc_full);
-                    tc_commit(bar.res_empty);
-                    ++nr;
+            auto commit = [&](uint32_t b) {
+                if (elect_one()) tc_commit(b);
+            };
+            // Scores of tile A (first ring) or B (second ring) against a resident tile.
+            auto scores_a = [&](uint32_t d, uint32_t full) {
+                if (!wait_all(bar.a_full + 8 * sa, pa, ab, 4)) return false;
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_scores<DP>(d, sR0, sA + sa * TILE);
+                    tc_commit(full);
                 }
-                ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+                if (++sa == NA) sa = 0, pa ^= 1u;
+                return true;
+            };
+            auto scores_b = [&](uint32_t d) {
+                if (!wait_all(bar.b_full + 8 * sb, pb, ab, 5)) return false;
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_scores<DP>(d, sR1, sB + sb * TILE);
+                    tc_commit(bar.dp_full);
+                    if (!DKV) tc_commit(bar.b_empty + 8 * sb);
+                }
+                if (++sb == NB) sb = 0, pb ^= 1u;
+                return true;
+            };
+            uint32_t ra = 0, rb = 0;                     // stages of the tile whose second products come next
+            auto rows_a = [&](uint32_t d, uint32_t a, bool first) {
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_rows<DP>(d, a, sA + ra * TILE, first, 64);
+                    tc_commit(bar.a_empty + 8 * ra);
+                }
+                if (++ra == NA) ra = 0;
+            };
+            for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
+                const int n = uniform(wp->n);
+                if (n == 0) continue;
+                if (!(ok = wait_all(bar.res_full, nr & 1, ab, 3))) break;
+                ++nr;
+                if (DKV) {
+                    // S^T = K Q^T, dP^T = V dO^T; dV += P^T dO, dK += dS^T Q.  S of the next
+                    // tile is issued behind dV (it takes P's place), dP behind dK.
+                    ok = scores_a(tm + 256, bar.s_full) && scores_b(tm + 384);
+                    for (int j = 0; j < n && ok; ++j, ++nt) {
+                        if (!(ok = wait_all(bar.p_ready, nt & 1, ab, 6))) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            mma_rows<DP>(tm, tm + 256, sB + rb * TILE, j == 0, 64);
+                            tc_commit(bar.b_empty + 8 * rb);
+                        }
+                        if (++rb == NB) rb = 0;
+                        if (j + 1 < n && !(ok = scores_a(tm + 256, bar.s_full))) break;
+                        if (!(ok = wait_all(bar.ds_ready, nt & 1, ab, 7))) break;
+                        rows_a(tm + 128, tm + 384, j == 0);
+                        if (j + 1 < n) ok = scores_b(tm + 384);
+                    }
+                } else {
+                    // S = Q K^T, dP = dO V^T; dQ += dS K.  Scores run two tiles ahead in two
+                    // buffers; dP of the next tile goes first once dS of this one is out.
+                    ok = scores_a(tm, bar.s_full) && scores_b(tm + 256);
+                    if (ok && n > 1) ok = scores_a(tm + 128, bar.s_full + 8);
+                    for (int j = 0; j < n && ok; ++j, ++nt) {
+                        const uint32_t buf = j & 1;
+                        if (!(ok = wait_all(bar.ds_ready, nt & 1, ab, 7))) break;
+                        if (j + 1 < n && !(ok = scores_b(tm + 256))) break;
+                        rows_a(tm + 384, tm + buf * 128, j == 0);
+                        if (j + 2 < n) ok = scores_a(tm + buf * 128, bar.s_full + 8 * buf);
+                    }
+                }
+                commit(bar.acc_full);
+                commit(bar.res_empty);
             }
-            if (lane == 0) {
-                tc_commit(bar.drain);
-                wait_bar(bar.drain, 0, ab, 10, true);
-            }
+            commit(bar.drain);
+            if (lane == 0) wait_bar(bar.drain, 0, ab, 10, true);
             __syncwarp();
         } else if (DKV) {
             // ---------------- row statistics: 64 rows of a tile per warp

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                const __grid_constant__ CUtensorMap map_v, const Params p)
 {
     using C = FwdCfg<DP, SPLIT>;
-    constexpr int NST = C::STAGES, STAGE = C::KV_STAGE, BLK = KT * 128;   // 64-column blocks of 16 KiB
+    constexpr int NST = C::STAGES, STAGE = C::KV_STAGE;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *const gbase = smem_raw + (base - raw);
@@ -279,8 +279,14 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 ok = publish(++it, next);
                 if (!ok || max(w.n[0], w.n[1]) == 0) continue;
                 if (lane == 0) {
-                    ok = wait_bar(q_empty, (nq & 1) ^ 1u, ab, 1);
-                    if (ok) {
+                    // The query tiles wait for the previous unit's last scores; the first
+                    // key and value tiles do not, and go ahead of them.
+                    constexpr uint32_t AHEAD = NST - 2;
+                    const uint32_t e0 = e;
+                    bool have_q = false;
+                    auto load_q = [&]() {
+                        have_q = true;
+                        if (!wait_bar(q_empty, (nq & 1) ^ 1u, ab, 1)) return false;
                         const uint32_t box = (uint32_t)(p.G * p.TT) * 128u;
                         const int tiles = !SPLIT && w.ntok[1] > 0 ? 2 : 1;
                         mbar_expect_tx(q_full, box * (DP / 64) * tiles);
@@ -289,7 +295,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                                 tma_load_5d(sQ + t * STAGE + d * BLK, &map_q, d * 64, 0, w.s.q0 + w.tok + t * p.TT, w.hk,
                                             w.slot, q_full);
                         ++nq;
-                        for_entries<SPLIT>(w, [&](bool is_v, int t, int j) {
+                        return true;
+                    };
+                    for_entries<SPLIT>(w, [&](bool is_v, int t, int j) {
+                            if (!have_q && e - e0 == AHEAD && !(ok = load_q())) return false;
                             const uint32_t st = e % NST;
                             if (!wait_bar(empty_bar + 8 * st, ((e / NST) & 1) ^ 1u, ab, 2)) {
                                 ok = false;
@@ -302,7 +311,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                             ++e;
                             return true;
                         });
-                    }
+                    if (ok && !have_q) ok = load_q();
                 }
                 ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
             }
@@ -314,124 +323,118 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             }
             __syncwarp();
         } else if (warp == 9) {
-            // ---------------- MMA issuer
-            constexpr uint32_t kIdS = idesc_bf16_f32(KT, KT);
-            constexpr uint32_t kIdO = idesc_bf16_f32(KT, DP) | kIdescBMnMajor;
-            uint32_t e = 0, nq = 0, guard_phase = 0, np[2] = {0, 0};
+            // ---------------- MMA issuer (the whole warp, one elected lane issues)
+            uint32_t st = 0, ph = 0;                       // ring position: stage and phase
+            uint32_t nq = 0, guard_phase = 0, np0 = 0, np1 = 0;
             bool ok = true;
+            const uint32_t tm = (uint32_t)uniform((int)tmem);
             const Unit *wp;
-            for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
-                const Unit &w = *wp;
-                const int n = max(w.n[0], w.n[1]);
-                if (n == 0) continue;
-                if (lane == 0) {
-                    ok = wait_bar(q_full, nq & 1, ab, 3);
-                    // S_t = Q_t K^T with the keys of ring stage st
-                    auto score = [&](int t, uint32_t st) {
-    #pragma unroll
-                        for (int kk = 0; kk < DP / 16; ++kk)
-                            tc_mma(tmem + t * KT, smem_desc_sw128(sQ + (SPLIT ? 0 : t * STAGE) + (kk >> 2) * BLK) + 2 * (kk & 3),
-                                   smem_desc_sw128(sKV + st * STAGE + (kk >> 2) * BLK) + 2 * (kk & 3), kIdS, kk != 0);
-                        tc_commit(s_full + 8 * t);
-                    };
-                    // O_t += P_t V with the values of ring stage st
-                    auto weigh = [&](int t, uint32_t st, bool first) {
-                        const uint64_t vd = smem_desc_mn_sw128(sKV + st * STAGE, BLK);
-    #pragma unroll
-                        for (int kk = 0; kk < KT / 16; ++kk)
-                            tc_mma_ta(tmem + 256 + t * KT, tmem + t * KT + kk * 8, vd + 128 * kk, kIdO, !first || kk);
-                    };
-                    auto take = [&](uint32_t en, bool guarded) {
-                        const uint32_t st = en % NST;
-                        if (guarded) {
-                            if (!wait_bar(guard_bar + 8 * st, (guard_phase >> st) & 1, ab, 5)) return false;
-                            guard_phase ^= 1u << st;
-                            return true;
-                        }
-                        return wait_bar(full_bar + 8 * st, (en / NST) & 1, ab, 4);
-                    };
-                    auto weights = [&](int t) { return wait_bar(p_ready + 8 * t, np[t]++ & 1, ab, 6); };
-                    bool last_s = false;
-                    auto q_done = [&](int left) {
-                        if (left == 0 && !last_s) {
-                            tc_commit(q_empty);
-                            last_s = true;
-                        }
-                    };
-                    int left = w.n[0] + w.n[1];
-                    if (!SPLIT) {
-                        if (ok) ok = take(e, false);
-                        if (ok) {
-                            tc_fence_after();
-                            for (int t = 0; t < 2; ++t)
-                                if (w.n[t] > 0) score(t, e % NST), --left;
-                            tc_commit(empty_bar + 8 * (e % NST));
-                            q_done(left);
-                            ++e;
-                        }
-                        for (int j = 0; j < n && ok; ++j) {
-                            const uint32_t ev = e, ek = e + 1;
-                            const bool more = j + 1 < n;
-                            ok = take(ev, w.jb[0] + j >= w.guard);
-                            bool have_k = false;
-                            for (int t = 0; t < 2 && ok; ++t) {
-                                if (j >= w.n[t]) continue;
-                                if (!(ok = weights(t))) break;
-                                tc_fence_after();
-                                weigh(t, ev % NST, j == 0);
-                                if (j + 1 == w.n[t]) tc_commit(o_full + 8 * t);
-                                if (t == 1 || j >= w.n[1]) tc_commit(empty_bar + 8 * (ev % NST));
-                                if (j + 1 < w.n[t]) {
-                                    if (!have_k && !(ok = take(ek, false))) break;
-                                    have_k = true;
-                                    tc_fence_after();
-                                    score(t, ek % NST);
-                                    --left;
-                                }
-                            }
-                            if (more && ok) tc_commit(empty_bar + 8 * (ek % NST));
-                            q_done(left);
-                            e += more ? 2 : 1;
-                        }
-                    } else {
-                        for (int t = 0; t < 2 && ok; ++t)
-                            if (w.n[t] > 0) {
-                                if (!(ok = take(e, false))) break;
-                                tc_fence_after();
-                                score(t, e % NST);
-                                tc_commit(empty_bar + 8 * (e % NST));
-                                --left;
-                                ++e;
-                            }
-                        q_done(left);
-                        for (int j = 0; j < n && ok; ++j)
-                            for (int t = 0; t < 2 && ok; ++t) {
-                                if (j >= w.n[t]) continue;
-                                if (!(ok = take(e, w.jb[t] + j >= w.guard)) || !(ok = weights(t))) break;
-                                tc_fence_after();
-                                weigh(t, e % NST, j == 0);
-                                tc_commit(empty_bar + 8 * (e % NST));
-                                if (j + 1 == w.n[t]) tc_commit(o_full + 8 * t);
-                                ++e;
-                                if (j + 1 < w.n[t]) {
-                                    if (!(ok = take(e, false))) break;
-                                    tc_fence_after();
-                                    score(t, e % NST);
-                                    tc_commit(empty_bar + 8 * (e % NST));
-                                    --left;
-                                    ++e;
-                                }
-                                q_done(left);
-                            }
-                    }
-                    ++nq;
+            auto advance = [&]() {
+                if (++st == NST) st = 0, ph ^= 1u;
+            };
+            // The ring's current entry has landed (and been looked over, if guarded).
+            auto take = [&](bool guarded) {
+                if (guarded) {
+                    if (!wait_all(guard_bar + 8 * st, (guard_phase >> st) & 1, ab, 5)) return false;
+                    guard_phase ^= 1u << st;
+                    return true;
                 }
-                ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+                return wait_all(full_bar + 8 * st, ph, ab, 4);
+            };
+            auto weights = [&](int t) {
+                const bool got = wait_all(p_ready + 8 * t, (t ? np1 : np0) & 1, ab, 6);
+                if (t) ++np1;
+                else ++np0;
+                return got;
+            };
+            // S_t = Q_t K^T with the keys of stage s
+            auto score = [&](int t, uint32_t s) {
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_scores<DP>(tm + t * KT, sQ + (SPLIT ? 0 : t * STAGE), sKV + s * STAGE);
+                    tc_commit(s_full + 8 * t);
+                }
+            };
+            // O_t += P_t V with the values of stage s
+            auto weigh = [&](int t, uint32_t s, bool first, bool last) {
+                tc_fence_after();
+                if (elect_one()) {
+                    mma_rows<DP>(tm + 256 + t * KT, tm + t * KT, sKV + s * STAGE, first, 32);
+                    if (last) tc_commit(o_full + 8 * t);
+                }
+            };
+            auto commit = [&](uint32_t bar) {
+                if (elect_one()) tc_commit(bar);
+            };
+            for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
+                const int n0 = uniform(wp->n[0]), n1 = uniform(wp->n[1]);
+                const int g0 = uniform(wp->guard - wp->jb[0]), g1 = uniform(wp->guard - wp->jb[1]);   // first guarded tile
+                const int n = max(n0, n1);
+                if (n == 0) continue;
+                if (!(ok = wait_all(q_full, nq & 1, ab, 3))) break;
+                ++nq;
+                int left = n0 + n1;                        // scores to issue with this unit's queries
+                if (!SPLIT) {
+                    if (!(ok = take(false))) break;
+                    if (n0 > 0) score(0, st), --left;
+                    if (n1 > 0) score(1, st), --left;
+                    commit(empty_bar + 8 * st);
+                    advance();
+                    if (left == 0) commit(q_empty);
+                    for (int j = 0; j < n; ++j) {
+                        const uint32_t sv = st;
+                        if (!(ok = take(j >= g0))) break;
+                        advance();
+                        const uint32_t sk = st;            // the next key tile, if there is one
+                        const bool more = j + 1 < n;
+                        bool have = false;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int nt = t ? n1 : n0;
+                            if (j >= nt) continue;
+                            if (!(ok = weights(t))) break;
+                            weigh(t, sv, j == 0, j + 1 == nt);
+                            if (t == 1 || j >= n1) commit(empty_bar + 8 * sv);
+                            if (j + 1 < nt) {
+                                if (!have && !(ok = take(false))) break;
+                                have = true;
+                                score(t, sk);
+                                if (--left == 0) commit(q_empty);
+                            }
+                        }
+                        if (!ok) break;
+                        if (more) {
+                            commit(empty_bar + 8 * sk);
+                            advance();
+                        }
+                    }
+                } else {
+                    auto scored = [&](int t) {
+                        if (!take(false)) return false;
+                        score(t, st);
+                        commit(empty_bar + 8 * st);
+                        advance();
+                        if (--left == 0) commit(q_empty);
+                        return true;
+                    };
+                    if (n0 > 0) ok = scored(0);
+                    if (ok && n1 > 0) ok = scored(1);
+                    for (int j = 0; j < n && ok; ++j) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            const int nt = t ? n1 : n0;
+                            if (j >= nt || !ok) continue;
+                            if (!(ok = take(j >= (t ? g1 : g0)) && weights(t))) continue;
+                            weigh(t, st, j == 0, j + 1 == nt);
+                            commit(empty_bar + 8 * st);
+                            advance();
+                            if (j + 1 < nt) ok = scored(t);
+                        }
+                    }
+                }
             }
-            if (lane == 0) {
-                tc_commit(drain_bar);
-                wait_bar(drain_bar, 0, ab, 10, true);
-            }
+            commit(drain_bar);
+            if (lane == 0) wait_bar(drain_bar, 0, ab, 10, true);
             __syncwarp();
         } else {
             // ---------------- guard: rows [64 g, 64 g + 64) of a value tile
@@ -512,7 +515,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             int here = lim - w.jb[t] * KT;                             // and from this key tile on
             float m = -INFINITY, mc = 0.f, l = 0.f;                    // mc = c * m, 0 while nothing was seen
             for (int j = 0; j < n; ++j, here -= KT) {
-                if (!(ok = __all_sync(0xFFFFFFFFu, wait_bar(s_full + 8 * t, ns & 1, ab, 8)))) break;
+                if (!(ok = wait_all(s_full + 8 * t, ns & 1, ab, 8))) break;
                 ++ns;
                 tc_fence_after();
                 uint32_t v[4][32];
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             }
             if (!ok) break;
             if (n > 0) {
-                if (!(ok = __all_sync(0xFFFFFFFFu, wait_bar(o_full + 8 * t, no & 1, ab, 11)))) break;
+                if (!(ok = wait_all(o_full + 8 * t, no & 1, ab, 11))) break;
                 ++no;
                 tc_fence_after();
             }
@@ -639,76 +642,83 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Joins the parts of split rows in part order: one warp a row,
+// Joins the parts of split rows in part order: one block a row,
 //   lse = m + ln sum_c exp(lse_c - m),  o = sum_c exp(lse_c - lse) o_c.
+// Warp w adds parts w, w + 8, ..., and the warps' sums are added in warp order.
+constexpr int JOIN_WARPS = 8;
+
 template <int DP, bool SPLIT>
-__global__ void __launch_bounds__(256) k_attn_join(const Params p)
+__global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
 {
-    const int lane = threadIdx.x & 31;
-    const Plan pl = make_plan<SPLIT>(p, lane);
-    const long long rows = (long long)p.P * p.Tq * p.Hq;
+    __shared__ float acc_s[JOIN_WARPS][DP + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int qi = blockIdx.x / p.Hq, head = blockIdx.x % p.Hq, slot = blockIdx.y;
     const int HP = p.P * p.Hkv;
-    for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
-        const int head = (int)(row % p.Hq);
-        const int qi = (int)(row / p.Hq % p.Tq), slot = (int)(row / p.Hq / p.Tq);
-        // the sequence of token qi, and the units before it
-        int units = 0, b_hit = -1;
-        Seq s{};
-        for (int b0 = 0; b0 < p.B && b_hit < 0; b0 += 32) {
-            const int b = b0 + lane;
-            Seq sb{};
-            int n = 0;
-            if (b < p.B) {
-                sb = seq_of(p, b);
-                const int kt = (sb.kl + KT - 1) / KT;
-                n = ((sb.ql + p.TPU - 1) / p.TPU) * units_per_tile<SPLIT>(kt, pl.cs);
-            }
-            const int inc = warp_incl_scan(n, lane);
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, b < p.B && qi >= sb.q0 && qi < sb.q0 + sb.ql);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                b_hit = b0 + src;
-                units += __shfl_sync(0xFFFFFFFFu, inc - n, src);
-            } else {
-                units += __shfl_sync(0xFFFFFFFFu, inc, 31);
-            }
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written
+    const Plan pl = make_plan<SPLIT>(p, lane);
+    // the sequence of token qi, and the units before it
+    int units = 0, b_hit = -1;
+    for (int b0 = 0; b0 < p.B && b_hit < 0; b0 += 32) {
+        const int b = b0 + lane;
+        Seq sb{};
+        int n = 0;
+        if (b < p.B) {
+            sb = seq_of(p, b);
+            n = ((sb.ql + p.TPU - 1) / p.TPU) * units_per_tile<SPLIT>((sb.kl + KT - 1) / KT, pl.cs);
         }
-        if (b_hit < 0) continue;
-        s = seq_of(p, b_hit);
-        const int kt = (s.kl + KT - 1) / KT, cs = pl.cs;
-        const int np = parts_of(kt, cs), upt = units_per_tile<SPLIT>(kt, cs);
-        if (np == 1) continue;
-        const int i = qi - s.q0, tile = i / p.TPU, nt = (s.ql + p.TPU - 1) / p.TPU;
-        const int in_tile = i - tile * p.TPU, t_pair = in_tile / p.TT;
-        const int r = (in_tile % p.TT) * p.G + head % p.G;
-        const int x0 = units + (nt - 1 - tile) * upt, hp = slot * p.Hkv + head / p.G;
-        auto slot_of = [&](int c) {
-            const size_t u = (size_t)(x0 + (SPLIT ? c >> 1 : c)) * HP + hp;
-            return (2 * u + (SPLIT ? c & 1 : t_pair)) * p.part_rows + r;
-        };
-        float m = -INFINITY;
-        for (int c = lane; c < np; c += 32) m = fmaxf(m, p.part_lse[slot_of(c)]);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const float base = m == -INFINITY ? 0.f : m;
-        float acc[DP / 32] = {}, sum = 0.f;
-        for (int c = 0; c < np; ++c) {
-            const size_t sl = slot_of(c);
-            const float wgt = expf(p.part_lse[sl] - base);
-            sum += wgt;
-#pragma unroll
-            for (int d = 0; d < DP / 32; ++d) acc[d] += wgt * p.part_o[sl * DP + d * 32 + lane];
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        char *const dst = p.out.base + slot * p.out.slot + (size_t)qi * p.out.token + head * p.out.head;
-#pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
-            if (d * 32 + lane < p.D) st_u16(dst + (d * 32 + lane) * 2, (uint16_t)pack2(acc[d] * inv, 0.f));
-        if (lane == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
+        const int inc = warp_incl_scan(n, lane);
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, b < p.B && qi >= sb.q0 && qi < sb.q0 + sb.ql);
+        const int src = hit ? __ffs(hit) - 1 : 31;
+        units += __shfl_sync(0xFFFFFFFFu, hit ? inc - n : inc, src);
+        if (hit) b_hit = b0 + src;
     }
+    if (b_hit < 0) return;
+    const Seq s = seq_of(p, b_hit);
+    const int kt = (s.kl + KT - 1) / KT;
+    const int np = parts_of(kt, pl.cs), upt = units_per_tile<SPLIT>(kt, pl.cs);
+    if (np == 1) return;
+    const int i = qi - s.q0, tile = i / p.TPU, nt = (s.ql + p.TPU - 1) / p.TPU;
+    const int in_tile = i - tile * p.TPU, t_pair = in_tile / p.TT;
+    const int r = (in_tile % p.TT) * p.G + head % p.G;
+    const int x0 = units + (nt - 1 - tile) * upt, hp = slot * p.Hkv + head / p.G;
+    auto slot_of = [&](int c) {
+        const size_t u = (size_t)(x0 + (SPLIT ? c >> 1 : c)) * HP + hp;
+        return (2 * u + (SPLIT ? c & 1 : t_pair)) * p.part_rows + r;
+    };
+    float m = -INFINITY;
+    for (int c = lane; c < np; c += 32) m = fmaxf(m, p.part_lse[slot_of(c)]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    float acc[DP / 32] = {}, sum = 0.f;
+#pragma unroll 4
+    for (int c = warp; c < np; c += JOIN_WARPS) {
+        const size_t sl = slot_of(c);
+        const float wgt = expf(p.part_lse[sl] - base);
+        sum += wgt;
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d) acc[d] = fmaf(wgt, p.part_o[sl * DP + d * 32 + lane], acc[d]);
+    }
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d) acc_s[warp][d * 32 + lane] = acc[d];
+    if (lane == 0) acc_s[warp][DP] = sum;
+    __syncthreads();
+    float o = 0.f;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w) sum += acc_s[w][DP];
+    const int d = threadIdx.x;
+    if (d < p.D) {
+#pragma unroll
+        for (int w = 0; w < JOIN_WARPS; ++w) o += acc_s[w][d];
+        char *const dst = p.out.base + slot * p.out.slot + (size_t)qi * p.out.token + head * p.out.head;
+        st_u16(dst + d * 2, (uint16_t)pack2(sum == 0.f ? 0.f : o / sum, 0.f));
+    }
+    if (d == 0 && p.lse) p.lse[((size_t)slot * p.Tq + qi) * p.Hq + head] = sum == 0.f ? -INFINITY : base + logf(sum);
 }
 
 template <int DP, bool SPLIT>
@@ -725,10 +735,17 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
     k_attn_fwd<DP, SPLIT><<<p.sms, FWD_THREADS, FwdCfg<DP, SPLIT>::SMEM, st>>>(mq, mk, mv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.may_split) return e;
-    const long long rows = (long long)p.P * p.Tq * p.Hq;
-    const long long blocks = (rows + 7) / 8;
-    k_attn_join<DP, SPLIT><<<(unsigned)(blocks < 8ll * p.sms ? blocks : 8ll * p.sms), 256, 0, st>>>(p);
-    return cudaGetLastError();
+    // The join's blocks may be set up while the last units still run.
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.Tq * p.Hq), (unsigned)p.P);
+    cfg.blockDim = dim3(32 * JOIN_WARPS);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attn_join<DP, SPLIT>, p);
 }
 
 cudaError_t launch_attn_fwd(const Params &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
