@@ -180,6 +180,7 @@ static int run_fwd(const rc_attn_args *args, void *stream)
     p.part_o = (float *)scratch;
     p.part_lse = (float *)(scratch + 2 * f.units * (size_t)p.part_rows * (p.D <= 64 ? 64 : 128) * 4);
     p.out = strided(a.out);
+    p.out32 = !(((uintptr_t)a.out.base | a.out.slot | a.out.token | a.out.head) & 31u) && a.D % 16 == 0;
     p.v = (const char *)a.v.base;
     p.v_slot = a.v.slot;
     p.v_token = a.v.token;

@@ -373,42 +373,55 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 if (n == 0) continue;
                 if (!(ok = wait_all(q_full, nq & 1, ab, 3))) break;
                 ++nq;
-                int left = n0 + n1;                        // scores to issue with this unit's queries
                 if (!SPLIT) {
                     if (!(ok = take(false))) break;
-                    if (n0 > 0) score(0, st), --left;
-                    if (n1 > 0) score(1, st), --left;
-                    commit(empty_bar + 8 * st);
+                    tc_fence_after();
+                    if (elect_one()) {
+                        if (n0 > 0) mma_scores<DP>(tm, sQ, sKV + st * STAGE), tc_commit(s_full);
+                        if (n1 > 0) mma_scores<DP>(tm + KT, sQ + STAGE, sKV + st * STAGE), tc_commit(s_full + 8);
+                        tc_commit(empty_bar + 8 * st);
+                        if (n == 1) tc_commit(q_empty);
+                    }
                     advance();
-                    if (left == 0) commit(q_empty);
                     for (int j = 0; j < n; ++j) {
+                        // The values of this tile and the keys of the next are there before the
+                        // weights are waited for, so nothing stands between the two products.
                         const uint32_t sv = st;
                         if (!(ok = take(j >= g0))) break;
                         advance();
-                        const uint32_t sk = st;            // the next key tile, if there is one
+                        const uint32_t sk = st;
                         const bool more = j + 1 < n;
-                        bool have = false;
+                        if (more) {
+                            if (!(ok = take(false))) break;
+                            advance();
+                        }
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             const int nt = t ? n1 : n0;
                             if (j >= nt) continue;
                             if (!(ok = weights(t))) break;
-                            weigh(t, sv, j == 0, j + 1 == nt);
-                            if (t == 1 || j >= n1) commit(empty_bar + 8 * sv);
-                            if (j + 1 < nt) {
-                                if (!have && !(ok = take(false))) break;
-                                have = true;
-                                score(t, sk);
-                                if (--left == 0) commit(q_empty);
+                            tc_fence_after();
+                            const bool last_v = t == 1 || j >= n1;                   // the tile's last use here
+                            const bool last_k = t == 1 || j + 1 >= n1;
+                            if (elect_one()) {
+                                mma_rows<DP>(tm + 256 + t * KT, tm + t * KT, sKV + sv * STAGE, j == 0, 32);
+                                if (j + 1 < nt) {
+                                    mma_scores<DP>(tm + t * KT, sQ + t * STAGE, sKV + sk * STAGE);
+                                    tc_commit(s_full + 8 * t);
+                                    if (last_k) {
+                                        tc_commit(empty_bar + 8 * sk);
+                                        if (j + 2 == n) tc_commit(q_empty);
+                                    }
+                                } else {
+                                    tc_commit(o_full + 8 * t);
+                                }
+                                if (last_v) tc_commit(empty_bar + 8 * sv);
                             }
                         }
                         if (!ok) break;
-                        if (more) {
-                            commit(empty_bar + 8 * sk);
-                            advance();
-                        }
                     }
                 } else {
+                    int left = n0 + n1;                    // scores to issue with this unit's queries
                     auto scored = [&](int t) {
                         if (!take(false)) return false;
                         score(t, st);
@@ -513,30 +526,60 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             const bool valid = ti < w.ntok[t];
             const int lim = valid ? seen(p, w.s, tok) : 0;             // keys this row sees
             int here = lim - w.jb[t] * KT;                             // and from this key tile on
+            // From this tile on some row of the warp does not see every key.
+            const bool any = __any_sync(0xFFFFFFFFu, valid);
+            const int mask_from = __reduce_min_sync(0xFFFFFFFFu, valid ? max(here, 0) : kNoSplit) / KT;
             float m = -INFINITY, mc = 0.f, l = 0.f;                    // mc = c * m, 0 while nothing was seen
             for (int j = 0; j < n; ++j, here -= KT) {
                 if (!(ok = wait_all(s_full + 8 * t, ns & 1, ab, 8))) break;
                 ++ns;
                 tc_fence_after();
+                if (SPLIT && !any) {      // no row of this warp is in use: whatever P holds is not read
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_ready + 8 * t);
+                    continue;
+                }
                 uint32_t v[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_ld32_async(tS + q * 32, v[q]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_wait_ld32(v[q]);
-                if (__any_sync(0xFFFFFFFFu, here < KT)) {
+                if (j >= mask_from) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (q * 32 + i >= here) v[q][i] = 0xFF800000u;
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // 32 weights and their share of the row sum
+                uint64_t sum = 0;
+                auto weights32 = [&](const uint32_t (&x)[32], uint32_t (&pk)[16], uint64_t acc) {
+                    const uint64_t c2 = f2(c, c), m2 = f2(-mc, -mc);
+                    uint64_t s0 = acc, s1 = 0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                    for (int i = 0; i < 16; ++i) {
+                        float a, b;
+                        unf2(fma2(f2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, m2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        if (i & 1) s1 = add2(s1, f2(a, b));
+                        else s0 = add2(s0, f2(a, b));
+                        pk[i] = pack2(a, b);
+                    }
+                    return add2(s0, s1);
+                };
+                // The first 32 weights are taken with the maximum so far, under the search for
+                // the new one, and taken again in the rare case that it has to move.
+                uint32_t p0[16];
+                uint64_t w0 = weights32(v[0], p0, 0);
+                float mx[4];
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(v[q][i]), __uint_as_float(v[q][i + 1])));
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                for (int q = 0; q < 4; ++q) {
+                    mx[q] = fmaxf(__uint_as_float(v[q][0]), __uint_as_float(v[q][1]));
+#pragma unroll
+                    for (int i = 2; i < 32; i += 2) mx[q] = max3(mx[q], __uint_as_float(v[q][i]), __uint_as_float(v[q][i + 1]));
+                }
+                const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 // Move m when it would grow by more than 8 / c, or off -inf.
                 const bool move = mt > m && (m == -INFINITY || (mt - m) * c > 8.f);
                 if (__any_sync(0xFFFFFFFFu, move)) {
@@ -548,7 +591,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     l *= f;
                     if (j > 0) {
                         uint32_t o[32];
-#pragma unroll
+#pragma unroll 1
                         for (int q = 0; q < DP / 32; ++q) {
                             tmem_ld32(tO + q * 32, o);
 #pragma unroll
@@ -556,21 +599,19 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                             tmem_st32(tO + q * 32, o);
                         }
                     }
+                    w0 = weights32(v[0], p0, 0);
                 }
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                sum = w0;
+                tmem_st16(tS, p0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 1; q < 4; ++q) {
                     uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float a = ex2(fmaf(__uint_as_float(v[q][2 * i]), c, -mc));
-                        const float b = ex2(fmaf(__uint_as_float(v[q][2 * i + 1]), c, -mc));
-                        sum[i & 3] += a + b;
-                        pk[i] = pack2(a, b);
-                    }
+                    sum = weights32(v[q], pk, sum);
                     tmem_st16(tS + q * 16, pk);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float sa, sb;
+                unf2(sum, sa, sb);
+                l += sa + sb;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -617,7 +658,16 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                             }
                     }
                 }
-                if (final_) {
+                if (final_ && p.out32) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 16)
+                        if (q * 32 + i < p.D)
+                            st8<kStNormal>(dst + (q * 32 + i) * 2,
+                                           make_uint4(pack2(f[i], f[i + 1]), pack2(f[i + 2], f[i + 3]),
+                                                      pack2(f[i + 4], f[i + 5]), pack2(f[i + 6], f[i + 7])),
+                                           make_uint4(pack2(f[i + 8], f[i + 9]), pack2(f[i + 10], f[i + 11]),
+                                                      pack2(f[i + 12], f[i + 13]), pack2(f[i + 14], f[i + 15])));
+                } else if (final_) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8)
                         if (q * 32 + i < p.D)
@@ -625,8 +675,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                                                                      pack2(f[i + 4], f[i + 5]), pack2(f[i + 6], f[i + 7])));
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        *(float4 *)(part + q * 32 + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+                    for (int i = 0; i < 32; i += 8)
+                        st8<kStNormal>(part + q * 32 + i,
+                                       make_uint4(__float_as_uint(f[i]), __float_as_uint(f[i + 1]),
+                                                  __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3])),
+                                       make_uint4(__float_as_uint(f[i + 4]), __float_as_uint(f[i + 5]),
+                                                  __float_as_uint(f[i + 6]), __float_as_uint(f[i + 7])));
                 }
             }
             if (valid) {
