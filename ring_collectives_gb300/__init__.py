@@ -501,10 +501,22 @@ def ring_allreduce_noalloc(bufs: torch.Tensor, N: int | None = None, stream=None
 # rc_attn_args of include/ringcoll.h: eight rc_heads, six pointers and sizes, eight ints, scale, reserved
 _ATTN_ARGS = struct.Struct("@32Q6Q8ifi")
 _NO_HEADS = (0, 0, 0, 0)
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _launch(fn, args: bytes, device, stream) -> None:
+    """One call of a struct-argument entry point on `stream` (default: the current one)."""
+    if stream is None and device.index == torch.cuda.current_device():
+        rc = fn(args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(args, _stream(stream, device))
+    if rc != RC_OK:
+        _check(rc)
 
 
 def _heads(t: torch.Tensor, name: str, shape=None):
-    if not t.is_cuda or t.dtype != torch.bfloat16:
+    if t.dtype != _BF16 or not t.is_cuda:
         raise TypeError(f"{name} must be a bf16 CUDA tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
@@ -515,7 +527,7 @@ def _heads(t: torch.Tensor, name: str, shape=None):
 
 
 def _index(t, name: str, n: int) -> int:
-    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or t.size(0) != n or not t.is_contiguous():
+    if t.dtype != _I32 or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 CUDA tensor of {n} elements")
     return t.data_ptr()
 
@@ -544,13 +556,12 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
         _index(cu_k, "cu_k", B + 1), 0 if used_k is None else _index(used_k, "used_k", B),
         *((0, 0) if workspace is None else _ws(workspace)),
         *_attn_sizes(P, B, Tq, kshape[1], Hq, kshape[2], D, causal, scale))
-    with torch.cuda.device(q.device):
-        _check(load().attn_fwd(args, _stream(stream, q.device)))
+    _launch(load().attn_fwd, args, q.device, stream)
     return out
 
 
 def _lse(lse, P, Tq, Hq):
-    if not lse.is_cuda or lse.dtype != torch.float32 or lse.shape != (P, Tq, Hq) or not lse.is_contiguous():
+    if lse.dtype != _F32 or lse.shape != (P, Tq, Hq) or not lse.is_cuda or not lse.is_contiguous():
         raise TypeError(f"lse must be a contiguous float32 CUDA tensor of shape {[P, Tq, Hq]}")
     return lse.data_ptr()
 
@@ -577,8 +588,7 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
         _index(cu_k, "cu_k", B + 1), 0 if used_k is None else _index(used_k, "used_k", B),
         *((0, 0) if workspace is None else _ws(workspace)),
         *_attn_sizes(P, B, Tq, kshape[1], Hq, kshape[2], D, causal, scale))
-    with torch.cuda.device(q.device):
-        _check(load().attn_bwd(args, _stream(stream, q.device)))
+    _launch(load().attn_bwd, args, q.device, stream)
     return dq, dk, dv
 
 
@@ -592,7 +602,7 @@ _QK_NORM_ARGS = struct.Struct("@24Q9Q7if")
 
 
 def _f32(t, name: str, shape) -> int:
-    if not t.is_cuda or t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+    if t.dtype != _F32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of shape {list(shape)}")
     return t.data_ptr()
 
@@ -619,8 +629,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, gamma_q: torch.Tensor, gamma_
     q, q_out [P, T, Hq, D], k, k_out [P, T, Hkv, D] bf16, any strides as for attn_fwd; in
     place when q_out is q and k_out is k."""
     args = _qk_norm(q, k, gamma_q, gamma_k, cos, sin, pos, layout, eps, q_out, k_out, None, None)
-    with torch.cuda.device(q.device):
-        _check(load().qk_norm_rope(args, _stream(stream, q.device)))
+    _launch(load().qk_norm_rope, args, q.device, stream)
     return q_out, k_out
 
 
@@ -634,8 +643,7 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, gamma_q: torch.Tensor, ga
     the weight gradients, dgamma_q and dgamma_k (float32 [P, D])."""
     args = _qk_norm(q, k, gamma_q, gamma_k, cos, sin, pos, layout, eps, dq_out, dk_out, (dq, dk, dgamma_q, dgamma_k),
                     workspace)
-    with torch.cuda.device(q.device):
-        _check(load().qk_norm_rope_bwd(args, _stream(stream, q.device)))
+    _launch(load().qk_norm_rope_bwd, args, q.device, stream)
     return dq, dk
 
 

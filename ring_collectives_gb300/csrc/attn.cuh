@@ -286,6 +286,27 @@ constexpr int kNoSplit = 1 << 28;          // key tiles of a part when keys are 
 // Parts (SPLIT) or units (PAIR) that a split launch aims at.
 __host__ __device__ constexpr long long split_target(bool split, int sms) { return (split ? 8ll : 3ll) * sms; }
 
+// Units go to blocks as they come free: block i starts with unit i and takes
+// the next one from a counter.  Two words of the status header that nothing
+// else uses hold the counter and the blocks that are done; the last block
+// clears both, also in a launch that gave up (every block reaches its end).
+// Which block runs a unit changes no result.
+__device__ __forceinline__ int claim_unit(const Params &p, int lane)
+{
+    int u = 0;
+    if (lane == 0) u = (int)(gridDim.x + atomicAdd(&p.hdr->pad[2], 1u));
+    return __shfl_sync(0xFFFFFFFFu, u, 0);
+}
+
+__device__ __forceinline__ void units_done(const Params &p)
+{
+    __threadfence();
+    if (atomicAdd(&p.hdr->pad[3], 1u) == gridDim.x - 1) {
+        atomicExch(&p.hdr->pad[2], 0u);
+        atomicExch(&p.hdr->pad[3], 0u);
+    }
+}
+
 // Host helpers (attn_api.cu).
 int head_map5(CUtensorMap *map, const rc_heads &h, int P, int T, int Hkv, int G, int D, int box_tokens);
 int head_map4(CUtensorMap *map, const rc_heads &h, int P, int T, int Hkv, int D);

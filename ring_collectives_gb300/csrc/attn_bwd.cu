@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             bool ok = publish(0, next);
             while (ok && next.index >= 0) {
                 const BUnit w = next;
-                u += gridDim.x;
+                u = claim_unit(p, lane);
                 if (u < total) next = bunit_of<DKV>(p, u, lane);
                 else next.index = -1;
                 ok = publish(++it, next);
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                 }
                 ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
             }
+            if (lane == 0) units_done(p);
             if (lane == 0 && *(volatile int *)abort_flag) {
                 // let the copies in flight land before the block gives up its shared memory
                 for (uint32_t s = 0; s < NA; ++s)

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             bool ok = publish(0, next);
             while (ok && next.index >= 0) {
                 const Unit w = next;
-                u += gridDim.x;
+                u = claim_unit(p, lane);
                 if (u < total) next = unit_of<SPLIT>(p, pl, u, lane);
                 else next.index = -1;
                 ok = publish(++it, next);
@@ -315,6 +315,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 }
                 ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
             }
+            if (lane == 0) units_done(p);
             if (lane == 0 && *(volatile int *)abort_flag) {
                 // let the copies in flight land before the block gives up its shared memory
                 for (uint32_t s = 0; s < NST; ++s)
@@ -700,79 +701,97 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Joins the parts of split rows in part order: one block a row,
+// Joins the parts of split rows in part order:
 //   lse = m + ln sum_c exp(lse_c - m),  o = sum_c exp(lse_c - lse) o_c.
-// Warp w adds parts w, w + 8, ..., and the warps' sums are added in warp order.
+// SPLIT has few rows with up to hundreds of parts: a block of 8 warps takes a
+// row, warp w adds parts w, w + 8, ..., and the warps' sums are added in warp
+// order.  PAIR has many rows of about ten parts: a warp takes a row.
 constexpr int JOIN_WARPS = 8;
 
 template <int DP, bool SPLIT>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
 {
-    __shared__ float acc_s[JOIN_WARPS][DP + 1];
+    constexpr int W = SPLIT ? JOIN_WARPS : 1;              // warps of a row
+    constexpr int ROWS = JOIN_WARPS / W;                   // rows of a block at a time
+    __shared__ float acc_s[SPLIT ? W : 1][DP + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int qi = blockIdx.x / p.Hq, head = blockIdx.x % p.Hq, slot = blockIdx.y;
-    const int HP = p.P * p.Hkv;
     asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written
     const Plan pl = make_plan<SPLIT>(p, lane);
-    // the sequence of token qi, and the units before it
-    int units = 0, b_hit = -1;
-    for (int b0 = 0; b0 < p.B && b_hit < 0; b0 += 32) {
-        const int b = b0 + lane;
-        Seq sb{};
-        int n = 0;
-        if (b < p.B) {
-            sb = seq_of(p, b);
-            n = ((sb.ql + p.TPU - 1) / p.TPU) * units_per_tile<SPLIT>((sb.kl + KT - 1) / KT, pl.cs);
+    const int HP = p.P * p.Hkv;
+    const long long rows = (long long)p.P * p.Tq * p.Hq;
+    for (long long row = (long long)blockIdx.x * ROWS + warp / W; row < rows; row += (long long)gridDim.x * ROWS) {
+        const int head = (int)(row % p.Hq), qi = (int)(row / p.Hq % p.Tq), slot = (int)(row / p.Hq / p.Tq);
+        // the sequence of token qi, and the units before it
+        int units = 0, b_hit = -1;
+        for (int b0 = 0; b0 < p.B && b_hit < 0; b0 += 32) {
+            const int b = b0 + lane;
+            Seq sb{};
+            int n = 0;
+            if (b < p.B) {
+                sb = seq_of(p, b);
+                n = ((sb.ql + p.TPU - 1) / p.TPU) * units_per_tile<SPLIT>((sb.kl + KT - 1) / KT, pl.cs);
+            }
+            const int inc = warp_incl_scan(n, lane);
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, b < p.B && qi >= sb.q0 && qi < sb.q0 + sb.ql);
+            const int src = hit ? __ffs(hit) - 1 : 31;
+            units += __shfl_sync(0xFFFFFFFFu, hit ? inc - n : inc, src);
+            if (hit) b_hit = b0 + src;
         }
-        const int inc = warp_incl_scan(n, lane);
-        const unsigned hit = __ballot_sync(0xFFFFFFFFu, b < p.B && qi >= sb.q0 && qi < sb.q0 + sb.ql);
-        const int src = hit ? __ffs(hit) - 1 : 31;
-        units += __shfl_sync(0xFFFFFFFFu, hit ? inc - n : inc, src);
-        if (hit) b_hit = b0 + src;
-    }
-    if (b_hit < 0) return;
-    const Seq s = seq_of(p, b_hit);
-    const int kt = (s.kl + KT - 1) / KT;
-    const int np = parts_of(kt, pl.cs), upt = units_per_tile<SPLIT>(kt, pl.cs);
-    if (np == 1) return;
-    const int i = qi - s.q0, tile = i / p.TPU, nt = (s.ql + p.TPU - 1) / p.TPU;
-    const int in_tile = i - tile * p.TPU, t_pair = in_tile / p.TT;
-    const int r = (in_tile % p.TT) * p.G + head % p.G;
-    const int x0 = units + (nt - 1 - tile) * upt, hp = slot * p.Hkv + head / p.G;
-    auto slot_of = [&](int c) {
-        const size_t u = (size_t)(x0 + (SPLIT ? c >> 1 : c)) * HP + hp;
-        return (2 * u + (SPLIT ? c & 1 : t_pair)) * p.part_rows + r;
-    };
-    float m = -INFINITY;
-    for (int c = lane; c < np; c += 32) m = fmaxf(m, p.part_lse[slot_of(c)]);
+        if (b_hit < 0) continue;
+        const Seq s = seq_of(p, b_hit);
+        const int kt = (s.kl + KT - 1) / KT;
+        const int np = parts_of(kt, pl.cs), upt = units_per_tile<SPLIT>(kt, pl.cs);
+        if (np == 1) continue;
+        const int i = qi - s.q0, tile = i / p.TPU, nt = (s.ql + p.TPU - 1) / p.TPU;
+        const int in_tile = i - tile * p.TPU, t_pair = in_tile / p.TT;
+        const int r = (in_tile % p.TT) * p.G + head % p.G;
+        const int x0 = units + (nt - 1 - tile) * upt, hp = slot * p.Hkv + head / p.G;
+        auto slot_of = [&](int c) {
+            const size_t u = (size_t)(x0 + (SPLIT ? c >> 1 : c)) * HP + hp;
+            return (2 * u + (SPLIT ? c & 1 : t_pair)) * p.part_rows + r;
+        };
+        float m = -INFINITY;
+        for (int c = lane; c < np; c += 32) m = fmaxf(m, p.part_lse[slot_of(c)]);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const float base = m == -INFINITY ? 0.f : m;
-    float acc[DP / 32] = {}, sum = 0.f;
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float base = m == -INFINITY ? 0.f : m;
+        constexpr int E = DP / 32;                         // elements of a lane, next to each other
+        float acc[E] = {}, sum = 0.f;
 #pragma unroll 4
-    for (int c = warp; c < np; c += JOIN_WARPS) {
-        const size_t sl = slot_of(c);
-        const float wgt = expf(p.part_lse[sl] - base);
-        sum += wgt;
+        for (int c = warp % W; c < np; c += W) {
+            const size_t sl = slot_of(c);
+            const float wgt = expf(p.part_lse[sl] - base);
+            sum += wgt;
+            float x[E];
+            if (E == 4) *(float4 *)x = *(const float4 *)(p.part_o + sl * DP + lane * E);
+            else *(float2 *)x = *(const float2 *)(p.part_o + sl * DP + lane * E);
 #pragma unroll
-        for (int d = 0; d < DP / 32; ++d) acc[d] = fmaf(wgt, p.part_o[sl * DP + d * 32 + lane], acc[d]);
-    }
-#pragma unroll
-    for (int d = 0; d < DP / 32; ++d) acc_s[warp][d * 32 + lane] = acc[d];
-    if (lane == 0) acc_s[warp][DP] = sum;
-    __syncthreads();
-    float o = 0.f;
-    sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < JOIN_WARPS; ++w) sum += acc_s[w][DP];
-    const int d = threadIdx.x;
-    if (d < p.D) {
-#pragma unroll
-        for (int w = 0; w < JOIN_WARPS; ++w) o += acc_s[w][d];
+            for (int d = 0; d < E; ++d) acc[d] = fmaf(wgt, x[d], acc[d]);
+        }
         char *const dst = p.out.base + slot * p.out.slot + (size_t)qi * p.out.token + head * p.out.head;
-        st_u16(dst + d * 2, (uint16_t)pack2(sum == 0.f ? 0.f : o / sum, 0.f));
+        if (SPLIT) {
+#pragma unroll
+            for (int d = 0; d < E; ++d) acc_s[warp][lane * E + d] = acc[d];
+            if (lane == 0) acc_s[warp][DP] = sum;
+            __syncthreads();                               // the row is the whole block's
+            sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) sum += acc_s[w][DP];
+            const int d = threadIdx.x;
+            if (d < p.D) {
+                float o = 0.f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) o += acc_s[w][d];
+                st_u16(dst + d * 2, (uint16_t)pack2(sum == 0.f ? 0.f : o / sum, 0.f));
+            }
+            __syncthreads();
+        } else if (lane * E < p.D) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+            for (int d = 0; d < E; d += 2) st_u32(dst + (lane * E + d) * 2, pack2(acc[d] * inv, acc[d + 1] * inv));
+        }
+        if (lane == 0 && warp % W == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : base + logf(sum);
     }
-    if (d == 0 && p.lse) p.lse[((size_t)slot * p.Tq + qi) * p.Hq + head] = sum == 0.f ? -INFINITY : base + logf(sum);
 }
 
 template <int DP, bool SPLIT>
@@ -791,7 +810,8 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
     if (e != cudaSuccess || !p.may_split) return e;
     // The join's blocks may be set up while the last units still run.
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(p.Tq * p.Hq), (unsigned)p.P);
+    const long long blocks = ((long long)p.P * p.Tq * p.Hq + (SPLIT ? 0 : JOIN_WARPS - 1)) / (SPLIT ? 1 : JOIN_WARPS);
+    cfg.gridDim = dim3((unsigned)(blocks < 8ll * p.sms ? blocks : 8ll * p.sms));
     cfg.blockDim = dim3(32 * JOIN_WARPS);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
