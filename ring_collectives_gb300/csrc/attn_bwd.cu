@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     BUnit *const units = (BUnit *)(ctl + 512);
     uint32_t *const tmem_slot = (uint32_t *)(ctl + 1000);
     int *const abort_flag = (int *)(ctl + 1004);
-    float *const stats = (float *)(ctl + 1024);       // dkv: [2 stages][lse, delta][128 rows]
+    float *const stats = (float *)(ctl + 1024);       // dkv: [2 stages][-lse log2 e, -delta][128 rows]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -420,8 +420,8 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int r = (warp - 10) * 64 + h * 32 + lane;
-                        stats[st * 256 + r] = l2[h];
-                        stats[st * 256 + 128 + r] = dl[h];
+                        stats[st * 256 + r] = -l2[h];
+                        stats[st * 256 + 128 + r] = -dl[h];
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar.stat_full + 8 * st);
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         const int wg = warp >> 2, r = threadIdx.x & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tm = tmem + lane_off;
-        const float c = p.scale * kLog2e;
+        const uint64_t c2 = f2(p.scale * kLog2e, p.scale * kLog2e);
         uint32_t ns = 0, nu = 0, nsb[2] = {0, 0};
         bool ok = true;
         const BUnit *wp;
@@ -470,11 +470,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
-                            const float4 l4 = *(const float4 *)(sl + q * 32 + i);
-                            pr[q * 32 + i] = ex2(fmaf(__uint_as_float(s[q][i]), c, -l4.x));
-                            pr[q * 32 + i + 1] = ex2(fmaf(__uint_as_float(s[q][i + 1]), c, -l4.y));
-                            pr[q * 32 + i + 2] = ex2(fmaf(__uint_as_float(s[q][i + 2]), c, -l4.z));
-                            pr[q * 32 + i + 3] = ex2(fmaf(__uint_as_float(s[q][i + 3]), c, -l4.w));
+                            const ulonglong2 l4 = *(const ulonglong2 *)(sl + q * 32 + i);   // minus the row's log-sum
+                            float *const x = pr + q * 32 + i;
+                            unf2(fma2(f2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), c2, l4.x), x[0], x[1]);
+                            unf2(fma2(f2(__uint_as_float(s[q][i + 2]), __uint_as_float(s[q][i + 3])), c2, l4.y), x[2], x[3]);
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) x[h] = ex2(x[h]);
                         }
                     if (mask) {
 #pragma unroll
@@ -511,11 +512,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
                         for (int i = 0; i < 32; i += 4) {
-                            const float4 d4 = *(const float4 *)(sd + q * 32 + i);
-                            pr[q * 32 + i] *= __uint_as_float(s[q][i]) - d4.x;
-                            pr[q * 32 + i + 1] *= __uint_as_float(s[q][i + 1]) - d4.y;
-                            pr[q * 32 + i + 2] *= __uint_as_float(s[q][i + 2]) - d4.z;
-                            pr[q * 32 + i + 3] *= __uint_as_float(s[q][i + 3]) - d4.w;
+                            const ulonglong2 d4 = *(const ulonglong2 *)(sd + q * 32 + i);   // minus the row's delta
+                            float *const x = pr + q * 32 + i;
+                            unf2(mul2(f2(x[0], x[1]), add2(f2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), d4.x)),
+                                 x[0], x[1]);
+                            unf2(mul2(f2(x[2], x[3]), add2(f2(__uint_as_float(s[q][i + 2]), __uint_as_float(s[q][i + 3])), d4.y)),
+                                 x[2], x[3]);
                         }
                     if (mask) {
 #pragma unroll
@@ -588,7 +590,12 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) pr[q * 32 + i] = ex2(fmaf(__uint_as_float(s[q][i]), c, -l2));
+                        for (int i = 0; i < 32; i += 2) {
+                            float *const x = pr + q * 32 + i;
+                            unf2(fma2(f2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), c2, f2(-l2, -l2)), x[0], x[1]);
+                            x[0] = ex2(x[0]);
+                            x[1] = ex2(x[1]);
+                        }
                     if (!(ok = wait_all(bar.dp_full, ns & 1, ab, 16))) break;
                     tc_fence_after();
                     tmem_ld32_async(tm + 256 + wg * 64, s[0]);
@@ -598,7 +605,11 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
 #pragma unroll
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) pr[q * 32 + i] *= __uint_as_float(s[q][i]) - delta;
+                        for (int i = 0; i < 32; i += 2) {
+                            float *const x = pr + q * 32 + i;
+                            const uint64_t d = add2(f2(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])), f2(-delta, -delta));
+                            unf2(mul2(f2(x[0], x[1]), d), x[0], x[1]);
+                        }
                     if (__any_sync(0xFFFFFFFFu, here < 64)) {
 #pragma unroll
                         for (int i = 0; i < 64; ++i)

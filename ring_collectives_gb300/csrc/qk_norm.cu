@@ -8,11 +8,14 @@
 //   dx = r (t - xh mean_i(t_i xh_i)),   dg = sum over rows of dy xh.
 //
 // Bound by memory: each head is read and written once (three passes in the
-// gradient), the rows of cos and sin once per token and rank.  Lanes hold two
-// chunks of V elements, c and c + D/2 further on, so both members of either
-// kind of pair are in one thread and only the mean crosses lanes: a group of
-// D / 2V lanes (rounded up to a power of two) covers a head.  A group keeps
-// its token's angles in registers and takes up to 4 heads, all loads first.
+// gradient), the rows of cos and sin once per token, rank and run of heads.
+// Lanes hold two chunks of V elements, c and c + D/2 further on, so both
+// members of either kind of pair are in one thread and only the mean crosses
+// lanes: a group of D / 2V lanes (rounded up to a power of two) covers a head.
+// All arithmetic is on pairs of binary32 (one issue slot for two), and norm
+// weight and rotation become two factors an element, z = r (x a + x' b) with x'
+// the element's partner, formed once per token for a run of heads: with the
+// plain formula the kernel was bound by issue, not by memory.
 #include <cmath>
 #include <cuda_bf16.h>
 
@@ -23,8 +26,10 @@
 namespace rc {
 namespace qkn {
 
-constexpr int THREADS = 256;
-constexpr int HB = 4;            // heads in flight per group
+constexpr int THREADS = 256;     // of qk_norm_rope
+constexpr int BTHREADS = 128;    // of its gradient: up to 168 registers at three blocks per SM
+constexpr int HB = 4;            // heads of a run in qk_norm_rope: all loaded before the first is used
+constexpr int GB = 2;            // heads in flight in its gradient
 
 struct Heads {
     char *base;
@@ -37,63 +42,112 @@ struct Params {
     const int32_t *pos;
     float *part;                 // gradient: [blocks of a slot][slot][2][D] partial weight gradients
     float *dg[2];                // [P][D]
-    int P, T, H[2], D, npos, pairs, chunks, blocks;   // blocks: of one slot (gradient)
+    int P, T, H[2], D, npos, pairs;
+    int runs[2], blocks;         // runs of HB heads of either kind; gradient: rows of `part`
     float eps;
 };
 
-template <int V>
-struct Vec;
-template <>
-struct Vec<8> {
-    uint4 v;
-    __device__ __forceinline__ uint32_t at(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-};
-template <>
-struct Vec<4> {
-    uint2 v;
-    __device__ __forceinline__ uint32_t at(int i) const { return i == 0 ? v.x : v.y; }
-};
-
-template <int V>
-__device__ __forceinline__ Vec<V> ld(const char *p)
+// ------------------------------------------------------------ pairs of binary32
+typedef uint64_t f32x2;
+__device__ __forceinline__ f32x2 mk(float a, float b)
 {
-    Vec<V> r;
-    if (V == 8) *(uint4 *)&r = __ldcs((const uint4 *)p);
-    else *(uint2 *)&r = __ldcs((const uint2 *)p);
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
     return r;
 }
-
-template <int V>
-__device__ __forceinline__ void unpack(const Vec<V> &v, float *f)
+__device__ __forceinline__ void un(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 swap(f32x2 v)
 {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        f[2 * i] = __uint_as_float(v.at(i) << 16);
-        f[2 * i + 1] = __uint_as_float(v.at(i) & 0xFFFF0000u);
-    }
+    float a, b;
+    un(v, a, b);
+    return mk(b, a);
+}
+__device__ __forceinline__ f32x2 mul(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float hsum(f32x2 v)
+{
+    float a, b;
+    un(v, a, b);
+    return a + b;
 }
 
-__device__ __forceinline__ uint32_t pack(float lo, float hi)
+// A thread's share of a head as loaded: V elements from c and V from c + D/2.
+template <int V>
+struct Raw {
+    uint32_t w[V];               // V / 2 words of the first chunk, then of the second
+};
+
+template <int V>
+__device__ __forceinline__ void ld(Raw<V> &r, const char *p, int half_bytes)
 {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (V == 8) {
+            const uint4 v = __ldcs((const uint4 *)(p + k * half_bytes));
+            r.w[4 * k] = v.x, r.w[4 * k + 1] = v.y, r.w[4 * k + 2] = v.z, r.w[4 * k + 3] = v.w;
+        } else {
+            const uint2 v = __ldcs((const uint2 *)(p + k * half_bytes));
+            r.w[2 * k] = v.x, r.w[2 * k + 1] = v.y;
+        }
+}
+
+template <int V>
+__device__ __forceinline__ void unpack(const Raw<V> &r, f32x2 (&f)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = mk(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ uint32_t pack(f32x2 v)
+{
+    float a, b;
     uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    un(v, a, b);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
 
 template <int V>
-__device__ __forceinline__ void st(char *p, const float *f)
-{
-    if (V == 8)
-        __stcs((uint4 *)p, make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[V - 4], f[V - 3]), pack(f[V - 2], f[V - 1])));
-    else
-        __stcs((uint2 *)p, make_uint2(pack(f[0], f[1]), pack(f[2], f[3])));
-}
-
-template <int V>
-__device__ __forceinline__ void ldf(const float *p, float *f)
+__device__ __forceinline__ void st(char *p, int half_bytes, const f32x2 (&f)[V])
 {
 #pragma unroll
-    for (int i = 0; i < V; i += 4) *(float4 *)(f + i) = __ldg((const float4 *)(p + i));
+    for (int k = 0; k < 2; ++k)
+        if (V == 8)
+            __stcs((uint4 *)(p + k * half_bytes), make_uint4(pack(f[4 * k]), pack(f[4 * k + 1]), pack(f[V / 2 * k + 2]), pack(f[V / 2 * k + V / 2 - 1])));
+        else
+            __stcs((uint2 *)(p + k * half_bytes), make_uint2(pack(f[2 * k]), pack(f[2 * k + 1])));
+}
+
+// The elements' partners: the other chunk, or the other element of the pair.
+template <int V, bool PAIRS>
+__device__ __forceinline__ void partners(const f32x2 (&f)[V], f32x2 (&q)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) q[i] = PAIRS ? swap(f[i]) : f[(i + V / 2) % V];
+}
+
+// 2V floats in the same order.
+template <int V>
+__device__ __forceinline__ void ldf(const float *p, int half, f32x2 (&f)[V])
+{
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 v = __ldg((const float4 *)(p + k * half + i));
+            f[k * V / 2 + i / 2] = mk(v.x, v.y);
+            f[k * V / 2 + i / 2 + 1] = mk(v.z, v.w);
+        }
 }
 
 // Sum over the L lanes of a group.
@@ -105,200 +159,186 @@ __device__ __forceinline__ float group_sum(float v)
     return v;
 }
 
-// The angles of this thread's V pairs, in the order its pairs are kept.
-// Half layout: pair i is (lo[i], hi[i]), angle c + i.  Adjacent pairs: pair i is
-// (lo[2i], lo[2i + 1]) for i < V/2, angle c/2 + i, then the same of hi, D/4 on.
-// A position outside the table gives NaN.
-template <int V>
-__device__ __forceinline__ void angles(const Params &p, int t, int c, float (&cs)[V], float (&sn)[V])
+// cos of every element's angle, and sin with the sign it has on the element's
+// partner in the forward rotation: z = x cs + x' sn.  Position t's row of the
+// table; one outside the table gives NaN.
+template <int V, bool PAIRS>
+__device__ __forceinline__ void angles(const Params &p, int t, int c, f32x2 (&cs)[V], f32x2 (&sn)[V])
 {
     const int pos = __ldg(p.pos + t);
     if (pos < 0 || pos >= p.npos) {
+        const float nan = __int_as_float(0x7FC00000);
 #pragma unroll
-        for (int i = 0; i < V; ++i) cs[i] = sn[i] = __int_as_float(0x7FC00000);
+        for (int i = 0; i < V; ++i) cs[i] = sn[i] = mk(nan, nan);
         return;
     }
     const float *const ct = p.cos + (size_t)pos * (p.D / 2), *const st_ = p.sin + (size_t)pos * (p.D / 2);
-    if (!p.pairs) {
-        ldf<V>(ct + c, cs);
-        ldf<V>(st_ + c, sn);
+    if (!PAIRS) {
+        // both chunks turn by angles c .. c + V - 1
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 a = __ldg((const float4 *)(ct + c + i)), b = __ldg((const float4 *)(st_ + c + i));
+            cs[i / 2] = cs[V / 2 + i / 2] = mk(a.x, a.y);
+            cs[i / 2 + 1] = cs[V / 2 + i / 2 + 1] = mk(a.z, a.w);
+            sn[i / 2] = mk(-b.x, -b.y);
+            sn[i / 2 + 1] = mk(-b.z, -b.w);
+            sn[V / 2 + i / 2] = mk(b.x, b.y);
+            sn[V / 2 + i / 2 + 1] = mk(b.z, b.w);
+        }
     } else {
+        // word i of either chunk is a pair; the chunks' angles start at c / 2 and D / 4 + c / 2
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            cs[i] = __ldg(ct + c / 2 + i);
-            sn[i] = __ldg(st_ + c / 2 + i);
-            cs[V / 2 + i] = __ldg(ct + p.D / 4 + c / 2 + i);
-            sn[V / 2 + i] = __ldg(st_ + p.D / 4 + c / 2 + i);
+        for (int i = 0; i < V; ++i) {
+            const int k = (i < V / 2 ? 0 : p.D / 4) + c / 2 + i % (V / 2);
+            const float a = __ldg(ct + k), b = __ldg(st_ + k);
+            cs[i] = mk(a, a);
+            sn[i] = mk(-b, b);
         }
     }
 }
 
-// Rotates the thread's 2V elements f (lo then hi) in place; back: by the opposite angles.
-template <int V>
-__device__ __forceinline__ void rotate(float (&f)[2 * V], const float (&cs)[V], const float (&sn)[V], bool pairs, bool back)
-{
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const float s = back ? -sn[i] : sn[i];
-        if (pairs) {
-            const float a = f[2 * i], b = f[2 * i + 1];
-            f[2 * i] = a * cs[i] - b * s;
-            f[2 * i + 1] = a * s + b * cs[i];
-        } else {
-            const float a = f[i], b = f[V + i];
-            f[i] = a * cs[i] - b * s;
-            f[V + i] = a * s + b * cs[i];
-        }
-    }
-}
-
-// Work item: token, slot and one of `chunks` runs of heads (queries then keys).
+// Block (x, y): tokens y * groups.. of slot x / runs, run x % runs of heads (the
+// runs of query heads, then those of key heads).  Blocks that run together
+// then cover whole tokens, which lie together in memory.
 template <int V, int L, bool PAIRS>
 __global__ void __launch_bounds__(THREADS, 2) k_qk_norm(const Params p)
 {
-    const int lane = threadIdx.x % L, c = lane * V, h = p.D / 2, HT = p.H[0] + p.H[1];
-    const bool on = c < h;
-    const long long items = (long long)p.T * p.P * p.chunks;
+    const int lane = threadIdx.x % L, c = lane * V, hb = p.D;      // hb: bytes of half a head
+    const bool on = c < p.D / 2;
+    const int runs = p.runs[0] + p.runs[1], slot = blockIdx.x / runs, run = blockIdx.x % runs;
+    const int w = run >= p.runs[0];
+    const int h0 = (w ? run - p.runs[0] : run) * HB, heads = min(HB, p.H[w] - h0);
+    const Heads x = p.x[w], z = p.z[w];
+    const char *const src = x.base + slot * x.slot + h0 * x.head + c * 2;
+    char *const dst = z.base + slot * z.slot + h0 * z.head + c * 2;
     const float inv_d = 1.f / (float)p.D;
     // every lane of a warp stays in the loop: the sums are warp-wide shuffles
-    const long long step = (long long)gridDim.x * (THREADS / L);
-    for (long long i0 = (long long)blockIdx.x * (THREADS / L) + (threadIdx.x & ~31) / L; i0 < items; i0 += step) {
-        const long long i = i0 + (threadIdx.x & 31) / L;
-        const bool live = on && i < items;
-        const int ch = (int)(i % p.chunks);
-        const long long ts = i / p.chunks;
-        const int slot = (int)(ts % p.P), t = (int)(ts / p.P);
-        const int h0 = ch * HT / p.chunks, h1 = (ch + 1) * HT / p.chunks;
-        Vec<V> lo[HB], hi[HB];
-        float cs[V], sn[V];
+    for (int t0 = blockIdx.y * (THREADS / L); t0 < p.T; t0 += gridDim.y * (THREADS / L)) {
+        const int t = t0 + threadIdx.x / L;
+        const bool live = on && t < p.T;
+        Raw<V> raw[HB];
 #pragma unroll
         for (int k = 0; k < HB; ++k)
-            if (live && h0 + k < h1) {
-                const int w = h0 + k >= p.H[0];
-                const Heads &x = p.x[w];
-                const char *a = x.base + slot * x.slot + t * x.token + (h0 + k - (w ? p.H[0] : 0)) * x.head + c * 2;
-                lo[k] = ld<V>(a);
-                hi[k] = ld<V>(a + h * 2);
-            }
-        if (live) angles<V>(p, t, c, cs, sn);
+            if (live && k < heads) ld<V>(raw[k], src + t * x.token + k * x.head, hb);
+        f32x2 a[V], b[V];
+        if (live) {
+            f32x2 g[V], gp[V];
+            ldf<V>(p.g[w] + c, p.D / 2, g);
+            angles<V, PAIRS>(p, t, c, a, b);
+            partners<V, PAIRS>(g, gp);
+#pragma unroll
+            for (int i = 0; i < V; ++i) a[i] = mul(a[i], g[i]), b[i] = mul(b[i], gp[i]);
+        }
 #pragma unroll
         for (int k = 0; k < HB; ++k) {
-            const bool here = live && h0 + k < h1;
-            float f[2 * V], sum = 0.f;
+            const bool here = live && k < heads;
+            f32x2 f[V], q[V], ss = 0;
             if (here) {
-                unpack<V>(lo[k], f);
-                unpack<V>(hi[k], f + V);
+                unpack<V>(raw[k], f);
 #pragma unroll
-                for (int j = 0; j < 2 * V; ++j) sum = fmaf(f[j], f[j], sum);
+                for (int i = 0; i < V; ++i) ss = fma(f[i], f[i], ss);
             }
-            sum = group_sum<L>(sum);
+            const float sum = group_sum<L>(hsum(ss));
             if (!here) continue;
             const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
-            const int w = h0 + k >= p.H[0];
-            float g[2 * V];
-            ldf<V>(p.g[w] + c, g);
-            ldf<V>(p.g[w] + h + c, g + V);
+            const f32x2 r2 = mk(r, r);
+            partners<V, PAIRS>(f, q);
 #pragma unroll
-            for (int j = 0; j < 2 * V; ++j) f[j] = f[j] * r * g[j];
-            rotate<V>(f, cs, sn, PAIRS, false);
-            const Heads &z = p.z[w];
-            char *a = z.base + slot * z.slot + t * z.token + (h0 + k - (w ? p.H[0] : 0)) * z.head + c * 2;
-            st<V>(a, f);
-            st<V>(a + h * 2, f + V);
+            for (int i = 0; i < V; ++i) q[i] = mul(fma(f[i], a[i], mul(q[i], b[i])), r2);
+            st<V>(dst + t * z.token + k * z.head, hb, q);
         }
     }
 }
 
-// The gradient.  A block stays within one slot; its threads keep the weight
+// The gradient.  A block stays within one slot and one share of its heads; its threads keep the weight
 // gradients of their columns over all their rows, and the block's sums go to
 // one row of `part`, added up by k_qk_norm_dg in block order.
 template <int V, int L, bool PAIRS>
-__global__ void __launch_bounds__(THREADS, 2) k_qk_norm_bwd(const Params p)
+__global__ void __launch_bounds__(BTHREADS, 3) k_qk_norm_bwd(const Params p)
 {
-    __shared__ float red[THREADS / 32][2][512];
-    const int lane = threadIdx.x % L, c = lane * V, h = p.D / 2;
-    const bool on = c < h;
-    const int slot = blockIdx.x / p.blocks, blk = blockIdx.x % p.blocks;
+    __shared__ float red[BTHREADS / 32][2][256];
+    const int lane = threadIdx.x % L, c = lane * V, hb = p.D;
+    const bool on = c < p.D / 2;
+    const int slot = blockIdx.x, blk = blockIdx.y, share = blockIdx.z, shares = gridDim.z;
     const float inv_d = 1.f / (float)p.D;
+#pragma unroll 1
     for (int w = 0; w < 2; ++w) {
-        float acc[2 * V] = {};
-        float g[2 * V] = {};
-        if (on) {
-            ldf<V>(p.g[w] + c, g);
-            ldf<V>(p.g[w] + h + c, g + V);
-        }
-        const Heads &xh_ = p.x[w], &zh = p.z[w], &dh = p.dx[w];
-        const int chunks = (p.H[w] + HB / 2 - 1) / (HB / 2);
-        const long long items = (long long)p.T * chunks;
-        for (long long i0 = (long long)blk * (THREADS / L) + (threadIdx.x & ~31) / L; i0 < items;
-             i0 += (long long)p.blocks * (THREADS / L)) {
-            const long long i = i0 + (threadIdx.x & 31) / L;
-            const bool live = on && i < items;
-            const int t = (int)(i / chunks), hb = (int)(i % chunks) * (HB / 2);
-            Vec<V> xl[HB / 2], xu[HB / 2], zl[HB / 2], zu[HB / 2];
-            float cs[V], sn[V];
+        f32x2 acc[V] = {}, g[V] = {};
+        if (on) ldf<V>(p.g[w] + c, p.D / 2, g);
+        const Heads x = p.x[w], z = p.z[w], d = p.dx[w];
+        const char *const xs = x.base + slot * x.slot + c * 2, *const zs = z.base + slot * z.slot + c * 2;
+        char *const ds = d.base + slot * d.slot + c * 2;
+        const int h0 = share * p.H[w] / shares, h1 = (share + 1) * p.H[w] / shares;
+        for (int t0 = blk * (BTHREADS / L); t0 < p.T && h0 < h1; t0 += gridDim.y * (BTHREADS / L)) {
+            const int t = t0 + threadIdx.x / L;
+            const bool live = on && t < p.T;
+            f32x2 cs[V], sn[V];
+            for (int h = h0; h < h1; h += GB) {
+                Raw<V> xr[GB], zr[GB];
 #pragma unroll
-            for (int k = 0; k < HB / 2; ++k)
-                if (live && hb + k < p.H[w]) {
-                    const char *a = xh_.base + slot * xh_.slot + t * xh_.token + (hb + k) * xh_.head + c * 2;
-                    const char *b = zh.base + slot * zh.slot + t * zh.token + (hb + k) * zh.head + c * 2;
-                    xl[k] = ld<V>(a);
-                    xu[k] = ld<V>(a + h * 2);
-                    zl[k] = ld<V>(b);
-                    zu[k] = ld<V>(b + h * 2);
-                }
-            if (live) angles<V>(p, t, c, cs, sn);
-#pragma unroll
-            for (int k = 0; k < HB / 2; ++k) {
-                const bool here = live && hb + k < p.H[w];
-                float x[2 * V], d[2 * V], ss = 0.f, st_ = 0.f;
-                if (here) {
-                    unpack<V>(xl[k], x);
-                    unpack<V>(xu[k], x + V);
-                    unpack<V>(zl[k], d);
-                    unpack<V>(zu[k], d + V);
-                    rotate<V>(d, cs, sn, PAIRS, true);
-#pragma unroll
-                    for (int j = 0; j < 2 * V; ++j) {
-                        ss = fmaf(x[j], x[j], ss);
-                        st_ = fmaf(d[j] * g[j], x[j], st_);
+                for (int k = 0; k < GB; ++k)
+                    if (live && h + k < h1) {
+                        ld<V>(xr[k], xs + t * x.token + (h + k) * x.head, hb);
+                        ld<V>(zr[k], zs + t * z.token + (h + k) * z.head, hb);
                     }
-                }
-                ss = group_sum<L>(ss);
-                st_ = group_sum<L>(st_);
-                if (!here) continue;
-                const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-                const float m = st_ * r * inv_d;            // mean of t xh
+                if (live && h == h0) angles<V, PAIRS>(p, t, c, cs, sn);
 #pragma unroll
-                for (int j = 0; j < 2 * V; ++j) {
-                    const float xh = x[j] * r;
-                    acc[j] = fmaf(d[j], xh, acc[j]);
-                    d[j] = r * fmaf(-xh, m, d[j] * g[j]);
+                for (int k = 0; k < GB; ++k) {
+                    const bool here = live && h + k < h1;
+                    f32x2 f[V], u[V], q[V], ss = 0, tt = 0;
+                    if (here) {
+                        unpack<V>(xr[k], f);
+                        unpack<V>(zr[k], u);
+                        partners<V, PAIRS>(u, q);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            // turned back: the partner's sine changes sign
+                            float s0, s1;
+                            un(sn[i], s0, s1);
+                            u[i] = fma(u[i], cs[i], mul(q[i], mk(-s0, -s1)));    // dy
+                            q[i] = mul(u[i], g[i]);                             // t
+                            ss = fma(f[i], f[i], ss);
+                            tt = fma(q[i], f[i], tt);
+                        }
+                    }
+                    const float sum = group_sum<L>(hsum(ss)), dot = group_sum<L>(hsum(tt));
+                    if (!here) continue;
+                    const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
+                    const float m = -dot * inv_d * r * r * r;      // dx = r t - x r^3 mean(t x)
+                    const f32x2 r2 = mk(r, r), m2 = mk(m, m);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        acc[i] = fma(u[i], mul(f[i], r2), acc[i]);
+                        q[i] = fma(q[i], r2, mul(f[i], m2));
+                    }
+                    st<V>(ds + t * d.token + (h + k) * d.head, hb, q);
                 }
-                char *a = dh.base + slot * dh.slot + t * dh.token + (hb + k) * dh.head + c * 2;
-                st<V>(a, d);
-                st<V>(a + h * 2, d + V);
             }
         }
         // sum the groups of the warp, then the warps
 #pragma unroll
-        for (int j = 0; j < 2 * V; ++j)
+        for (int i = 0; i < V; ++i) {
+            float s0, s1;
+            un(acc[i], s0, s1);
 #pragma unroll
-            for (int o = 16; o >= L; o >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], o);
-        if (on && (threadIdx.x & 31) < L)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                red[threadIdx.x >> 5][w][c + j] = acc[j];
-                red[threadIdx.x >> 5][w][h + c + j] = acc[V + j];
+            for (int o = 16; o >= L; o >>= 1) {
+                s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
+                s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
             }
+            if (on && (threadIdx.x & 31) < L) {
+                const int at = (i < V / 2 ? 0 : p.D / 2) + c + 2 * (i % (V / 2));
+                red[threadIdx.x >> 5][w][at] = s0;
+                red[threadIdx.x >> 5][w][at + 1] = s1;
+            }
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.D; i += THREADS) {
+    for (int i = threadIdx.x; i < 2 * p.D; i += BTHREADS) {
         const int w = i >= p.D, d = w ? i - p.D : i;
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < THREADS / 32; ++k) s += red[k][w][d];
-        p.part[((size_t)blk * p.P + slot) * 2 * p.D + i] = s;
+        for (int k = 0; k < BTHREADS / 32; ++k) s += red[k][w][d];
+        p.part[((size_t)(blk * shares + share) * p.P + slot) * 2 * p.D + i] = s;
     }
 }
 
@@ -315,11 +355,11 @@ __global__ void __launch_bounds__(THREADS) k_qk_norm_dg(const Params p)
 }
 
 template <int V, int L>
-static void launch(const Params &p, bool grad, int blocks, cudaStream_t st)
+static void launch(const Params &p, bool grad, dim3 blocks, cudaStream_t st)
 {
     if (grad) {
-        if (p.pairs) k_qk_norm_bwd<V, L, true><<<p.P * p.blocks, THREADS, 0, st>>>(p);
-        else k_qk_norm_bwd<V, L, false><<<p.P * p.blocks, THREADS, 0, st>>>(p);
+        if (p.pairs) k_qk_norm_bwd<V, L, true><<<blocks, BTHREADS, 0, st>>>(p);
+        else k_qk_norm_bwd<V, L, false><<<blocks, BTHREADS, 0, st>>>(p);
         k_qk_norm_dg<<<(p.P * 2 * p.D + THREADS / 32 - 1) / (THREADS / 32), THREADS, 0, st>>>(p);
     } else {
         if (p.pairs) k_qk_norm<V, L, true><<<blocks, THREADS, 0, st>>>(p);
@@ -335,7 +375,7 @@ static int group_lanes(int D, int V)
     return l;
 }
 
-static void launch_any(const Params &p, bool grad, int blocks, cudaStream_t st)
+static void launch_any(const Params &p, bool grad, dim3 blocks, cudaStream_t st)
 {
     // V = 8 needs both halves of a head on 16-byte boundaries
     if (p.D % 16 == 0) {
@@ -372,16 +412,16 @@ static int check_heads(const rc_heads &in, Heads &h, const char *name, int P, in
     return RC_OK;
 }
 
-// Blocks of one slot in the gradient: four per SM over all slots, or fewer
-// when the rows do not fill them.
-static int bwd_blocks(const rc_qk_norm_args &a, int sms)
+// The gradient's blocks: for each slot three per SM over all slots, or one per
+// group of tokens where that is less; then the heads are shared out too.
+static void bwd_blocks(const rc_qk_norm_args &a, int sms, int &blocks, int &shares)
 {
-    const long long per_block = THREADS / group_lanes(a.D, a.D % 16 ? 4 : 8);
-    const long long rows = (long long)a.T * ((a.Hq > a.Hkv ? a.Hq : a.Hkv) + 1) / 2;
-    long long n = (rows + per_block - 1) / per_block;
-    const long long most = (4ll * sms + a.P - 1) / a.P;
-    if (n > most) n = most;
-    return n < 1 ? 1 : (int)n;
+    const int groups = BTHREADS / group_lanes(a.D, a.D % 16 ? 4 : 8);
+    const long long n = ((long long)a.T + groups - 1) / groups, most = (3ll * sms + a.P - 1) / a.P;
+    blocks = (int)(n > most ? most : n < 1 ? 1 : n);
+    const int heads = ((a.Hq > a.Hkv ? a.Hq : a.Hkv) + GB - 1) / GB;
+    shares = (int)(most / blocks);
+    shares = shares > heads ? heads : shares < 1 ? 1 : shares;
 }
 
 static int check_sizes(const rc_qk_norm_args &a)
@@ -429,11 +469,14 @@ static int run(const rc_qk_norm_args *args, bool grad, void *stream)
     p.npos = a.npos;
     p.pairs = a.layout == RC_ROPE_PAIRS;
     p.eps = a.eps;
-    long long blocks = 0;
+    dim3 blocks(1);
     if (grad) {
         p.dg[0] = a.dgamma_q;
         p.dg[1] = a.dgamma_k;
-        p.blocks = bwd_blocks(a, sms);
+        int per_slot, shares;
+        bwd_blocks(a, sms, per_slot, shares);
+        p.blocks = per_slot * shares;
+        blocks = dim3((unsigned)a.P, (unsigned)per_slot, (unsigned)shares);
         const size_t bytes = (size_t)p.blocks * a.P * 2 * a.D * 4;
         void *s = a.workspace;
         if (a.workspace && ((uintptr_t)a.workspace & 255u)) return set_error(RC_ERR_INVALID, "workspace must be 256-byte aligned");
@@ -442,12 +485,13 @@ static int run(const rc_qk_norm_args *args, bool grad, void *stream)
         if (!a.workspace && (rc_ = prepare_scratch(bytes, &s))) return rc_;
         p.part = (float *)s;
     } else {
-        p.chunks = (a.Hq + a.Hkv + HB - 1) / HB;
-        const long long per_block = THREADS / group_lanes(a.D, a.D % 16 ? 4 : 8);
-        blocks = ((long long)a.T * a.P * p.chunks + per_block - 1) / per_block;
-        if (blocks > 64ll * sms) blocks = 64ll * sms;
+        p.runs[0] = (a.Hq + HB - 1) / HB;
+        p.runs[1] = (a.Hkv + HB - 1) / HB;
+        const int groups = THREADS / group_lanes(a.D, a.D % 16 ? 4 : 8);
+        const long long n = ((long long)a.T + groups - 1) / groups;
+        blocks = dim3((unsigned)(a.P * (p.runs[0] + p.runs[1])), (unsigned)(n < 65535 ? n : 65535));
     }
-    launch_any(p, grad, (int)blocks, (cudaStream_t)stream);
+    launch_any(p, grad, blocks, (cudaStream_t)stream);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return set_error(RC_ERR_CUDA, "qk_norm_rope launch: %s", cudaGetErrorString(e));
     return RC_OK;
@@ -465,5 +509,7 @@ extern "C" size_t qk_norm_rope_bwd_workspace_bytes(const rc_qk_norm_args *args)
     using namespace rc::qkn;
     int sms = 0;
     if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
-    return (size_t)bwd_blocks(*args, sms) * args->P * 2 * args->D * 4;
+    int blocks, shares;
+    bwd_blocks(*args, sms, blocks, shares);
+    return (size_t)blocks * shares * args->P * 2 * args->D * 4;
 }
