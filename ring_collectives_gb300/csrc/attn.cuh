@@ -283,8 +283,8 @@ __device__ __forceinline__ long long warp_sum(long long v)
 
 constexpr int kNoSplit = 1 << 28;          // key tiles of a part when keys are not split
 
-// Parts (SPLIT) or units (PAIR) that a split launch aims at.
-__host__ __device__ constexpr long long split_target(bool split, int sms) { return (split ? 8ll : 3ll) * sms; }
+// Units that a split adds at most: parts are no smaller than 4 rounds of units need.
+constexpr long long split_units(int sms) { return 4ll * sms; }
 
 // Units go to blocks as they come free: block i starts with unit i and takes
 // the next one from a counter.  Two words of the status header that nothing

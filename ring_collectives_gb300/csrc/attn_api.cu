@@ -130,7 +130,7 @@ static FwdPlan plan_fwd(Params &p, int sms)
     if (p.may_split) {
         long long n0 = p.Tq / p.TPU + p.B;     // row tiles (pairs), at most
         if (n0 > p.Tq) n0 = p.Tq;
-        f.units = (size_t)(n0 * HP + split_target(f.split, sms));
+        f.units = (size_t)(n0 * HP + split_units(sms));
         const size_t DP = p.D <= 64 ? 64 : 128;
         f.bytes = 2 * f.units * (size_t)p.part_rows * (DP + 1) * 4;
     }

@@ -65,10 +65,13 @@ __device__ __forceinline__ int units_per_tile(int kt, int cs)
     return SPLIT ? (np + 1) / 2 : np;
 }
 
-// Splitting rule (p.may_split: decided on the host, which sizes the partial
-// results by it).  PAIR: when unsplit units would not give two waves of
-// blocks, parts of at least 4 key tiles, about 3 units per SM.  SPLIT: below 4
-// units per SM, parts of at least 2 tiles, about 8 parts per SM (two to a unit).
+// How far keys are split (p.may_split: the host found too few unsplit units to
+// fill the GPU and made room for partial results).  Every lane tries one part
+// size -- 1 to 4 rounds of units over the SMs, with up to 44 % of slack, and no
+// split -- and the warp takes the one with the least rounds x (key tiles of a
+// unit + the cost of a unit's ends, about 3 tiles; 2 in the SPLIT form).
+// Measured on GB300 against parts for a fixed 3 (SPLIT: 4) units per SM: token
+// 1 x 32768 keys 45 -> 32 us, prompt pieces 60 -> 46 us.
 template <bool SPLIT>
 __device__ Plan make_plan(const Params &p, int lane)
 {
@@ -77,19 +80,41 @@ __device__ Plan make_plan(const Params &p, int lane)
     pl.cs = kNoSplit;
     if (p.may_split) {
         long long work = 0;
+        int most = 0;
         for (int b = lane; b < p.B; b += 32) {
             const Seq s = seq_of(p, b);
-            work += (long long)((s.ql + p.TPU - 1) / p.TPU) * ((s.kl + KT - 1) / KT);
+            const int kt = (s.kl + KT - 1) / KT;
+            work += (long long)((s.ql + p.TPU - 1) / p.TPU) * kt;
+            most = max(most, kt);
         }
         work = warp_sum(work) * HP;
-        const long long target = split_target(SPLIT, p.sms), c = (work + target - 1) / target;
-        pl.cs = (int)max(c, SPLIT ? 2ll : 4ll);
+        most = max(1, __reduce_max_sync(0xFFFFFFFFu, most));
+        const long long per = (long long)p.sms * (SPLIT ? 2 : 1) * (1 + (lane & 3)) * 16;
+        long long c = (work * (16 + (lane >> 2)) + per - 1) / per;
+        c = max(c, SPLIT ? 2ll : 4ll);
+        int cs = c >= most || lane == 31 ? most : (int)c;
+        long long units = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            int nt = 0, kt = 0;
+            if (b < p.B) {
+                const Seq s = seq_of(p, b);
+                nt = (s.ql + p.TPU - 1) / p.TPU;
+                kt = (s.kl + KT - 1) / KT;
+            }
+            for (int i = 0; i < min(32, p.B - b0); ++i)
+                units += (long long)__shfl_sync(0xFFFFFFFFu, nt, i) *
+                         units_per_tile<SPLIT>(__shfl_sync(0xFFFFFFFFu, kt, i), cs);
+        }
+        const long long cost = (units * HP + p.sms - 1) / p.sms * (cs + (SPLIT ? 2 : 3));
+        const unsigned least = __reduce_min_sync(0xFFFFFFFFu, (unsigned)min(cost, 0x7FFFFFFFll));
+        const int pick = __ffs(__ballot_sync(0xFFFFFFFFu, (unsigned)min(cost, 0x7FFFFFFFll) == least)) - 1;
+        pl.cs = __shfl_sync(0xFFFFFFFFu, cs, pick);
+        pl.units = (int)__shfl_sync(0xFFFFFFFFu, units, pick);
+        return pl;
     }
     long long u = 0;
-    for (int b = lane; b < p.B; b += 32) {
-        const Seq s = seq_of(p, b);
-        u += (long long)((s.ql + p.TPU - 1) / p.TPU) * units_per_tile<SPLIT>((s.kl + KT - 1) / KT, pl.cs);
-    }
+    for (int b = lane; b < p.B; b += 32) u += (seq_of(p, b).ql + p.TPU - 1) / p.TPU;
     pl.units = (int)warp_sum(u);
     return pl;
 }
@@ -406,6 +431,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                             const bool last_k = t == 1 || j + 1 >= n1;
                             if (elect_one()) {
                                 mma_rows<DP>(tm + 256 + t * KT, tm + t * KT, sKV + sv * STAGE, j == 0, 32);
+                                if (last_v) tc_commit(empty_bar + 8 * sv);
+                            }
+                            if (elect_one()) {
                                 if (j + 1 < nt) {
                                     mma_scores<DP>(tm + t * KT, sQ + t * STAGE, sKV + sk * STAGE);
                                     tc_commit(s_full + 8 * t);
@@ -416,7 +444,6 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                                 } else {
                                     tc_commit(o_full + 8 * t);
                                 }
-                                if (last_v) tc_commit(empty_bar + 8 * sv);
                             }
                         }
                         if (!ok) break;
@@ -703,20 +730,22 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 
 // Joins the parts of split rows in part order:
 //   lse = m + ln sum_c exp(lse_c - m),  o = sum_c exp(lse_c - lse) o_c.
-// SPLIT has few rows with up to hundreds of parts: a block of 8 warps takes a
-// row, warp w adds parts w, w + 8, ..., and the warps' sums are added in warp
-// order.  PAIR has many rows of about ten parts: a warp takes a row.
+// Few rows have up to hundreds of parts: a block of 8 warps takes a row, warp w
+// adds parts w, w + 8, ..., and the warps' sums are added in warp order.  Many
+// rows (kJoinRows a multiprocessor on average) have few parts: a warp takes a row.
 constexpr int JOIN_WARPS = 8;
 
-template <int DP, bool SPLIT>
+constexpr int kJoinRows = 8;
+
+template <int DP, bool SPLIT, bool WIDE>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
 {
-    constexpr int W = SPLIT ? JOIN_WARPS : 1;              // warps of a row
+    constexpr int W = WIDE ? JOIN_WARPS : 1;               // warps of a row
     constexpr int ROWS = JOIN_WARPS / W;                   // rows of a block at a time
-    __shared__ float acc_s[SPLIT ? W : 1][DP + 1];
+    __shared__ float acc_s[W][DP + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Plan pl = make_plan<SPLIT>(p, lane);             // reads what the launch before was given, too
     asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written
-    const Plan pl = make_plan<SPLIT>(p, lane);
     const int HP = p.P * p.Hkv;
     const long long rows = (long long)p.P * p.Tq * p.Hq;
     for (long long row = (long long)blockIdx.x * ROWS + warp / W; row < rows; row += (long long)gridDim.x * ROWS) {
@@ -769,7 +798,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
             for (int d = 0; d < E; ++d) acc[d] = fmaf(wgt, x[d], acc[d]);
         }
         char *const dst = p.out.base + slot * p.out.slot + (size_t)qi * p.out.token + head * p.out.head;
-        if (SPLIT) {
+        if (WIDE) {
 #pragma unroll
             for (int d = 0; d < E; ++d) acc_s[warp][lane * E + d] = acc[d];
             if (lane == 0) acc_s[warp][DP] = sum;
@@ -810,7 +839,9 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
     if (e != cudaSuccess || !p.may_split) return e;
     // The join's blocks may be set up while the last units still run.
     cudaLaunchConfig_t cfg{};
-    const long long blocks = ((long long)p.P * p.Tq * p.Hq + (SPLIT ? 0 : JOIN_WARPS - 1)) / (SPLIT ? 1 : JOIN_WARPS);
+    const long long rows = (long long)p.P * p.Tq * p.Hq;
+    const bool wide = rows < (long long)kJoinRows * p.sms;
+    const long long blocks = wide ? rows : (rows + JOIN_WARPS - 1) / JOIN_WARPS;
     cfg.gridDim = dim3((unsigned)(blocks < 8ll * p.sms ? blocks : 8ll * p.sms));
     cfg.blockDim = dim3(32 * JOIN_WARPS);
     cfg.stream = st;
@@ -819,7 +850,8 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attn_join<DP, SPLIT>, p);
+    return wide ? cudaLaunchKernelEx(&cfg, k_attn_join<DP, SPLIT, true>, p)
+                : cudaLaunchKernelEx(&cfg, k_attn_join<DP, SPLIT, false>, p);
 }
 
 cudaError_t launch_attn_fwd(const Params &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
