@@ -26,10 +26,10 @@
 namespace rc {
 namespace qkn {
 
-constexpr int THREADS = 256;     // of qk_norm_rope
-constexpr int BTHREADS = 128;    // of its gradient: up to 168 registers at three blocks per SM
-constexpr int HB = 4;            // heads of a run in qk_norm_rope: all loaded before the first is used
-constexpr int GB = 2;            // heads in flight in its gradient
+constexpr int THREADS = 128;     // three blocks per SM: up to 168 registers, 576 bytes of staging a thread
+constexpr int STAGES = 3;        // steps of a thread's staging ring
+constexpr int HB = 4;            // heads of a step of qk_norm_rope
+constexpr int GB = 2;            // heads of a step of its gradient (two tensors)
 
 struct Heads {
     char *base;
@@ -43,7 +43,7 @@ struct Params {
     float *part;                 // gradient: [blocks of a slot][slot][2][D] partial weight gradients
     float *dg[2];                // [P][D]
     int P, T, H[2], D, npos, pairs;
-    int runs[2], blocks;         // runs of HB heads of either kind; gradient: rows of `part`
+    int blocks;                  // gradient: rows of `part`
     float eps;
 };
 
@@ -81,31 +81,57 @@ __device__ __forceinline__ float hsum(f32x2 v)
     return a + b;
 }
 
-// A thread's share of a head as loaded: V elements from c and V from c + D/2.
-template <int V>
-struct Raw {
-    uint32_t w[V];               // V / 2 words of the first chunk, then of the second
+// ------------------------------------------------------------ staging
+// Every thread copies what it will use itself into its own shared-memory slots
+// (cp.async, STAGES - 1 steps ahead) and reads it back: no barrier, and the
+// loads in flight do not depend on registers or on which phase a block is in.
+// Loading into registers instead, with whole blocks taking turns, reached
+// 4.6 TB/s on 16383 tokens x 8 ranks x 5 heads of 128.
+// A slot: W chunks of V elements, then V cosines and V sines.
+template <int V, int W>
+struct Stage {
+    static constexpr int CHUNK = 2 * V, BYTES = W * CHUNK + 8 * V;
+    static constexpr int TOTAL = STAGES * BYTES * THREADS;
+    // 16-byte pieces (8 for V = 4) of the threads side by side: no bank conflicts
+    static __device__ __forceinline__ uint32_t chunk(uint32_t base, int stage, int i)
+    {
+        return base + stage * (BYTES * THREADS) + (i * THREADS + threadIdx.x) * CHUNK;
+    }
+    // piece i of 16 bytes of the angles: V / 4 of cosines, V / 4 of sines
+    static __device__ __forceinline__ uint32_t angle(uint32_t base, int stage, int i)
+    {
+        return base + stage * (BYTES * THREADS) + W * CHUNK * THREADS + (i * THREADS + threadIdx.x) * 16;
+    }
 };
 
-template <int V>
-__device__ __forceinline__ void ld(Raw<V> &r, const char *p, int half_bytes)
+template <int B>
+__device__ __forceinline__ void copy(uint32_t dst, const void *src)
 {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        if (V == 8) {
-            const uint4 v = __ldcs((const uint4 *)(p + k * half_bytes));
-            r.w[4 * k] = v.x, r.w[4 * k + 1] = v.y, r.w[4 * k + 2] = v.z, r.w[4 * k + 3] = v.w;
-        } else {
-            const uint2 v = __ldcs((const uint2 *)(p + k * half_bytes));
-            r.w[2 * k] = v.x, r.w[2 * k + 1] = v.y;
-        }
+    if (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void wait_oldest() { asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory"); }
+__device__ __forceinline__ void lds4(uint32_t a, uint32_t &x, uint32_t &y, uint32_t &z, uint32_t &w)
+{
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "r"(a) : "memory");
 }
 
+// A thread's share of a head: V elements from c and V from c + D/2, as the
+// pairs 2i, 2i + 1 of the first chunk, then of the second.
 template <int V>
-__device__ __forceinline__ void unpack(const Raw<V> &r, f32x2 (&f)[V])
+__device__ __forceinline__ void take(uint32_t lo, uint32_t hi, f32x2 (&f)[V])
 {
+    uint32_t w[V];
+    if (V == 8) {
+        lds4(lo, w[0], w[1], w[2], w[3]);
+        lds4(hi, w[V - 4], w[V - 3], w[V - 2], w[V - 1]);
+    } else {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(lo) : "memory");
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "r"(hi) : "memory");
+    }
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = mk(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xFFFF0000u));
+    for (int i = 0; i < V; ++i) f[i] = mk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ uint32_t pack(f32x2 v)
@@ -159,72 +185,126 @@ __device__ __forceinline__ float group_sum(float v)
     return v;
 }
 
-// cos of every element's angle, and sin with the sign it has on the element's
-// partner in the forward rotation: z = x cs + x' sn.  Position t's row of the
-// table; one outside the table gives NaN.
-template <int V, bool PAIRS>
-__device__ __forceinline__ void angles(const Params &p, int t, int c, f32x2 (&cs)[V], f32x2 (&sn)[V])
+// Starts the copies of position pos's angles: with halves the V angles from c
+// (both chunks turn by them), with adjacent pairs the V / 2 from c / 2 and the
+// V / 2 from D / 4 + c / 2.  A position outside the table gives NaN.
+template <int V, int W, bool PAIRS>
+__device__ __forceinline__ void fetch_angles(const Params &p, uint32_t base, int stage, int pos, int c)
 {
-    const int pos = __ldg(p.pos + t);
+    using S = Stage<V, W>;
     if (pos < 0 || pos >= p.npos) {
-        const float nan = __int_as_float(0x7FC00000);
 #pragma unroll
-        for (int i = 0; i < V; ++i) cs[i] = sn[i] = mk(nan, nan);
+        for (int i = 0; i < V / 2; ++i)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(S::angle(base, stage, i)), "r"(0x7FC00000) : "memory");
         return;
     }
-    const float *const ct = p.cos + (size_t)pos * (p.D / 2), *const st_ = p.sin + (size_t)pos * (p.D / 2);
-    if (!PAIRS) {
-        // both chunks turn by angles c .. c + V - 1
+    const size_t row = (size_t)pos * (p.D / 2);
 #pragma unroll
-        for (int i = 0; i < V; i += 4) {
-            const float4 a = __ldg((const float4 *)(ct + c + i)), b = __ldg((const float4 *)(st_ + c + i));
-            cs[i / 2] = cs[V / 2 + i / 2] = mk(a.x, a.y);
-            cs[i / 2 + 1] = cs[V / 2 + i / 2 + 1] = mk(a.z, a.w);
-            sn[i / 2] = mk(-b.x, -b.y);
-            sn[i / 2 + 1] = mk(-b.z, -b.w);
-            sn[V / 2 + i / 2] = mk(b.x, b.y);
-            sn[V / 2 + i / 2 + 1] = mk(b.z, b.w);
-        }
-    } else {
-        // word i of either chunk is a pair; the chunks' angles start at c / 2 and D / 4 + c / 2
+    for (int k = 0; k < 2; ++k) {
+        const float *const t = (k ? p.sin : p.cos) + row;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int k = (i < V / 2 ? 0 : p.D / 4) + c / 2 + i % (V / 2);
-            const float a = __ldg(ct + k), b = __ldg(st_ + k);
-            cs[i] = mk(a, a);
-            sn[i] = mk(-b, b);
+        for (int i = 0; i < V / 4; ++i) {
+            const uint32_t dst = S::angle(base, stage, k * (V / 4) + i);
+            if (!PAIRS) {
+                copy<16>(dst, t + c + 4 * i);
+            } else if (V == 8) {
+                copy<16>(dst, t + i * (p.D / 4) + c / 2);
+            } else {
+                copy<8>(dst, t + c / 2);
+                copy<8>(dst + 8, t + p.D / 4 + c / 2);
+            }
         }
     }
 }
 
-// Block (x, y): tokens y * groups.. of slot x / runs, run x % runs of heads (the
-// runs of query heads, then those of key heads).  Blocks that run together
-// then cover whole tokens, which lie together in memory.
-template <int V, int L, bool PAIRS>
-__global__ void __launch_bounds__(THREADS, 2) k_qk_norm(const Params p)
+// cos of every element's angle, and sin with the sign it has on the element's
+// partner in the forward rotation: z = x cs + x' sn.
+template <int V, int W, bool PAIRS>
+__device__ __forceinline__ void angles(uint32_t base, int stage, f32x2 (&cs)[V], f32x2 (&sn)[V])
 {
-    const int lane = threadIdx.x % L, c = lane * V, hb = p.D;      // hb: bytes of half a head
-    const bool on = c < p.D / 2;
-    const int runs = p.runs[0] + p.runs[1], slot = blockIdx.x / runs, run = blockIdx.x % runs;
-    const int w = run >= p.runs[0];
-    const int h0 = (w ? run - p.runs[0] : run) * HB, heads = min(HB, p.H[w] - h0);
-    const Heads x = p.x[w], z = p.z[w];
-    const char *const src = x.base + slot * x.slot + h0 * x.head + c * 2;
-    char *const dst = z.base + slot * z.slot + h0 * z.head + c * 2;
-    const float inv_d = 1.f / (float)p.D;
-    // every lane of a warp stays in the loop: the sums are warp-wide shuffles
-    for (int t0 = blockIdx.y * (THREADS / L); t0 < p.T; t0 += gridDim.y * (THREADS / L)) {
-        const int t = t0 + threadIdx.x / L;
-        const bool live = on && t < p.T;
-        Raw<V> raw[HB];
+    using S = Stage<V, W>;
+    float c[V], s[V];
 #pragma unroll
-        for (int k = 0; k < HB; ++k)
-            if (live && k < heads) ld<V>(raw[k], src + t * x.token + k * x.head, hb);
+    for (int i = 0; i < V / 4; ++i) {
+        uint32_t w[4];
+        lds4(S::angle(base, stage, i), w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[4 * i + k] = __uint_as_float(w[k]);
+        lds4(S::angle(base, stage, V / 4 + i), w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[4 * i + k] = __uint_as_float(w[k]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (PAIRS) {
+            cs[i] = mk(c[i], c[i]);
+            sn[i] = mk(-s[i], s[i]);
+        } else {
+            const int k = 2 * (i % (V / 2));
+            const float g = i < V / 2 ? -1.f : 1.f;
+            cs[i] = mk(c[k], c[k + 1]);
+            sn[i] = mk(g * s[k], g * s[k + 1]);
+        }
+    }
+}
+
+// The steps of a block: its token groups, y, y + gridDim.y, ..., and for each the
+// batches [b0, b1) of heads.  Every lane of a warp takes every step.
+struct Walk {
+    int t, b;
+    __device__ __forceinline__ void next(int b0, int b1, int stride)
+    {
+        if (++b == b1) b = b0, t += stride;
+    }
+};
+
+// Block (x, y, z): slot x, token groups y.., share z of the batches of HB heads
+// (those of the queries, then those of the keys).
+template <int V, int L, bool PAIRS>
+__global__ void __launch_bounds__(THREADS, 3) k_qk_norm(const Params p)
+{
+    using S = Stage<V, 2 * HB>;
+    extern __shared__ __align__(16) uint8_t sm[];
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(sm);
+    constexpr int GROUPS = THREADS / L;
+    const int c = threadIdx.x % L * V, hb = p.D;                   // hb: bytes of half a head
+    const bool on = c < p.D / 2;
+    const int slot = blockIdx.x, nq = (p.H[0] + HB - 1) / HB, nb = nq + (p.H[1] + HB - 1) / HB;
+    const int b0 = blockIdx.z * nb / gridDim.z, b1 = (blockIdx.z + 1) * nb / gridDim.z;
+    const int stride = gridDim.y * GROUPS, first = blockIdx.y * GROUPS + threadIdx.x / L, warp_off = threadIdx.x % 32 / L;
+    const float inv_d = 1.f / (float)p.D;
+    if (b0 == b1) return;
+    int pos = on && first < p.T ? __ldg(p.pos + first) : 0;        // of the next token group to fetch
+    auto fetch = [&](const Walk &k, int stage) {
+        if (on && k.t < p.T) {
+            const int w = k.b >= nq, h0 = (w ? k.b - nq : k.b) * HB;
+            const Heads &x = p.x[w];
+            const char *const src = x.base + slot * x.slot + k.t * x.token + h0 * x.head + c * 2;
+#pragma unroll
+            for (int i = 0; i < HB; ++i)
+                if (h0 + i < p.H[w]) {
+                    copy<2 * V>(S::chunk(base, stage, 2 * i), src + i * x.head);
+                    copy<2 * V>(S::chunk(base, stage, 2 * i + 1), src + i * x.head + hb);
+                }
+            // every stage carries its angles: batches of one token fetch the same lines again
+            fetch_angles<V, 2 * HB, PAIRS>(p, base, stage, pos, c);
+            if (k.b == b1 - 1 && k.t + stride < p.T) pos = __ldg(p.pos + k.t + stride);
+        }
+        copies_done();
+    };
+    Walk ahead{first, b0}, now{first, b0};
+    for (int s = 0; s < STAGES - 1; ++s) fetch(ahead, s), ahead.next(b0, b1, stride);
+    for (int stage = 0; now.t - warp_off < p.T; now.next(b0, b1, stride)) {
+        wait_oldest();
+        const bool live = on && now.t < p.T;
+        const int w = now.b >= nq, h0 = (w ? now.b - nq : now.b) * HB, heads = min(HB, p.H[w] - h0);
+        const Heads &z = p.z[w];
+        char *const dst = z.base + slot * z.slot + now.t * z.token + h0 * z.head + c * 2;
         f32x2 a[V], b[V];
         if (live) {
             f32x2 g[V], gp[V];
             ldf<V>(p.g[w] + c, p.D / 2, g);
-            angles<V, PAIRS>(p, t, c, a, b);
+            angles<V, 2 * HB, PAIRS>(base, stage, a, b);
             partners<V, PAIRS>(g, gp);
 #pragma unroll
             for (int i = 0; i < V; ++i) a[i] = mul(a[i], g[i]), b[i] = mul(b[i], gp[i]);
@@ -234,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_qk_norm(const Params p)
             const bool here = live && k < heads;
             f32x2 f[V], q[V], ss = 0;
             if (here) {
-                unpack<V>(raw[k], f);
+                take<V>(S::chunk(base, stage, 2 * k), S::chunk(base, stage, 2 * k + 1), f);
 #pragma unroll
                 for (int i = 0; i < V; ++i) ss = fma(f[i], f[i], ss);
             }
@@ -245,100 +325,129 @@ __global__ void __launch_bounds__(THREADS, 2) k_qk_norm(const Params p)
             partners<V, PAIRS>(f, q);
 #pragma unroll
             for (int i = 0; i < V; ++i) q[i] = mul(fma(f[i], a[i], mul(q[i], b[i])), r2);
-            st<V>(dst + t * z.token + k * z.head, hb, q);
+            st<V>(dst + k * z.head, hb, q);
         }
+        // the slot of the step before this one is free
+        const int into = stage == 0 ? STAGES - 1 : stage - 1;
+        fetch(ahead, into);
+        ahead.next(b0, b1, stride);
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
     }
 }
 
-// The gradient.  A block stays within one slot and one share of its heads; its threads keep the weight
-// gradients of their columns over all their rows, and the block's sums go to
-// one row of `part`, added up by k_qk_norm_dg in block order.
+// The gradient.  A block stays within one slot and one share of its heads; its
+// threads keep the weight gradients of their columns over all their rows, and
+// the block's sums go to one row of `part`, added up by k_qk_norm_dg in block
+// order.
 template <int V, int L, bool PAIRS>
-__global__ void __launch_bounds__(BTHREADS, 3) k_qk_norm_bwd(const Params p)
+__global__ void __launch_bounds__(THREADS, 3) k_qk_norm_bwd(const Params p)
 {
-    __shared__ float red[BTHREADS / 32][2][256];
-    const int lane = threadIdx.x % L, c = lane * V, hb = p.D;
+    using S = Stage<V, 4 * GB>;
+    extern __shared__ __align__(16) uint8_t sm[];
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(sm);
+    float *const red = (float *)sm;                                 // [warps][2][D], once the staging is done with
+    constexpr int GROUPS = THREADS / L;
+    const int c = threadIdx.x % L * V, hb = p.D;
     const bool on = c < p.D / 2;
-    const int slot = blockIdx.x, blk = blockIdx.y, share = blockIdx.z, shares = gridDim.z;
+    const int slot = blockIdx.x, share = blockIdx.z, shares = gridDim.z;
+    const int stride = gridDim.y * GROUPS, first = blockIdx.y * GROUPS + threadIdx.x / L, warp_off = threadIdx.x % 32 / L;
     const float inv_d = 1.f / (float)p.D;
-#pragma unroll 1
+    f32x2 acc[2][V] = {};
+#pragma unroll
     for (int w = 0; w < 2; ++w) {
-        f32x2 acc[V] = {}, g[V] = {};
+        const int nb = (p.H[w] + GB - 1) / GB, b0 = share * nb / shares, b1 = (share + 1) * nb / shares;
+        if (b0 == b1) continue;
+        f32x2 g[V] = {};
         if (on) ldf<V>(p.g[w] + c, p.D / 2, g);
-        const Heads x = p.x[w], z = p.z[w], d = p.dx[w];
-        const char *const xs = x.base + slot * x.slot + c * 2, *const zs = z.base + slot * z.slot + c * 2;
-        char *const ds = d.base + slot * d.slot + c * 2;
-        const int h0 = share * p.H[w] / shares, h1 = (share + 1) * p.H[w] / shares;
-        for (int t0 = blk * (BTHREADS / L); t0 < p.T && h0 < h1; t0 += gridDim.y * (BTHREADS / L)) {
-            const int t = t0 + threadIdx.x / L;
-            const bool live = on && t < p.T;
+        const Heads &x = p.x[w], &z = p.z[w], &d = p.dx[w];
+        int pos = on && first < p.T ? __ldg(p.pos + first) : 0;
+        auto fetch = [&](const Walk &k, int stage) {
+            if (on && k.t < p.T) {
+                const char *const xs = x.base + slot * x.slot + k.t * x.token + k.b * GB * x.head + c * 2;
+                const char *const zs = z.base + slot * z.slot + k.t * z.token + k.b * GB * z.head + c * 2;
+#pragma unroll
+                for (int i = 0; i < GB; ++i)
+                    if (k.b * GB + i < p.H[w]) {
+                        copy<2 * V>(S::chunk(base, stage, 4 * i), xs + i * x.head);
+                        copy<2 * V>(S::chunk(base, stage, 4 * i + 1), xs + i * x.head + hb);
+                        copy<2 * V>(S::chunk(base, stage, 4 * i + 2), zs + i * z.head);
+                        copy<2 * V>(S::chunk(base, stage, 4 * i + 3), zs + i * z.head + hb);
+                    }
+                fetch_angles<V, 4 * GB, PAIRS>(p, base, stage, pos, c);
+                if (k.b == b1 - 1 && k.t + stride < p.T) pos = __ldg(p.pos + k.t + stride);
+            }
+            copies_done();
+        };
+        Walk ahead{first, b0}, now{first, b0};
+        for (int s = 0; s < STAGES - 1; ++s) fetch(ahead, s), ahead.next(b0, b1, stride);
+        for (int stage = 0; now.t - warp_off < p.T; now.next(b0, b1, stride)) {
+            wait_oldest();
+            const bool live = on && now.t < p.T;
+            char *const ds = d.base + slot * d.slot + now.t * d.token + now.b * GB * d.head + c * 2;
             f32x2 cs[V], sn[V];
-            for (int h = h0; h < h1; h += GB) {
-                Raw<V> xr[GB], zr[GB];
+            if (live) angles<V, 4 * GB, PAIRS>(base, stage, cs, sn);
 #pragma unroll
-                for (int k = 0; k < GB; ++k)
-                    if (live && h + k < h1) {
-                        ld<V>(xr[k], xs + t * x.token + (h + k) * x.head, hb);
-                        ld<V>(zr[k], zs + t * z.token + (h + k) * z.head, hb);
-                    }
-                if (live && h == h0) angles<V, PAIRS>(p, t, c, cs, sn);
-#pragma unroll
-                for (int k = 0; k < GB; ++k) {
-                    const bool here = live && h + k < h1;
-                    f32x2 f[V], u[V], q[V], ss = 0, tt = 0;
-                    if (here) {
-                        unpack<V>(xr[k], f);
-                        unpack<V>(zr[k], u);
-                        partners<V, PAIRS>(u, q);
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            // turned back: the partner's sine changes sign
-                            float s0, s1;
-                            un(sn[i], s0, s1);
-                            u[i] = fma(u[i], cs[i], mul(q[i], mk(-s0, -s1)));    // dy
-                            q[i] = mul(u[i], g[i]);                             // t
-                            ss = fma(f[i], f[i], ss);
-                            tt = fma(q[i], f[i], tt);
-                        }
-                    }
-                    const float sum = group_sum<L>(hsum(ss)), dot = group_sum<L>(hsum(tt));
-                    if (!here) continue;
-                    const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
-                    const float m = -dot * inv_d * r * r * r;      // dx = r t - x r^3 mean(t x)
-                    const f32x2 r2 = mk(r, r), m2 = mk(m, m);
+            for (int k = 0; k < GB; ++k) {
+                const bool here = live && now.b * GB + k < p.H[w];
+                f32x2 f[V], u[V], q[V], ss = 0, tt = 0;
+                if (here) {
+                    take<V>(S::chunk(base, stage, 4 * k), S::chunk(base, stage, 4 * k + 1), f);
+                    take<V>(S::chunk(base, stage, 4 * k + 2), S::chunk(base, stage, 4 * k + 3), u);
+                    partners<V, PAIRS>(u, q);
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
-                        acc[i] = fma(u[i], mul(f[i], r2), acc[i]);
-                        q[i] = fma(q[i], r2, mul(f[i], m2));
+                        // turned back: the partner's sine changes sign
+                        float s0, s1;
+                        un(sn[i], s0, s1);
+                        u[i] = fma(u[i], cs[i], mul(q[i], mk(-s0, -s1)));    // dy
+                        q[i] = mul(u[i], g[i]);                             // t
+                        ss = fma(f[i], f[i], ss);
+                        tt = fma(q[i], f[i], tt);
                     }
-                    st<V>(ds + t * d.token + (h + k) * d.head, hb, q);
                 }
+                const float sum = group_sum<L>(hsum(ss)), dot = group_sum<L>(hsum(tt));
+                if (!here) continue;
+                const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
+                const float m = -dot * inv_d * r * r * r;      // dx = r t - x r^3 mean(t x)
+                const f32x2 r2 = mk(r, r), m2 = mk(m, m);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    acc[w][i] = fma(u[i], mul(f[i], r2), acc[w][i]);
+                    q[i] = fma(q[i], r2, mul(f[i], m2));
+                }
+                st<V>(ds + k * d.head, hb, q);
             }
+            const int into = stage == 0 ? STAGES - 1 : stage - 1;
+            fetch(ahead, into);
+            ahead.next(b0, b1, stride);
+            stage = stage == STAGES - 1 ? 0 : stage + 1;
         }
-        // sum the groups of the warp, then the warps
+    }
+    // sum the groups of the warp, then the warps
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float s0, s1;
-            un(acc[i], s0, s1);
+            un(acc[w][i], s0, s1);
 #pragma unroll
             for (int o = 16; o >= L; o >>= 1) {
                 s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
                 s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
             }
             if (on && (threadIdx.x & 31) < L) {
-                const int at = (i < V / 2 ? 0 : p.D / 2) + c + 2 * (i % (V / 2));
-                red[threadIdx.x >> 5][w][at] = s0;
-                red[threadIdx.x >> 5][w][at + 1] = s1;
+                const int at = (threadIdx.x / 32 * 2 + w) * p.D + (i < V / 2 ? 0 : p.D / 2) + c + 2 * (i % (V / 2));
+                red[at] = s0;
+                red[at + 1] = s1;
             }
         }
-    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.D; i += BTHREADS) {
-        const int w = i >= p.D, d = w ? i - p.D : i;
+    for (int i = threadIdx.x; i < 2 * p.D; i += THREADS) {
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < BTHREADS / 32; ++k) s += red[k][w][d];
-        p.part[((size_t)(blk * shares + share) * p.P + slot) * 2 * p.D + i] = s;
+        for (int k = 0; k < THREADS / 32; ++k) s += red[k * 2 * p.D + i];
+        p.part[((size_t)(blockIdx.y * shares + share) * p.P + slot) * 2 * p.D + i] = s;
     }
 }
 
@@ -354,17 +463,29 @@ __global__ void __launch_bounds__(THREADS) k_qk_norm_dg(const Params p)
     if (lane == 0) p.dg[k >= p.D][slot * p.D + (k >= p.D ? k - p.D : k)] = s;
 }
 
-template <int V, int L>
-static void launch(const Params &p, bool grad, dim3 blocks, cudaStream_t st)
+template <auto KERNEL, int SMEM>
+static cudaError_t start(dim3 blocks, const Params &p, cudaStream_t st)
 {
-    if (grad) {
-        if (p.pairs) k_qk_norm_bwd<V, L, true><<<blocks, BTHREADS, 0, st>>>(p);
-        else k_qk_norm_bwd<V, L, false><<<blocks, BTHREADS, 0, st>>>(p);
-        k_qk_norm_dg<<<(p.P * 2 * p.D + THREADS / 32 - 1) / (THREADS / 32), THREADS, 0, st>>>(p);
-    } else {
-        if (p.pairs) k_qk_norm<V, L, true><<<blocks, THREADS, 0, st>>>(p);
-        else k_qk_norm<V, L, false><<<blocks, THREADS, 0, st>>>(p);
+    static const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    KERNEL<<<blocks, THREADS, SMEM, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int V, int L>
+static cudaError_t launch(const Params &p, bool grad, dim3 blocks, cudaStream_t st)
+{
+    if (!grad) {
+        constexpr int smem = Stage<V, 2 * HB>::TOTAL;
+        return p.pairs ? start<k_qk_norm<V, L, true>, smem>(blocks, p, st) : start<k_qk_norm<V, L, false>, smem>(blocks, p, st);
     }
+    constexpr int smem = Stage<V, 4 * GB>::TOTAL;
+    static_assert(smem >= THREADS / 32 * 2 * 2 * V * L * 4, "the block's sums fit the staging area");
+    const cudaError_t e = p.pairs ? start<k_qk_norm_bwd<V, L, true>, smem>(blocks, p, st)
+                                  : start<k_qk_norm_bwd<V, L, false>, smem>(blocks, p, st);
+    if (e != cudaSuccess) return e;
+    k_qk_norm_dg<<<(p.P * 2 * p.D + THREADS / 32 - 1) / (THREADS / 32), THREADS, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
 // Lanes of a group for a head of D: D / 2V rounded up to a power of two.
@@ -375,7 +496,7 @@ static int group_lanes(int D, int V)
     return l;
 }
 
-static void launch_any(const Params &p, bool grad, dim3 blocks, cudaStream_t st)
+static cudaError_t launch_any(const Params &p, bool grad, dim3 blocks, cudaStream_t st)
 {
     // V = 8 needs both halves of a head on 16-byte boundaries
     if (p.D % 16 == 0) {
@@ -412,17 +533,18 @@ static int check_heads(const rc_heads &in, Heads &h, const char *name, int P, in
     return RC_OK;
 }
 
-// The gradient's blocks: for each slot three per SM over all slots, or one per
-// group of tokens where that is less; then the heads are shared out too.
-static void bwd_blocks(const rc_qk_norm_args &a, int sms, int &blocks, int &shares)
+// Blocks of a launch: for each slot three per SM over all slots, or one per
+// group of tokens where that is less; then batches of heads are shared out too.
+static void grid_of(const rc_qk_norm_args &a, int sms, int batches, int &blocks, int &shares)
 {
-    const int groups = BTHREADS / group_lanes(a.D, a.D % 16 ? 4 : 8);
+    const int groups = THREADS / group_lanes(a.D, a.D % 16 ? 4 : 8);
     const long long n = ((long long)a.T + groups - 1) / groups, most = (3ll * sms + a.P - 1) / a.P;
     blocks = (int)(n > most ? most : n < 1 ? 1 : n);
-    const int heads = ((a.Hq > a.Hkv ? a.Hq : a.Hkv) + GB - 1) / GB;
     shares = (int)(most / blocks);
-    shares = shares > heads ? heads : shares < 1 ? 1 : shares;
+    shares = shares > batches ? batches : shares < 1 ? 1 : shares;
 }
+
+static int grad_batches(const rc_qk_norm_args &a) { return ((a.Hq > a.Hkv ? a.Hq : a.Hkv) + GB - 1) / GB; }
 
 static int check_sizes(const rc_qk_norm_args &a)
 {
@@ -474,7 +596,7 @@ static int run(const rc_qk_norm_args *args, bool grad, void *stream)
         p.dg[0] = a.dgamma_q;
         p.dg[1] = a.dgamma_k;
         int per_slot, shares;
-        bwd_blocks(a, sms, per_slot, shares);
+        grid_of(a, sms, grad_batches(a), per_slot, shares);
         p.blocks = per_slot * shares;
         blocks = dim3((unsigned)a.P, (unsigned)per_slot, (unsigned)shares);
         const size_t bytes = (size_t)p.blocks * a.P * 2 * a.D * 4;
@@ -485,14 +607,11 @@ static int run(const rc_qk_norm_args *args, bool grad, void *stream)
         if (!a.workspace && (rc_ = prepare_scratch(bytes, &s))) return rc_;
         p.part = (float *)s;
     } else {
-        p.runs[0] = (a.Hq + HB - 1) / HB;
-        p.runs[1] = (a.Hkv + HB - 1) / HB;
-        const int groups = THREADS / group_lanes(a.D, a.D % 16 ? 4 : 8);
-        const long long n = ((long long)a.T + groups - 1) / groups;
-        blocks = dim3((unsigned)(a.P * (p.runs[0] + p.runs[1])), (unsigned)(n < 65535 ? n : 65535));
+        int per_slot, shares;
+        grid_of(a, sms, (a.Hq + HB - 1) / HB + (a.Hkv + HB - 1) / HB, per_slot, shares);
+        blocks = dim3((unsigned)a.P, (unsigned)per_slot, (unsigned)shares);
     }
-    launch_any(p, grad, blocks, (cudaStream_t)stream);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_any(p, grad, blocks, (cudaStream_t)stream);
     if (e != cudaSuccess) return set_error(RC_ERR_CUDA, "qk_norm_rope launch: %s", cudaGetErrorString(e));
     return RC_OK;
 }
@@ -510,6 +629,6 @@ extern "C" size_t qk_norm_rope_bwd_workspace_bytes(const rc_qk_norm_args *args)
     int sms = 0;
     if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
     int blocks, shares;
-    bwd_blocks(*args, sms, blocks, shares);
+    grid_of(*args, sms, grad_batches(*args), blocks, shares);
     return (size_t)blocks * shares * args->P * 2 * args->D * 4;
 }
