@@ -286,14 +286,16 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm(const Params p)
                     copy<2 * V>(S::chunk(base, stage, 2 * i), src + i * x.head);
                     copy<2 * V>(S::chunk(base, stage, 2 * i + 1), src + i * x.head + hb);
                 }
-            // every stage carries its angles: batches of one token fetch the same lines again
-            fetch_angles<V, 2 * HB, PAIRS>(p, base, stage, pos, c);
-            if (k.b == b1 - 1 && k.t + stride < p.T) pos = __ldg(p.pos + k.t + stride);
+            if (k.b == b0) {                                       // the first batch brings the token's angles
+                fetch_angles<V, 2 * HB, PAIRS>(p, base, stage, pos, c);
+                if (k.t + stride < p.T) pos = __ldg(p.pos + k.t + stride);
+            }
         }
         copies_done();
     };
     Walk ahead{first, b0}, now{first, b0};
     for (int s = 0; s < STAGES - 1; ++s) fetch(ahead, s), ahead.next(b0, b1, stride);
+    f32x2 cs[V], sn[V];
     for (int stage = 0; now.t - warp_off < p.T; now.next(b0, b1, stride)) {
         wait_oldest();
         const bool live = on && now.t < p.T;
@@ -304,10 +306,10 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm(const Params p)
         if (live) {
             f32x2 g[V], gp[V];
             ldf<V>(p.g[w] + c, p.D / 2, g);
-            angles<V, 2 * HB, PAIRS>(base, stage, a, b);
+            if (now.b == b0) angles<V, 2 * HB, PAIRS>(base, stage, cs, sn);
             partners<V, PAIRS>(g, gp);
 #pragma unroll
-            for (int i = 0; i < V; ++i) a[i] = mul(a[i], g[i]), b[i] = mul(b[i], gp[i]);
+            for (int i = 0; i < V; ++i) a[i] = mul(cs[i], g[i]), b[i] = mul(sn[i], gp[i]);
         }
 #pragma unroll
         for (int k = 0; k < HB; ++k) {
@@ -357,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm_bwd(const Params p)
     for (int w = 0; w < 2; ++w) {
         const int nb = (p.H[w] + GB - 1) / GB, b0 = share * nb / shares, b1 = (share + 1) * nb / shares;
         if (b0 == b1) continue;
-        f32x2 g[V] = {};
+        f32x2 g[V] = {}, cs[V], sn[V];
         if (on) ldf<V>(p.g[w] + c, p.D / 2, g);
         const Heads &x = p.x[w], &z = p.z[w], &d = p.dx[w];
         int pos = on && first < p.T ? __ldg(p.pos + first) : 0;
@@ -373,8 +375,10 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm_bwd(const Params p)
                         copy<2 * V>(S::chunk(base, stage, 4 * i + 2), zs + i * z.head);
                         copy<2 * V>(S::chunk(base, stage, 4 * i + 3), zs + i * z.head + hb);
                     }
-                fetch_angles<V, 4 * GB, PAIRS>(p, base, stage, pos, c);
-                if (k.b == b1 - 1 && k.t + stride < p.T) pos = __ldg(p.pos + k.t + stride);
+                if (k.b == b0) {
+                    fetch_angles<V, 4 * GB, PAIRS>(p, base, stage, pos, c);
+                    if (k.t + stride < p.T) pos = __ldg(p.pos + k.t + stride);
+                }
             }
             copies_done();
         };
@@ -384,8 +388,7 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm_bwd(const Params p)
             wait_oldest();
             const bool live = on && now.t < p.T;
             char *const ds = d.base + slot * d.slot + now.t * d.token + now.b * GB * d.head + c * 2;
-            f32x2 cs[V], sn[V];
-            if (live) angles<V, 4 * GB, PAIRS>(base, stage, cs, sn);
+            if (live && now.b == b0) angles<V, 4 * GB, PAIRS>(base, stage, cs, sn);
 #pragma unroll
             for (int k = 0; k < GB; ++k) {
                 const bool here = live && now.b * GB + k < p.H[w];
@@ -451,16 +454,28 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm_bwd(const Params p)
     }
 }
 
-// dg[w][slot][d]: the sum over blocks, one warp per output.
-__global__ void __launch_bounds__(THREADS) k_qk_norm_dg(const Params p)
+// dg[w][slot][d]: the sum over the rows of `part`.  A lane owns an output, warp k
+// adds rows k, k + 32, ... and the warps' sums are added in order.
+constexpr int DG_WARPS = 32;
+
+__global__ void __launch_bounds__(32 * DG_WARPS) k_qk_norm_dg(const Params p)
 {
-    const int i = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (i >= p.P * 2 * p.D) return;
+    __shared__ float red[DG_WARPS][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, width = p.P * 2 * p.D;
+    const int i = blockIdx.x * 32 + lane;                  // the width is a multiple of 16
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // the rows are written
     float s = 0.f;
-    for (int b = lane; b < p.blocks; b += 32) s += p.part[(size_t)b * p.P * 2 * p.D + i];
-    s = group_sum<32>(s);
+    if (i < width)
+#pragma unroll 8
+        for (int b = warp; b < p.blocks; b += DG_WARPS) s += p.part[(size_t)b * width + i];
+    red[warp][lane] = s;
+    __syncthreads();
+    if (warp || i >= width) return;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < DG_WARPS; ++k) s += red[k][lane];
     const int slot = i / (2 * p.D), k = i % (2 * p.D);
-    if (lane == 0) p.dg[k >= p.D][slot * p.D + (k >= p.D ? k - p.D : k)] = s;
+    p.dg[k >= p.D][slot * p.D + (k >= p.D ? k - p.D : k)] = s;
 }
 
 template <auto KERNEL, int SMEM>
@@ -484,8 +499,17 @@ static cudaError_t launch(const Params &p, bool grad, dim3 blocks, cudaStream_t 
     const cudaError_t e = p.pairs ? start<k_qk_norm_bwd<V, L, true>, smem>(blocks, p, st)
                                   : start<k_qk_norm_bwd<V, L, false>, smem>(blocks, p, st);
     if (e != cudaSuccess) return e;
-    k_qk_norm_dg<<<(p.P * 2 * p.D + THREADS / 32 - 1) / (THREADS / 32), THREADS, 0, st>>>(p);
-    return cudaGetLastError();
+    // set up while the last blocks of the gradient still run
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((p.P * 2 * p.D + 31) / 32));
+    cfg.blockDim = dim3(32 * DG_WARPS);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_qk_norm_dg, p);
 }
 
 // Lanes of a group for a head of D: D / 2V rounded up to a power of two.
@@ -535,16 +559,16 @@ static int check_heads(const rc_heads &in, Heads &h, const char *name, int P, in
 
 // Blocks of a launch: for each slot three per SM over all slots, or one per
 // group of tokens where that is less; then batches of heads are shared out too.
-static void grid_of(const rc_qk_norm_args &a, int sms, int batches, int &blocks, int &shares)
+static void grid_of(const rc_qk_norm_args &a, int sms, int most_shares, int &blocks, int &shares)
 {
     const int groups = THREADS / group_lanes(a.D, a.D % 16 ? 4 : 8);
     const long long n = ((long long)a.T + groups - 1) / groups, most = (3ll * sms + a.P - 1) / a.P;
     blocks = (int)(n > most ? most : n < 1 ? 1 : n);
     shares = (int)(most / blocks);
-    shares = shares > batches ? batches : shares < 1 ? 1 : shares;
+    shares = shares > most_shares ? most_shares : shares < 1 ? 1 : shares;
 }
 
-static int grad_batches(const rc_qk_norm_args &a) { return ((a.Hq > a.Hkv ? a.Hq : a.Hkv) + GB - 1) / GB; }
+static int batches(const rc_qk_norm_args &a, int n) { return (a.Hq + n - 1) / n + (a.Hkv + n - 1) / n; }
 
 static int check_sizes(const rc_qk_norm_args &a)
 {
@@ -596,7 +620,7 @@ static int run(const rc_qk_norm_args *args, bool grad, void *stream)
         p.dg[0] = a.dgamma_q;
         p.dg[1] = a.dgamma_k;
         int per_slot, shares;
-        grid_of(a, sms, grad_batches(a), per_slot, shares);
+        grid_of(a, sms, batches(a, GB), per_slot, shares);
         p.blocks = per_slot * shares;
         blocks = dim3((unsigned)a.P, (unsigned)per_slot, (unsigned)shares);
         const size_t bytes = (size_t)p.blocks * a.P * 2 * a.D * 4;
@@ -608,7 +632,7 @@ static int run(const rc_qk_norm_args *args, bool grad, void *stream)
         p.part = (float *)s;
     } else {
         int per_slot, shares;
-        grid_of(a, sms, (a.Hq + HB - 1) / HB + (a.Hkv + HB - 1) / HB, per_slot, shares);
+        grid_of(a, sms, batches(a, HB), per_slot, shares);
         blocks = dim3((unsigned)a.P, (unsigned)per_slot, (unsigned)shares);
     }
     const cudaError_t e = launch_any(p, grad, blocks, (cudaStream_t)stream);
@@ -629,6 +653,6 @@ extern "C" size_t qk_norm_rope_bwd_workspace_bytes(const rc_qk_norm_args *args)
     int sms = 0;
     if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
     int blocks, shares;
-    grid_of(*args, sms, grad_batches(*args), blocks, shares);
+    grid_of(*args, sms, batches(*args, GB), blocks, shares);
     return (size_t)blocks * shares * args->P * 2 * args->D * 4;
 }
