@@ -290,20 +290,23 @@ constexpr long long split_units(int sms) { return 4ll * sms; }
 // the next one from a counter.  Two words of the status header that nothing
 // else uses hold the counter and the blocks that are done; the last block
 // clears both, also in a launch that gave up (every block reaches its end).
-// Which block runs a unit changes no result.
+// Which block runs a unit changes no result.  SET: the words of this kernel
+// (the dK/dV launch overlaps the end of the dQ launch).
+template <int SET>
 __device__ __forceinline__ int claim_unit(const Params &p, int lane)
 {
     int u = 0;
-    if (lane == 0) u = (int)(gridDim.x + atomicAdd(&p.hdr->pad[2], 1u));
+    if (lane == 0) u = (int)(gridDim.x + atomicAdd(&p.hdr->pad[2 + 2 * SET], 1u));
     return __shfl_sync(0xFFFFFFFFu, u, 0);
 }
 
+template <int SET>
 __device__ __forceinline__ void units_done(const Params &p)
 {
     __threadfence();
-    if (atomicAdd(&p.hdr->pad[3], 1u) == gridDim.x - 1) {
-        atomicExch(&p.hdr->pad[2], 0u);
-        atomicExch(&p.hdr->pad[3], 0u);
+    if (atomicAdd(&p.hdr->pad[3 + 2 * SET], 1u) == gridDim.x - 1) {
+        atomicExch(&p.hdr->pad[2 + 2 * SET], 0u);
+        atomicExch(&p.hdr->pad[3 + 2 * SET], 0u);
     }
 }
 

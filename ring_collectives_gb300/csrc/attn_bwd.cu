@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             bool ok = publish(0, next);
             while (ok && next.index >= 0) {
                 const BUnit w = next;
-                u = claim_unit(p, lane);
+                u = claim_unit<DKV ? 1 : 0>(p, lane);
                 if (u < total) next = bunit_of<DKV>(p, u, lane);
                 else next.index = -1;
                 ok = publish(++it, next);
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                 }
                 ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
             }
-            if (lane == 0) units_done(p);
+            if (lane == 0) units_done<DKV ? 1 : 0>(p);
             if (lane == 0 && *(volatile int *)abort_flag) {
                 // let the copies in flight land before the block gives up its shared memory
                 for (uint32_t s = 0; s < NA; ++s)
@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             __syncwarp();
         } else if (DKV) {
             // ---------------- row statistics: 64 rows of a tile per warp
+            asm volatile("griddepcontrol.wait;" ::: "memory");      // the dQ launch has written delta
             uint32_t e = 0;
             bool ok = true;
             const BUnit *wp;
@@ -648,6 +649,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.launch_dependents;");
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
@@ -670,8 +672,18 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && p.Tk) {
-        k_attn_bwd<DP, true><<<p.sms, BWD_THREADS, BwdCfg<DP>::SMEM, st>>>(mq, mdo, mk, mv, p);
-        e = cudaGetLastError();
+        // Blocks start on SMs that the dQ launch has left and run up to the first use of delta.
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)p.sms);
+        cfg.blockDim = dim3(BWD_THREADS);
+        cfg.dynamicSmemBytes = BwdCfg<DP>::SMEM;
+        cfg.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = p.Tq ? 1 : 0;
+        e = cudaLaunchKernelEx(&cfg, k_attn_bwd<DP, true>, mq, mdo, mk, mv, p);
     }
     return e;
 }

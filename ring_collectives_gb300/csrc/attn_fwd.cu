@@ -66,12 +66,13 @@ __device__ __forceinline__ int units_per_tile(int kt, int cs)
 }
 
 // How far keys are split (p.may_split: the host found too few unsplit units to
-// fill the GPU and made room for partial results).  Every lane tries one part
-// size -- 1 to 4 rounds of units over the SMs, with up to 44 % of slack, and no
-// split -- and the warp takes the one with the least rounds x (key tiles of a
-// unit + the cost of a unit's ends, about 3 tiles; 2 in the SPLIT form).
-// Measured on GB300 against parts for a fixed 3 (SPLIT: 4) units per SM: token
-// 1 x 32768 keys 45 -> 32 us, prompt pieces 60 -> 46 us.
+// fill the GPU and made room for partial results).  Eight part sizes are tried
+// -- 1 to 4 rounds of units over the SMs, some with slack, and no split -- by
+// eight lanes each, a quarter of the sequences to a lane of them, and the one with
+// the least rounds x (key tiles of a unit + the cost of a unit's ends, about 3
+// tiles; 2 in the SPLIT form) is taken.  Measured on GB300 against parts for a
+// fixed 3 (SPLIT: 4) units per SM: token 1 x 32768 keys 45 -> 34 us, prompt pieces
+// 60 -> 46 us.
 template <bool SPLIT>
 __device__ Plan make_plan(const Params &p, int lane)
 {
@@ -89,28 +90,23 @@ __device__ Plan make_plan(const Params &p, int lane)
         }
         work = warp_sum(work) * HP;
         most = max(1, __reduce_max_sync(0xFFFFFFFFu, most));
-        const long long per = (long long)p.sms * (SPLIT ? 2 : 1) * (1 + (lane & 3)) * 16;
-        long long c = (work * (16 + (lane >> 2)) + per - 1) / per;
-        c = max(c, SPLIT ? 2ll : 4ll);
-        int cs = c >= most || lane == 31 ? most : (int)c;
-        long long units = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const int b = b0 + lane;
-            int nt = 0, kt = 0;
-            if (b < p.B) {
-                const Seq s = seq_of(p, b);
-                nt = (s.ql + p.TPU - 1) / p.TPU;
-                kt = (s.kl + KT - 1) / KT;
-            }
-            for (int i = 0; i < min(32, p.B - b0); ++i)
-                units += (long long)__shfl_sync(0xFFFFFFFFu, nt, i) *
-                         units_per_tile<SPLIT>(__shfl_sync(0xFFFFFFFFu, kt, i), cs);
+        const int k = lane & 7;                                    // rounds 1 1 1 2 2 3 4, slack 0 2 5 0 3 0 0 sixteenths
+        const int rounds = k < 3 ? 1 : k < 5 ? 2 : k - 2, slack = k == 1 ? 2 : k == 2 ? 5 : k == 4 ? 3 : 0;
+        const long long per = (long long)p.sms * (SPLIT ? 2 : 1) * rounds * 16;
+        const long long c = max((work * (16 + slack) + per - 1) / per, SPLIT ? 2ll : 4ll);
+        const int cs = c >= most || k == 7 ? most : (int)c;
+        int units = 0;
+        for (int b = lane >> 3; b < p.B; b += 4) {
+            const Seq s = seq_of(p, b);
+            units += (s.ql + p.TPU - 1) / p.TPU * units_per_tile<SPLIT>((s.kl + KT - 1) / KT, cs);
         }
-        const long long cost = (units * HP + p.sms - 1) / p.sms * (cs + (SPLIT ? 2 : 3));
-        const unsigned least = __reduce_min_sync(0xFFFFFFFFu, (unsigned)min(cost, 0x7FFFFFFFll));
-        const int pick = __ffs(__ballot_sync(0xFFFFFFFFu, (unsigned)min(cost, 0x7FFFFFFFll) == least)) - 1;
+        units += __shfl_xor_sync(0xFFFFFFFFu, units, 8);
+        units += __shfl_xor_sync(0xFFFFFFFFu, units, 16);
+        const long long cost = ((long long)units * HP + p.sms - 1) / p.sms * (cs + (SPLIT ? 2 : 3));
+        const unsigned mine = (unsigned)min(cost, 0x7FFFFFFFll), least = __reduce_min_sync(0xFFFFFFFFu, mine);
+        const int pick = __ffs(__ballot_sync(0xFFFFFFFFu, mine == least)) - 1;
         pl.cs = __shfl_sync(0xFFFFFFFFu, cs, pick);
-        pl.units = (int)__shfl_sync(0xFFFFFFFFu, units, pick);
+        pl.units = __shfl_sync(0xFFFFFFFFu, units, pick);
         return pl;
     }
     long long u = 0;
@@ -279,6 +275,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             // ---------------- units, one ahead of the loads, and the TMA loads
             const Plan pl = make_plan<SPLIT>(p, lane);
             const int total = pl.units * p.P * p.Hkv;
+            if (p.may_split && blockIdx.x == 0 && lane == 0) p.hdr->pad[6] = (uint32_t)pl.cs;   // for the join
             auto publish = [&](uint32_t it, const Unit &w) {
                 bool ok = true;
                 if (lane == 0) {
@@ -298,7 +295,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             bool ok = publish(0, next);
             while (ok && next.index >= 0) {
                 const Unit w = next;
-                u = claim_unit(p, lane);
+                u = claim_unit<0>(p, lane);
                 if (u < total) next = unit_of<SPLIT>(p, pl, u, lane);
                 else next.index = -1;
                 ok = publish(++it, next);
@@ -340,7 +337,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 }
                 ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
             }
-            if (lane == 0) units_done(p);
+            if (lane == 0) units_done<0>(p);
             if (lane == 0 && *(volatile int *)abort_flag) {
                 // let the copies in flight land before the block gives up its shared memory
                 for (uint32_t s = 0; s < NST; ++s)
@@ -744,8 +741,9 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
     constexpr int ROWS = JOIN_WARPS / W;                   // rows of a block at a time
     __shared__ float acc_s[W][DP + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Plan pl = make_plan<SPLIT>(p, lane);             // reads what the launch before was given, too
-    asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written, and their size
+    Plan pl;
+    pl.cs = (int)ld_relaxed_gpu(&p.hdr->pad[6]);
     const int HP = p.P * p.Hkv;
     const long long rows = (long long)p.P * p.Tq * p.Hq;
     for (long long row = (long long)blockIdx.x * ROWS + warp / W; row < rows; row += (long long)gridDim.x * ROWS) {

@@ -16,7 +16,8 @@ struct WsHeader {
     uint32_t err_step;
     uint32_t err_slice;
     uint32_t pad[26];   // pad[0]: abort word of the running launch; pad[1]: debug grid-barrier counter;
-                        // pad[2], pad[3]: unit counter and finished blocks of an attention launch
+                        // pad[2], pad[3] (dK/dV: 4, 5): unit counter and finished blocks of an attention launch;
+                        // pad[6]: key tiles of a part of the last split one
 };
 static_assert(sizeof(WsHeader) == 128, "header is one 128-byte line");
 
