@@ -108,25 +108,30 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
                  : "memory");
 }
 
-// D = A B^T over DP columns, both tiles K-major in shared memory.
-template <int DP>
+// Head sizes come in three classes, KS steps of 16 columns that the MMAs do: 4
+// (D <= 64), 6 (D <= 96) and 8 (D <= 128).  Tiles lie in 64-column blocks, filled
+// with zeros past D.  With the steps as a run-time bound every size paid 2 %.
+constexpr int tile_cols(int ks) { return ks <= 4 ? 64 : 128; }
+
+// D = A B^T over 16 KS columns, both tiles K-major in shared memory.
+template <int KS>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b)
 {
     constexpr uint32_t id = idesc_bf16_f32(KT, KT);
     const uint32_t ad = desc_k(a), bd = desc_k(b);
 #pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk) {
+    for (int kk = 0; kk < KS; ++kk) {
         const uint32_t off = (kk >> 2) * (BLK >> 4) + 2 * (kk & 3);
         mma_ss(d, ad + off, bd + off, id, kk != 0);
     }
 }
 
-// D (+)= A B over the 128 rows of B, a tile of DP columns; A in TMEM, the
-// second 64 of its columns (of bf16) `half` TMEM columns from the first.
-template <int DP>
+// D (+)= A B over the 128 rows of B, its first 16 KS columns; A in TMEM, the second
+// 64 of its columns (of bf16) `half` TMEM columns from the first.
+template <int KS>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, bool first, int half)
 {
-    constexpr uint32_t id = idesc_bf16_f32(KT, DP) | kIdescBMnMajor;
+    constexpr uint32_t id = idesc_bf16_f32(KT, 16 * KS) | kIdescBMnMajor;
     const uint32_t bd = desc_mn(b);
 #pragma unroll
     for (int kk = 0; kk < KT / 16; ++kk)

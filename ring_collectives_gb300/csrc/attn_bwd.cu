@@ -170,11 +170,12 @@ __device__ __forceinline__ Bars bars_at(uint32_t x)
     return b;
 }
 
-template <int DP, bool DKV>
+template <int KS, bool DKV>
 __global__ void __launch_bounds__(BWD_THREADS, 1)
     k_attn_bwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
                const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const Params p)
 {
+    constexpr int DP = tile_cols(KS);
     using C = BwdCfg<DP>;
     constexpr int TILE = C::TILE, NA = C::NA, NB = C::NB;
     constexpr int READERS = DKV ? 11 : 9;     // warps that release a unit
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                 if (!wait_all(bar.a_full + 8 * sa, pa, ab, 4)) return false;
                 tc_fence_after();
                 if (elect_one()) {
-                    mma_scores<DP>(d, sR0, sA + sa * TILE);
+                    mma_scores<KS>(d, sR0, sA + sa * TILE);
                     tc_commit(full);
                 }
                 if (++sa == NA) sa = 0, pa ^= 1u;
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                 if (!wait_all(bar.b_full + 8 * sb, pb, ab, 5)) return false;
                 tc_fence_after();
                 if (elect_one()) {
-                    mma_scores<DP>(d, sR1, sB + sb * TILE);
+                    mma_scores<KS>(d, sR1, sB + sb * TILE);
                     tc_commit(bar.dp_full);
                     if (!DKV) tc_commit(bar.b_empty + 8 * sb);
                 }
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
             auto rows_a = [&](uint32_t d, uint32_t a, bool first) {
                 tc_fence_after();
                 if (elect_one()) {
-                    mma_rows<DP>(d, a, sA + ra * TILE, first, 64);
+                    mma_rows<KS>(d, a, sA + ra * TILE, first, 64);
                     tc_commit(bar.a_empty + 8 * ra);
                 }
                 if (++ra == NA) ra = 0;
@@ -363,7 +364,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                         if (!(ok = wait_all(bar.p_ready, nt & 1, ab, 6))) break;
                         tc_fence_after();
                         if (elect_one()) {
-                            mma_rows<DP>(tm, tm + 256, sB + rb * TILE, j == 0, 64);
+                            mma_rows<KS>(tm, tm + 256, sB + rb * TILE, j == 0, 64);
                             tc_commit(bar.b_empty + 8 * rb);
                         }
                         if (++rb == NB) rb = 0;
@@ -653,22 +654,23 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-template <int DP>
+template <int KS>
 static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensorMap &mdo, const CUtensorMap &mk,
                           const CUtensorMap &mv, cudaStream_t st)
 {
+    constexpr int DP = tile_cols(KS);
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(k_attn_bwd<DP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdCfg<DP>::SMEM);
+        attr = cudaFuncSetAttribute(k_attn_bwd<KS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdCfg<DP>::SMEM);
         if (attr == cudaSuccess)
-            attr = cudaFuncSetAttribute(k_attn_bwd<DP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            attr = cudaFuncSetAttribute(k_attn_bwd<KS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         BwdCfg<DP>::SMEM);
     });
     if (attr != cudaSuccess) return attr;
     cudaError_t e = cudaSuccess;
     if (p.Tq) {
-        k_attn_bwd<DP, false><<<p.sms, BWD_THREADS, BwdCfg<DP>::SMEM, st>>>(mq, mdo, mk, mv, p);
+        k_attn_bwd<KS, false><<<p.sms, BWD_THREADS, BwdCfg<DP>::SMEM, st>>>(mq, mdo, mk, mv, p);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && p.Tk) {
@@ -683,7 +685,7 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
         at[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
         cfg.numAttrs = p.Tq ? 1 : 0;
-        e = cudaLaunchKernelEx(&cfg, k_attn_bwd<DP, true>, mq, mdo, mk, mv, p);
+        e = cudaLaunchKernelEx(&cfg, k_attn_bwd<KS, true>, mq, mdo, mk, mv, p);
     }
     return e;
 }
@@ -691,7 +693,7 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
 cudaError_t launch_attn_bwd(const Params &p, const CUtensorMap &mq, const CUtensorMap &mdo, const CUtensorMap &mk,
                             const CUtensorMap &mv, cudaStream_t st)
 {
-    return p.D <= 64 ? launch<64>(p, mq, mdo, mk, mv, st) : launch<128>(p, mq, mdo, mk, mv, st);
+    return p.D <= 64 ? launch<4>(p, mq, mdo, mk, mv, st) : p.D <= 96 ? launch<6>(p, mq, mdo, mk, mv, st) : launch<8>(p, mq, mdo, mk, mv, st);
 }
 
 } // namespace attn

@@ -194,11 +194,12 @@ __device__ __forceinline__ void for_entries(const Unit &w, F f)
 
 __device__ __forceinline__ bool nonfinite_bf16(uint32_t bits16) { return (bits16 & 0x7F80u) == 0x7F80u; }
 
-template <int DP, bool SPLIT>
+template <int KS, bool SPLIT>
 __global__ void __launch_bounds__(FWD_THREADS, 1)
     k_attn_fwd(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v, const Params p)
 {
+    constexpr int DP = tile_cols(KS);
     using C = FwdCfg<DP, SPLIT>;
     constexpr int NST = C::STAGES, STAGE = C::KV_STAGE;
     extern __shared__ uint8_t smem_raw[];
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             auto score = [&](int t, uint32_t s) {
                 tc_fence_after();
                 if (elect_one()) {
-                    mma_scores<DP>(tm + t * KT, sQ + (SPLIT ? 0 : t * STAGE), sKV + s * STAGE);
+                    mma_scores<KS>(tm + t * KT, sQ + (SPLIT ? 0 : t * STAGE), sKV + s * STAGE);
                     tc_commit(s_full + 8 * t);
                 }
             };
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             auto weigh = [&](int t, uint32_t s, bool first, bool last) {
                 tc_fence_after();
                 if (elect_one()) {
-                    mma_rows<DP>(tm + 256 + t * KT, tm + t * KT, sKV + s * STAGE, first, 32);
+                    mma_rows<KS>(tm + 256 + t * KT, tm + t * KT, sKV + s * STAGE, first, 32);
                     if (last) tc_commit(o_full + 8 * t);
                 }
             };
@@ -400,8 +401,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     if (!(ok = take(false))) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        if (n0 > 0) mma_scores<DP>(tm, sQ, sKV + st * STAGE), tc_commit(s_full);
-                        if (n1 > 0) mma_scores<DP>(tm + KT, sQ + STAGE, sKV + st * STAGE), tc_commit(s_full + 8);
+                        if (n0 > 0) mma_scores<KS>(tm, sQ, sKV + st * STAGE), tc_commit(s_full);
+                        if (n1 > 0) mma_scores<KS>(tm + KT, sQ + STAGE, sKV + st * STAGE), tc_commit(s_full + 8);
                         tc_commit(empty_bar + 8 * st);
                         if (n == 1) tc_commit(q_empty);
                     }
@@ -427,12 +428,12 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                             const bool last_v = t == 1 || j >= n1;                   // the tile's last use here
                             const bool last_k = t == 1 || j + 1 >= n1;
                             if (elect_one()) {
-                                mma_rows<DP>(tm + 256 + t * KT, tm + t * KT, sKV + sv * STAGE, j == 0, 32);
+                                mma_rows<KS>(tm + 256 + t * KT, tm + t * KT, sKV + sv * STAGE, j == 0, 32);
                                 if (last_v) tc_commit(empty_bar + 8 * sv);
                             }
                             if (elect_one()) {
                                 if (j + 1 < nt) {
-                                    mma_scores<DP>(tm + t * KT, sQ + t * STAGE, sKV + sk * STAGE);
+                                    mma_scores<KS>(tm + t * KT, sQ + t * STAGE, sKV + sk * STAGE);
                                     tc_commit(s_full + 8 * t);
                                     if (last_k) {
                                         tc_commit(empty_bar + 8 * sk);
@@ -821,18 +822,19 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
     }
 }
 
-template <int DP, bool SPLIT>
+template <int KS, bool SPLIT>
 static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                           cudaStream_t st)
 {
+    constexpr int DP = tile_cols(KS);
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(k_attn_fwd<DP, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr = cudaFuncSetAttribute(k_attn_fwd<KS, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     FwdCfg<DP, SPLIT>::SMEM);
     });
     if (attr != cudaSuccess) return attr;
-    k_attn_fwd<DP, SPLIT><<<p.sms, FWD_THREADS, FwdCfg<DP, SPLIT>::SMEM, st>>>(mq, mk, mv, p);
+    k_attn_fwd<KS, SPLIT><<<p.sms, FWD_THREADS, FwdCfg<DP, SPLIT>::SMEM, st>>>(mq, mk, mv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.may_split) return e;
     // The join's blocks may be set up while the last units still run.
@@ -855,9 +857,9 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
 cudaError_t launch_attn_fwd(const Params &p, const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
                             bool split, cudaStream_t st)
 {
-    if (p.D <= 64)
-        return split ? launch<64, true>(p, mq, mk, mv, st) : launch<64, false>(p, mq, mk, mv, st);
-    return split ? launch<128, true>(p, mq, mk, mv, st) : launch<128, false>(p, mq, mk, mv, st);
+    if (p.D <= 64) return split ? launch<4, true>(p, mq, mk, mv, st) : launch<4, false>(p, mq, mk, mv, st);
+    if (p.D <= 96) return split ? launch<6, true>(p, mq, mk, mv, st) : launch<6, false>(p, mq, mk, mv, st);
+    return split ? launch<8, true>(p, mq, mk, mv, st) : launch<8, false>(p, mq, mk, mv, st);
 }
 
 } // namespace attn
