@@ -138,10 +138,31 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, boo
         mma_ts(d, a + (kk >> 2) * half + (kk & 3) * 8, bd + 128 * kk, id, kk ? 1u : (first ? 0u : 1u));
 }
 
-// Every lane waits; the same answer in all.
+// Every lane waits; the same answer in all.  (A wait by one lane, handed on by a
+// shuffle, costs the warp over 100 clocks more: the softmax warps waiting that way
+// made a 16384-token prompt 11 % slower.)
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Abort &ab, int where)
 {
     return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, ab, where));
+}
+
+// The same for a warp in no hurry: asleep between polls, which would take issue
+// slots from the warps that share its scheduler.
+__device__ __forceinline__ bool wait_idle(uint32_t bar, uint32_t parity, const Abort &ab, int where)
+{
+    uint64_t t0 = 0;
+    while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) {
+        __nanosleep(64);
+        bool over = *(volatile int *)ab.flag != 0;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (!over && now - t0 > ab.timeout_ns) {
+            record_timeout(ab, where);
+            over = true;
+        }
+        if (__any_sync(0xFFFFFFFFu, over)) return false;
+    }
+    return true;
 }
 
 // Stores 16 / 32 columns of this thread's TMEM lane; tmem_wait_st() ends them.

@@ -231,9 +231,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     const Abort ab{abort_flag, p.hdr, p.timeout_ns, DKV ? 0xB3u : 0xB2u, 0};
 
     auto next_unit = [&](uint32_t it) -> const BUnit * {
-        const int got = lane == 0 ? (int)wait_bar(bar.u_full + 8 * (it % BUNITS), (it / BUNITS) & 1, ab, 12) : 0;
-        if (!__shfl_sync(0xFFFFFFFFu, got, 0)) return nullptr;
-        __syncwarp();
+        if (!wait_all(bar.u_full + 8 * (it % BUNITS), (it / BUNITS) & 1, ab, 12)) return nullptr;
         const BUnit *w = units + it % BUNITS;
         return w->index < 0 ? nullptr : w;
     };
@@ -245,60 +243,62 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
-            // ---------------- units, one ahead of the loads, and the TMA loads
+            // ---------------- units and TMA loads (the whole warp, one elected lane issues)
             const int total = bunits_total<DKV>(p, lane) * p.P * p.Hkv;
             const uint32_t rows = (uint32_t)(p.G * p.TT) * 128u * (DP / 64);
-            auto publish = [&](uint32_t it, const BUnit &w) {
-                bool ok = true;
-                if (lane == 0) {
-                    ok = wait_bar(bar.u_empty + 8 * (it % BUNITS), ((it / BUNITS) & 1) ^ 1u, ab, 13);
-                    if (ok) {
-                        units[it % BUNITS] = w;
-                        mbar_arrive(bar.u_full + 8 * (it % BUNITS));
-                    }
-                }
-                return __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
-            };
             uint32_t ea = 0, eb = 0, nr = 0, it = 0;
-            int u = blockIdx.x;
+            bool ok = true;
             BUnit next;
-            if (u < total) next = bunit_of<DKV>(p, u, lane);
-            else next.index = -1;
-            bool ok = publish(0, next);
-            while (ok && next.index >= 0) {
-                const BUnit w = next;
-                u = claim_unit<DKV ? 1 : 0>(p, lane);
+            // Makes unit u (or the end of all units) the block's next one.
+            auto publish = [&](int u) {
                 if (u < total) next = bunit_of<DKV>(p, u, lane);
                 else next.index = -1;
-                ok = publish(++it, next);
-                if (!ok || w.n == 0) continue;
-                if (lane == 0 && (ok = wait_bar(bar.res_empty, (nr & 1) ^ 1u, ab, 1))) {
-                    if (DKV) {
-                        mbar_expect_tx(bar.res_full, 2 * TILE);
-                        load_keys<DP>(sR0, &map_k, w.s.k0 + w.first, w.hk, w.slot, bar.res_full);
-                        load_keys<DP>(sR1, &map_v, w.s.k0 + w.first, w.hk, w.slot, bar.res_full);
-                    } else {
-                        mbar_expect_tx(bar.res_full, 2 * rows);
-                        load_rows<DP>(sR0, &map_q, w.s.q0 + w.first, w.hk, w.slot, bar.res_full);
-                        load_rows<DP>(sR1, &map_do, w.s.q0 + w.first, w.hk, w.slot, bar.res_full);
+                if (!(ok = wait_all(bar.u_empty + 8 * (it % BUNITS), ((it / BUNITS) & 1) ^ 1u, ab, 13))) return;
+                if (lane == 0) {
+                    units[it % BUNITS] = next;
+                    mbar_arrive(bar.u_full + 8 * (it % BUNITS));
+                }
+                __syncwarp();
+                ++it;
+            };
+            publish(blockIdx.x);
+            while (ok && next.index >= 0) {
+                const BUnit w = next;
+                if (w.n > 0) {
+                    if (!(ok = wait_all(bar.res_empty, (nr & 1) ^ 1u, ab, 1))) break;
+                    if (elect_one()) {
+                        mbar_expect_tx(bar.res_full, DKV ? 2 * TILE : 2 * rows);
+                        if (DKV) {
+                            load_keys<DP>(sR0, &map_k, w.s.k0 + w.first, w.hk, w.slot, bar.res_full);
+                            load_keys<DP>(sR1, &map_v, w.s.k0 + w.first, w.hk, w.slot, bar.res_full);
+                        } else {
+                            load_rows<DP>(sR0, &map_q, w.s.q0 + w.first, w.hk, w.slot, bar.res_full);
+                            load_rows<DP>(sR1, &map_do, w.s.q0 + w.first, w.hk, w.slot, bar.res_full);
+                        }
                     }
                     ++nr;
-                    for (int j = 0; j < w.n && ok; ++j) {
-                        const uint32_t st = ea % NA, su = eb % NB;
-                        const int at = DKV ? w.s.q0 + (w.from + j) * p.TT : w.s.k0 + j * KT;
-                        if (!(ok = wait_bar(bar.a_empty + 8 * st, ((ea / NA) & 1) ^ 1u, ab, 2))) break;
+                }
+                for (int j = 0; j < w.n && ok; ++j) {
+                    // the next unit is worked out once this one has two tiles to go on with
+                    if (j == 2) publish(claim_unit<DKV ? 1 : 0>(p, lane));
+                    const uint32_t st = ea % NA, su = eb % NB;
+                    const int at = DKV ? w.s.q0 + (w.from + j) * p.TT : w.s.k0 + j * KT;
+                    if (!ok || !(ok = wait_all(bar.a_empty + 8 * st, ((ea / NA) & 1) ^ 1u, ab, 2))) break;
+                    if (elect_one()) {
                         mbar_expect_tx(bar.a_full + 8 * st, DKV ? rows : TILE);
                         if (DKV) load_rows<DP>(sA + st * TILE, &map_q, at, w.hk, w.slot, bar.a_full + 8 * st);
                         else load_keys<DP>(sA + st * TILE, &map_k, at, w.hk, w.slot, bar.a_full + 8 * st);
-                        ++ea;
-                        if (!(ok = wait_bar(bar.b_empty + 8 * su, ((eb / NB) & 1) ^ 1u, ab, 2))) break;
+                    }
+                    ++ea;
+                    if (!(ok = wait_all(bar.b_empty + 8 * su, ((eb / NB) & 1) ^ 1u, ab, 2))) break;
+                    if (elect_one()) {
                         mbar_expect_tx(bar.b_full + 8 * su, DKV ? rows : TILE);
                         if (DKV) load_rows<DP>(sB + su * TILE, &map_do, at, w.hk, w.slot, bar.b_full + 8 * su);
                         else load_keys<DP>(sB + su * TILE, &map_v, at, w.hk, w.slot, bar.b_full + 8 * su);
-                        ++eb;
                     }
+                    ++eb;
                 }
-                ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+                if (ok && w.n <= 2) publish(claim_unit<DKV ? 1 : 0>(p, lane));
             }
             if (lane == 0) units_done<DKV ? 1 : 0>(p);
             if (lane == 0 && *(volatile int *)abort_flag) {
@@ -416,9 +416,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                             dl[h] = p.delta[at];
                         }
                     }
-                    int got = lane == 0 ? (int)wait_bar(bar.stat_empty + 8 * st, ((e >> 1) & 1) ^ 1u, ab, 14) : 0;
-                    ok = __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
-                    if (!ok) break;
+                    if (!(ok = wait_all(bar.stat_empty + 8 * st, ((e >> 1) & 1) ^ 1u, ab, 14))) break;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int r = (warp - 10) * 64 + h * 32 + lane;

@@ -257,9 +257,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
 
     // The next unit of the block's ring; null when there is none or the block gave up.
     auto next_unit = [&](uint32_t it) -> const Unit * {
-        const int got = lane == 0 ? (int)wait_bar(u_full + 8 * (it % UNITS), (it / UNITS) & 1, ab, 12) : 0;
-        if (!__shfl_sync(0xFFFFFFFFu, got, 0)) return nullptr;
-        __syncwarp();
+        if (!wait_all(u_full + 8 * (it % UNITS), (it / UNITS) & 1, ab, 12)) return nullptr;
         const Unit *w = units + it % UNITS;
         return w->index < 0 ? nullptr : w;
     };
@@ -273,70 +271,65 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
-            // ---------------- units, one ahead of the loads, and the TMA loads
+            // ---------------- units and TMA loads (the whole warp, one elected lane issues)
             const Plan pl = make_plan<SPLIT>(p, lane);
             const int total = pl.units * p.P * p.Hkv;
             if (p.may_split && blockIdx.x == 0 && lane == 0) p.hdr->pad[6] = (uint32_t)pl.cs;   // for the join
-            auto publish = [&](uint32_t it, const Unit &w) {
-                bool ok = true;
-                if (lane == 0) {
-                    ok = wait_bar(u_empty + 8 * (it % UNITS), ((it / UNITS) & 1) ^ 1u, ab, 13);
-                    if (ok) {
-                        units[it % UNITS] = w;
-                        mbar_arrive(u_full + 8 * (it % UNITS));
-                    }
-                }
-                return __shfl_sync(0xFFFFFFFFu, (int)ok, 0) != 0;
-            };
             uint32_t e = 0, nq = 0, it = 0;
-            int u = blockIdx.x;
+            bool ok = true;
             Unit next;
-            if (u < total) next = unit_of<SPLIT>(p, pl, u, lane);
-            else next.index = -1;
-            bool ok = publish(0, next);
-            while (ok && next.index >= 0) {
-                const Unit w = next;
-                u = claim_unit<0>(p, lane);
+            // Makes unit u (or the end of all units) the block's next one.
+            auto publish = [&](int u) {
                 if (u < total) next = unit_of<SPLIT>(p, pl, u, lane);
                 else next.index = -1;
-                ok = publish(++it, next);
-                if (!ok || max(w.n[0], w.n[1]) == 0) continue;
+                if (!(ok = wait_all(u_empty + 8 * (it % UNITS), ((it / UNITS) & 1) ^ 1u, ab, 13))) return false;
                 if (lane == 0) {
-                    // The query tiles wait for the previous unit's last scores; the first
-                    // key and value tiles do not, and go ahead of them.
-                    constexpr uint32_t AHEAD = NST - 2;
-                    const uint32_t e0 = e;
-                    bool have_q = false;
-                    auto load_q = [&]() {
-                        have_q = true;
-                        if (!wait_bar(q_empty, (nq & 1) ^ 1u, ab, 1)) return false;
-                        const uint32_t box = (uint32_t)(p.G * p.TT) * 128u;
+                    units[it % UNITS] = next;
+                    mbar_arrive(u_full + 8 * (it % UNITS));
+                }
+                __syncwarp();
+                ++it;
+                return true;
+            };
+            const uint32_t q_bytes = (uint32_t)(p.G * p.TT) * 128u * (DP / 64);
+            publish(blockIdx.x);
+            while (ok && next.index >= 0) {
+                const Unit w = next;
+                const uint32_t e0 = e;
+                // The query tiles wait for the previous unit's last scores; the first key and
+                // value tiles do not, and go ahead of them.  The next unit is worked out with
+                // those on the way: that takes about 2000 clocks.
+                const uint32_t ahead = nq == 0 ? 1 : NST - 2;
+                bool begun = max(w.n[0], w.n[1]) == 0;
+                auto begin = [&]() {
+                    begun = true;
+                    if (!(ok = wait_all(q_empty, (nq & 1) ^ 1u, ab, 1))) return false;
+                    if (elect_one()) {
                         const int tiles = !SPLIT && w.ntok[1] > 0 ? 2 : 1;
-                        mbar_expect_tx(q_full, box * (DP / 64) * tiles);
+                        mbar_expect_tx(q_full, q_bytes * tiles);
                         for (int t = 0; t < tiles; ++t)
                             for (int d = 0; d < DP / 64; ++d)
                                 tma_load_5d(sQ + t * STAGE + d * BLK, &map_q, d * 64, 0, w.s.q0 + w.tok + t * p.TT, w.hk,
                                             w.slot, q_full);
-                        ++nq;
-                        return true;
-                    };
-                    for_entries<SPLIT>(w, [&](bool is_v, int t, int j) {
-                            if (!have_q && e - e0 == AHEAD && !(ok = load_q())) return false;
-                            const uint32_t st = e % NST;
-                            if (!wait_bar(empty_bar + 8 * st, ((e / NST) & 1) ^ 1u, ab, 2)) {
-                                ok = false;
-                                return false;
-                            }
-                            mbar_expect_tx(full_bar + 8 * st, STAGE);
-                            for (int d = 0; d < DP / 64; ++d)
-                                tma_load_4d(sKV + st * STAGE + d * BLK, is_v ? &map_v : &map_k, d * 64,
-                                            w.s.k0 + (w.jb[t] + j) * KT, w.hk, w.slot, full_bar + 8 * st);
-                            ++e;
-                            return true;
-                        });
-                    if (ok && !have_q) ok = load_q();
-                }
-                ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+                    }
+                    ++nq;
+                    return publish(claim_unit<0>(p, lane));
+                };
+                for_entries<SPLIT>(w, [&](bool is_v, int t, int j) {
+                    if (!begun && e - e0 == ahead && !begin()) return false;
+                    const uint32_t st = e % NST;
+                    if (!(ok = wait_all(empty_bar + 8 * st, ((e / NST) & 1) ^ 1u, ab, 2))) return false;
+                    if (elect_one()) {
+                        mbar_expect_tx(full_bar + 8 * st, STAGE);
+                        for (int d = 0; d < DP / 64; ++d)
+                            tma_load_4d(sKV + st * STAGE + d * BLK, is_v ? &map_v : &map_k, d * 64,
+                                        w.s.k0 + (w.jb[t] + j) * KT, w.hk, w.slot, full_bar + 8 * st);
+                    }
+                    ++e;
+                    return true;
+                });
+                if (max(w.n[0], w.n[1]) == 0) publish(claim_unit<0>(p, lane));
+                else if (ok && !begun) begin();
             }
             if (lane == 0) units_done<0>(p);
             if (lane == 0 && *(volatile int *)abort_flag) {
@@ -489,13 +482,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     // whole round early or late, where the phase parity says nothing.
                     const uint32_t en = e++, st = en % NST;
                     const int jt = w.jb[t] + j;
-                    int got = lane == 0 ? (int)wait_bar(full_bar + 8 * st, (en / NST) & 1, ab, 7) : 0;
-                    got = __shfl_sync(0xFFFFFFFFu, got, 0);
-                    if (!got) {
-                        ok = false;
-                        return false;
-                    }
-                    __syncwarp();
+                    if (!(ok = wait_idle(full_bar + 8 * st, (en / NST) & 1, ab, 7))) return false;
                     if (!is_v || jt < w.guard) {
                         if (lane == 0) mbar_arrive(empty_bar + 8 * st);
                         return true;
