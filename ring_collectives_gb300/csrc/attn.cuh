@@ -143,7 +143,26 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, boo
 // made a 16384-token prompt 11 % slower.)
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Abort &ab, int where)
 {
-    return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, ab, where));
+    uint64_t t0 = 0;
+    for (uint32_t it = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++it) {
+        if ((it & 63u) != 63u) continue;
+        bool over = *(volatile int *)ab.flag != 0;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (!over && now - t0 > ab.timeout_ns) {
+            record_timeout(ab, where);
+            over = true;
+        }
+        if (__any_sync(0xFFFFFFFFu, over)) return false;
+    }
+    return true;
+}
+
+// One arrival by a warp whose lanes are all here (no branch around it).
+__device__ __forceinline__ void arrive_warp(uint32_t bar, int lane)
+{
+    __syncwarp();
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"(lane) : "memory");
 }
 
 // The same for a warp in no hurry: asleep between polls, which would take issue

@@ -236,8 +236,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
         return w->index < 0 ? nullptr : w;
     };
     auto release_unit = [&](uint32_t it) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar.u_empty + 8 * (it % BUNITS));
+        arrive_warp(bar.u_empty + 8 * (it % BUNITS), lane);
     };
 
     if (warp >= 8) {
@@ -423,8 +422,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                         stats[st * 256 + r] = -l2[h];
                         stats[st * 256 + 128 + r] = -dl[h];
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar.stat_full + 8 * st);
+                    arrive_warp(bar.stat_full + 8 * st, lane);
                 }
             }
         }
@@ -500,8 +498,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                         fence_smem_async();
                     }
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar.p_ready);
+                    arrive_warp(bar.p_ready, lane);
                     if (!(ok = wait_all(bar.dp_full, ns & 1, ab, 16))) break;
                     tc_fence_after();
                     tmem_ld32_async(tm + 384 + wg * 64, s[0]);
@@ -524,8 +521,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                         for (int i = 0; i < 64; ++i)
                             if (i < lo || i >= hi) pr[i] = 0.f;
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar.stat_empty + 8 * st);
+                    arrive_warp(bar.stat_empty + 8 * st, lane);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
 #pragma unroll
@@ -534,8 +530,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                     }
                     tmem_wait_st();
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar.ds_ready);
+                    arrive_warp(bar.ds_ready, lane);
                 }
                 if (!ok) break;
                 if (n > 0) {
@@ -629,8 +624,7 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                         fence_smem_async();
                     }
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar.ds_ready);
+                    arrive_warp(bar.ds_ready, lane);
                 }
                 if (!ok) break;
                 if (n > 0) {

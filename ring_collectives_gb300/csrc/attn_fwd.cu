@@ -262,8 +262,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         return w->index < 0 ? nullptr : w;
     };
     auto release_unit = [&](uint32_t it) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(u_empty + 8 * (it % UNITS));
+        arrive_warp(u_empty + 8 * (it % UNITS), lane);
     };
 
     // 384 x 168 registers at launch = 256 x 216 + 128 x 72.  Set inside
@@ -484,7 +483,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     const int jt = w.jb[t] + j;
                     if (!(ok = wait_idle(full_bar + 8 * st, (en / NST) & 1, ab, 7))) return false;
                     if (!is_v || jt < w.guard) {
-                        if (lane == 0) mbar_arrive(empty_bar + 8 * st);
+                        arrive_warp(empty_bar + 8 * st, lane);
                         return true;
                     }
                     const int valid = w.s.kl - jt * KT;    // rows from here on are past the end
@@ -548,8 +547,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 ++ns;
                 tc_fence_after();
                 if (SPLIT && !any) {      // no row of this warp is in use: whatever P holds is not read
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_ready + 8 * t);
+                    arrive_warp(p_ready + 8 * t, lane);
                     continue;
                 }
                 uint32_t v[4][32];
@@ -627,8 +625,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 l += sa + sb;
                 tmem_wait_st();
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + 8 * t);
+                arrive_warp(p_ready + 8 * t, lane);
             }
             if (!ok) break;
             if (n > 0) {
