@@ -506,8 +506,9 @@ _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 def _launch(fn, args: bytes, device, stream) -> None:
     """One call of a struct-argument entry point on `stream` (default: the current one)."""
-    if stream is None and device.index == torch.cuda.current_device():
-        rc = fn(args, torch._C._cuda_getCurrentRawStream(device.index))
+    index = device.index
+    if stream is None and index == torch._C._cuda_getDevice():
+        rc = fn(args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
             rc = fn(args, _stream(stream, device))
@@ -516,7 +517,7 @@ def _launch(fn, args: bytes, device, stream) -> None:
 
 
 def _heads(t: torch.Tensor, name: str, shape=None):
-    if t.dtype != _BF16 or not t.is_cuda:
+    if t.dtype is not _BF16 or not t.is_cuda:
         raise TypeError(f"{name} must be a bf16 CUDA tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
@@ -527,7 +528,7 @@ def _heads(t: torch.Tensor, name: str, shape=None):
 
 
 def _index(t, name: str, n: int) -> int:
-    if t.dtype != _I32 or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not _I32 or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 CUDA tensor of {n} elements")
     return t.data_ptr()
 
@@ -547,21 +548,22 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
     and keys cu_k[b]:cu_k[b+1], or the first used_k[b] of them (a cache); int32 on the
     device.  causal: the last query of a sequence sees all its keys, each earlier one a
     key less.  scale defaults to D ** -0.5.  workspace: as for the ``_ex`` calls."""
-    P, Tq, Hq, D = q.shape
-    kshape = (P, k.size(1), k.size(2), D)
+    P, Tq, Hq, D = qshape = q.shape
+    _, Tk, Hkv, _ = k.shape
+    kshape = (P, Tk, Hkv, D)
     B = cu_q.numel() - 1
     args = _ATTN_ARGS.pack(
-        *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(v, "v", kshape), *_heads(out, "out", q.shape),
+        *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(v, "v", kshape), *_heads(out, "out", qshape),
         *_NO_HEADS * 4, 0 if lse is None else _lse(lse, P, Tq, Hq), _index(cu_q, "cu_q", B + 1),
         _index(cu_k, "cu_k", B + 1), 0 if used_k is None else _index(used_k, "used_k", B),
         *((0, 0) if workspace is None else _ws(workspace)),
-        *_attn_sizes(P, B, Tq, kshape[1], Hq, kshape[2], D, causal, scale))
+        *_attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, causal, scale))
     _launch(load().attn_fwd, args, q.device, stream)
     return out
 
 
 def _lse(lse, P, Tq, Hq):
-    if lse.dtype != _F32 or lse.shape != (P, Tq, Hq) or not lse.is_cuda or not lse.is_contiguous():
+    if lse.dtype is not _F32 or lse.shape != (P, Tq, Hq) or not lse.is_cuda or not lse.is_contiguous():
         raise TypeError(f"lse must be a contiguous float32 CUDA tensor of shape {[P, Tq, Hq]}")
     return lse.data_ptr()
 
@@ -578,8 +580,9 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
     """Gradients of :func:`attn_fwd` (``out`` and ``lse`` are its results): writes dq
     [P, Tq, Hq, D] and dk, dv [P, Tk, Hkv, D], which may be views of one fused gradient
     buffer.  The other arguments are those of the forward call."""
-    P, Tq, Hq, D = q.shape
-    qshape, kshape = q.shape, (P, k.size(1), k.size(2), D)
+    P, Tq, Hq, D = qshape = q.shape
+    _, Tk, Hkv, _ = k.shape
+    kshape = (P, Tk, Hkv, D)
     B = cu_q.numel() - 1
     args = _ATTN_ARGS.pack(
         *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(v, "v", kshape), *_heads(out, "out", qshape),
@@ -587,7 +590,7 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
         *_heads(dv, "dv", kshape), _lse(lse, P, Tq, Hq), _index(cu_q, "cu_q", B + 1),
         _index(cu_k, "cu_k", B + 1), 0 if used_k is None else _index(used_k, "used_k", B),
         *((0, 0) if workspace is None else _ws(workspace)),
-        *_attn_sizes(P, B, Tq, kshape[1], Hq, kshape[2], D, causal, scale))
+        *_attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, causal, scale))
     _launch(load().attn_bwd, args, q.device, stream)
     return dq, dk, dv
 
@@ -602,20 +605,20 @@ _QK_NORM_ARGS = struct.Struct("@24Q9Q7if")
 
 
 def _f32(t, name: str, shape) -> int:
-    if t.dtype != _F32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not _F32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of shape {list(shape)}")
     return t.data_ptr()
 
 
 def _qk_norm(q, k, gamma_q, gamma_k, cos, sin, pos, layout, eps, q_out, k_out, grads, workspace):
-    P, T, Hq, D = q.shape
-    kshape = (P, T, k.size(2), D)
-    table = (cos.size(0), D // 2)
-    heads = _NO_HEADS * 2 if grads is None else _heads(grads[0], "dq", q.shape) + _heads(grads[1], "dk", kshape)
+    P, T, Hq, D = qshape = q.shape
+    kshape = (P, T, k.shape[2], D)
+    table = (cos.shape[0], D // 2)
+    heads = _NO_HEADS * 2 if grads is None else _heads(grads[0], "dq", qshape) + _heads(grads[1], "dk", kshape)
     dg = (0, 0) if grads is None else (_f32(grads[2], "dgamma_q", (P, D)), _f32(grads[3], "dgamma_k", (P, D)))
     names = ("q_out", "k_out") if grads is None else ("dq_out", "dk_out")
     return _QK_NORM_ARGS.pack(
-        *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(q_out, names[0], q.shape), *_heads(k_out, names[1], kshape),
+        *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(q_out, names[0], qshape), *_heads(k_out, names[1], kshape),
         *heads, _f32(gamma_q, "gamma_q", (D,)), _f32(gamma_k, "gamma_k", (D,)), _f32(cos, "cos", table),
         _f32(sin, "sin", table), _index(pos, "pos", T), *dg, *((0, 0) if workspace is None else _ws(workspace)),
         P, T, Hq, kshape[2], D, table[0], layout, eps)

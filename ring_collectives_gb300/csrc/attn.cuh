@@ -328,6 +328,12 @@ __device__ __forceinline__ long long warp_sum(long long v)
 
 constexpr int kNoSplit = 1 << 28;          // key tiles of a part when keys are not split
 
+// Key ranges up to this many tiles are never split: the join's launch, about 4 us of
+// host time, costs more than it gives.  (Asked on the host of what the tensors
+// could hold and on the device of what they hold, so the room in a cache
+// changes no result.)
+__host__ __device__ constexpr int whole_tiles(bool split) { return split ? 6 : 8; }
+
 // Units that a split adds at most: parts are no smaller than 4 rounds of units need.
 constexpr long long split_units(int sms) { return 4ll * sms; }
 

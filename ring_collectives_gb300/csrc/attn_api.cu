@@ -124,8 +124,7 @@ static FwdPlan plan_fwd(Params &p, int sms)
     p.TPU = f.split ? p.TT : 2 * p.TT;
     const long long HP = (long long)p.P * p.Hkv, tiles = (p.Tq + p.TPU - 1) / p.TPU;
     p.may_split = f.split ? (tiles > p.B ? tiles : p.B) * HP < 4ll * sms : tiles * HP < 2ll * sms;
-    // a range of at most the smallest part never splits
-    if ((p.Tk + KT - 1) / KT <= (f.split ? 2 : 4)) p.may_split = 0;
+    if ((p.Tk + KT - 1) / KT <= whole_tiles(f.split)) p.may_split = 0;
     p.part_rows = p.G * (p.TT < p.Tq ? p.TT : p.Tq);
     if (p.may_split) {
         long long n0 = p.Tq / p.TPU + p.B;     // row tiles (pairs), at most

@@ -94,7 +94,7 @@ __device__ Plan make_plan(const Params &p, int lane)
         const int rounds = k < 3 ? 1 : k < 5 ? 2 : k - 2, slack = k == 1 ? 2 : k == 2 ? 5 : k == 4 ? 3 : 0;
         const long long per = (long long)p.sms * (SPLIT ? 2 : 1) * rounds * 16;
         const long long c = max((work * (16 + slack) + per - 1) / per, SPLIT ? 2ll : 4ll);
-        const int cs = c >= most || k == 7 ? most : (int)c;
+        const int cs = c >= most || k == 7 || most <= whole_tiles(SPLIT) ? most : (int)c;
         int units = 0;
         for (int b = lane >> 3; b < p.B; b += 4) {
             const Seq s = seq_of(p, b);
