@@ -730,9 +730,12 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
     Plan pl;
     pl.cs = (int)ld_relaxed_gpu(&p.hdr->pad[6]);
     const int HP = p.P * p.Hkv;
-    const long long rows = (long long)p.P * p.Tq * p.Hq;
-    for (long long row = (long long)blockIdx.x * ROWS + warp / W; row < rows; row += (long long)gridDim.x * ROWS) {
-        const int head = (int)(row % p.Hq), qi = (int)(row / p.Hq % p.Tq), slot = (int)(row / p.Hq / p.Tq);
+    // Split launches have few rows (well below 2^31), so 32-bit divisions do; with 64-bit ones
+    // they were most of the kernel.
+    const unsigned rows = (unsigned)p.P * p.Tq * p.Hq;
+    for (unsigned row = blockIdx.x * ROWS + warp / W; row < rows; row += gridDim.x * ROWS) {
+        const unsigned tok = row / p.Hq;
+        const int head = (int)(row - tok * p.Hq), slot = (int)(tok / p.Tq), qi = (int)(tok - slot * p.Tq);
         // the sequence of token qi, and the units before it
         int units = 0, b_hit = -1;
         for (int b0 = 0; b0 < p.B && b_hit < 0; b0 += 32) {
@@ -769,16 +772,24 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
         const float base = m == -INFINITY ? 0.f : m;
         constexpr int E = DP / 32;                         // elements of a lane, next to each other
         float acc[E] = {}, sum = 0.f;
-#pragma unroll 4
-        for (int c = warp % W; c < np; c += W) {
-            const size_t sl = slot_of(c);
-            const float wgt = expf(p.part_lse[sl] - base);
-            sum += wgt;
-            float x[E];
-            if (E == 4) *(float4 *)x = *(const float4 *)(p.part_o + sl * DP + lane * E);
-            else *(float2 *)x = *(const float2 *)(p.part_o + sl * DP + lane * E);
+        for (int c0 = warp % W; c0 < np; c0 += 4 * W) {    // four parts' loads at a time
+            float x[4][E], wgt[4];
 #pragma unroll
-            for (int d = 0; d < E; ++d) acc[d] = fmaf(wgt, x[d], acc[d]);
+            for (int k = 0; k < 4; ++k) {
+                const int c = c0 + k * W;
+                const size_t sl = slot_of(c < np ? c : c0);
+                wgt[k] = c < np ? p.part_lse[sl] : -INFINITY;
+                if (E == 4) *(float4 *)x[k] = *(const float4 *)(p.part_o + sl * DP + lane * E);
+                else *(float2 *)x[k] = *(const float2 *)(p.part_o + sl * DP + lane * E);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c0 + k * W < np) {
+                    wgt[k] = expf(wgt[k] - base);
+                    sum += wgt[k];
+#pragma unroll
+                    for (int d = 0; d < E; ++d) acc[d] = fmaf(wgt[k], x[k][d], acc[d]);
+                }
         }
         char *const dst = p.out.base + slot * p.out.slot + (size_t)qi * p.out.token + head * p.out.head;
         if (WIDE) {
