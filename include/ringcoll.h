@@ -1,6 +1,7 @@
 /*
  * ringcoll.h -- C ABI of libringcoll.so: ring collectives over P logical
- * ranks that live in one GPU's HBM.
+ * ranks that live in one GPU's HBM, the two collective matmuls, and the
+ * attention that runs between them.
  *
  * Model.  The P ranks are P symmetric slots of device memory: slot r starts
  * at base + r*stride bytes, so the symmetric-memory lookup symm_at(ptr, r) of
@@ -416,6 +417,10 @@ typedef struct {
  * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, B >= 1, Hq a
  * multiple of Hkv with Hq/Hkv <= 128, D a multiple of 8 up to 128,
  * 0 < scale < inf, layouts as for rc_heads, reserved 0.  Tq = 0 does nothing.
+ * The library's own workspace holds partial results here (grown on demand like
+ * the signal words: make the first call, at the largest sizes, before
+ * capturing).  One device wait may last as long as a row tile's pass over its
+ * keys (about 12 ns a key), so ring_set_timeout_ms has to allow for that.
  */
 int attn_fwd(const rc_attn_args *args, void *stream);
 

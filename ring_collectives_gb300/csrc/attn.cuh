@@ -328,11 +328,12 @@ __device__ __forceinline__ long long warp_sum(long long v)
 
 constexpr int kNoSplit = 1 << 28;          // key tiles of a part when keys are not split
 
-// Key ranges up to this many tiles are never split: the join's launch, about 4 us of
-// host time, costs more than it gives.  (Asked on the host of what the tensors
-// could hold and on the device of what they hold, so the room in a cache
-// changes no result.)
-__host__ __device__ constexpr int whole_tiles(bool split) { return split ? 6 : 8; }
+// Key ranges up to this many tiles are never split.  Measured in graphs, 8 heads,
+// split / whole: a token on 8 tiles 16.0 / 13.9 us, on 12 tiles 16.0 / 16.7 us; 64
+// tokens on 8 tiles 21.6 / 20.1, on 12 tiles 21.5 / 25.4 us; and the join's launch is
+// about 4 us of host time.  (Asked on the host of what the tensors could hold and
+// on the device of what they hold, so the room in a cache changes no result.)
+constexpr int kWholeTiles = 10;
 
 // Units that a split adds at most: parts are no smaller than 4 rounds of units need.
 constexpr long long split_units(int sms) { return 4ll * sms; }

@@ -111,27 +111,30 @@ static void fill(Params &p, const rc_attn_args &a)
 // The form of a forward launch and the bytes of its partial results.
 struct FwdPlan {
     bool split;
-    size_t units, bytes;
+    size_t units, rows, bytes;
 };
 
 // SPLIT when the queries of a sequence fill at most one row tile on average.
-// Measured on GB300: see the table in attn_fwd.cu.
+// Measured, SPLIT / PAIR: 1 sequence x 8 heads on 16384 keys, 4 rows 20.6 / 22.6 us,
+// 128 rows 27.1 / 28.6 us, 160 rows 33.9 / 29.1 us; 64 sequences x 8 heads on 2048
+// keys, 4 rows 102 / 109 us, 160 rows 145 / 124 us.
 static FwdPlan plan_fwd(Params &p, int sms)
 {
     FwdPlan f{};
     f.split = (long long)p.Tq * p.G <= (long long)KT * p.B;
     p.sms = sms;
     p.TPU = f.split ? p.TT : 2 * p.TT;
-    const long long HP = (long long)p.P * p.Hkv, tiles = (p.Tq + p.TPU - 1) / p.TPU;
-    p.may_split = f.split ? (tiles > p.B ? tiles : p.B) * HP < 4ll * sms : tiles * HP < 2ll * sms;
-    if ((p.Tk + KT - 1) / KT <= whole_tiles(f.split)) p.may_split = 0;
+    const long long HP = (long long)p.P * p.Hkv, rows = (p.Tq + p.TPU - 1) / p.TPU;
+    p.may_split = (rows > p.B ? rows : p.B) * HP < (f.split ? 4ll : 2ll) * sms;   // units, about
+    if ((p.Tk + KT - 1) / KT <= kWholeTiles) p.may_split = 0;
     p.part_rows = p.G * (p.TT < p.Tq ? p.TT : p.Tq);
     if (p.may_split) {
         long long n0 = p.Tq / p.TPU + p.B;     // row tiles (pairs), at most
         if (n0 > p.Tq) n0 = p.Tq;
         f.units = (size_t)(n0 * HP + split_units(sms));
         const size_t DP = p.D <= 64 ? 64 : 128;
-        f.bytes = 2 * f.units * (size_t)p.part_rows * (DP + 1) * 4;
+        f.rows = (f.split ? 1 : 2) * f.units * (size_t)p.part_rows;
+        f.bytes = f.rows * (DP + 1) * 4;
     }
     return f;
 }
@@ -179,7 +182,7 @@ static int run_fwd(const rc_attn_args *args, void *stream)
     char *scratch = nullptr;
     if ((rc_ = take_workspace(a, f.bytes, p, &scratch))) return rc_;
     p.part_o = (float *)scratch;
-    p.part_lse = (float *)(scratch + 2 * f.units * (size_t)p.part_rows * (p.D <= 64 ? 64 : 128) * 4);
+    p.part_lse = (float *)(scratch + f.rows * (p.D <= 64 ? 64 : 128) * 4);
     p.out = strided(a.out);
     p.out32 = !(((uintptr_t)a.out.base | a.out.slot | a.out.token | a.out.head) & 31u) && a.D % 16 == 0;
     p.v = (const char *)a.v.base;

@@ -27,9 +27,11 @@
 // Two forms.  PAIR: the two row tiles are 256 consecutive rows and share every
 // key tile.  SPLIT (few rows per sequence, single tokens above all): both are
 // the same rows, over two halves of a key range, so the loads of one hide the
-// latency of the other and the kernel runs at the rate of the key cache.
-// When there are too few units to fill the GPU, key ranges are split further
-// and k_attn_join adds the partial results in a fixed order.
+// latency of the other and the kernel runs at the rate of the key cache.  Warps
+// w and w + 4 then hold the same rows in the same TMEM lanes: they exchange
+// maxima and sums and each joins half of the columns.
+// When there are too few units to fill the GPU, key ranges are split over
+// units and k_attn_join adds the partial results in a fixed order.
 #include <mutex>
 
 #include "attn.cuh"
@@ -44,12 +46,14 @@ struct FwdCfg {
     static constexpr int KV_STAGE = KT * DP * 2;
     static constexpr int NQ = SPLIT ? 1 : 2;
     static constexpr int STAGES = DP == 128 ? (SPLIT ? 6 : 5) : 8;
-    static constexpr int SMEM = (NQ + STAGES) * KV_STAGE + 1024 + 1024;
+    static constexpr int CTL = 3072;      // barriers and units; maxima and sums of the halves.  With 32 KiB
+                                          // tiles this is exactly the 227 KiB of a block
+    static constexpr int SMEM = (NQ + STAGES) * KV_STAGE + CTL;
 };
 
 // The split of this launch's keys, the same in every warp and kernel of it.
 struct Plan {
-    int cs;        // key tiles per part (a huge number: no split)
+    int cs;        // key tiles per part (kNoSplit: no key range is split)
     int units;     // units of one key head
 };
 
@@ -58,24 +62,16 @@ __device__ __forceinline__ int parts_of(int kt, int cs)
     return max(1, (kt + cs - 1) / cs);
 }
 
-template <bool SPLIT>
-__device__ __forceinline__ int units_per_tile(int kt, int cs)
-{
-    const int np = parts_of(kt, cs);
-    return SPLIT ? (np + 1) / 2 : np;
-}
-
 // How far keys are split (p.may_split: the host found too few unsplit units to
-// fill the GPU and made room for partial results).  Eight part sizes are tried
-// -- 1 to 4 rounds of units over the SMs, some with slack, and no split -- by
-// eight lanes each, a quarter of the sequences to a lane of them, and the one with
-// the least rounds x (key tiles of a unit + the cost of a unit's ends, about 3
-// tiles; 2 in the SPLIT form) is taken.  Measured on GB300 against parts for a
-// fixed 3 (SPLIT: 4) units per SM: token 1 x 32768 keys 45 -> 34 us, prompt pieces
-// 60 -> 46 us.
+// fill the GPU and made room for partial results).  Each lane tries a part
+// size -- 1 to 4 rounds of units over the SMs, with 0 to 7 sixteenths of slack,
+// and in the last lane no split -- and the one with the least rounds x (tiles
+// that a unit's row tiles run through + the cost of its ends), in tiles, plus
+// the join's, is taken.
 template <bool SPLIT>
 __device__ Plan make_plan(const Params &p, int lane)
 {
+    constexpr int kEnds = SPLIT ? 2 : 3, kJoin = 4;
     const int HP = p.P * p.Hkv;
     Plan pl;
     pl.cs = kNoSplit;
@@ -90,22 +86,25 @@ __device__ Plan make_plan(const Params &p, int lane)
         }
         work = warp_sum(work) * HP;
         most = max(1, __reduce_max_sync(0xFFFFFFFFu, most));
-        const int k = lane & 7;                                    // rounds 1 1 1 2 2 3 4, slack 0 2 5 0 3 0 0 sixteenths
-        const int rounds = k < 3 ? 1 : k < 5 ? 2 : k - 2, slack = k == 1 ? 2 : k == 2 ? 5 : k == 4 ? 3 : 0;
-        const long long per = (long long)p.sms * (SPLIT ? 2 : 1) * rounds * 16;
-        const long long c = max((work * (16 + slack) + per - 1) / per, SPLIT ? 2ll : 4ll);
-        const int cs = c >= most || k == 7 || most <= whole_tiles(SPLIT) ? most : (int)c;
+        const long long per = (long long)p.sms * (1 + (lane >> 3)) * 16;
+        const long long c = max((work * (16 + (lane & 7)) + per - 1) / per, 4ll);
+        const int cs = c >= most || lane == 31 || most <= kWholeTiles ? most : (int)c;
         int units = 0;
-        for (int b = lane >> 3; b < p.B; b += 4) {
-            const Seq s = seq_of(p, b);
-            units += (s.ql + p.TPU - 1) / p.TPU * units_per_tile<SPLIT>((s.kl + KT - 1) / KT, cs);
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int nt = 0, kt = 0;
+            if (b0 + lane < p.B) {
+                const Seq s = seq_of(p, b0 + lane);
+                nt = (s.ql + p.TPU - 1) / p.TPU;
+                kt = (s.kl + KT - 1) / KT;
+            }
+            for (int i = 0; i < min(32, p.B - b0); ++i)
+                units += __shfl_sync(0xFFFFFFFFu, nt, i) * parts_of(__shfl_sync(0xFFFFFFFFu, kt, i), cs);
         }
-        units += __shfl_xor_sync(0xFFFFFFFFu, units, 8);
-        units += __shfl_xor_sync(0xFFFFFFFFu, units, 16);
-        const long long cost = ((long long)units * HP + p.sms - 1) / p.sms * (cs + (SPLIT ? 2 : 3));
+        const long long cost = ((long long)units * HP + p.sms - 1) / p.sms * ((SPLIT ? (cs + 1) / 2 : cs) + kEnds) +
+                               (cs < most ? kJoin : 0);
         const unsigned mine = (unsigned)min(cost, 0x7FFFFFFFll), least = __reduce_min_sync(0xFFFFFFFFu, mine);
-        const int pick = __ffs(__ballot_sync(0xFFFFFFFFu, mine == least)) - 1;
-        pl.cs = __shfl_sync(0xFFFFFFFFu, cs, pick);
+        const int pick = 31 - __clz(__ballot_sync(0xFFFFFFFFu, mine == least));   // the largest of the best
+        pl.cs = __shfl_sync(0xFFFFFFFFu, cs < most ? cs : kNoSplit, pick);
         pl.units = __shfl_sync(0xFFFFFFFFu, units, pick);
         return pl;
     }
@@ -142,25 +141,29 @@ __device__ Unit unit_of(const Params &p, const Plan &pl, int u, int lane)
     locate(p.B, x, lane,
            [&](int bb) {
                const Seq s = seq_of(p, bb);
-               return ((s.ql + p.TPU - 1) / p.TPU) * units_per_tile<SPLIT>((s.kl + KT - 1) / KT, pl.cs);
+               return ((s.ql + p.TPU - 1) / p.TPU) * parts_of((s.kl + KT - 1) / KT, pl.cs);
            },
            b, local);
     w.s = seq_of(p, b);
     const int kt = (w.s.kl + KT - 1) / KT, cs = pl.cs;
-    const int upt = units_per_tile<SPLIT>(kt, cs), nt = (w.s.ql + p.TPU - 1) / p.TPU;
-    const int tile = nt - 1 - local / upt, c = local % upt;   // the tiles that see most keys first
     w.nparts = parts_of(kt, cs);
+    const int nt = (w.s.ql + p.TPU - 1) / p.TPU;
+    const int tile = nt - 1 - local / w.nparts, c = local % w.nparts;   // the tiles that see most keys first
     w.tok = tile * p.TPU;
     const int left = w.s.ql - w.tok;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int first = SPLIT ? w.tok : w.tok + t * p.TT;
         w.ntok[t] = SPLIT ? min(left, p.TT) : min(max(left - t * p.TT, 0), p.TT);
-        const int part = SPLIT ? 2 * c + t : c;
         const int see = w.ntok[t] > 0 ? seen(p, w.s, first + w.ntok[t] - 1) : 0;
-        const int je = min((see + KT - 1) / KT, cs >= kNoSplit ? kNoSplit : (part + 1) * cs);
-        w.jb[t] = part * (cs >= kNoSplit ? 0 : cs);
-        w.n[t] = part < w.nparts ? max(0, je - w.jb[t]) : 0;
+        const int je = min((see + KT - 1) / KT, cs >= kNoSplit ? kNoSplit : (c + 1) * cs);
+        w.jb[t] = c * (cs >= kNoSplit ? 0 : cs);
+        w.n[t] = max(0, je - w.jb[t]);
+    }
+    if (SPLIT) {
+        w.n[0] = (w.n[0] + 1) / 2;
+        w.n[1] -= w.n[0];
+        w.jb[1] += w.n[0];
     }
     w.guard = seen(p, w.s, w.tok) / KT;
     w.poison = 0;
@@ -202,10 +205,8 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     constexpr int DP = tile_cols(KS);
     using C = FwdCfg<DP, SPLIT>;
     constexpr int NST = C::STAGES, STAGE = C::KV_STAGE;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-    uint8_t *const gbase = smem_raw + (base - raw);
-    const uint32_t sQ = base, sKV = base + C::NQ * STAGE;
+    extern __shared__ __align__(1024) uint8_t gbase[];   // swizzled tiles start on 1024 bytes
+    const uint32_t base = smem_u32(gbase), sQ = base, sKV = base + C::NQ * STAGE;
     uint8_t *const gKV = gbase + C::NQ * STAGE;
     uint8_t *const ctl = gKV + NST * STAGE;
     const uint32_t bars = smem_u32(ctl);
@@ -215,8 +216,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
     uint32_t *const tmem_slot = (uint32_t *)(ctl + 24 * NST + 72);
     int *const abort_flag = (int *)(ctl + 24 * NST + 76);
     const uint32_t u_full = q_full + 80, u_empty = u_full + 8 * UNITS;
-    Unit *const units = (Unit *)(ctl + 24 * NST + 80 + 16 * UNITS);
-    static_assert(24 * NST + 80 + 16 * UNITS + UNITS * sizeof(Unit) <= 1024, "control area");
+    const uint32_t swap_bar = u_empty + 8 * UNITS, joined_bar = swap_bar + 32;   // SPLIT: of warps w and w + 4
+    Unit *const units = (Unit *)(ctl + 24 * NST + 80 + 16 * UNITS + 64);
+    static_assert(24 * NST + 80 + 16 * UNITS + 64 + UNITS * sizeof(Unit) <= 1024, "control area");
+    float2 *const half_stats = (float2 *)(ctl + 1024);                           // SPLIT: [half][row] maximum, sum
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -231,6 +234,10 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             mbar_init(s_full + 8 * t, 1);
             mbar_init(p_ready + 8 * t, 4);
             mbar_init(o_full + 8 * t, 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(swap_bar + 8 * i, 2);
+            mbar_init(joined_bar + 8 * i, 2);
         }
         mbar_init(drain_bar, 1);
         for (int i = 0; i < UNITS; ++i) {
@@ -488,7 +495,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     }
                     const int valid = w.s.kl - jt * KT;    // rows from here on are past the end
                     bool found = false;
-    #pragma unroll 4
+#pragma unroll 4
                     for (int i = lane; i < 64 * 8 * (DP / 64); i += 32) {
                         const int row = g * 64 + ((i >> 3) & 63), blk = i >> 9;
                         uint4 *const a = (uint4 *)(gKV + st * STAGE + blk * BLK + row * 128 + (i & 7) * 16);
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                         }
                         uint32_t x[4] = {a->x, a->y, a->z, a->w};
                         bool bad = false;
-    #pragma unroll
+#pragma unroll
                         for (int h = 0; h < 4; ++h) {
                             if (nonfinite_bf16(x[h])) x[h] &= 0xFFFF0000u, bad = true;
                             if (nonfinite_bf16(x[h] >> 16)) x[h] &= 0x0000FFFFu, bad = true;
@@ -527,7 +534,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lane_off + t * KT, tO = tmem + lane_off + 256 + t * KT;
         const float c = p.scale * kLog2e;
-        uint32_t ns = 0, no = 0;
+        uint32_t ns = 0, no[2] = {0, 0}, nswap = 0;
         bool ok = true;
         const Unit *wp;
         for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
@@ -628,36 +635,71 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 arrive_warp(p_ready + 8 * t, lane);
             }
             if (!ok) break;
-            if (n > 0) {
-                if (!(ok = wait_all(o_full + 8 * t, no & 1, ab, 11))) break;
-                ++no;
-                tc_fence_after();
+            // The accumulators: this row tile's, or in the SPLIT form those of both halves.
+            float mcs[2] = {mc, mc}, ls[2] = {l, 0.f};
+            if (SPLIT && any) {
+                const uint32_t pair = 8 * (warp & 3);
+                half_stats[t * KT + r] = make_float2(mc, l);
+                arrive_warp(swap_bar + pair, lane);
+                if (!(ok = wait_all(swap_bar + pair, nswap & 1, ab, 14))) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float2 x = half_stats[h * KT + r];
+                    mcs[h] = x.x;
+                    ls[h] = x.y;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!SPLIT && h != t) continue;
+                if (w.n[h] > 0) {
+                    if (!(SPLIT && !any) && !(ok = wait_all(o_full + 8 * h, no[h] & 1, ab, 11))) break;
+                    ++no[h];
+                }
+            }
+            if (!ok) break;
+            if (SPLIT && !any) continue;                               // nor in the other half's warp
+            tc_fence_after();
+            float fac[2];
+            if (SPLIT) {
+                // a half without keys for this row has the sum 0, whatever its maximum
+                mc = ls[0] == 0.f ? mcs[1] : ls[1] == 0.f ? mcs[0] : fmaxf(mcs[0], mcs[1]);
+                fac[0] = ls[0] == 0.f ? 0.f : ex2(mcs[0] - mc);
+                fac[1] = ls[1] == 0.f ? 0.f : ex2(mcs[1] - mc);
+                l = ls[0] * fac[0] + ls[1] * fac[1];
+            } else {
+                fac[0] = 1.f;
             }
             const int head = w.hk * p.G + r % p.G;
             const bool final_ = w.nparts == 1;
-            if (SPLIT && final_ && t == 1) continue;                  // one part: row tile 0 has it
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t qi = (size_t)w.s.q0 + tok;
             const bool add_back = *(volatile const int *)&w.poison != 0;
             char *const dst = p.out.base + w.slot * p.out.slot + qi * p.out.token + head * p.out.head;
-            float *const part = p.part_o + ((size_t)(2 * w.index + t) * p.part_rows + r) * DP;
+            const size_t part_row = (size_t)(SPLIT ? w.index : 2 * w.index + t) * p.part_rows + r;
+            float *const part = p.part_o + part_row * DP;
+            const int end = SPLIT ? w.jb[1] + w.n[1] : w.jb[t] + n;    // of the unit's key tiles
+            constexpr int QN = SPLIT ? DP / 64 : DP / 32;              // blocks of 32 columns of a warp
 #pragma unroll
-            for (int q = 0; q < DP / 32; ++q) {
-                uint32_t o[32];
-                if (n > 0) {
-                    tmem_ld32(tO + q * 32, o);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0u;
-                }
-                if (!valid) continue;
+            for (int q_ = 0; q_ < QN; ++q_) {
+                const int q = SPLIT ? t * QN + q_ : q_;
                 float f[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
+                for (int i = 0; i < 32; ++i) f[i] = 0.f;
+#pragma unroll
+                for (int h = 0; h < (SPLIT ? 2 : 1); ++h) {
+                    if ((SPLIT ? w.n[h] : n) == 0) continue;
+                    const float fh = fac[h] * inv;
+                    uint32_t o[32];
+                    tmem_ld32((SPLIT ? tmem + lane_off + 256 + h * KT : tO) + q * 32, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) f[i] = fmaf(__uint_as_float(o[i]), fh, f[i]);
+                }
+                if (!valid) continue;
                 if (add_back) {
                     // non-finite values that this row does see, taken out by the guard
-                    const int k1 = min(lim, (w.jb[t] + n) * KT);
-                    for (int k = max(w.guard, w.jb[t]) * KT; k < k1; ++k) {
+                    const int k1 = min(lim, end * KT);
+                    for (int k = max(w.guard, w.jb[SPLIT ? 0 : t]) * KT; k < k1; ++k) {
                         const uint16_t *vr = (const uint16_t *)(p.v + w.slot * p.v_slot +
                                                                 ((size_t)w.s.k0 + k) * p.v_token + w.hk * p.v_head);
 #pragma unroll
@@ -693,10 +735,19 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                                                   __float_as_uint(f[i + 6]), __float_as_uint(f[i + 7])));
                 }
             }
-            if (valid) {
+            if (SPLIT) {
+                // the accumulators are overwritten when this warp and its partner hand over new weights
+                const uint32_t pair = 8 * (warp & 3);
+                tc_fence_before();
+                arrive_warp(joined_bar + pair, lane);
+                if (!(ok = wait_all(joined_bar + pair, nswap & 1, ab, 15))) break;
+                tc_fence_after();
+                ++nswap;
+            }
+            if (valid && !(SPLIT && t == 1)) {
                 const float lse = l == 0.f ? -INFINITY : (mc + log2f(l)) * kLn2;
                 if (!final_)
-                    p.part_lse[(size_t)(2 * w.index + t) * p.part_rows + r] = lse;
+                    p.part_lse[part_row] = lse;
                 else if (p.lse)
                     p.lse[((size_t)w.slot * p.Tq + qi) * p.Hq + head] = lse;
             }
@@ -729,6 +780,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
     asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written, and their size
     Plan pl;
     pl.cs = (int)ld_relaxed_gpu(&p.hdr->pad[6]);
+    if (pl.cs >= kNoSplit) return;
     const int HP = p.P * p.Hkv;
     // Split launches have few rows (well below 2^31), so 32-bit divisions do; with 64-bit ones
     // they were most of the kernel.
@@ -744,7 +796,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
             int n = 0;
             if (b < p.B) {
                 sb = seq_of(p, b);
-                n = ((sb.ql + p.TPU - 1) / p.TPU) * units_per_tile<SPLIT>((sb.kl + KT - 1) / KT, pl.cs);
+                n = ((sb.ql + p.TPU - 1) / p.TPU) * parts_of((sb.kl + KT - 1) / KT, pl.cs);
             }
             const int inc = warp_incl_scan(n, lane);
             const unsigned hit = __ballot_sync(0xFFFFFFFFu, b < p.B && qi >= sb.q0 && qi < sb.q0 + sb.ql);
@@ -755,15 +807,15 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) k_attn_join(const Params p)
         if (b_hit < 0) continue;
         const Seq s = seq_of(p, b_hit);
         const int kt = (s.kl + KT - 1) / KT;
-        const int np = parts_of(kt, pl.cs), upt = units_per_tile<SPLIT>(kt, pl.cs);
+        const int np = parts_of(kt, pl.cs);
         if (np == 1) continue;
         const int i = qi - s.q0, tile = i / p.TPU, nt = (s.ql + p.TPU - 1) / p.TPU;
         const int in_tile = i - tile * p.TPU, t_pair = in_tile / p.TT;
         const int r = (in_tile % p.TT) * p.G + head % p.G;
-        const int x0 = units + (nt - 1 - tile) * upt, hp = slot * p.Hkv + head / p.G;
+        const int x0 = units + (nt - 1 - tile) * np, hp = slot * p.Hkv + head / p.G;
         auto slot_of = [&](int c) {
-            const size_t u = (size_t)(x0 + (SPLIT ? c >> 1 : c)) * HP + hp;
-            return (2 * u + (SPLIT ? c & 1 : t_pair)) * p.part_rows + r;
+            const size_t u = (size_t)(x0 + c) * HP + hp;
+            return (SPLIT ? u : 2 * u + t_pair) * p.part_rows + r;
         };
         float m = -INFINITY;
         for (int c = lane; c < np; c += 32) m = fmaxf(m, p.part_lse[slot_of(c)]);
