@@ -16,8 +16,9 @@
 //   warps 0-3, 4-7  softmax of row tile 0 / 1: one thread a row, so maxima and
 //                   sums need no shuffles; S arrives in TMEM, P goes back to
 //                   TMEM over S and is the A operand of the second product
-//   warp 8          TMA loads: query tiles, then key and value tiles through
-//                   one ring of stages in the order the MMAs consume them
+//   warp 8          units (claimed as blocks come free) and TMA loads: query
+//                   tiles, then key and value tiles through one ring of stages
+//                   in the order the MMAs consume them
 //   warp 9          MMA issue: S_t = Q_t K^T, O_t += P_t V for the two tiles in
 //                   turn, so one tile's softmax runs under the other's MMAs
 //   warps 10-11     guard: in tiles that some row does not see whole, clears
@@ -32,6 +33,15 @@
 // maxima and sums and each joins half of the columns.
 // When there are too few units to fill the GPU, key ranges are split over
 // units and k_attn_join adds the partial results in a fixed order.
+//
+// Bounds.  PAIR: 4 products of 128 x 128 x 128 a pair of tiles are 2048 clocks of
+// tensor cores; the chain scores - softmax - weights of one tile, half hidden by
+// the other's, makes it about 2800.  16384 tokens, 32 heads of 128: 1.28 ms,
+// 1716 TFLOP/s (called back to back, at the power limit, 1.37 ms).  A unit's
+// ends cost about 3 tiles, so six prompts of 1 to 4097 tokens, 32 heads: 231 us, 1238
+// TFLOP/s.  SPLIT: memory; 64 tokens on caches of 200 to 7982 keys, 8 key heads:
+// 183 us, 5.8 TB/s with the join; one token on 32768 keys of 8 heads: 35 us, 3.9
+// TB/s, because the first loads and the join's launch do not overlap anything.
 #include <mutex>
 
 #include "attn.cuh"
