@@ -43,7 +43,7 @@ struct Params {
     int P, B, Tq, Tk, Hq, Hkv, G, D, causal;
     int TT;                                // tokens per 128-row tile
     int TPU;                               // query tokens per work unit
-    int sms, part_rows;
+    int sms, part_rows, max_units;         // max_units: units that partial results have room for
     int out32;                             // 1: rows of out are whole 32-byte vectors
     int may_split;                         // 1: key ranges may be split (part_o / part_lse are there)
     float scale;

@@ -132,6 +132,7 @@ static FwdPlan plan_fwd(Params &p, int sms)
         long long n0 = p.Tq / p.TPU + p.B;     // row tiles (pairs), at most
         if (n0 > p.Tq) n0 = p.Tq;
         f.units = (size_t)(n0 * HP + split_units(sms));
+        p.max_units = (int)f.units;
         const size_t DP = p.D <= 64 ? 64 : 128;
         f.rows = (f.split ? 1 : 2) * f.units * (size_t)p.part_rows;
         f.bytes = f.rows * (DP + 1) * 4;

@@ -116,7 +116,9 @@ __device__ Plan make_plan(const Params &p, int lane)
         const long long n = (long long)units * HP, t = (SPLIT ? (cs + 1) / 2 : cs) + kEnds;
         const long long cost = min((n + p.sms - 1) / p.sms * t, ((SPLIT ? work / 2 : work) + n * kEnds) / p.sms + t) +
                                (cs < most ? kJoin : 0);
-        const unsigned mine = (unsigned)min(cost, 0x7FFFFFFFll), least = __reduce_min_sync(0xFFFFFFFFu, mine);
+        // More units than there is room for: only where offsets decrease, so that sequences overlap.
+        const bool fits = cs == most || n <= p.max_units;
+        const unsigned mine = fits ? (unsigned)min(cost, 0x7FFFFFFFll) : 0xFFFFFFFFu, least = __reduce_min_sync(0xFFFFFFFFu, mine);
         const int pick = 31 - __clz(__ballot_sync(0xFFFFFFFFu, mine == least));   // the largest of the best
         pl.cs = __shfl_sync(0xFFFFFFFFu, cs < most ? cs : kNoSplit, pick);
         pl.units = __shfl_sync(0xFFFFFFFFu, units, pick);

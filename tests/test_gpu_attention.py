@@ -290,6 +290,24 @@ def test_offsets_outside_the_tensors_are_clamped():
     assert torch.equal(a, out) and torch.equal(b, lse)
 
 
+@pytest.mark.parametrize("B, tokens, keys", [(599, 1, 16500), (9, 128, 9000), (75, 5, 4097)])
+def test_decreasing_offsets_stay_inside_the_workspace(B, tokens, keys):
+    """Offsets that go back and forth give every other sequence all tokens: more units than
+    disjoint sequences could have.  The call writes nothing past its workspace, and equal
+    sequences write equal rows."""
+    p = problem([tokens], [keys], P=1, Hq=2, Hkv=1, D=64, seed=23)
+    want, wlse, ob, lb = oa.attn_fwd(f64(p["q"]), f64(p["k"]), f64(p["v"]), seqs(p))
+    size = rc.attn_fwd_workspace_bytes(1, B, tokens, keys, 2, 1, 64)
+    space = torch.full((size + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    space[:size] = 0
+    back = dict(p, cu_q=[tokens * (b & 1) for b in range(B + 1)], cu_k=[keys * (b & 1) for b in range(B + 1)])
+    out, lse = forward(back, workspace=space[:size])
+    assert rc.ring_status_ex(space) == 0
+    assert bool((space[size:] == 0x5A).all())
+    inside(out, want, ob, "out")
+    inside(lse, wlse, lb, "lse")
+
+
 def test_streams_and_workspaces():
     """Calls with their own workspaces on two streams, tensors made on the default stream."""
     ps = [problem([1] * 5, [3000, 20, 900, 1, 4000], P=2, Hq=8, Hkv=2, D=128, seed=s) for s in (17, 18)]
