@@ -21,9 +21,8 @@
 //                   in the order the MMAs consume them
 //   warp 9          MMA issue: S_t = Q_t K^T, O_t += P_t V for the two tiles in
 //                   turn, so one tile's softmax runs under the other's MMAs
-//   warps 10-11     guard: in tiles that some row does not see whole, clears
-//                   value rows past the end and non-finite values, because
-//                   0 x inf would reach rows that must not see them; rows that
+//   warps 10-11     guard: clears non-finite values from the value rows that some
+//                   row does not see, because 0 x inf would reach it; rows that
 //                   do see one add it in the epilogue
 // Two forms.  PAIR: the two row tiles are 256 consecutive rows and share every
 // key tile.  SPLIT (few rows per sequence, single tokens above all): both are
@@ -136,7 +135,7 @@ struct Unit {
     int tok;         // first query token of row tile 0, within the sequence
     int ntok[2];     // valid tokens of the row tiles
     int jb[2], n[2]; // first key tile and number of key tiles of each row tile
-    int guard;       // key tiles from here on are not seen whole by every row
+    int guard;       // keys from here on are not seen by every row
     int nparts;      // parts of this unit's rows (1: results are final)
     int index;       // unit number (partial results); -1: no more units
     int poison;      // set by the guard when it cleared a value of this unit
@@ -181,7 +180,7 @@ __device__ Unit unit_of(const Params &p, const Plan &pl, int u, int lane)
         w.n[1] -= w.n[0];
         w.jb[1] += w.n[0];
     }
-    w.guard = seen(p, w.s, w.tok) / KT;
+    w.guard = seen(p, w.s, w.tok);
     w.poison = 0;
     return w;
 }
@@ -209,6 +208,14 @@ __device__ __forceinline__ void for_entries(const Unit &w, F f)
                 if (j + 1 < w.n[t] && !f(false, t, j + 1)) return;
             }
     }
+}
+
+// a * 0 + c on pairs of bf16
+__device__ __forceinline__ uint32_t fma0_bf16x2(uint32_t a, uint32_t c)
+{
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(0u), "r"(c));
+    return d;
 }
 
 __device__ __forceinline__ bool nonfinite_bf16(uint32_t bits16) { return (bits16 & 0x7F80u) == 0x7F80u; }
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             };
             for (uint32_t it = 0; ok && (wp = next_unit(it)); release_unit(it++)) {
                 const int n0 = uniform(wp->n[0]), n1 = uniform(wp->n[1]);
-                const int g0 = uniform(wp->guard - wp->jb[0]), g1 = uniform(wp->guard - wp->jb[1]);   // first guarded tile
+                const int gt = uniform(wp->guard) / KT, g0 = gt - uniform(wp->jb[0]), g1 = gt - uniform(wp->jb[1]);   // first guarded tile
                 const int n = max(n0, n1);
                 if (n == 0) continue;
                 if (!(ok = wait_all(q_full, nq & 1, ab, 3))) break;
@@ -505,34 +512,45 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     const uint32_t en = e++, st = en % NST;
                     const int jt = w.jb[t] + j;
                     if (!(ok = wait_idle(full_bar + 8 * st, (en / NST) & 1, ab, 7))) return false;
-                    if (!is_v || jt < w.guard) {
+                    if (!is_v || jt < w.guard / KT) {
                         arrive_warp(empty_bar + 8 * st, lane);
                         return true;
                     }
-                    const int valid = w.s.kl - jt * KT;    // rows from here on are past the end
-                    bool found = false;
+                    // The rows from here on, 16 bytes a lane at a time: x * 0 is NaN for x
+                    // infinite or NaN, and stays in the sum.  Values to clear are rare,
+                    // so they are looked for again.
+                    const int lo = max(w.guard - jt * KT, 0), n16 = (KT - lo) * 8;
+                    uint8_t *const rows = gKV + st * STAGE + lo * 128;
+                    uint32_t sum[4] = {0, 0, 0, 0};
 #pragma unroll 4
-                    for (int i = lane; i < 64 * 8 * (DP / 64); i += 32) {
-                        const int row = g * 64 + ((i >> 3) & 63), blk = i >> 9;
-                        uint4 *const a = (uint4 *)(gKV + st * STAGE + blk * BLK + row * 128 + (i & 7) * 16);
-                        if (row >= valid) {
-                            *a = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        uint32_t x[4] = {a->x, a->y, a->z, a->w};
-                        bool bad = false;
+                    for (int i = g * 32 + lane; i < n16; i += 64)
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            if (nonfinite_bf16(x[h])) x[h] &= 0xFFFF0000u, bad = true;
-                            if (nonfinite_bf16(x[h] >> 16)) x[h] &= 0x0000FFFFu, bad = true;
+                        for (int b = 0; b < DP / 64; ++b) {
+                            const uint4 x = *(const uint4 *)(rows + b * BLK + i * 16);
+                            sum[0] = fma0_bf16x2(x.x, sum[0]);
+                            sum[1] = fma0_bf16x2(x.y, sum[1]);
+                            sum[2] = fma0_bf16x2(x.z, sum[2]);
+                            sum[3] = fma0_bf16x2(x.w, sum[3]);
                         }
-                        if (bad) {
-                            *a = make_uint4(x[0], x[1], x[2], x[3]);
-                            found = true;
+                    uint32_t all = fma0_bf16x2(sum[0], sum[1]);
+                    all = fma0_bf16x2(all, fma0_bf16x2(sum[2], sum[3]));
+                    if (__any_sync(0xFFFFFFFFu, nonfinite_bf16(all) || nonfinite_bf16(all >> 16))) {
+                        const int valid = w.s.kl - jt * KT - lo;    // rows from here on are past the end
+#pragma unroll 1
+                        for (int i = g * 32 + lane; i < n16 * (DP / 64); i += 64) {
+                            const int b = i >= n16 ? 1 : 0, at = i - b * n16;
+                            uint32_t *const a = (uint32_t *)(rows + b * BLK + at * 16);
+#pragma unroll 1
+                            for (int h = 0; h < 4; ++h) {
+                                const uint32_t x = a[h];
+                                const uint32_t keep = (nonfinite_bf16(x) ? 0u : 0xFFFFu) | (nonfinite_bf16(x >> 16) ? 0u : 0xFFFF0000u);
+                                if (keep == 0xFFFFFFFFu) continue;
+                                a[h] = x & keep;
+                                if (at / 8 < valid) *(volatile int *)&units[it % UNITS].poison = 1;
+                            }
                         }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
-                    if (found) *(volatile int *)&units[it % UNITS].poison = 1;
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(guard_bar + 8 * st);
@@ -715,7 +733,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                 if (add_back) {
                     // non-finite values that this row does see, taken out by the guard
                     const int k1 = min(lim, end * KT);
-                    for (int k = max(w.guard, w.jb[SPLIT ? 0 : t]) * KT; k < k1; ++k) {
+                    for (int k = max(w.guard, w.jb[SPLIT ? 0 : t] * KT); k < k1; ++k) {
                         const uint16_t *vr = (const uint16_t *)(p.v + w.slot * p.v_slot +
                                                                 ((size_t)w.s.k0 + k) * p.v_token + w.hk * p.v_head);
 #pragma unroll
