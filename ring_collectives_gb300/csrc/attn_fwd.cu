@@ -429,7 +429,34 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                         if (n == 1) tc_commit(q_empty);
                     }
                     advance();
-                    for (int j = 0; j < n; ++j) {
+                    int j = 0;
+                    // Tiles that both row tiles have, and another after them.  Written without a
+                    // condition more than it needs: this loop's issue is on the critical path.
+                    for (const int both = n0 == n1 ? n - 1 : 0; j < both; ++j) {
+                        const uint32_t sv = st;
+                        if (!(ok = take(j >= g0))) break;
+                        advance();
+                        const uint32_t sk = st;
+                        if (!(ok = take(false))) break;
+                        advance();
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!(ok = weights(t))) break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                mma_rows<KS>(tm + 256 + t * KT, tm + t * KT, sKV + sv * STAGE, j == 0, 32);
+                                if (t == 1) tc_commit(empty_bar + 8 * sv);
+                            }
+                            if (elect_one()) {
+                                mma_scores<KS>(tm + t * KT, sQ + t * STAGE, sKV + sk * STAGE);
+                                tc_commit(s_full + 8 * t);
+                                if (t == 1) tc_commit(empty_bar + 8 * sk);
+                                if (t == 1 && j + 2 == n) tc_commit(q_empty);
+                            }
+                        }
+                        if (!ok) break;
+                    }
+                    for (; ok && j < n; ++j) {
                         // The values of this tile and the keys of the next are there before the
                         // weights are waited for, so nothing stands between the two products.
                         const uint32_t sv = st;
