@@ -366,30 +366,43 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                     // S^T = K Q^T, dP^T = V dO^T; dV += P^T dO, dK += dS^T Q.  S of the next
                     // tile is issued behind dV (it takes P's place), dP behind dK.
                     ok = scores_a(tm + 256, bar.s_full) && scores_b(tm + 384);
-                    for (int j = 0; j < n && ok; ++j, ++nt) {
-                        if (!(ok = wait_all(bar.p_ready, nt & 1, ab, 6))) break;
+                    auto rows_b = [&](bool first) {
+                        if (!wait_all(bar.p_ready, nt & 1, ab, 6)) return false;
                         tc_fence_after();
                         if (elect_one()) {
-                            mma_rows<KS>(tm, tm + 256, sB + rb * TILE, j == 0, 64);
+                            mma_rows<KS>(tm, tm + 256, sB + rb * TILE, first, 64);
                             tc_commit(bar.b_empty + 8 * rb);
                         }
                         if (++rb == NB) rb = 0;
-                        if (j + 1 < n && !(ok = scores_a(tm + 256, bar.s_full))) break;
+                        return true;
+                    };
+                    // Tiles with another after them, without a condition more than that takes.
+                    for (int j = 0; j < n - 1 && ok; ++j, ++nt) {
+                        if (!(ok = rows_b(j == 0) && scores_a(tm + 256, bar.s_full))) break;
                         if (!(ok = wait_all(bar.ds_ready, nt & 1, ab, 7))) break;
                         rows_a(tm + 128, tm + 384, j == 0);
-                        if (j + 1 < n) ok = scores_b(tm + 384);
+                        ok = scores_b(tm + 384);
                     }
+                    if (!ok || !(ok = rows_b(n == 1) && wait_all(bar.ds_ready, nt & 1, ab, 7))) break;
+                    rows_a(tm + 128, tm + 384, n == 1);
+                    ++nt;
                 } else {
                     // S = Q K^T, dP = dO V^T; dQ += dS K.  Scores run two tiles ahead in two
                     // buffers; dP of the next tile goes first once dS of this one is out.
                     ok = scores_a(tm, bar.s_full) && scores_b(tm + 256);
                     if (ok && n > 1) ok = scores_a(tm + 128, bar.s_full + 8);
-                    for (int j = 0; j < n && ok; ++j, ++nt) {
+                    int j = 0;
+                    for (; j < n - 2 && ok; ++j, ++nt) {
+                        const uint32_t buf = j & 1;
+                        if (!(ok = wait_all(bar.ds_ready, nt & 1, ab, 7) && scores_b(tm + 256))) break;
+                        rows_a(tm + 384, tm + buf * 128, j == 0);
+                        ok = scores_a(tm + buf * 128, bar.s_full + 8 * buf);
+                    }
+                    for (; j < n && ok; ++j, ++nt) {
                         const uint32_t buf = j & 1;
                         if (!(ok = wait_all(bar.ds_ready, nt & 1, ab, 7))) break;
                         if (j + 1 < n && !(ok = scores_b(tm + 256))) break;
                         rows_a(tm + 384, tm + buf * 128, j == 0);
-                        if (j + 2 < n) ok = scores_a(tm + buf * 128, bar.s_full + 8 * buf);
                     }
                 }
                 commit(bar.acc_full);
