@@ -20,10 +20,11 @@
 // are the A operands of the second products; all sums are binary32.
 //
 // Bounds: tensor cores, 3 products a tile pair for dQ and 4 for dK and dV.  8192
-// tokens, 32 heads of 128: dQ 568 us, 1452 TFLOP/s, held back by the chain of
-// its one tile (two score products, elementwise work, second product); dK and dV
-// 668 us, 1646 TFLOP/s.  The two-kernel form was taken for its fixed order of
-// sums; 5 products would be 742 us at the measured peak.
+// tokens, 32 heads of 128: dQ 559 us, 1474 TFLOP/s; dK and dV 653 us, 1685
+// TFLOP/s.  dQ is further from the peak; giving its products more buffers or its
+// warpgroups separate halves of a tile made it no faster.  The two-kernel form
+// was taken for its fixed order of sums; 5 products would be 742 us at the
+// measured peak.
 #include <mutex>
 
 #include "attn.cuh"

@@ -35,9 +35,9 @@
 //
 // Bounds.  PAIR: 4 products of 128 x 128 x 128 a pair of tiles are 2048 clocks of
 // tensor cores; the chain scores - softmax - weights of one tile, half hidden by
-// the other's, makes it about 2800.  16384 tokens, 32 heads of 128: 1.28 ms,
-// 1716 TFLOP/s (called back to back, at the power limit, 1.37 ms).  A unit's
-// ends cost about 3 tiles, so six prompts of 1 to 4097 tokens, 32 heads: 231 us, 1238
+// the other's, makes it about 2700.  16384 tokens, 32 heads of 128: 1.22 ms,
+// 1810 TFLOP/s (called back to back, at the power limit, 1.31 ms).  A unit's
+// ends cost 2 to 3 tiles, so six prompts of 1 to 4097 tokens, 32 heads: 220 us, 1298
 // TFLOP/s.  SPLIT: memory; 64 tokens on caches of 200 to 7982 keys, 8 key heads:
 // 183 us, 5.8 TB/s with the join; one token on 32768 keys of 8 heads: 35 us, 3.9
 // TB/s, because the first loads and the join's launch do not overlap anything.

@@ -17,8 +17,8 @@
 // the element's partner, formed once per token for a run of heads: with the
 // plain formula the kernel was bound by issue, not by memory.
 //
-// Measured: 16383 tokens x 8 ranks x 5 heads of 128, 66.7 us, 5.2 TB/s with the
-// tables (78 % of the copy rate; ncu: issue slots 42 % busy); the gradient on 8192
+// Measured: 16383 tokens x 8 ranks x 5 heads of 128, 65.5 us, 5.25 TB/s with the
+// tables (79 % of the copy rate; ncu: issue slots 42 % busy); the gradient on 8192
 // tokens, 46.7 us + 2.5 us for the sums of the weight gradient, 5.2 TB/s.
 #include <cmath>
 #include <cuda_bf16.h>
