@@ -37,9 +37,9 @@
 // tensor cores; the chain scores - softmax - weights of one tile, half hidden by
 // the other's, makes it about 2700.  16384 tokens, 32 heads of 128: 1.22 ms,
 // 1810 TFLOP/s (called back to back, at the power limit, 1.31 ms).  A unit's
-// ends cost 2 to 3 tiles, so six prompts of 1 to 4097 tokens, 32 heads: 220 us, 1298
+// ends cost 2 to 3 tiles, so six prompts of 1 to 4097 tokens, 32 heads: 214 us, 1334
 // TFLOP/s.  SPLIT: memory; 64 tokens on caches of 200 to 7982 keys, 8 key heads:
-// 183 us, 5.8 TB/s with the join; one token on 32768 keys of 8 heads: 35 us, 3.9
+// 183 us, 5.8 TB/s with the join; one token on 32768 keys of 8 heads: 34 us, 3.9
 // TB/s, because the first loads and the join's launch do not overlap anything.
 #include <mutex>
 
@@ -741,7 +741,9 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             float *const part = p.part_o + part_row * DP;
             const int end = SPLIT ? w.jb[1] + w.n[1] : w.jb[t] + n;    // of the unit's key tiles
             constexpr int QN = SPLIT ? DP / 64 : DP / 32;              // blocks of 32 columns of a warp
-#pragma unroll
+            // Not unrolled: run once a unit, its instructions are fetched anew each time (unrolled,
+            // ragged prompts took 219.5 us for 214.4, one token on 32768 keys 35.5 for 34.1).
+#pragma unroll 1
             for (int q_ = 0; q_ < QN; ++q_) {
                 const int q = SPLIT ? t * QN + q_ : q_;
                 float f[32];
