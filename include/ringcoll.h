@@ -412,8 +412,8 @@ typedef struct {
  * Rows of q outside every sequence leave out and lse untouched.  The result
  * does not depend on timing: splits of long key ranges are joined in order.
  * A sequence may have any number of queries: a whole prompt, a later piece of
- * one (keys in a cache), or one token.  Where queries fill few rows (mean
- * Tq/B times Hq/Hkv at most 128) key ranges are divided over the GPU.
+ * one (keys in a cache), or one token.  Where whole sequences would not fill
+ * the GPU, long key ranges are divided over it and joined by a second launch.
  * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, B >= 1, Hq a
  * multiple of Hkv with Hq/Hkv <= 128, D a multiple of 8 up to 128,
  * 0 < scale < inf, layouts as for rc_heads, reserved 0.  Tq = 0 does nothing.
