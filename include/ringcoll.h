@@ -387,7 +387,10 @@ typedef struct {
  * see none).  scale > 0 multiplies the scores.
  * workspace: null for the library's own, else DEVICE memory of ws_bytes bytes
  * (256-byte aligned, zeroed once before first use; at least the call's
- * *_workspace_bytes), under the rules of ring_all_gather_ex.
+ * *_workspace_bytes), under the rules of ring_all_gather_ex.  It may be one
+ * that other calls use too, in stream order: what a call puts behind the
+ * header it zeroes again before it ends, so no number of its own is ever taken
+ * for another call's signal.
  */
 typedef struct {
     rc_heads q, k, v, out;

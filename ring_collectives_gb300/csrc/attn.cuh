@@ -46,6 +46,7 @@ struct Params {
     int sms, part_rows, max_units;         // max_units: units that partial results have room for
     int out32;                             // 1: rows of out are whole 32-byte vectors
     int may_split;                         // 1: key ranges may be split (part_o / part_lse are there)
+    int clear;                             // 1: partial results are zeroed once read (a caller's workspace)
     float scale;
     unsigned long long timeout_ns;
 };

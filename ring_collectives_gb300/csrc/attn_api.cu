@@ -142,6 +142,10 @@ static FwdPlan plan_fwd(Params &p, int sms)
 
 constexpr size_t kWsHead = 256;   // the status header of a caller's workspace, padded
 
+// The status header and `bytes` of space for intermediate results.  In a caller's
+// workspace that space is where calls that signal keep words which they compare with the
+// epoch in the header, and almost any other number there reads as a signal given.  So it
+// is left zeroed (p.clear): a word that no launch has signalled yet.
 static int take_workspace(const rc_attn_args &a, size_t bytes, Params &p, char **scratch)
 {
     uint32_t *unused = nullptr;
@@ -153,6 +157,7 @@ static int take_workspace(const rc_attn_args &a, size_t bytes, Params &p, char *
     if (rc_) return rc_;
     if (a.workspace) {
         *scratch = (char *)a.workspace + kWsHead;
+        p.clear = 1;
         return RC_OK;
     }
     void *s = nullptr;
@@ -254,7 +259,8 @@ static int run_bwd(const rc_attn_args *args, void *stream)
         return rc_;
     if (!a.Tq) mq = mdo = mk;   // without queries (or keys) no tile of theirs is read
     if (!a.Tk) mk = mv = mq;
-    const cudaError_t e = launch_attn_bwd(p, mq, mdo, mk, mv, (cudaStream_t)stream);
+    cudaError_t e = launch_attn_bwd(p, mq, mdo, mk, mv, (cudaStream_t)stream);
+    if (e == cudaSuccess && p.clear && a.Tq) e = cudaMemsetAsync(p.delta, 0, delta_bytes(a), (cudaStream_t)stream);
     if (e != cudaSuccess) return set_error(RC_ERR_CUDA, "attn_bwd launch: %s", cudaGetErrorString(e));
     return RC_OK;
 }

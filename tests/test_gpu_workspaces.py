@@ -1,0 +1,105 @@
+"""One caller-owned workspace shared by different calls in stream order (needs a GB300).
+
+The signalling calls keep words after the 128-byte header that compare with
+the header's epoch, so whatever other calls put there has to be gone when they
+return: zero is a word that no launch has signalled yet.
+"""
+import numpy as np
+import pytest
+import torch
+
+import ring_collectives_gb300 as rc
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF = torch.bfloat16
+HEADER = 128
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(DEV)
+    rc.ring_set_timeout_ms(2000)
+
+
+def ints(x):
+    return torch.tensor([int(v) for v in x], dtype=torch.int32, device=DEV)
+
+
+class Attention:
+    """One attention problem, forward and backward, on the library's workspace or a caller's."""
+
+    def __init__(self, ql, kl, P, Hq, Hkv, D, seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        r = lambda T, H: torch.randn(P, T, H, D, generator=g, device=DEV).to(BF)  # noqa: E731
+        self.q, self.dout = r(sum(ql), Hq), r(sum(ql), Hq)
+        self.k, self.v = r(sum(kl), Hkv), r(sum(kl), Hkv)
+        self.cu = ints(np.cumsum([0] + ql)), ints(np.cumsum([0] + kl))
+        self.sizes = P, len(ql), sum(ql), sum(kl), Hq, Hkv, D
+
+    def forward(self, ws=None):
+        out, lse = torch.empty_like(self.q), torch.empty(self.q.shape[:3], device=DEV)
+        rc.attn_fwd(self.q, self.k, self.v, out, lse, *self.cu, workspace=ws)
+        return out, lse
+
+    def backward(self, out, lse, ws=None):
+        grads = [torch.empty_like(x) for x in (self.q, self.k, self.v)]
+        rc.attn_bwd(self.q, self.k, self.v, out, lse, self.dout, *grads, *self.cu, workspace=ws)
+        return grads
+
+
+def equal(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+# Few rows on long key ranges, which are divided: single tokens, few and many rows, both row forms and head classes
+DIVIDED = [([1], [9000], 2, 4, 1, 128), ([1, 1, 1], [5000, 20, 3100], 1, 8, 8, 64), ([40, 3], [3000, 2600], 1, 8, 2, 96),
+           ([300], [4097], 1, 4, 2, 128)]
+
+
+@pytest.mark.parametrize("shape", DIVIDED, ids=str)
+def test_attention_leaves_no_words_behind(shape):
+    a = Attention(*shape, seed=1)
+    want = a.forward()
+    grads = a.backward(*want)
+    size = max(rc.attn_fwd_workspace_bytes(*a.sizes), rc.attn_bwd_workspace_bytes(*a.sizes))
+    assert rc.attn_fwd_workspace_bytes(*a.sizes) > 4096
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    for _ in range(2):
+        assert equal(a.forward(ws), want)
+        assert rc.ring_status_ex(ws) == 0
+        assert not ws[HEADER:].any()
+        assert equal(a.backward(*want, ws), grads)
+        assert rc.ring_status_ex(ws) == 0
+        assert not ws[HEADER:].any()
+
+
+def test_attention_and_signalling_calls_share_a_workspace():
+    """The layers of a block on one workspace: gather + matmul of new shards each time (a wait that
+    ended early would use the rows gathered before), attention, and a ring all-reduce."""
+    P, M_r, N, K = 4, 256, 512, 256
+    a = Attention([1, 40], [9000, 3000], P, 4, 1, 128, seed=2)
+    want = a.forward()
+    grads = a.backward(*want)
+    size = max(rc.attn_fwd_workspace_bytes(*a.sizes), rc.attn_bwd_workspace_bytes(*a.sizes),
+               rc.ag_gemm_workspace_bytes(P, M_r), rc.ring_allreduce_workspace_bytes(P, 64 * P * 300, torch.float32))
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    B = torch.randn(N, K, generator=g, device=DEV).to(BF)
+    gathered, C = torch.empty(P * M_r, K, dtype=BF, device=DEV), torch.empty(P * M_r, N, dtype=BF, device=DEV)
+    wanted, Cw = torch.empty_like(gathered), torch.empty_like(C)
+    for it in range(6):
+        shards = torch.randn(P, M_r, K, generator=g, device=DEV).to(BF)
+        x = torch.randn(P, 64 * P * 300, generator=g, device=DEV)
+        y = x.clone()
+        rc.ag_gemm(shards, wanted, B, Cw, rank=it % P)
+        rc.ring_allreduce(y)
+        gathered.fill_(float(it))
+        rc.ag_gemm_ex(shards, gathered, B, C, it % P, ws)
+        assert equal(a.forward(ws), want)
+        rc.ring_allreduce_ex(x, ws)
+        assert equal(a.backward(*want, ws), grads)
+        assert rc.ring_status_ex(ws) == 0, rc.ring_last_error()
+        assert torch.equal(gathered, shards.view(P * M_r, K)) and torch.equal(C, Cw) and torch.equal(x, y)
