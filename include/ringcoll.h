@@ -461,7 +461,9 @@ typedef enum { RC_ROPE_HALF = 0, RC_ROPE_PAIRS = 1 } rc_rope_layout;
  * dgamma_q, dgamma_k: f32 [P][D] (written): rank r's own sums, which a
  * ring_allreduce of the slots turns into the gradient of the shared weights.
  * workspace (qk_norm_rope_bwd): null for the library's own, else DEVICE memory
- * of ws_bytes bytes, 256-byte aligned, contents arbitrary.
+ * of ws_bytes bytes, 256-byte aligned, contents arbitrary.  It may be one that
+ * other calls use too, in stream order: the header at its start is left alone
+ * and what is written behind it is zeroed again, as by attn_fwd.
  */
 typedef struct {
     rc_heads q, k, q_out, k_out;

@@ -643,7 +643,9 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, gamma_q: torch.Tensor, ga
                      workspace: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Gradient of :func:`qk_norm_rope` from its inputs and the gradients dq_out, dk_out of
     its outputs: writes dq, dk (bf16; may be dq_out, dk_out) and each rank's own sums of
-    the weight gradients, dgamma_q and dgamma_k (float32 [P, D])."""
+    the weight gradients, dgamma_q and dgamma_k (float32 [P, D]).  workspace: a CUDA tensor
+    of at least qk_norm_rope_bwd_workspace_bytes bytes, which other calls may use too in
+    stream order; None takes the library's own."""
     args = _qk_norm(q, k, gamma_q, gamma_k, cos, sin, pos, layout, eps, dq_out, dk_out, (dq, dk, dgamma_q, dgamma_k),
                     workspace)
     _launch(load().qk_norm_rope_bwd, args, q.device, stream)

@@ -48,6 +48,7 @@ struct Params {
     float *dg[2];                // [P][D]
     int P, T, H[2], D, npos, pairs;
     int blocks;                  // gradient: rows of `part`
+    int clear;                   // gradient: 1: `part` is zeroed once read (a caller's workspace)
     float eps;
 };
 
@@ -459,9 +460,12 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm_bwd(const Params p)
 }
 
 // dg[w][slot][d]: the sum over the rows of `part`.  A lane owns an output, warp k
-// adds rows k, k + 32, ... and the warps' sums are added in order.
+// adds rows k, k + 32, ... and the warps' sums are added in order.  CLEAR: in a
+// caller's workspace the rows are zeroed once read, because other calls keep signal
+// words there and almost any other number reads as a signal given.
 constexpr int DG_WARPS = 32;
 
+template <bool CLEAR>
 __global__ void __launch_bounds__(32 * DG_WARPS) k_qk_norm_dg(const Params p)
 {
     __shared__ float red[DG_WARPS][33];
@@ -472,6 +476,8 @@ __global__ void __launch_bounds__(32 * DG_WARPS) k_qk_norm_dg(const Params p)
     if (i < width)
 #pragma unroll 8
         for (int b = warp; b < p.blocks; b += DG_WARPS) s += p.part[(size_t)b * width + i];
+    if (CLEAR && i < width)                                // in a loop of its own: stores would hold up the loads
+        for (int b = warp; b < p.blocks; b += DG_WARPS) p.part[(size_t)b * width + i] = 0.f;
     red[warp][lane] = s;
     __syncthreads();
     if (warp || i >= width) return;
@@ -513,7 +519,7 @@ static cudaError_t launch(const Params &p, bool grad, dim3 blocks, cudaStream_t 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_qk_norm_dg, p);
+    return p.clear ? cudaLaunchKernelEx(&cfg, k_qk_norm_dg<true>, p) : cudaLaunchKernelEx(&cfg, k_qk_norm_dg<false>, p);
 }
 
 // Lanes of a group for a head of D: D / 2V rounded up to a power of two.
@@ -545,6 +551,9 @@ static cudaError_t launch_any(const Params &p, bool grad, dim3 blocks, cudaStrea
     default: return launch<4, 32>(p, grad, blocks, st);
     }
 }
+
+constexpr size_t kWsHead = 256;   // a caller's workspace begins with the status header of other calls
+static_assert(kWsHead >= sizeof(WsHeader), "the header is left alone");
 
 static int check_heads(const rc_heads &in, Heads &h, const char *name, int P, int T, int H, int D)
 {
@@ -630,9 +639,10 @@ static int run(const rc_qk_norm_args *args, bool grad, void *stream)
         const size_t bytes = (size_t)p.blocks * a.P * 2 * a.D * 4;
         void *s = a.workspace;
         if (a.workspace && ((uintptr_t)a.workspace & 255u)) return set_error(RC_ERR_INVALID, "workspace must be 256-byte aligned");
-        if (a.workspace && a.ws_bytes < bytes)
-            return set_error(RC_ERR_INVALID, "workspace of %zu bytes is below the %zu this call needs", a.ws_bytes, bytes);
-        if (!a.workspace && (rc_ = prepare_scratch(bytes, &s))) return rc_;
+        if (a.workspace && a.ws_bytes < kWsHead + bytes)
+            return set_error(RC_ERR_INVALID, "workspace of %zu bytes is below the %zu this call needs", a.ws_bytes, kWsHead + bytes);
+        if (a.workspace) s = (char *)s + kWsHead, p.clear = 1;
+        else if ((rc_ = prepare_scratch(bytes, &s))) return rc_;
         p.part = (float *)s;
     } else {
         int per_slot, shares;
@@ -658,5 +668,5 @@ extern "C" size_t qk_norm_rope_bwd_workspace_bytes(const rc_qk_norm_args *args)
     if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
     int blocks, shares;
     grid_of(*args, sms, batches(*args, GB), blocks, shares);
-    return (size_t)blocks * shares * args->P * 2 * args->D * 4;
+    return kWsHead + (size_t)blocks * shares * args->P * 2 * args->D * 4;
 }

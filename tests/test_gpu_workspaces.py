@@ -103,3 +103,47 @@ def test_attention_and_signalling_calls_share_a_workspace():
         assert equal(a.backward(*want, ws), grads)
         assert rc.ring_status_ex(ws) == 0, rc.ring_last_error()
         assert torch.equal(gathered, shards.view(P * M_r, K)) and torch.equal(C, Cw) and torch.equal(x, y)
+
+
+class Norm:
+    """One gradient of the query/key norm, on the library's workspace or a caller's."""
+
+    def __init__(self, P, T, Hq, Hkv, D, seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+        self.heads = [r(P, T, h, D).to(BF) for h in (Hq, Hkv, Hq, Hkv)]
+        angle = r(T, D // 2)
+        self.rest = r(D), r(D), angle.cos(), angle.sin(), torch.arange(T, dtype=torch.int32, device=DEV)
+        self.sizes = P, T, Hq, Hkv, D
+
+    def backward(self, ws=None):
+        q, k, dqo, dko = self.heads
+        P, D = q.size(0), q.size(3)
+        res = [torch.empty_like(q), torch.empty_like(k), torch.empty(P, D, device=DEV), torch.empty(P, D, device=DEV)]
+        rc.qk_norm_rope_bwd(q, k, *self.rest, dqo, dko, *res, workspace=ws)
+        return res
+
+
+@pytest.mark.parametrize("shape", [(1, 3, 2, 1, 64), (4, 700, 4, 2, 128), (2, 45, 3, 1, 24)], ids=str)
+def test_norm_gradient_leaves_the_header_and_no_words_behind(shape):
+    n = Norm(*shape, seed=4)
+    want = n.backward()
+    ws = torch.zeros(rc.qk_norm_rope_bwd_workspace_bytes(*n.sizes), dtype=torch.uint8, device=DEV)
+    ws[:HEADER] = 0x5A
+    for _ in range(2):
+        assert equal(n.backward(ws), want)
+        assert (ws[:HEADER] == 0x5A).all() and not ws[HEADER:].any()
+
+
+def test_norm_and_attention_share_a_workspace():
+    n = Norm(4, 700, 4, 2, 128, seed=5)
+    a = Attention([1, 40], [9000, 3000], 4, 4, 1, 128, seed=6)
+    dx, want = n.backward(), a.forward()
+    grads = a.backward(*want)
+    size = max(rc.qk_norm_rope_bwd_workspace_bytes(*n.sizes), rc.attn_fwd_workspace_bytes(*a.sizes),
+               rc.attn_bwd_workspace_bytes(*a.sizes))
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    for _ in range(3):
+        assert equal(n.backward(ws), dx)
+        assert equal(a.forward(ws), want) and equal(a.backward(*want, ws), grads)
+        assert rc.ring_status_ex(ws) == 0, rc.ring_last_error()
