@@ -29,7 +29,9 @@
  *   - The library owns one signal workspace per device, created on the first
  *     call on that device (a cudaMalloc and a synchronous zeroing), grown on
  *     demand and released by ring_finalize().  Make the first call (at the
- *     largest P used) before capturing calls into a CUDA graph.  Calls that
+ *     largest P used) before capturing calls into a CUDA graph.  A workspace
+ *     that is outgrown stays valid until ring_finalize(), so what was captured
+ *     before can still be replayed.  Calls that
  *     share a device's workspace must not run concurrently: issue them on one
  *     stream, or order the streams.  Every collective that signals also has
  *     an _ex variant taking a caller-owned workspace instead (sized by its
@@ -63,7 +65,7 @@ typedef enum {
     RC_ERR_CUDA = 2,        /* a CUDA runtime call failed (message in ring_last_error) */
     RC_ERR_TIMEOUT = 3,     /* a device-side bounded wait ran out (from ring_status) */
     RC_ERR_UNSUPPORTED = 4, /* no CUDA device, wrong architecture, or grid cannot be co-resident */
-    RC_ERR_NOMEM = 5        /* the signal workspace could not be allocated */
+    RC_ERR_NOMEM = 5        /* the library's workspace could not be allocated */
 } rc_status;
 
 #define RC_MAX_P 64 /* largest number of logical ranks */
@@ -420,9 +422,12 @@ typedef struct {
  * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, B >= 1, Hq a
  * multiple of Hkv with Hq/Hkv <= 128, D a multiple of 8 up to 128,
  * 0 < scale < inf, layouts as for rc_heads, reserved 0.  Tq = 0 does nothing.
- * The library's own workspace holds partial results here (grown on demand like
- * the signal words: make the first call, at the largest sizes, before
- * capturing).  One device wait may last as long as a row tile's pass over its
+ * The library's own space for partial results grows on demand, also while a
+ * stream is being captured (after one earlier call of attn_fwd or attn_bwd, of
+ * any size, on the device), and what it outgrows stays valid until
+ * ring_finalize: captured calls can be replayed after larger ones.  attn_fwd, attn_bwd and qk_norm_rope_bwd
+ * share it, so calls of theirs without a workspace must not run concurrently.
+ * One device wait may last as long as a row tile's pass over its
  * keys (about 12 ns a key), so ring_set_timeout_ms has to allow for that.
  */
 int attn_fwd(const rc_attn_args *args, void *stream);
@@ -443,6 +448,7 @@ size_t attn_fwd_workspace_bytes(const rc_attn_args *args);
  * gradients of its own sequence and head group non-finite, also where the
  * mask hides it.  Arguments and requirements as attn_fwd, lse not null;
  * the gradients may be views of one fused buffer and must not overlap inputs.
+ * The library's own space for row sums is that of attn_fwd, with its rules.
  */
 int attn_bwd(const rc_attn_args *args, void *stream);
 
@@ -494,7 +500,8 @@ int qk_norm_rope(const rc_qk_norm_args *args, void *stream);
  * qk_norm_rope_bwd -- its gradient: q, k are the forward inputs, q_out and
  * k_out the gradients of the outputs (read); writes dq, dk (which may be
  * q_out and k_out) and dgamma_q, dgamma_k, summed in binary32 in an order
- * that does not depend on timing.  T = 0 gives dgamma = 0.
+ * that does not depend on timing.  T = 0 gives dgamma = 0.  The library's own
+ * space for partial sums is that of attn_fwd, with its rules.
  */
 int qk_norm_rope_bwd(const rc_qk_norm_args *args, void *stream);
 

@@ -9,6 +9,7 @@
 #include <mutex>
 #include <string>
 
+#include "blocks.h"
 #include "internal.h"
 #include "ringcoll.h"
 
@@ -164,11 +165,10 @@ struct DeviceState {
     int sm_count = 0;
     int max_blocks[3] = {0, 0, 0}; // co-resident ring blocks per dtype
     int pair_blocks[3] = {0, 0, 0}; // co-resident k_ring_pair blocks per dtype (0: pair kernel unavailable)
-    void *ws = nullptr;  // WsHeader followed by the signal words
-    size_t ws_bytes = 0;
+    rc::Block ws;        // WsHeader followed by the signal words
+    bool ws_zeroed = false;
     uint64_t launches = 0;
-    void *scratch = nullptr; // prepare_scratch
-    size_t scratch_bytes = 0;
+    rc::Block scratch;   // prepare_scratch
 };
 DeviceState g_dev[kMaxDevices];
 
@@ -256,35 +256,27 @@ int current_device(int *dev_out, DeviceState **st_out)
 }
 
 // Makes the workspace at least `sig_bytes` of signal words (after the header).
+// A new one starts zeroed; the one it replaces keeps serving the graphs that
+// were captured with it.
 int ensure_workspace(DeviceState &st, size_t sig_bytes)
 {
     const size_t need = sizeof(rc::WsHeader) + sig_bytes;
     cudaError_t e;
-    if (st.ws && (st.ws_bytes < need || st.launches >= kEpochResetAt)) {
+    if (st.ws.bytes < need) {
+        const void *const before = st.ws.ptr;
+        e = rc::grow(st.ws, need);
+        if (st.ws.ptr != before) st.ws_zeroed = false;
+        if (e != cudaSuccess) return fail(RC_ERR_NOMEM, "signal workspace of %zu bytes: %s", need, cudaGetErrorString(e));
+    } else if (st.launches >= kEpochResetAt) {
         e = cudaDeviceSynchronize();
-        if (e != cudaSuccess) return cuda_fail(e, "synchronise before workspace resize");
-        if (st.ws_bytes < need) {
-            cudaFree(st.ws);
-            st.ws = nullptr;
-            st.ws_bytes = 0;
-        } else {
-            e = cudaMemset(st.ws, 0, st.ws_bytes);
-            if (e == cudaSuccess) e = cudaDeviceSynchronize();
-            if (e != cudaSuccess) return cuda_fail(e, "workspace reset");
-            st.launches = 0;
-        }
+        if (e != cudaSuccess) return cuda_fail(e, "synchronise before workspace reset");
+        st.ws_zeroed = false;
     }
-    if (!st.ws) {
-        size_t bytes = (need + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
-        e = cudaMalloc(&st.ws, bytes);
-        if (e != cudaSuccess) {
-            st.ws = nullptr;
-            return fail(RC_ERR_NOMEM, "signal workspace of %zu bytes: %s", bytes, cudaGetErrorString(e));
-        }
-        e = cudaMemset(st.ws, 0, bytes);
+    if (!st.ws_zeroed) {
+        e = cudaMemset(st.ws.ptr, 0, st.ws.bytes);
         if (e == cudaSuccess) e = cudaDeviceSynchronize();
         if (e != cudaSuccess) return cuda_fail(e, "workspace zeroing");
-        st.ws_bytes = bytes;
+        st.ws_zeroed = true;
         st.launches = 0;
     }
     return RC_OK;
@@ -409,8 +401,8 @@ int run_ring(rc::RingParams &p, int dtype, cudaStream_t st_cuda, void *ext_ws = 
         lock.lock();
         rc_ = ensure_workspace(*st, sig_bytes);
         if (rc_) return rc_;
-        p.hdr = (rc::WsHeader *)st->ws;
-        p.sig = (uint32_t *)((char *)st->ws + sizeof(rc::WsHeader));
+        p.hdr = (rc::WsHeader *)st->ws.ptr;
+        p.sig = (uint32_t *)((char *)st->ws.ptr + sizeof(rc::WsHeader));
     }
     p.timeout_ns = (unsigned long long)g_timeout_ms.load() * 1000000ull;
     p.skip_rank = g_skip_rank.exchange(-1);
@@ -463,8 +455,8 @@ int prepare_workspace(size_t sig_words, WsHeader **hdr, uint32_t **sig, int *sm_
     std::lock_guard<std::mutex> lock(g_mu);
     rc_ = ensure_workspace(*st, sig_words * 4);
     if (rc_) return rc_;
-    *hdr = (WsHeader *)st->ws;
-    *sig = (uint32_t *)((char *)st->ws + sizeof(WsHeader));
+    *hdr = (WsHeader *)st->ws.ptr;
+    *sig = (uint32_t *)((char *)st->ws.ptr + sizeof(WsHeader));
     *sm_count = st->sm_count;
     *timeout_ns = (unsigned long long)g_timeout_ms.load() * 1000000ull;
     st->launches++;
@@ -506,25 +498,9 @@ int prepare_scratch(size_t bytes, void **out)
     int rc_ = current_device(&dev, &st);
     if (rc_) return rc_;
     std::lock_guard<std::mutex> lock(g_mu);
-    if (st->scratch_bytes < bytes) {
-        cudaError_t e;
-        if (st->scratch) {
-            e = cudaDeviceSynchronize();   // earlier calls may still use the old block
-            if (e != cudaSuccess) return cuda_fail(e, "synchronise before scratch resize");
-            cudaFree(st->scratch);
-            st->scratch = nullptr;
-            st->scratch_bytes = 0;
-        }
-        const size_t want = (bytes + (1u << 20) - 1) & ~(size_t)((1u << 20) - 1);
-        e = cudaMalloc(&st->scratch, want);
-        if (e != cudaSuccess) {
-            st->scratch = nullptr;
-            (void)cudaGetLastError();
-            return fail(RC_ERR_NOMEM, "scratch of %zu bytes: %s", want, cudaGetErrorString(e));
-        }
-        st->scratch_bytes = want;
-    }
-    *out = st->scratch;
+    const cudaError_t e = grow(st->scratch, bytes);
+    if (e != cudaSuccess) return fail(RC_ERR_NOMEM, "scratch of %zu bytes: %s", bytes, cudaGetErrorString(e));
+    *out = st->scratch.ptr;
     return RC_OK;
 }
 
@@ -1032,15 +1008,23 @@ int ring_status(void *stream)
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return RC_OK;
     // The library's two signal areas on this device: the workspace of the
     // regular entry points and the fixed array of ring_allreduce_noalloc.
-    void *ws = nullptr;
+    // Workspaces that were outgrown count too: captured graphs still use them.
+    rc::Block b;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        ws = g_dev[dev].ws;
+        b = g_dev[dev].ws;
+        if (!g_dev[dev].ws_zeroed) b.ptr = nullptr;
     }
     void *na = noalloc_scratch_if_set_up(dev);
     rc::WsHeader h{}, hn{};
-    const int st_ws = ws ? read_and_clear_status(ws, s, &h, "status read") : RC_OK;
-    if (st_ws == RC_ERR_CUDA) return st_ws;
+    int st_ws = RC_OK;
+    for (int i = 0; i <= b.olds; ++i) {
+        void *const ws = i < b.olds ? b.old[i] : b.ptr;
+        rc::WsHeader x{};
+        const int st = ws ? read_and_clear_status(ws, s, &x, "status read") : RC_OK;
+        if (st == RC_ERR_CUDA) return st;
+        if (st && !st_ws) st_ws = st, h = x;
+    }
     const int st_na = na ? read_and_clear_status(na, s, &hn, "status read (allocation-free array)") : RC_OK;
     if (st_na == RC_ERR_CUDA) return st_na;
     if (st_ws && st_na)
@@ -1147,20 +1131,13 @@ int ring_finalize(void)
     int prev = 0;
     cudaGetDevice(&prev);
     for (int d = 0; d < kMaxDevices; ++d) {
-        if (g_dev[d].ws) {
+        if (g_dev[d].ws.ptr || g_dev[d].scratch.ptr) {
             cudaSetDevice(d);
             cudaDeviceSynchronize();
-            cudaFree(g_dev[d].ws);
-            g_dev[d].ws = nullptr;
-            g_dev[d].ws_bytes = 0;
+            rc::release(g_dev[d].ws);
+            rc::release(g_dev[d].scratch);
+            g_dev[d].ws_zeroed = false;
             g_dev[d].launches = 0;
-        }
-        if (g_dev[d].scratch) {
-            cudaSetDevice(d);
-            cudaDeviceSynchronize();
-            cudaFree(g_dev[d].scratch);
-            g_dev[d].scratch = nullptr;
-            g_dev[d].scratch_bytes = 0;
         }
         if (g_pipe[d].in) {
             cudaSetDevice(d);

@@ -82,9 +82,10 @@ int prepare_workspace_ext(void *ext, size_t ext_bytes, size_t sig_words, WsHeade
                           int *sm_count, unsigned long long *timeout_ns);
 
 // prepare_scratch: at least `bytes` of plain device memory of the current
-// device (256-byte aligned, contents arbitrary), grown on demand and released
-// by ring_finalize.  Kept apart from the signal words, whose old values must
-// survive between launches.
+// device (256-byte aligned, contents arbitrary), grown on demand, also while a
+// stream is captured; what it outgrows stays valid until ring_finalize, so a
+// captured launch and one that is about to be made keep their memory.  Kept
+// apart from the signal words, whose old values must survive between launches.
 int prepare_scratch(size_t bytes, void **out);
 // The current device must be an sm_103 GPU; gives its SM count.
 int device_sms(int *sms);

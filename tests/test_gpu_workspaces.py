@@ -147,3 +147,46 @@ def test_norm_and_attention_share_a_workspace():
         assert equal(n.backward(ws), dx)
         assert equal(a.forward(ws), want) and equal(a.backward(*want, ws), grads)
         assert rc.ring_status_ex(ws) == 0, rc.ring_last_error()
+
+
+def captured(a, out, lse):
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        rc.attn_fwd(a.q, a.k, a.v, out, lse, *a.cu)
+    return graph
+
+
+def test_the_library_space_grows_while_a_stream_is_captured():
+    """A long prompt needs no space for parts, eight tokens do: their first call may be a captured one."""
+    rc.ring_finalize()
+    prompt, tokens = Attention([4096], [4096], 1, 32, 8, 128, seed=7), Attention([8], [4096], 1, 32, 8, 128, seed=8)
+    assert rc.attn_fwd_workspace_bytes(*prompt.sizes) < 1024 < rc.attn_fwd_workspace_bytes(*tokens.sizes)
+    prompt.forward()
+    out, lse = torch.zeros_like(tokens.q), torch.zeros(tokens.q.shape[:3], device=DEV)
+    captured(tokens, out, lse).replay()
+    assert rc.ring_status() == 0, rc.ring_last_error()
+    assert equal((out, lse), tokens.forward())
+
+
+def test_captured_calls_outlive_larger_ones():
+    """Calls that outgrow the library's space (parts) and its signal words (the header that
+    attention counts its units in) leave what a captured call uses in place."""
+    rc.ring_finalize()
+    tokens = Attention([8], [4096], 1, 32, 8, 128, seed=9)
+    want = tokens.forward()
+    out, lse = torch.zeros_like(tokens.q), torch.zeros(tokens.q.shape[:3], device=DEV)
+    graph = captured(tokens, out, lse)
+    larger = Attention([2048], [2048], 1, 32, 8, 128, seed=10)
+    assert rc.attn_fwd_workspace_bytes(*larger.sizes) > 2 * rc.attn_fwd_workspace_bytes(*tokens.sizes)
+    wide = larger.forward()
+    assert rc.ring_allreduce_workspace_bytes(64, 64 * 4096, torch.float32) > 1 << 20
+    x = torch.randn(64, 64 * 4096, device=DEV)
+    total = x.double().sum(0)
+    rc.ring_allreduce(x)
+    assert (x[3].double() - total).abs().max() <= 64 * 2.0 ** -24 * 64 * 6
+    for _ in range(3):
+        out.zero_(), lse.zero_()
+        graph.replay()
+        assert rc.ring_status() == 0, rc.ring_last_error()
+        assert equal((out, lse), want) and equal(larger.forward(), wide)
