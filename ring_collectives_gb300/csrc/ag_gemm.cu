@@ -43,6 +43,7 @@
 #include <mutex>
 
 #include "gemm_cfg.h"
+#include "per_device.h"
 #include "tc.cuh"
 
 namespace rc {
@@ -937,12 +938,10 @@ static int ag_gemm_run(const void *a_shards, size_t a_stride, void *a_gathered, 
     }
 
     p.skip_row = g_skip_row.exchange(-1);
-    static std::once_flag attr_once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once, [] {
-        attr_err = cudaFuncSetAttribute(k_ag_gemm, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-        if (attr_err == cudaSuccess)
-            attr_err = cudaFuncSetAttribute(k_ag_gemm2, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM2_BYTES);
+    static OncePerDevice attr_once;
+    const cudaError_t attr_err = attr_once([] {
+        const cudaError_t x = cudaFuncSetAttribute(k_ag_gemm, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        return x != cudaSuccess ? x : cudaFuncSetAttribute(k_ag_gemm2, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM2_BYTES);
     });
     if (attr_err != cudaSuccess)
         return set_error(RC_ERR_CUDA, "shared-memory attribute: %s", cudaGetErrorString(attr_err));

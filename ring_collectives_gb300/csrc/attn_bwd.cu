@@ -25,9 +25,8 @@
 // warpgroups separate halves of a tile made it no faster.  The two-kernel form
 // was taken for its fixed order of sums; 5 products would be 742 us at the
 // measured peak.
-#include <mutex>
-
 #include "attn.cuh"
+#include "per_device.h"
 
 namespace rc {
 namespace attn {
@@ -672,16 +671,14 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
                           const CUtensorMap &mv, cudaStream_t st)
 {
     constexpr int DP = tile_cols(KS);
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(k_attn_bwd<KS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, BwdCfg<DP>::SMEM);
-        if (attr == cudaSuccess)
-            attr = cudaFuncSetAttribute(k_attn_bwd<KS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        BwdCfg<DP>::SMEM);
+    static OncePerDevice once;
+    cudaError_t e = once([] {
+        const cudaError_t x = cudaFuncSetAttribute(k_attn_bwd<KS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   BwdCfg<DP>::SMEM);
+        return x != cudaSuccess ? x : cudaFuncSetAttribute(k_attn_bwd<KS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                           BwdCfg<DP>::SMEM);
     });
-    if (attr != cudaSuccess) return attr;
-    cudaError_t e = cudaSuccess;
+    if (e != cudaSuccess) return e;
     if (p.Tq) {
         k_attn_bwd<KS, false><<<p.sms, BWD_THREADS, BwdCfg<DP>::SMEM, st>>>(mq, mdo, mk, mv, p);
         e = cudaGetLastError();

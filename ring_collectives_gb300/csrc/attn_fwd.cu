@@ -41,9 +41,8 @@
 // TFLOP/s.  SPLIT: memory; 64 tokens on caches of 200 to 7982 keys, 8 key heads:
 // 183 us, 5.8 TB/s with the join; one token on 32768 keys of 8 heads: 34 us, 3.9
 // TB/s, because the first loads and the join's launch do not overlap anything.
-#include <mutex>
-
 #include "attn.cuh"
+#include "per_device.h"
 
 namespace rc {
 namespace attn {
@@ -955,15 +954,14 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
                           cudaStream_t st)
 {
     constexpr int DP = tile_cols(KS);
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(k_attn_fwd<KS, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    static OncePerDevice once;
+    cudaError_t e = once([] {
+        return cudaFuncSetAttribute(k_attn_fwd<KS, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     FwdCfg<DP, SPLIT>::SMEM);
     });
-    if (attr != cudaSuccess) return attr;
+    if (e != cudaSuccess) return e;
     k_attn_fwd<KS, SPLIT><<<p.sms, FWD_THREADS, FwdCfg<DP, SPLIT>::SMEM, st>>>(mq, mk, mv, p);
-    cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess || !p.may_split) return e;
     // The join's blocks may be set up while the last units still run.
     cudaLaunchConfig_t cfg{};

@@ -29,6 +29,7 @@
 #include <mutex>
 
 #include "gemm_cfg.h"
+#include "per_device.h"
 #include "tc.cuh"
 
 namespace rc {
@@ -678,12 +679,10 @@ static int gemm_rs_run(const void *A, size_t a_stride, const void *B, size_t b_s
         if ((rc_ = make_map3(&map_a, A, (size_t)K, (size_t)M, P, ars, BM))) return rc_;
         if ((rc_ = make_map3(&map_b, B, (size_t)K, (size_t)N, P, brs, BN))) return rc_;
     }
-    static std::once_flag attr_once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once, [] {
-        attr_err = cudaFuncSetAttribute(k_gemm_rs, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-        if (attr_err == cudaSuccess)
-            attr_err = cudaFuncSetAttribute(k_gemm_rs2, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM2_BYTES);
+    static OncePerDevice attr_once;
+    const cudaError_t attr_err = attr_once([] {
+        const cudaError_t x = cudaFuncSetAttribute(k_gemm_rs, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+        return x != cudaSuccess ? x : cudaFuncSetAttribute(k_gemm_rs2, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM2_BYTES);
     });
     if (attr_err != cudaSuccess)
         return set_error(RC_ERR_CUDA, "shared-memory attribute: %s", cudaGetErrorString(attr_err));

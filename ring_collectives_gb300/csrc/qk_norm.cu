@@ -26,6 +26,7 @@
 #include "internal.h"
 #include "ringcoll.h"
 #include "dev.cuh"
+#include "per_device.h"
 
 namespace rc {
 namespace qkn {
@@ -491,7 +492,8 @@ __global__ void __launch_bounds__(32 * DG_WARPS) k_qk_norm_dg(const Params p)
 template <auto KERNEL, int SMEM>
 static cudaError_t start(dim3 blocks, const Params &p, cudaStream_t st)
 {
-    static const cudaError_t e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    static OncePerDevice once;
+    const cudaError_t e = once([] { return cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
     if (e != cudaSuccess) return e;
     KERNEL<<<blocks, THREADS, SMEM, st>>>(p);
     return cudaGetLastError();
