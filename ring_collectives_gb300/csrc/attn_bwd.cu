@@ -475,8 +475,9 @@ __global__ void __launch_bounds__(BWD_THREADS, 1)
                     tmem_wait_ld32(s[0]);
                     tmem_wait_ld32(s[1]);
                     const float *const sl = stats + st * 256 + wg * 64, *const sd = sl + 128;
-                    // rows [lo, hi) of the tile see this key
-                    int lo = p.causal ? (key - (w.s.kl - w.s.ql) - tok0) * p.G : 0;
+                    // rows [lo, hi) of the tile see this key; the tokens are limited to the tile's
+                    // before they become rows, or few tokens on a long key range would pass 32 bits
+                    int lo = p.causal ? min(max(key - (w.s.kl - w.s.ql) - tok0, 0), p.TT) * p.G : 0;
                     int hi = rows;
                     if (!valid) lo = KT;
                     lo -= wg * 64;
