@@ -421,7 +421,9 @@ typedef struct {
  * the GPU, long key ranges are divided over it and joined by a second launch.
  * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, B >= 1, Hq a
  * multiple of Hkv with Hq/Hkv <= 128, D a multiple of 8 up to 128,
- * 0 < scale < inf, layouts as for rc_heads, reserved 0.  Tq = 0 does nothing.
+ * 0 < scale < inf, layouts as for rc_heads, reserved 0; at most 2^31 - 2^20 - 1
+ * tokens, and as many tiles (of 128 rows or keys, over all sequences, ranks and
+ * key heads).  Tq = 0 does nothing.
  * The library's own space for partial results grows on demand, also while a
  * stream is being captured (after one earlier call of attn_fwd or attn_bwd, of
  * any size, on the device), and what it outgrows stays valid until
@@ -492,7 +494,7 @@ typedef struct {
  * place) and must not overlap them otherwise.
  * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, D a multiple of 8
  * up to 256, layouts as for rc_heads, gamma, cos and sin 16-byte aligned,
- * eps >= 0.  T = 0 does nothing.
+ * eps >= 0, T < 2^31 - 2^20.  T = 0 does nothing.
  */
 int qk_norm_rope(const rc_qk_norm_args *args, void *stream);
 

@@ -283,7 +283,7 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int b)
 __device__ __forceinline__ int seen(const Params &p, const Seq &s, int i)
 {
     if (!p.causal) return s.kl;
-    return min(max(i + 1 + s.kl - s.ql, 0), s.kl);
+    return min(max(i + 1 + (s.kl - s.ql), 0), s.kl);
 }
 
 __device__ __forceinline__ int warp_incl_scan(int v, int lane)

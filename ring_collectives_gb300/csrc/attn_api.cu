@@ -2,6 +2,7 @@
 // checks, tensor maps, the form and split of a launch, partial-result space.
 #include <cudaTypedefs.h>
 
+#include <climits>
 #include <cmath>
 #include <mutex>
 
@@ -74,12 +75,26 @@ static int check_heads(rc_heads &h, const char *name, int P, int T, int H, int D
     return RC_OK;
 }
 
+// Tokens: the kernels count up to a few tiles past them in 32 bits.
+constexpr int kMostTokens = INT_MAX - (1 << 20);
+
+// An upper bound of the row or key tiles of all sequences, ranks and key heads: one
+// for every `tile` tokens and one more for each sequence that has any.
+static long long most_tiles(const rc_attn_args &a, int tokens, int tile)
+{
+    return (long long)a.P * a.Hkv * (tokens / tile + (long long)(a.B < tokens ? a.B : tokens));
+}
+
 static int check_sizes(const rc_attn_args &a)
 {
     if (a.P < 1 || a.P > RC_MAX_P) return set_error(RC_ERR_INVALID, "P=%d outside 1..%d", a.P, RC_MAX_P);
     if (a.B < 1 || a.Tq < 0 || a.Tk < 0) return set_error(RC_ERR_INVALID, "need B >= 1, Tq >= 0 and Tk >= 0 (got %d, %d, %d)", a.B, a.Tq, a.Tk);
     if (a.Hq < 1 || a.Hkv < 1 || a.Hq % a.Hkv || a.Hq / a.Hkv > KT || a.Hq > 65536)
         return set_error(RC_ERR_INVALID, "need Hq a multiple of Hkv and Hq/Hkv <= %d (got %d, %d)", KT, a.Hq, a.Hkv);
+    if (a.Tq > kMostTokens || a.Tk > kMostTokens)
+        return set_error(RC_ERR_INVALID, "Tq=%d or Tk=%d is above %d", a.Tq, a.Tk, kMostTokens);
+    if (most_tiles(a, a.Tq, KT / (a.Hq / a.Hkv)) > kMostTokens || most_tiles(a, a.Tk, KT) > kMostTokens)
+        return set_error(RC_ERR_INVALID, "more than %d tiles over all sequences, ranks and key heads", kMostTokens);
     if (a.D < 8 || a.D > 128 || a.D % 8) return set_error(RC_ERR_INVALID, "D=%d is not a multiple of 8 up to 128", a.D);
     if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return set_error(RC_ERR_INVALID, "scale must be positive and finite");
     if (a.causal != 0 && a.causal != 1) return set_error(RC_ERR_INVALID, "causal must be 0 or 1");

@@ -20,6 +20,7 @@
 // Measured: 16383 tokens x 8 ranks x 5 heads of 128, 65.5 us, 5.25 TB/s with the
 // tables (79 % of the copy rate; ncu: issue slots 42 % busy); the gradient on 8192
 // tokens, 46.7 us + 2.5 us for the sums of the weight gradient, 5.2 TB/s.
+#include <climits>
 #include <cmath>
 #include <cuda_bf16.h>
 
@@ -585,11 +586,15 @@ static void grid_of(const rc_qk_norm_args &a, int sms, int most_shares, int &blo
 
 static int batches(const rc_qk_norm_args &a, int n) { return (a.Hq + n - 1) / n + (a.Hkv + n - 1) / n; }
 
+// Tokens: blocks step past the last one by up to their stride, in 32 bits.
+constexpr int kMostTokens = INT_MAX - (1 << 20);
+
 static int check_sizes(const rc_qk_norm_args &a)
 {
     if (a.P < 1 || a.P > RC_MAX_P) return set_error(RC_ERR_INVALID, "P=%d outside 1..%d", a.P, RC_MAX_P);
     if (a.T < 0 || a.Hq < 1 || a.Hkv < 1 || a.Hq > 65536 || a.Hkv > 65536 || a.npos < 1)
         return set_error(RC_ERR_INVALID, "need T >= 0, 1 <= Hq, Hkv <= 65536 and npos >= 1 (got %d, %d, %d, %d)", a.T, a.Hq, a.Hkv, a.npos);
+    if (a.T > kMostTokens) return set_error(RC_ERR_INVALID, "T=%d is above %d", a.T, kMostTokens);
     if (a.D < 8 || a.D > 256 || a.D % 8) return set_error(RC_ERR_INVALID, "D=%d is not a multiple of 8 up to 256", a.D);
     if (a.layout != RC_ROPE_HALF && a.layout != RC_ROPE_PAIRS) return set_error(RC_ERR_INVALID, "unknown rotation layout %d", a.layout);
     if (!(a.eps >= 0.f) || !std::isfinite(a.eps)) return set_error(RC_ERR_INVALID, "eps must be finite and not negative");
