@@ -424,6 +424,8 @@ typedef struct {
  * 0 < scale < inf, layouts as for rc_heads, reserved 0; at most 2^31 - 2^20 - 1
  * tokens, and as many tiles (of 128 rows or keys, over all sequences, ranks and
  * key heads).  Tq = 0 does nothing.
+ * out and lse must not overlap q, k, v, one another or themselves (refused with
+ * RC_ERR_INVALID where found: always where the layouts nest or share strides).
  * The library's own space for partial results grows on demand, also while a
  * stream is being captured (after one earlier call of attn_fwd or attn_bwd, of
  * any size, on the device), and what it outgrows stays valid until
@@ -449,7 +451,8 @@ size_t attn_fwd_workspace_bytes(const rc_attn_args *args);
  * not reach one another, whatever they hold; a non-finite value makes
  * gradients of its own sequence and head group non-finite, also where the
  * mask hides it.  Arguments and requirements as attn_fwd, lse not null;
- * the gradients may be views of one fused buffer and must not overlap inputs.
+ * the gradients may be views of one fused buffer and must not overlap inputs
+ * or one another (refused as by attn_fwd).
  * The library's own space for row sums is that of attn_fwd, with its rules.
  */
 int attn_bwd(const rc_attn_args *args, void *stream);
@@ -491,7 +494,7 @@ typedef struct {
  *     y = x (mean x^2 + eps)^(-1/2) gamma,
  *     (z_a, z_b) = (y_a cos - y_b sin, y_a sin + y_b cos) for each pair (a, b),
  * in binary32, rounded once to bf16.  q_out and k_out may be q and k (in
- * place) and must not overlap them otherwise.
+ * place) and must not overlap them otherwise (refused as by attn_fwd).
  * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, D a multiple of 8
  * up to 256, layouts as for rc_heads, gamma, cos and sin 16-byte aligned,
  * eps >= 0, T < 2^31 - 2^20.  T = 0 does nothing.

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "attn.cuh"
+#include "heads.h"
 
 namespace rc {
 namespace attn {
@@ -56,23 +57,6 @@ int head_map4(CUtensorMap *map, const rc_heads &h, int P, int T, int Hkv, int D)
     const cuuint64_t strides[3] = {h.token, h.head, h.slot};
     const cuuint32_t box[4] = {64, KT, 1, 1};
     return encode(map, h.base, 4, dims, strides, box);
-}
-
-// Checks one operand and gives the strides of extents of 1 a valid value.
-static int check_heads(rc_heads &h, const char *name, int P, int T, int H, int D)
-{
-    if (!h.base) return set_error(RC_ERR_INVALID, "%s is null", name);
-    const size_t least = (size_t)D * 2;
-    if (H == 1) h.head = least;
-    if (T == 1) h.token = least;
-    if (P == 1) h.slot = least;
-    if (((uintptr_t)h.base | h.slot | h.token | h.head) & 15u)
-        return set_error(RC_ERR_INVALID, "%s: base and strides must be multiples of 16 bytes", name);
-    if (h.head < least || h.token < least || h.slot < least)
-        return set_error(RC_ERR_INVALID, "%s: a stride is below the %zu bytes of a head", name, least);
-    if (h.slot >> 40 || h.token >> 40 || h.head >> 32)
-        return set_error(RC_ERR_INVALID, "%s: a stride is too large", name);
-    return RC_OK;
 }
 
 // Tokens: the kernels count up to a few tiles past them in 32 bits.
@@ -155,8 +139,6 @@ static FwdPlan plan_fwd(Params &p, int sms)
     return f;
 }
 
-constexpr size_t kWsHead = 256;   // the status header of a caller's workspace, padded
-
 // The status header and `bytes` of space for intermediate results.  In a caller's
 // workspace that space is where calls that signal keep words which they compare with the
 // epoch in the header, and almost any other number there reads as a signal given.  So it
@@ -181,6 +163,20 @@ static int take_workspace(const rc_attn_args &a, size_t bytes, Params &p, char *
     return RC_OK;
 }
 
+// Where operands lie; without tokens (and for no lse) nowhere.
+static Region queries_region(const char *name, const rc_heads &h, const rc_attn_args &a)
+{
+    return a.Tq ? Region(name, h, a.P, a.Tq, a.Hq, a.D) : Region();
+}
+static Region keys_region(const char *name, const rc_heads &h, const rc_attn_args &a)
+{
+    return a.Tk ? Region(name, h, a.P, a.Tk, a.Hkv, a.D) : Region();
+}
+static Region lse_region(const rc_attn_args &a)
+{
+    return a.Tq && a.lse ? Region("lse", a.lse, (size_t)a.P * a.Tq * a.Hq * 4) : Region();
+}
+
 static int run_fwd(const rc_attn_args *args, void *stream)
 {
     if (!args) return set_error(RC_ERR_INVALID, "null args");
@@ -193,8 +189,9 @@ static int run_fwd(const rc_attn_args *args, void *stream)
     if (a.Tk && ((rc_ = check_heads(a.k, "k", a.P, a.Tk, a.Hkv, a.D)) || (rc_ = check_heads(a.v, "v", a.P, a.Tk, a.Hkv, a.D))))
         return rc_;
     if (!a.cu_q || !a.cu_k) return set_error(RC_ERR_INVALID, "cu_q or cu_k is null");
-    if (a.out.base == a.q.base || (a.Tk && (a.out.base == a.k.base || a.out.base == a.v.base)))
-        return set_error(RC_ERR_INVALID, "out overlaps an input");
+    const Region res[] = {queries_region("out", a.out, a), lse_region(a)};
+    const Region in[] = {queries_region("q", a.q, a), keys_region("k", a.k, a), keys_region("v", a.v, a)};
+    if ((rc_ = check_apart(res, in))) return rc_;
     int sms = 0;
     if ((rc_ = device_sms(&sms))) return rc_;
     Params p{};
@@ -244,14 +241,10 @@ static int run_bwd(const rc_attn_args *args, void *stream)
         return rc_;
     if (!a.cu_q || !a.cu_k) return set_error(RC_ERR_INVALID, "cu_q or cu_k is null");
     if (a.Tq && !a.lse) return set_error(RC_ERR_INVALID, "lse is null");
-    const void *const in[] = {a.Tk ? a.k.base : nullptr, a.Tk ? a.v.base : nullptr, a.Tq ? a.q.base : nullptr,
-                              a.Tq ? a.out.base : nullptr, a.Tq ? a.dout.base : nullptr};
-    const void *const res[] = {a.Tq ? a.dq.base : nullptr, a.Tk ? a.dk.base : nullptr, a.Tk ? a.dv.base : nullptr};
-    for (int i = 0; i < 3; ++i) {
-        for (const void *x : in)
-            if (x && x == res[i]) return set_error(RC_ERR_INVALID, "a gradient overlaps an input");
-        if (res[i] && res[i] == res[(i + 1) % 3]) return set_error(RC_ERR_INVALID, "two gradients overlap");
-    }
+    const Region res[] = {queries_region("dq", a.dq, a), keys_region("dk", a.dk, a), keys_region("dv", a.dv, a)};
+    const Region in[] = {queries_region("q", a.q, a),     keys_region("k", a.k, a),          keys_region("v", a.v, a),
+                         queries_region("out", a.out, a), queries_region("dout", a.dout, a), lse_region(a)};
+    if ((rc_ = check_apart(res, in))) return rc_;
     Params p{};
     fill(p, a);
     if ((rc_ = device_sms(&p.sms))) return rc_;
@@ -290,7 +283,7 @@ extern "C" size_t attn_bwd_workspace_bytes(const rc_attn_args *args)
     using namespace rc::attn;
     int sms = 0;
     if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
-    return kWsHead + delta_bytes(*args);
+    return rc::kWsHead + delta_bytes(*args);
 }
 
 extern "C" int attn_fwd(const rc_attn_args *args, void *stream) { return rc::attn::run_fwd(args, stream); }
@@ -302,5 +295,5 @@ extern "C" size_t attn_fwd_workspace_bytes(const rc_attn_args *args)
     if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
     Params p{};
     fill(p, *args);
-    return kWsHead + plan_fwd(p, sms).bytes;
+    return rc::kWsHead + plan_fwd(p, sms).bytes;
 }

@@ -27,6 +27,7 @@
 #include "internal.h"
 #include "ringcoll.h"
 #include "dev.cuh"
+#include "heads.h"
 #include "per_device.h"
 
 namespace rc {
@@ -555,22 +556,12 @@ static cudaError_t launch_any(const Params &p, bool grad, dim3 blocks, cudaStrea
     }
 }
 
-constexpr size_t kWsHead = 256;   // a caller's workspace begins with the status header of other calls
-static_assert(kWsHead >= sizeof(WsHeader), "the header is left alone");
-
-static int check_heads(const rc_heads &in, Heads &h, const char *name, int P, int T, int H, int D)
+static int take_heads(const rc_heads &in, Heads &h, const char *name, int P, int T, int H, int D)
 {
-    const size_t least = (size_t)D * 2;
-    h = Heads{(char *)in.base, in.slot, in.token, in.head};
-    if (!h.base) return set_error(RC_ERR_INVALID, "%s is null", name);
-    if (H == 1) h.head = least;
-    if (T == 1) h.token = least;
-    if (P == 1) h.slot = least;
-    if (((uintptr_t)h.base | h.slot | h.token | h.head) & 15u)
-        return set_error(RC_ERR_INVALID, "%s: base and strides must be multiples of 16 bytes", name);
-    if (h.head < least || h.token < least || h.slot < least)
-        return set_error(RC_ERR_INVALID, "%s: a stride is below the %zu bytes of a head", name, least);
-    return RC_OK;
+    rc_heads x = in;
+    const int rc_ = check_heads(x, name, P, T, H, D);
+    h = Heads{(char *)x.base, x.slot, x.token, x.head};
+    return rc_;
 }
 
 // Blocks of a launch: for each slot three per SM over all slots, or one per
@@ -601,6 +592,27 @@ static int check_sizes(const rc_qk_norm_args &a)
     return RC_OK;
 }
 
+// Results apart from the inputs.  A thread has read its share of a head before it
+// writes there, so q_out may be q, dq may be q or dq_out, and k alike.
+static int check_places(const rc_qk_norm_args &a, const Params &p, const char *const (&zname)[2], bool grad)
+{
+    auto region = [&](const char *name, const Heads &h, int H) {
+        return a.T ? Region(name, rc_heads{h.base, h.slot, h.token, h.head}, a.P, a.T, H, a.D) : Region();
+    };
+    const Region q = region("q", p.x[0], a.Hq), k = region("k", p.x[1], a.Hkv), zq = region(zname[0], p.z[0], a.Hq),
+                 zk = region(zname[1], p.z[1], a.Hkv);
+    auto of_one = [](int out, int in) { return out == (in & 1); };   // queries 0, 2; keys 1, 3
+    if (!grad) {
+        const Region res[] = {zq, zk}, in[] = {q, k};
+        return check_apart(res, in, of_one);
+    }
+    const size_t bytes = (size_t)a.P * a.D * 4;
+    const Region res[] = {region("dq", p.dx[0], a.Hq), region("dk", p.dx[1], a.Hkv), Region("dgamma_q", a.dgamma_q, bytes),
+                          Region("dgamma_k", a.dgamma_k, bytes)};
+    const Region in[] = {q, k, zq, zk};
+    return check_apart(res, in, of_one);
+}
+
 static int run(const rc_qk_norm_args *args, bool grad, void *stream)
 {
     if (!args) return set_error(RC_ERR_INVALID, "null args");
@@ -609,17 +621,18 @@ static int run(const rc_qk_norm_args *args, bool grad, void *stream)
     if (rc_) return rc_;
     if (a.T == 0 && !grad) return RC_OK;
     Params p{};
-    const int T = a.T ? a.T : 1;
-    if (a.T && ((rc_ = check_heads(a.q, p.x[0], "q", a.P, T, a.Hq, a.D)) || (rc_ = check_heads(a.k, p.x[1], "k", a.P, T, a.Hkv, a.D)) ||
-                (rc_ = check_heads(a.q_out, p.z[0], grad ? "dq_out" : "q_out", a.P, T, a.Hq, a.D)) ||
-                (rc_ = check_heads(a.k_out, p.z[1], grad ? "dk_out" : "k_out", a.P, T, a.Hkv, a.D))))
+    const char *const zname[] = {grad ? "dq_out" : "q_out", grad ? "dk_out" : "k_out"};
+    if (a.T && ((rc_ = take_heads(a.q, p.x[0], "q", a.P, a.T, a.Hq, a.D)) || (rc_ = take_heads(a.k, p.x[1], "k", a.P, a.T, a.Hkv, a.D)) ||
+                (rc_ = take_heads(a.q_out, p.z[0], zname[0], a.P, a.T, a.Hq, a.D)) ||
+                (rc_ = take_heads(a.k_out, p.z[1], zname[1], a.P, a.T, a.Hkv, a.D))))
         return rc_;
-    if (a.T && grad && ((rc_ = check_heads(a.dq, p.dx[0], "dq", a.P, T, a.Hq, a.D)) || (rc_ = check_heads(a.dk, p.dx[1], "dk", a.P, T, a.Hkv, a.D))))
+    if (a.T && grad && ((rc_ = take_heads(a.dq, p.dx[0], "dq", a.P, a.T, a.Hq, a.D)) || (rc_ = take_heads(a.dk, p.dx[1], "dk", a.P, a.T, a.Hkv, a.D))))
         return rc_;
     if (!a.gamma_q || !a.gamma_k || !a.cos || !a.sin || (a.T && !a.pos)) return set_error(RC_ERR_INVALID, "null pointer");
     if (((uintptr_t)a.gamma_q | (uintptr_t)a.gamma_k | (uintptr_t)a.cos | (uintptr_t)a.sin) & 15u)
         return set_error(RC_ERR_INVALID, "gamma, cos and sin must be 16-byte aligned");
     if (grad && (!a.dgamma_q || !a.dgamma_k)) return set_error(RC_ERR_INVALID, "dgamma_q or dgamma_k is null");
+    if ((rc_ = check_places(a, p, zname, grad))) return rc_;
     int sms = 0;
     if ((rc_ = device_sms(&sms))) return rc_;
     p.g[0] = a.gamma_q;
@@ -675,5 +688,5 @@ extern "C" size_t qk_norm_rope_bwd_workspace_bytes(const rc_qk_norm_args *args)
     if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
     int blocks, shares;
     grid_of(*args, sms, batches(*args, GB), blocks, shares);
-    return kWsHead + (size_t)blocks * shares * args->P * 2 * args->D * 4;
+    return rc::kWsHead + (size_t)blocks * shares * args->P * 2 * args->D * 4;
 }
