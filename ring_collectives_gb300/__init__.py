@@ -516,9 +516,19 @@ def _launch(fn, args: bytes, device, stream) -> None:
         _check(rc)
 
 
-def _heads(t: torch.Tensor, name: str, shape=None):
-    if t.dtype is not _BF16 or not t.is_cuda:
+def _elsewhere(t, name: str, what: str) -> Exception:
+    """Why `t` is not on the device of a call's queries."""
+    if not t.is_cuda:
+        return TypeError(f"{name} must be {what}")
+    return ValueError(f"{name} must be on the device of q, not on GPU {t.get_device()}")
+
+
+def _heads(t: torch.Tensor, name: str, gpu: int, shape=None):
+    """gpu: the index of the queries' device (negative: not a GPU)."""
+    if t.dtype is not _BF16 or gpu < 0:
         raise TypeError(f"{name} must be a bf16 CUDA tensor")
+    if t.get_device() != gpu:
+        raise _elsewhere(t, name, "a bf16 CUDA tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
     st = t.stride()
@@ -527,10 +537,21 @@ def _heads(t: torch.Tensor, name: str, shape=None):
     return t.data_ptr(), 2 * st[0], 2 * st[1], 2 * st[2]
 
 
-def _index(t, name: str, n: int) -> int:
-    if t.dtype is not _I32 or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
+def _index(t, name: str, gpu: int, n: int) -> int:
+    if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 CUDA tensor of {n} elements")
+    if t.get_device() != gpu:
+        raise _elsewhere(t, name, "a CUDA tensor")
     return t.data_ptr()
+
+
+def _space(workspace, gpu: int):
+    if workspace is None:
+        return 0, 0
+    ws = _ws(workspace)
+    if workspace.get_device() != gpu:
+        raise _elsewhere(workspace, "workspace", "a CUDA tensor")
+    return ws
 
 
 def _attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, causal, scale):
@@ -552,19 +573,22 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
     _, Tk, Hkv, _ = k.shape
     kshape = (P, Tk, Hkv, D)
     B = cu_q.numel() - 1
+    gpu = q.get_device()
     args = _ATTN_ARGS.pack(
-        *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(v, "v", kshape), *_heads(out, "out", qshape),
-        *_NO_HEADS * 4, 0 if lse is None else _lse(lse, P, Tq, Hq), _index(cu_q, "cu_q", B + 1),
-        _index(cu_k, "cu_k", B + 1), 0 if used_k is None else _index(used_k, "used_k", B),
-        *((0, 0) if workspace is None else _ws(workspace)),
+        *_heads(q, "q", gpu), *_heads(k, "k", gpu, kshape), *_heads(v, "v", gpu, kshape), *_heads(out, "out", gpu, qshape),
+        *_NO_HEADS * 4, 0 if lse is None else _lse(lse, gpu, P, Tq, Hq), _index(cu_q, "cu_q", gpu, B + 1),
+        _index(cu_k, "cu_k", gpu, B + 1), 0 if used_k is None else _index(used_k, "used_k", gpu, B),
+        *_space(workspace, gpu),
         *_attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, causal, scale))
     _launch(load().attn_fwd, args, q.device, stream)
     return out
 
 
-def _lse(lse, P, Tq, Hq):
-    if lse.dtype is not _F32 or lse.shape != (P, Tq, Hq) or not lse.is_cuda or not lse.is_contiguous():
+def _lse(lse, gpu, P, Tq, Hq):
+    if lse.dtype is not _F32 or lse.shape != (P, Tq, Hq) or not lse.is_contiguous():
         raise TypeError(f"lse must be a contiguous float32 CUDA tensor of shape {[P, Tq, Hq]}")
+    if lse.get_device() != gpu:
+        raise _elsewhere(lse, "lse", "a CUDA tensor")
     return lse.data_ptr()
 
 
@@ -584,12 +608,13 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
     _, Tk, Hkv, _ = k.shape
     kshape = (P, Tk, Hkv, D)
     B = cu_q.numel() - 1
+    gpu = q.get_device()
     args = _ATTN_ARGS.pack(
-        *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(v, "v", kshape), *_heads(out, "out", qshape),
-        *_heads(dout, "dout", qshape), *_heads(dq, "dq", qshape), *_heads(dk, "dk", kshape),
-        *_heads(dv, "dv", kshape), _lse(lse, P, Tq, Hq), _index(cu_q, "cu_q", B + 1),
-        _index(cu_k, "cu_k", B + 1), 0 if used_k is None else _index(used_k, "used_k", B),
-        *((0, 0) if workspace is None else _ws(workspace)),
+        *_heads(q, "q", gpu), *_heads(k, "k", gpu, kshape), *_heads(v, "v", gpu, kshape), *_heads(out, "out", gpu, qshape),
+        *_heads(dout, "dout", gpu, qshape), *_heads(dq, "dq", gpu, qshape), *_heads(dk, "dk", gpu, kshape),
+        *_heads(dv, "dv", gpu, kshape), _lse(lse, gpu, P, Tq, Hq), _index(cu_q, "cu_q", gpu, B + 1),
+        _index(cu_k, "cu_k", gpu, B + 1), 0 if used_k is None else _index(used_k, "used_k", gpu, B),
+        *_space(workspace, gpu),
         *_attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, causal, scale))
     _launch(load().attn_bwd, args, q.device, stream)
     return dq, dk, dv
@@ -604,9 +629,11 @@ def attn_bwd_workspace_bytes(P: int, B: int, Tq: int, Tk: int, Hq: int, Hkv: int
 _QK_NORM_ARGS = struct.Struct("@24Q9Q7if")
 
 
-def _f32(t, name: str, shape) -> int:
-    if t.dtype is not _F32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+def _f32(t, name: str, gpu: int, shape) -> int:
+    if t.dtype is not _F32 or t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 CUDA tensor of shape {list(shape)}")
+    if t.get_device() != gpu:
+        raise _elsewhere(t, name, "a CUDA tensor")
     return t.data_ptr()
 
 
@@ -614,13 +641,15 @@ def _qk_norm(q, k, gamma_q, gamma_k, cos, sin, pos, layout, eps, q_out, k_out, g
     P, T, Hq, D = qshape = q.shape
     kshape = (P, T, k.shape[2], D)
     table = (cos.shape[0], D // 2)
-    heads = _NO_HEADS * 2 if grads is None else _heads(grads[0], "dq", qshape) + _heads(grads[1], "dk", kshape)
-    dg = (0, 0) if grads is None else (_f32(grads[2], "dgamma_q", (P, D)), _f32(grads[3], "dgamma_k", (P, D)))
+    gpu = q.get_device()
+    heads = _NO_HEADS * 2 if grads is None else _heads(grads[0], "dq", gpu, qshape) + _heads(grads[1], "dk", gpu, kshape)
+    dg = (0, 0) if grads is None else (_f32(grads[2], "dgamma_q", gpu, (P, D)), _f32(grads[3], "dgamma_k", gpu, (P, D)))
     names = ("q_out", "k_out") if grads is None else ("dq_out", "dk_out")
     return _QK_NORM_ARGS.pack(
-        *_heads(q, "q"), *_heads(k, "k", kshape), *_heads(q_out, names[0], qshape), *_heads(k_out, names[1], kshape),
-        *heads, _f32(gamma_q, "gamma_q", (D,)), _f32(gamma_k, "gamma_k", (D,)), _f32(cos, "cos", table),
-        _f32(sin, "sin", table), _index(pos, "pos", T), *dg, *((0, 0) if workspace is None else _ws(workspace)),
+        *_heads(q, "q", gpu), *_heads(k, "k", gpu, kshape), *_heads(q_out, names[0], gpu, qshape),
+        *_heads(k_out, names[1], gpu, kshape), *heads, _f32(gamma_q, "gamma_q", gpu, (D,)),
+        _f32(gamma_k, "gamma_k", gpu, (D,)), _f32(cos, "cos", gpu, table), _f32(sin, "sin", gpu, table),
+        _index(pos, "pos", gpu, T), *dg, *_space(workspace, gpu),
         P, T, Hq, kshape[2], D, table[0], layout, eps)
 
 
