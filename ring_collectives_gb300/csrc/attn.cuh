@@ -11,6 +11,7 @@
 #include <cuda.h>
 #include <stdint.h>
 
+#include "f32x2.cuh"
 #include "internal.h"
 #include "ringcoll.h"
 #include "tc.cuh"
@@ -216,32 +217,6 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// Pairs of binary32 values in one 64-bit register: one issue slot for two operations.
-__device__ __forceinline__ uint64_t f2(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unf2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 // The larger of three; NaN only when all are.
 __device__ __forceinline__ float max3(float a, float b, float c)
 {

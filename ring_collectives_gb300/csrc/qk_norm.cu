@@ -27,6 +27,7 @@
 #include "internal.h"
 #include "ringcoll.h"
 #include "dev.cuh"
+#include "f32x2.cuh"
 #include "heads.h"
 #include "per_device.h"
 
@@ -57,35 +58,16 @@ struct Params {
 
 // ------------------------------------------------------------ pairs of binary32
 typedef uint64_t f32x2;
-__device__ __forceinline__ f32x2 mk(float a, float b)
-{
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void un(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
 __device__ __forceinline__ f32x2 swap(f32x2 v)
 {
     float a, b;
-    un(v, a, b);
-    return mk(b, a);
-}
-__device__ __forceinline__ f32x2 mul(f32x2 a, f32x2 b)
-{
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma(f32x2 a, f32x2 b, f32x2 c)
-{
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
+    unf2(v, a, b);
+    return f2(b, a);
 }
 __device__ __forceinline__ float hsum(f32x2 v)
 {
     float a, b;
-    un(v, a, b);
+    unf2(v, a, b);
     return a + b;
 }
 
@@ -139,14 +121,14 @@ __device__ __forceinline__ void take(uint32_t lo, uint32_t hi, f32x2 (&f)[V])
         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "r"(hi) : "memory");
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = mk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    for (int i = 0; i < V; ++i) f[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
 
 __device__ __forceinline__ uint32_t pack(f32x2 v)
 {
     float a, b;
     uint32_t r;
-    un(v, a, b);
+    unf2(v, a, b);
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
@@ -179,8 +161,8 @@ __device__ __forceinline__ void ldf(const float *p, int half, f32x2 (&f)[V])
 #pragma unroll
         for (int i = 0; i < V; i += 4) {
             const float4 v = __ldg((const float4 *)(p + k * half + i));
-            f[k * V / 2 + i / 2] = mk(v.x, v.y);
-            f[k * V / 2 + i / 2 + 1] = mk(v.z, v.w);
+            f[k * V / 2 + i / 2] = f2(v.x, v.y);
+            f[k * V / 2 + i / 2 + 1] = f2(v.z, v.w);
         }
 }
 
@@ -245,13 +227,13 @@ __device__ __forceinline__ void angles(uint32_t base, int stage, f32x2 (&cs)[V],
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (PAIRS) {
-            cs[i] = mk(c[i], c[i]);
-            sn[i] = mk(-s[i], s[i]);
+            cs[i] = f2(c[i], c[i]);
+            sn[i] = f2(-s[i], s[i]);
         } else {
             const int k = 2 * (i % (V / 2));
             const float g = i < V / 2 ? -1.f : 1.f;
-            cs[i] = mk(c[k], c[k + 1]);
-            sn[i] = mk(g * s[k], g * s[k + 1]);
+            cs[i] = f2(c[k], c[k + 1]);
+            sn[i] = f2(g * s[k], g * s[k + 1]);
         }
     }
 }
@@ -317,7 +299,7 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm(const Params p)
             if (now.b == b0) angles<V, 2 * HB, PAIRS>(base, stage, cs, sn);
             partners<V, PAIRS>(g, gp);
 #pragma unroll
-            for (int i = 0; i < V; ++i) a[i] = mul(cs[i], g[i]), b[i] = mul(sn[i], gp[i]);
+            for (int i = 0; i < V; ++i) a[i] = mul2(cs[i], g[i]), b[i] = mul2(sn[i], gp[i]);
         }
 #pragma unroll
         for (int k = 0; k < HB; ++k) {
@@ -326,15 +308,15 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm(const Params p)
             if (here) {
                 take<V>(S::chunk(base, stage, 2 * k), S::chunk(base, stage, 2 * k + 1), f);
 #pragma unroll
-                for (int i = 0; i < V; ++i) ss = fma(f[i], f[i], ss);
+                for (int i = 0; i < V; ++i) ss = fma2(f[i], f[i], ss);
             }
             const float sum = group_sum<L>(hsum(ss));
             if (!here) continue;
             const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
-            const f32x2 r2 = mk(r, r);
+            const f32x2 r2 = f2(r, r);
             partners<V, PAIRS>(f, q);
 #pragma unroll
-            for (int i = 0; i < V; ++i) q[i] = mul(fma(f[i], a[i], mul(q[i], b[i])), r2);
+            for (int i = 0; i < V; ++i) q[i] = mul2(fma2(f[i], a[i], mul2(q[i], b[i])), r2);
             st<V>(dst + k * z.head, hb, q);
         }
         // the slot of the step before this one is free
@@ -409,22 +391,22 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm_bwd(const Params p)
                     for (int i = 0; i < V; ++i) {
                         // turned back: the partner's sine changes sign
                         float s0, s1;
-                        un(sn[i], s0, s1);
-                        u[i] = fma(u[i], cs[i], mul(q[i], mk(-s0, -s1)));    // dy
-                        q[i] = mul(u[i], g[i]);                             // t
-                        ss = fma(f[i], f[i], ss);
-                        tt = fma(q[i], f[i], tt);
+                        unf2(sn[i], s0, s1);
+                        u[i] = fma2(u[i], cs[i], mul2(q[i], f2(-s0, -s1)));    // dy
+                        q[i] = mul2(u[i], g[i]);                             // t
+                        ss = fma2(f[i], f[i], ss);
+                        tt = fma2(q[i], f[i], tt);
                     }
                 }
                 const float sum = group_sum<L>(hsum(ss)), dot = group_sum<L>(hsum(tt));
                 if (!here) continue;
                 const float r = rsqrtf(fmaf(sum, inv_d, p.eps));
                 const float m = -dot * inv_d * r * r * r;      // dx = r t - x r^3 mean(t x)
-                const f32x2 r2 = mk(r, r), m2 = mk(m, m);
+                const f32x2 r2 = f2(r, r), m2 = f2(m, m);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    acc[w][i] = fma(u[i], mul(f[i], r2), acc[w][i]);
-                    q[i] = fma(q[i], r2, mul(f[i], m2));
+                    acc[w][i] = fma2(u[i], mul2(f[i], r2), acc[w][i]);
+                    q[i] = fma2(q[i], r2, mul2(f[i], m2));
                 }
                 st<V>(ds + k * d.head, hb, q);
             }
@@ -441,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 3) k_qk_norm_bwd(const Params p)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float s0, s1;
-            un(acc[w][i], s0, s1);
+            unf2(acc[w][i], s0, s1);
 #pragma unroll
             for (int o = 16; o >= L; o >>= 1) {
                 s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
