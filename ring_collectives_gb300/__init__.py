@@ -546,8 +546,6 @@ def _index(t, name: str, gpu: int, n: int) -> int:
 
 
 def _space(workspace, gpu: int):
-    if workspace is None:
-        return 0, 0
     ws = _ws(workspace)
     if workspace.get_device() != gpu:
         raise _elsewhere(workspace, "workspace", "a CUDA tensor")
@@ -578,7 +576,7 @@ def attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
         *_heads(q, "q", gpu), *_heads(k, "k", gpu, kshape), *_heads(v, "v", gpu, kshape), *_heads(out, "out", gpu, qshape),
         *_NO_HEADS * 4, 0 if lse is None else _lse(lse, gpu, P, Tq, Hq), _index(cu_q, "cu_q", gpu, B + 1),
         _index(cu_k, "cu_k", gpu, B + 1), 0 if used_k is None else _index(used_k, "used_k", gpu, B),
-        *_space(workspace, gpu),
+        *((0, 0) if workspace is None else _space(workspace, gpu)),
         *_attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, causal, scale))
     _launch(load().attn_fwd, args, q.device, stream)
     return out
@@ -614,7 +612,7 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tenso
         *_heads(dout, "dout", gpu, qshape), *_heads(dq, "dq", gpu, qshape), *_heads(dk, "dk", gpu, kshape),
         *_heads(dv, "dv", gpu, kshape), _lse(lse, gpu, P, Tq, Hq), _index(cu_q, "cu_q", gpu, B + 1),
         _index(cu_k, "cu_k", gpu, B + 1), 0 if used_k is None else _index(used_k, "used_k", gpu, B),
-        *_space(workspace, gpu),
+        *((0, 0) if workspace is None else _space(workspace, gpu)),
         *_attn_sizes(P, B, Tq, Tk, Hq, Hkv, D, causal, scale))
     _launch(load().attn_bwd, args, q.device, stream)
     return dq, dk, dv
@@ -649,7 +647,7 @@ def _qk_norm(q, k, gamma_q, gamma_k, cos, sin, pos, layout, eps, q_out, k_out, g
         *_heads(q, "q", gpu), *_heads(k, "k", gpu, kshape), *_heads(q_out, names[0], gpu, qshape),
         *_heads(k_out, names[1], gpu, kshape), *heads, _f32(gamma_q, "gamma_q", gpu, (D,)),
         _f32(gamma_k, "gamma_k", gpu, (D,)), _f32(cos, "cos", gpu, table), _f32(sin, "sin", gpu, table),
-        _index(pos, "pos", gpu, T), *dg, *_space(workspace, gpu),
+        _index(pos, "pos", gpu, T), *dg, *((0, 0) if workspace is None else _space(workspace, gpu)),
         P, T, Hq, kshape[2], D, table[0], layout, eps)
 
 

@@ -164,18 +164,15 @@ static int take_workspace(const rc_attn_args &a, size_t bytes, Params &p, char *
 }
 
 // Where operands lie; without tokens (and for no lse) nowhere.
-static Region queries_region(const char *name, const rc_heads &h, const rc_attn_args &a)
+static Operand of_queries(const char *name, const rc_heads &h, const rc_attn_args &a)
 {
-    return a.Tq ? Region(name, h, a.P, a.Tq, a.Hq, a.D) : Region();
+    return heads_at(name, a.Tq ? h : rc_heads{}, a.P, a.Tq, a.Hq, a.D);
 }
-static Region keys_region(const char *name, const rc_heads &h, const rc_attn_args &a)
+static Operand of_keys(const char *name, const rc_heads &h, const rc_attn_args &a)
 {
-    return a.Tk ? Region(name, h, a.P, a.Tk, a.Hkv, a.D) : Region();
+    return heads_at(name, a.Tk ? h : rc_heads{}, a.P, a.Tk, a.Hkv, a.D);
 }
-static Region lse_region(const rc_attn_args &a)
-{
-    return a.Tq && a.lse ? Region("lse", a.lse, (size_t)a.P * a.Tq * a.Hq * 4) : Region();
-}
+static Operand of_lse(const rc_attn_args &a) { return bytes_at("lse", a.Tq ? a.lse : nullptr, (size_t)a.P * a.Tq * a.Hq * 4); }
 
 static int run_fwd(const rc_attn_args *args, void *stream)
 {
@@ -189,9 +186,9 @@ static int run_fwd(const rc_attn_args *args, void *stream)
     if (a.Tk && ((rc_ = check_heads(a.k, "k", a.P, a.Tk, a.Hkv, a.D)) || (rc_ = check_heads(a.v, "v", a.P, a.Tk, a.Hkv, a.D))))
         return rc_;
     if (!a.cu_q || !a.cu_k) return set_error(RC_ERR_INVALID, "cu_q or cu_k is null");
-    const Region res[] = {queries_region("out", a.out, a), lse_region(a)};
-    const Region in[] = {queries_region("q", a.q, a), keys_region("k", a.k, a), keys_region("v", a.v, a)};
-    if ((rc_ = check_apart(res, in))) return rc_;
+    const Operand res[] = {of_queries("out", a.out, a), of_lse(a)};
+    const Operand in[] = {of_queries("q", a.q, a), of_keys("k", a.k, a), of_keys("v", a.v, a)};
+    if ((rc_ = check_apart(res, 2, in, 3))) return rc_;
     int sms = 0;
     if ((rc_ = device_sms(&sms))) return rc_;
     Params p{};
@@ -241,10 +238,10 @@ static int run_bwd(const rc_attn_args *args, void *stream)
         return rc_;
     if (!a.cu_q || !a.cu_k) return set_error(RC_ERR_INVALID, "cu_q or cu_k is null");
     if (a.Tq && !a.lse) return set_error(RC_ERR_INVALID, "lse is null");
-    const Region res[] = {queries_region("dq", a.dq, a), keys_region("dk", a.dk, a), keys_region("dv", a.dv, a)};
-    const Region in[] = {queries_region("q", a.q, a),     keys_region("k", a.k, a),          keys_region("v", a.v, a),
-                         queries_region("out", a.out, a), queries_region("dout", a.dout, a), lse_region(a)};
-    if ((rc_ = check_apart(res, in))) return rc_;
+    const Operand res[] = {of_queries("dq", a.dq, a), of_keys("dk", a.dk, a), of_keys("dv", a.dv, a)};
+    const Operand in[] = {of_queries("q", a.q, a),     of_keys("k", a.k, a),          of_keys("v", a.v, a),
+                          of_queries("out", a.out, a), of_queries("dout", a.dout, a), of_lse(a)};
+    if ((rc_ = check_apart(res, 3, in, 6))) return rc_;
     Params p{};
     fill(p, a);
     if ((rc_ = device_sms(&p.sms))) return rc_;

@@ -578,21 +578,22 @@ static int check_sizes(const rc_qk_norm_args &a)
 // writes there, so q_out may be q, dq may be q or dq_out, and k alike.
 static int check_places(const rc_qk_norm_args &a, const Params &p, const char *const (&zname)[2], bool grad)
 {
-    auto region = [&](const char *name, const Heads &h, int H) {
-        return a.T ? Region(name, rc_heads{h.base, h.slot, h.token, h.head}, a.P, a.T, H, a.D) : Region();
+    auto at = [&](const char *name, const Heads &h, int H) {
+        return heads_at(name, a.T ? rc_heads{h.base, h.slot, h.token, h.head} : rc_heads{}, a.P, a.T, H, a.D);
     };
-    const Region q = region("q", p.x[0], a.Hq), k = region("k", p.x[1], a.Hkv), zq = region(zname[0], p.z[0], a.Hq),
-                 zk = region(zname[1], p.z[1], a.Hkv);
-    auto of_one = [](int out, int in) { return out == (in & 1); };   // queries 0, 2; keys 1, 3
+    const Operand q = at("q", p.x[0], a.Hq), k = at("k", p.x[1], a.Hkv), zq = at(zname[0], p.z[0], a.Hq),
+                  zk = at(zname[1], p.z[1], a.Hkv);
     if (!grad) {
-        const Region res[] = {zq, zk}, in[] = {q, k};
-        return check_apart(res, in, of_one);
+        const Operand res[] = {zq, zk}, in[] = {q, k};
+        const unsigned whole[] = {1, 2};
+        return check_apart(res, 2, in, 2, whole);
     }
     const size_t bytes = (size_t)a.P * a.D * 4;
-    const Region res[] = {region("dq", p.dx[0], a.Hq), region("dk", p.dx[1], a.Hkv), Region("dgamma_q", a.dgamma_q, bytes),
-                          Region("dgamma_k", a.dgamma_k, bytes)};
-    const Region in[] = {q, k, zq, zk};
-    return check_apart(res, in, of_one);
+    const Operand res[] = {at("dq", p.dx[0], a.Hq), at("dk", p.dx[1], a.Hkv), bytes_at("dgamma_q", a.dgamma_q, bytes),
+                           bytes_at("dgamma_k", a.dgamma_k, bytes)};
+    const Operand in[] = {q, k, zq, zk};
+    const unsigned whole[] = {1 | 4, 2 | 8, 0, 0};
+    return check_apart(res, 4, in, 4, whole);
 }
 
 static int run(const rc_qk_norm_args *args, bool grad, void *stream)
