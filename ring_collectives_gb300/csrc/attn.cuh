@@ -319,7 +319,7 @@ constexpr long long split_units(int sms) { return 4ll * sms; }
 // else uses hold the counter and the blocks that are done; the last block
 // clears both, also in a launch that gave up (every block reaches its end).
 // Which block runs a unit changes no result.  SET: the words of this kernel
-// (the dK/dV launch overlaps the end of the dQ launch).
+// (the dK/dV launch may begin before the dQ launch has quite ended).
 template <int SET>
 __device__ __forceinline__ int claim_unit(const Params &p, int lane)
 {

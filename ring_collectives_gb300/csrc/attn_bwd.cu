@@ -17,14 +17,19 @@
 // units and TMA loads, warp 9 the MMAs, and for dK and dV warps 10-11 bring
 // the row statistics.  P and dS are rounded to bf16 -- the tensor cores'
 // input type -- and written to TMEM over the scores they came from, where they
-// are the A operands of the second products; all sums are binary32.
+// are the A operands of the second products; all sums are binary32.  delta takes
+// the output as the forward pass left it, in bf16 (nothing else is kept), and sums
+// in binary32.  exp2 takes weights below 2^-126 for 0.  All of it together leaves
+// the gradients off by 1.3 times what bf16 in and out costs anyway.
 //
 // Bounds: tensor cores, 3 products a tile pair for dQ and 4 for dK and dV.  8192
 // tokens, 32 heads of 128: dQ 559 us, 1474 TFLOP/s; dK and dV 653 us, 1685
 // TFLOP/s.  dQ is further from the peak; giving its products more buffers or its
-// warpgroups separate halves of a tile made it no faster.  The two-kernel form
-// was taken for its fixed order of sums; 5 products would be 742 us at the
-// measured peak.
+// warpgroups separate halves of a tile made it no faster.  Units of dK and dV are
+// not divided, so with few key heads a few blocks work and the rest idle: 4096
+// tokens, 8 heads of 128 on 1 key head (32 units), 412 us for the whole gradient,
+// whose 5 products would be 46 us at the measured peak.  The two-kernel form was
+// taken for its fixed order of sums; 8192 tokens at the peak would be 742 us.
 #include "attn.cuh"
 #include "per_device.h"
 
@@ -685,7 +690,8 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && p.Tk) {
-        // Blocks start on SMs that the dQ launch has left and run up to the first use of delta.
+        // Set up while the dQ launch runs: blocks start once every block of it has come to its
+        // end, which hides the launch's latency and no more, and wait before the first use of delta.
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)p.sms);
         cfg.blockDim = dim3(BWD_THREADS);

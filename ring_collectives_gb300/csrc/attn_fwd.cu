@@ -10,7 +10,8 @@
 // the sums stay far inside binary32), which almost never happens after the
 // first tile, so the accumulator stays in TMEM.  The weights exp(s - m) are
 // rounded to bf16 for the second product -- the tensor cores' input type --
-// while l sums them unrounded.
+// while l sums them unrounded: the result is off by 1.2 to 1.4 times what bf16 in
+// and out costs anyway.  exp2 takes weights below 2^-126 for 0.
 //
 // One persistent block per SM, 12 warps:
 //   warps 0-3, 4-7  softmax of row tile 0 / 1: one thread a row, so maxima and
@@ -36,11 +37,11 @@
 // Bounds.  PAIR: 4 products of 128 x 128 x 128 a pair of tiles are 2048 clocks of
 // tensor cores; the chain scores - softmax - weights of one tile, half hidden by
 // the other's, makes it about 2700.  16384 tokens, 32 heads of 128: 1.22 ms,
-// 1810 TFLOP/s (called back to back, at the power limit, 1.31 ms).  A unit's
-// ends cost 2 to 3 tiles, so six prompts of 1 to 4097 tokens, 32 heads: 214 us, 1334
-// TFLOP/s.  SPLIT: memory; 64 tokens on caches of 200 to 7982 keys, 8 key heads:
+// 1810 TFLOP/s as a single launch (called back to back, at the power limit, 1.31 to
+// 1.37 ms).  A unit's ends cost 2 to 3 tiles, so six prompts of 1 to 4097 tokens, 32
+// heads: 214 us, 1334 TFLOP/s.  SPLIT: memory; 64 tokens on caches of 200 to 7982 keys, 8 key heads:
 // 183 us, 5.8 TB/s with the join; one token on 32768 keys of 8 heads: 34 us, 3.9
-// TB/s, because the first loads and the join's launch do not overlap anything.
+// TB/s, because the plan, the first loads and the join run one after the other.
 #include "attn.cuh"
 #include "per_device.h"
 
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
             if (lane == 0) wait_bar(drain_bar, 0, ab, 10, true);
             __syncwarp();
         } else {
-            // ---------------- guard: rows [64 g, 64 g + 64) of a value tile
+            // ---------------- guard: every other group of 32 16-byte pieces of a value tile
             const int g = warp - 10;
             uint32_t e = 0;
             bool ok = true;
@@ -963,7 +964,8 @@ static cudaError_t launch(const Params &p, const CUtensorMap &mq, const CUtensor
     k_attn_fwd<KS, SPLIT><<<p.sms, FWD_THREADS, FwdCfg<DP, SPLIT>::SMEM, st>>>(mq, mk, mv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || !p.may_split) return e;
-    // The join's blocks may be set up while the last units still run.
+    // Set up while the units run: the join's blocks start once every block has come to its end,
+    // which hides the launch's latency.
     cudaLaunchConfig_t cfg{};
     const long long rows = (long long)p.P * p.Tq * p.Hq;
     const bool wide = rows < (long long)kJoinRows * p.sms;

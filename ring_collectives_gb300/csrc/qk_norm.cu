@@ -495,7 +495,7 @@ static cudaError_t launch(const Params &p, bool grad, dim3 blocks, cudaStream_t 
     const cudaError_t e = p.pairs ? start<k_qk_norm_bwd<V, L, true>, smem>(blocks, p, st)
                                   : start<k_qk_norm_bwd<V, L, false>, smem>(blocks, p, st);
     if (e != cudaSuccess) return e;
-    // set up while the last blocks of the gradient still run
+    // set up while the gradient runs; its blocks start when that has ended
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((p.P * 2 * p.D + 31) / 32));
     cfg.blockDim = dim3(32 * DG_WARPS);
