@@ -392,7 +392,8 @@ typedef struct {
  * *_workspace_bytes), under the rules of ring_all_gather_ex.  It may be one
  * that other calls use too, in stream order: what a call puts behind the
  * header it zeroes again before it ends, so no number of its own is ever taken
- * for another call's signal.
+ * for another call's signal.  (Offsets that decrease, against the rule above, can
+ * leave some behind: zero the workspace before another kind of call uses it.)
  */
 typedef struct {
     rc_heads q, k, v, out;
