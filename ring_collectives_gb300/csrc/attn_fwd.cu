@@ -563,19 +563,18 @@ __global__ void __launch_bounds__(FWD_THREADS, 1)
                     all = fma0_bf16x2(all, fma0_bf16x2(sum[2], sum[3]));
                     if (__any_sync(0xFFFFFFFFu, nonfinite_bf16(all) || nonfinite_bf16(all >> 16))) {
                         const int valid = w.s.kl - jt * KT - lo;    // rows from here on are past the end
+                        // the same pieces that this warp looked at: the other may have found nothing
 #pragma unroll 1
-                        for (int i = g * 32 + lane; i < n16 * (DP / 64); i += 64) {
-                            const int b = i >= n16 ? 1 : 0, at = i - b * n16;
-                            uint32_t *const a = (uint32_t *)(rows + b * BLK + at * 16);
+                        for (int i = g * 32 + lane; i < n16; i += 64)
 #pragma unroll 1
-                            for (int h = 0; h < 4; ++h) {
-                                const uint32_t x = a[h];
+                            for (int h = 0; h < 4 * (DP / 64); ++h) {
+                                uint32_t *const a = (uint32_t *)(rows + (h >> 2) * BLK + i * 16) + (h & 3);
+                                const uint32_t x = *a;
                                 const uint32_t keep = (nonfinite_bf16(x) ? 0u : 0xFFFFu) | (nonfinite_bf16(x >> 16) ? 0u : 0xFFFF0000u);
                                 if (keep == 0xFFFFFFFFu) continue;
-                                a[h] = x & keep;
-                                if (at / 8 < valid) *(volatile int *)&units[it % UNITS].poison = 1;
+                                *a = x & keep;
+                                if (i / 8 < valid) *(volatile int *)&units[it % UNITS].poison = 1;
                             }
-                        }
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
                     __syncwarp();
