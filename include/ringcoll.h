@@ -1,7 +1,8 @@
 /*
  * ringcoll.h -- C ABI of libringcoll.so: ring collectives over P logical
- * ranks that live in one GPU's HBM, the two collective matmuls, and the
- * attention that runs between them.
+ * ranks that live in one GPU's HBM, the two collective matmuls, and what a
+ * transformer runs between them: attention, norms, gated activations, their
+ * gradients, and activation checkpoints in 8 bits.
  *
  * Model.  The P ranks are P symmetric slots of device memory: slot r starts
  * at base + r*stride bytes, so the symmetric-memory lookup symm_at(ptr, r) of
@@ -514,6 +515,143 @@ int qk_norm_rope_bwd(const rc_qk_norm_args *args, void *stream);
 /* Workspace bytes qk_norm_rope_bwd needs (pointers and strides are not read);
  * 0 for invalid sizes or when no sm_103 device is current. */
 size_t qk_norm_rope_bwd_workspace_bytes(const rc_qk_norm_args *args);
+
+/* Rows of channels of P logical ranks: element (rank r, row t, channel c) lies at
+ * base + r*slot + t*row + c*(bytes of an element).  Activations are bf16; base and
+ * the strides of extents above 1 are multiples of 16 bytes and rows do not
+ * overlap, so a part of the fused result of ag_gemm is taken in place. */
+typedef struct {
+    void *base;
+    size_t slot, row;
+} rc_rows;
+
+/* Activations held in 8 bits.  The 32 channels c in [32 i, 32 i + 32) of a row
+ * (fewer at its end) are a group: element c is q[c] * 2^(e[i] - 127), with q
+ * signed bytes in [-127, 127] (base and strides multiples of 8 bytes) and e
+ * unsigned bytes (any alignment), one for each of the ceil(N / 32) groups of a
+ * row.  e[i] = 255 makes a NaN of all its channels.  Every such value is a bf16
+ * number.  base 0 in q: not given. */
+typedef struct {
+    rc_rows q, e;
+} rc_act8;
+
+/* Arguments of act8_pack and act8_unpack: x bf16 [P][T][N], x8 its 8-bit form. */
+typedef struct {
+    rc_rows x;
+    rc_act8 x8;
+    int P, T, N;
+    int reserved; /* 0 */
+} rc_act8_args;
+
+/*
+ * act8_pack -- an activation checkpoint in 8 bits.  Of each group of 32 channels
+ * e is the least byte in [1, 248] with max |x| <= 127 * 2^(e - 127) (248 where none
+ * is), and q the nearest integer to x * 2^(127 - e), ties to even, kept within
+ * [-127, 127]: off by at most 1/127 of the group's largest magnitude (half a step
+ * 2^(e-127), of which that magnitude has more than 63.5), or by 2^-127 where that is more.  A group
+ * that holds an infinity or a NaN is marked (e = 255, q = 0).  The result is the
+ * same bit for bit wherever the same values are packed.
+ * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, N a multiple of 8
+ * up to 2^20, P*T < 2^31 - 2^20, layouts as for rc_rows and rc_act8, reserved 0,
+ * results apart from x and from one another.  T = 0 does nothing.
+ */
+int act8_pack(const rc_act8_args *args, void *stream);
+
+/* act8_unpack -- the bf16 values that x8 stands for, exactly.  Requirements as
+ * for act8_pack. */
+int act8_unpack(const rc_act8_args *args, void *stream);
+
+/*
+ * Arguments of block_norm and block_norm_bwd.  T rows (tokens) of N channels on
+ * each of P ranks; bf16 [P][T][N] (the row shards that ag_gemm gathers), except
+ * that y and dy may lie as gemm_rs leaves its result: y_cols, dy_cols = 1 for
+ * [P][P*T][N/P], column chunk k of all P*T rows in slot k (N/P a multiple of 8).
+ * gamma_post, gate, gamma_pre: f32 [N], 16-byte aligned, each may be null.
+ * y8, res8, z8: block_norm writes those given; block_norm_bwd reads y8 and res8
+ * in the place of y and res when y8.q.base is not null (then both).
+ * dgamma_post, dgate, dgamma_pre: f32 [P][N], given where the weight is: rank r's
+ * own sums, which a ring_allreduce of the slots turns into the gradient of shared
+ * weights.
+ * workspace (block_norm_bwd): as for rc_qk_norm_args.
+ */
+typedef struct {
+    rc_rows y, res, h, z;    /* h, z: results of block_norm */
+    rc_rows dh, dz, dy, dres; /* block_norm_bwd only */
+    rc_act8 y8, res8, z8;
+    const float *gamma_post, *gate, *gamma_pre;
+    float *dgamma_post, *dgate, *dgamma_pre; /* block_norm_bwd only */
+    void *workspace;
+    size_t ws_bytes;
+    int P, T, N, y_cols, dy_cols;
+    float alpha, eps;
+    int reserved; /* 0 */
+} rc_block_norm_args;
+
+/*
+ * block_norm -- what lies between a block's last matmul and the next one's first,
+ * in one pass over the rows:
+ *     u = y (mean y^2 + eps)^(-1/2) gamma_post     (u = y where gamma_post is null),
+ *     h = res + alpha * gate * u                   (gate 1 where null),
+ *     z = h (mean h^2 + eps)^(-1/2) gamma_pre      (z is null where gamma_pre is),
+ * in binary32, h and z rounded once to bf16 (z from h before its rounding).  y8 and
+ * res8 are the 8-bit forms of y and res, z8 that of the rounded z, as act8_pack
+ * would make them.  h may be res (in place); results are apart otherwise.
+ * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, N a multiple of 8 up
+ * to 16384, P*T < 2^31 - 2^20, layouts as for rc_rows, alpha finite, eps finite
+ * and not negative, z8 only with z, reserved 0.  T = 0 does nothing.
+ */
+int block_norm(const rc_block_norm_args *args, void *stream);
+
+/*
+ * block_norm_bwd -- its gradient, from its inputs or from what y8 and res8 hold
+ * (then at those values: the statistics are computed again, nothing else need be
+ * kept).  Reads dh (null: zero) and dz (null where gamma_pre is), the gradients of
+ * h and z; writes dy, dres, each rounded once, and the sums of the weights'
+ * gradients in binary32, in an order that does not depend on timing.  dres may be
+ * dh or dz, dy may be dh or dz where both are [P][T][N], as wholes; results are
+ * apart otherwise.  T = 0 gives sums of 0.  The library's own space for partial sums
+ * is that of attn_fwd, with its rules.  h, z, z8 are not used.
+ */
+int block_norm_bwd(const rc_block_norm_args *args, void *stream);
+
+/* Workspace bytes block_norm_bwd needs (of the pointers only those of the weights
+ * and of y8 are looked at, for being null); 0 for invalid sizes or when no sm_103
+ * device is current. */
+size_t block_norm_bwd_workspace_bytes(const rc_block_norm_args *args);
+
+/* Activations of glu: x s(x) with the logistic function s, or the tanh form of
+ * gelu, x s(2 sqrt(2/pi) (x + 0.044715 x^3)). */
+typedef enum { RC_GLU_SILU = 0, RC_GLU_GELU = 1 } rc_glu_act;
+
+/*
+ * Arguments of glu and glu_bwd: bf16 [P][T][N], a (the gate) and b commonly the
+ * halves of one fused ag_gemm result, da and db those of its gradient.
+ * a8, b8, h8: glu writes those given; glu_bwd reads a8 and b8 in the place of a
+ * and b when a8.q.base is not null (then both).
+ */
+typedef struct {
+    rc_rows a, b, h;
+    rc_rows dh, da, db; /* glu_bwd only */
+    rc_act8 a8, b8, h8;
+    int P, T, N, act;
+    int reserved[2]; /* 0 */
+} rc_glu_args;
+
+/*
+ * glu -- the gated activation between an MLP's matmuls: h = act(a) b in binary32,
+ * rounded once.  a8, b8 and h8 are the 8-bit forms of a, b and the rounded h.
+ * Requirements as for act8_pack, act an rc_glu_act value; results are apart from
+ * the inputs and from one another, except that h may be a or b, as a whole.
+ */
+int glu(const rc_glu_args *args, void *stream);
+
+/*
+ * glu_bwd -- its gradient, from a and b or from what a8 and b8 hold: da = dh b act'(a),
+ * db = dh act(a), each rounded once; h, where given, is written again (the
+ * operand of the next matmul's weight gradient), and h8 its 8-bit form.  da and
+ * db may each be a, b or dh, as wholes; results are apart otherwise.
+ */
+int glu_bwd(const rc_glu_args *args, void *stream);
 
 /*
  * ring_status -- waits for `stream`, then returns and clears the device

@@ -34,6 +34,8 @@ __all__ = [
     "ring_debug_set_trace", "ring_debug_l2_rate", "ring_finalize", "library_path", "load",
     "attn_fwd", "attn_fwd_workspace_bytes", "attn_bwd", "attn_bwd_workspace_bytes",
     "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes", "RC_ROPE_HALF", "RC_ROPE_PAIRS",
+    "act8_empty", "act8_pack", "act8_unpack", "block_norm", "block_norm_bwd", "block_norm_bwd_workspace_bytes",
+    "glu", "glu_bwd", "RC_GLU_SILU", "RC_GLU_GELU",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +43,7 @@ _LIB_PATH = os.path.join(_HERE, "libringcoll.so")
 
 RC_OK, RC_ERR_INVALID, RC_ERR_CUDA, RC_ERR_TIMEOUT, RC_ERR_UNSUPPORTED, RC_ERR_NOMEM = range(6)
 RC_ROPE_HALF, RC_ROPE_PAIRS = 0, 1   # rotated pairs (i, i + D/2) or (2i, 2i + 1)
+RC_GLU_SILU, RC_GLU_GELU = 0, 1      # glu activations: x s(x), or the tanh form of gelu
 RC_B_NK, RC_B_KN = 0, 1   # ag_gemm weight layouts: [N][K] (nn.Linear) or [K][N] (x @ W)
 _DTYPE = {torch.float32: 0, torch.bfloat16: 1, torch.int32: 2}
 
@@ -88,6 +91,13 @@ _SIGNATURES = {
     "qk_norm_rope": ([ctypes.c_char_p, _vp], _i),
     "qk_norm_rope_bwd": ([ctypes.c_char_p, _vp], _i),
     "qk_norm_rope_bwd_workspace_bytes": ([ctypes.c_char_p], _sz),
+    "act8_pack": ([ctypes.c_char_p, _vp], _i),
+    "act8_unpack": ([ctypes.c_char_p, _vp], _i),
+    "block_norm": ([ctypes.c_char_p, _vp], _i),
+    "block_norm_bwd": ([ctypes.c_char_p, _vp], _i),
+    "block_norm_bwd_workspace_bytes": ([ctypes.c_char_p], _sz),
+    "glu": ([ctypes.c_char_p, _vp], _i),
+    "glu_bwd": ([ctypes.c_char_p, _vp], _i),
 }
 
 _lib = None
@@ -682,3 +692,196 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor, gamma_q: torch.Tensor, ga
 def qk_norm_rope_bwd_workspace_bytes(P: int, T: int, Hq: int, Hkv: int, D: int) -> int:
     args = _QK_NORM_ARGS.pack(*(0,) * 33, P, T, Hq, Hkv, D, 1, RC_ROPE_HALF, 0.0)
     return int(load().qk_norm_rope_bwd_workspace_bytes(args))
+
+
+# rc_act8_args of include/ringcoll.h: three rc_rows, four ints; rc_block_norm_args: fourteen rc_rows, eight pointers and
+# sizes, five ints, alpha, eps, reserved; rc_glu_args: twelve rc_rows, six ints
+_ACT8_ARGS = struct.Struct("@9Q4i")
+_BLOCK_NORM_ARGS = struct.Struct("@42Q8Q5iffi")
+_GLU_ARGS = struct.Struct("@36Q6i")
+_NO_ROWS, _NO_ACT8 = (0,) * 3, (0,) * 6
+_I8, _U8 = torch.int8, torch.uint8
+
+
+def _here(t, name: str, kind: str, gpu: int) -> None:
+    """`t` has to be a CUDA tensor on the device of the call's rows; gpu: its index (negative: not a GPU)."""
+    if gpu < 0 or not t.is_cuda:
+        raise TypeError(f"{name} must be a {kind} CUDA tensor")
+    if t.get_device() != gpu:
+        raise ValueError(f"{name} must be on GPU {gpu} with the other tensors of the call, not on GPU {t.get_device()}")
+
+
+def _rows(t, name: str, gpu: int, shape, dtype=_BF16, kind="bf16"):
+    """Address and strides in bytes of rows [P, T, N]."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be a {kind} CUDA tensor")
+    if gpu < 0 or t.get_device() != gpu:
+        _here(t, name, kind, gpu)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    st = t.stride()
+    if len(st) != 3 or (st[2] != 1 and shape[2] > 1):
+        raise ValueError(f"{name} must be [P, T, N] with contiguous rows")
+    size = t.element_size()
+    return t.data_ptr(), size * st[0], size * st[1]
+
+
+def _act8(x8, name: str, gpu: int, shape):
+    if x8 is None:
+        return _NO_ACT8
+    q, e = x8
+    P, T, N = shape
+    return (*_rows(q, name + "[0]", gpu, shape, _I8, "int8"), *_rows(e, name + "[1]", gpu, (P, T, -(-N // 32)), _U8, "uint8"))
+
+
+def act8_empty(shape, device=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Room for the 8-bit form of an activation [P, T, N]: int8 [P, T, N] and uint8 [P, T, ceil(N / 32)]."""
+    P, T, N = shape
+    device = torch.device("cuda") if device is None else device
+    return torch.empty((P, T, N), dtype=_I8, device=device), torch.empty((P, T, -(-N // 32)), dtype=_U8, device=device)
+
+
+def _act8_call(fn, x, x8, stream):
+    P, T, N = shape = x.shape
+    gpu = x.get_device()
+    if x8 is None:
+        raise TypeError("x8 must be a pair of CUDA tensors")
+    _launch(fn, _ACT8_ARGS.pack(*_rows(x, "x", gpu, shape), *_act8(x8, "x8", gpu, shape), P, T, N, 0), x.device, stream)
+
+
+def act8_pack(x: torch.Tensor, x8, stream=None):
+    """The 8-bit form of a bf16 activation x [P, T, N] (any strides of 16-byte multiples with
+    contiguous rows), a pair x8 as act8_empty makes: signed bytes q and, for every 32 channels
+    of a row, the biased exponent e of the least power of two that keeps them within 127:
+    x is close to q * 2 ** (e - 127).  e = 255 marks a group that holds an infinity or a NaN."""
+    _act8_call(load().act8_pack, x, x8, stream)
+    return x8
+
+
+def act8_unpack(x8, x: torch.Tensor, stream=None) -> torch.Tensor:
+    """The bf16 values [P, T, N] that the pair x8 stands for, exactly."""
+    _act8_call(load().act8_unpack, x, x8, stream)
+    return x
+
+
+def _weights(t, name: str, gpu: int, shape) -> int:
+    if t is None:
+        return 0
+    if t.get_device() != gpu:
+        _here(t, name, "float32", gpu)
+    return _f32(t, name, gpu, shape)
+
+
+def _room(workspace, gpu: int):
+    if workspace is None:
+        return 0, 0
+    ws = _ws(workspace)
+    _here(workspace, "workspace", "contiguous", gpu)
+    return ws
+
+
+def _cols(t, shape) -> bool:
+    """Whether a block's output or its gradient lies in column chunks [P, P * T, N / P]."""
+    P, T, N = shape
+    return P > 1 and N % P == 0 and t.shape == (P, P * T, N // P) and t.shape != shape
+
+
+def _side(t, name: str, gpu: int, shape):
+    P, T, N = shape
+    cols = _cols(t, shape)
+    return _rows(t, name, gpu, (P, P * T, N // P) if cols else shape), int(cols)
+
+
+def block_norm(y: torch.Tensor, res: torch.Tensor, h: torch.Tensor, z: torch.Tensor | None = None,
+               gamma_post: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+               gamma_pre: torch.Tensor | None = None, alpha: float = 1.0, eps: float = 1e-6, y8=None, res8=None, z8=None,
+               stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """What lies between a block's last matmul and the next one's first, in one pass over rows:
+
+        u = rms_norm(y) * gamma_post   (u = y without gamma_post)
+        h = res + alpha * gate * u
+        z = rms_norm(h) * gamma_pre    (z and gamma_pre: both or neither)
+
+    res, h, z [P, T, N] bf16, the row shards that ag_gemm gathers; y alike or as gemm_rs leaves
+    it, [P, P * T, N / P].  Weights float32 [N].  h may be res.  y8, res8, z8: pairs as from
+    act8_empty that receive the 8-bit forms of y, res and z."""
+    P, T, N = shape = res.shape
+    gpu = res.get_device()
+    rows, cols = _side(y, "y", gpu, shape)
+    args = _BLOCK_NORM_ARGS.pack(
+        *rows, *_rows(res, "res", gpu, shape), *_rows(h, "h", gpu, shape), *(_NO_ROWS if z is None else _rows(z, "z", gpu, shape)),
+        *_NO_ROWS * 4, *_act8(y8, "y8", gpu, shape), *_act8(res8, "res8", gpu, shape), *_act8(z8, "z8", gpu, shape),
+        _weights(gamma_post, "gamma_post", gpu, (N,)), _weights(gate, "gate", gpu, (N,)), _weights(gamma_pre, "gamma_pre", gpu, (N,)),
+        0, 0, 0, 0, 0, P, T, N, cols, 0, alpha, eps, 0)
+    _launch(load().block_norm, args, res.device, stream)
+    return h, z
+
+
+def block_norm_bwd(y, res, dh: torch.Tensor | None, dz: torch.Tensor | None, dy: torch.Tensor, dres: torch.Tensor,
+                   dgamma_post: torch.Tensor | None = None, dgate: torch.Tensor | None = None,
+                   dgamma_pre: torch.Tensor | None = None, gamma_post: torch.Tensor | None = None,
+                   gate: torch.Tensor | None = None, gamma_pre: torch.Tensor | None = None, alpha: float = 1.0,
+                   eps: float = 1e-6, workspace: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradient of :func:`block_norm`.  y and res are its inputs, or both are the pairs y8 and
+    res8 that it left (the gradient is then that at their values).  dh (or None) and dz are the
+    gradients of h and z; writes dy (in either layout of y) and dres, and where the weight is
+    given each rank's own sums dgamma_post, dgate, dgamma_pre (float32 [P, N]).  dres may be dh
+    or dz.  workspace: a CUDA tensor of at least block_norm_bwd_workspace_bytes bytes, which
+    other calls may use too in stream order; None takes the library's own."""
+    P, T, N = shape = dres.shape
+    gpu = dres.get_device()
+    held = isinstance(y, tuple)
+    if held != isinstance(res, tuple):
+        raise TypeError("y and res are both tensors or both 8-bit pairs")
+    rows, cols = (_NO_ROWS, 0) if held else _side(y, "y", gpu, shape)
+    drows, dcols = _side(dy, "dy", gpu, shape)
+    args = _BLOCK_NORM_ARGS.pack(
+        *rows, *(_NO_ROWS if held else _rows(res, "res", gpu, shape)), *_NO_ROWS * 2,
+        *(_NO_ROWS if dh is None else _rows(dh, "dh", gpu, shape)), *(_NO_ROWS if dz is None else _rows(dz, "dz", gpu, shape)),
+        *drows, *_rows(dres, "dres", gpu, shape), *(_act8(y, "y", gpu, shape) if held else _NO_ACT8),
+        *(_act8(res, "res", gpu, shape) if held else _NO_ACT8), *_NO_ACT8,
+        _weights(gamma_post, "gamma_post", gpu, (N,)), _weights(gate, "gate", gpu, (N,)), _weights(gamma_pre, "gamma_pre", gpu, (N,)),
+        _weights(dgamma_post, "dgamma_post", gpu, (P, N)), _weights(dgate, "dgate", gpu, (P, N)), _weights(dgamma_pre, "dgamma_pre", gpu, (P, N)),
+        *_room(workspace, gpu), P, T, N, cols, dcols, alpha, eps, 0)
+    _launch(load().block_norm_bwd, args, dres.device, stream)
+    return dy, dres
+
+
+def block_norm_bwd_workspace_bytes(P: int, T: int, N: int, post: bool = True, gate: bool = True, pre: bool = True,
+                                   held: bool = False) -> int:
+    """Bytes of workspace that block_norm_bwd needs with these weights given (held: from 8-bit pairs)."""
+    args = _BLOCK_NORM_ARGS.pack(*(0,) * 24, int(held), *(0,) * 17, int(post), int(gate), int(pre), *(0,) * 5, P, T, N, 0, 0, 1.0, 0.0, 0)
+    return int(load().block_norm_bwd_workspace_bytes(args))
+
+
+def glu(a: torch.Tensor, b: torch.Tensor, h: torch.Tensor, act: int = RC_GLU_SILU, a8=None, b8=None, h8=None,
+        stream=None) -> torch.Tensor:
+    """h = act(a) * b, the gated activation between an MLP's matmuls; bf16 [P, T, N], a and b
+    commonly the halves of one fused ag_gemm result.  act: RC_GLU_SILU or RC_GLU_GELU (tanh
+    form).  a8, b8, h8: pairs as from act8_empty that receive the 8-bit forms.  h may be a or b."""
+    P, T, N = shape = a.shape
+    gpu = a.get_device()
+    args = _GLU_ARGS.pack(*_rows(a, "a", gpu, shape), *_rows(b, "b", gpu, shape), *_rows(h, "h", gpu, shape), *_NO_ROWS * 3,
+                          *_act8(a8, "a8", gpu, shape), *_act8(b8, "b8", gpu, shape), *_act8(h8, "h8", gpu, shape),
+                          P, T, N, act, 0, 0)
+    _launch(load().glu, args, a.device, stream)
+    return h
+
+
+def glu_bwd(a, b, dh: torch.Tensor, da: torch.Tensor, db: torch.Tensor, h: torch.Tensor | None = None,
+            act: int = RC_GLU_SILU, h8=None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Gradient of :func:`glu`, from a and b or from the pairs a8 and b8 that it left: writes
+    da = dh b act'(a) and db = dh act(a), and where given h = act(a) b again and its 8-bit form
+    h8.  da and db may each be a, b or dh."""
+    P, T, N = shape = dh.shape
+    gpu = dh.get_device()
+    held = isinstance(a, tuple)
+    if held != isinstance(b, tuple):
+        raise TypeError("a and b are both tensors or both 8-bit pairs")
+    args = _GLU_ARGS.pack(
+        *(_NO_ROWS * 2 if held else _rows(a, "a", gpu, shape) + _rows(b, "b", gpu, shape)),
+        *(_NO_ROWS if h is None else _rows(h, "h", gpu, shape)), *_rows(dh, "dh", gpu, shape), *_rows(da, "da", gpu, shape),
+        *_rows(db, "db", gpu, shape), *(_act8(a, "a", gpu, shape) + _act8(b, "b", gpu, shape) if held else _NO_ACT8 * 2),
+        *_act8(h8, "h8", gpu, shape), P, T, N, act, 0, 0)
+    _launch(load().glu_bwd, args, dh.device, stream)
+    return da, db

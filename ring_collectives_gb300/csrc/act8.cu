@@ -1,0 +1,83 @@
+// act8.cu -- activation checkpoints in 8 bits: bf16 rows to signed bytes with a
+// power of two for every 32 channels, and back (the format is act8.cuh's).
+//
+// Bound by memory: 2 bytes of an element on one side, 1 + 1/32 on the other.
+#include "act8.cuh"
+#include "heads.h"
+#include "internal.h"
+#include "ringcoll.h"
+
+namespace rc {
+namespace a8 {
+
+constexpr int THREADS = 256;
+constexpr int U = 4;                 // vectors of a thread, all loaded before the first is used
+
+struct Params {
+    Rows x;
+    Act8 x8;
+    Flat f;
+};
+
+template <bool PACK>
+__global__ void __launch_bounds__(THREADS) k_act8(const Params p)
+{
+    const uint64_t first = (uint64_t)blockIdx.x * (THREADS * U);
+    const uint32_t row0 = (uint32_t)(first / p.f.lanes.d), rem0 = (uint32_t)(first - (uint64_t)row0 * p.f.lanes.d);
+    uint4 w[U];
+    uint2 q[U];
+    uint32_t e[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const Spot s(p.f, row0, rem0, u * THREADS + threadIdx.x);
+        if (PACK) {
+            w[u] = make_uint4(0, 0, 0, 0);
+            if (s.on) w[u] = __ldcs((const uint4 *)(p.x.at(s.r, s.t) + s.v * 16));
+        } else if (s.on) {
+            q[u] = __ldcs((const uint2 *)(p.x8.q.at(s.r, s.t) + s.v * 8));
+            e[u] = *(const uint8_t *)(p.x8.e.at(s.r, s.t) + s.v / 4);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const Spot s(p.f, row0, rem0, u * THREADS + threadIdx.x);
+        if (PACK) {
+            put8(p.x8, s.r, s.t, s.v, s.on, w[u]);
+        } else if (s.on) {
+            f32x2 f[4];
+            held8(q[u], e[u], f);
+            __stcs((uint4 *)(p.x.at(s.r, s.t) + s.v * 16), narrow8(f));
+        }
+    }
+}
+
+static int run(const rc_act8_args *args, bool pack, void *stream)
+{
+    if (!args) return set_error(RC_ERR_INVALID, "null args");
+    rc_act8_args a = *args;
+    if (a.reserved) return set_error(RC_ERR_INVALID, "reserved is not 0");
+    int rc_ = check_row_sizes(a.P, a.T, a.N, 1 << 20);
+    if (rc_ || a.T == 0) return rc_;
+    if ((rc_ = check_rows(a.x, "x", a.P, a.T, (size_t)a.N * 2, 16)) || (rc_ = check_act8(a.x8, "x8", a.P, a.T, a.N))) return rc_;
+    const Operand x = rows_at("x", a.x, a.P, a.T, (size_t)a.N * 2), q = rows_at("x8.q", a.x8.q, a.P, a.T, (size_t)a.N),
+                  e = rows_at("x8.e", a.x8.e, a.P, a.T, (size_t)(a.N + 31) / 32);
+    const Operand bytes[] = {q, e}, values[] = {x};
+    if ((rc_ = pack ? check_apart(bytes, 2, values, 1) : check_apart(values, 1, bytes, 2))) return rc_;
+    int sms = 0;
+    if ((rc_ = device_sms(&sms))) return rc_;
+    const Params p{rows_of(a.x), act8_of(a.x8), Flat::of(a.P, a.T, a.N)};
+    const uint64_t blocks = p.f.blocks(THREADS * U);
+    if (blocks > 0x7FFFFFFFull) return set_error(RC_ERR_INVALID, "P*T rows of N=%d channels are too many", a.N);
+    if (pack) k_act8<true><<<(unsigned)blocks, THREADS, 0, (cudaStream_t)stream>>>(p);
+    else k_act8<false><<<(unsigned)blocks, THREADS, 0, (cudaStream_t)stream>>>(p);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return set_error(RC_ERR_CUDA, "act8 launch: %s", cudaGetErrorString(err));
+    return RC_OK;
+}
+
+} // namespace a8
+} // namespace rc
+
+extern "C" int act8_pack(const rc_act8_args *args, void *stream) { return rc::a8::run(args, true, stream); }
+
+extern "C" int act8_unpack(const rc_act8_args *args, void *stream) { return rc::a8::run(args, false, stream); }

@@ -1,5 +1,5 @@
-// heads.cu -- checks of head-strided operands, and whether two of them share
-// bytes (host code only).
+// heads.cu -- checks of operands in strided heads or rows, and whether two of them
+// share bytes (host code only).
 //
 // Every call asks, so the usual answer is found with few operations and little
 // code: operands whose spans do not meet, and results whose strides nest.  Only
@@ -24,6 +24,35 @@ int check_heads(rc_heads &h, const char *name, int P, int T, int H, int D)
         return set_error(RC_ERR_INVALID, "%s: a stride is below the %zu bytes of a head", name, least);
     if (h.slot >> 40 || h.token >> 40 || h.head >> 32)
         return set_error(RC_ERR_INVALID, "%s: a stride is too large", name);
+    return RC_OK;
+}
+
+int check_rows(rc_rows &r, const char *name, int P, int T, size_t bytes, size_t align, bool shared)
+{
+    if (!r.base) return set_error(RC_ERR_INVALID, "%s is null", name);
+    const size_t whole = (bytes + align - 1) / align * align;
+    if (T <= 1) r.row = whole;
+    if (P == 1) r.slot = whole;
+    if (((uintptr_t)r.base | r.slot | r.row) & (align - 1))
+        return set_error(RC_ERR_INVALID, "%s: base and strides must be multiples of %zu bytes", name, align);
+    if (r.row < bytes || (r.slot < bytes && !(shared && r.slot == 0)))
+        return set_error(RC_ERR_INVALID, "%s: a stride is below the %zu bytes of a row", name, bytes);
+    if (r.slot >> 40 || r.row >> 32) return set_error(RC_ERR_INVALID, "%s: a stride is too large", name);
+    return RC_OK;
+}
+
+int check_act8(rc_act8 &a, const char *name, int P, int T, int N, bool shared)
+{
+    if (!a.q.base || !a.e.base) return set_error(RC_ERR_INVALID, "%s: its bytes or exponents are null", name);
+    const int rc_ = check_rows(a.q, name, P, T, (size_t)N, 8, shared);
+    return rc_ ? rc_ : check_rows(a.e, name, P, T, (size_t)(N + 31) / 32, 1, shared);
+}
+
+int check_row_sizes(int P, int T, int N, int most_channels)
+{
+    if (P < 1 || P > RC_MAX_P) return set_error(RC_ERR_INVALID, "P=%d outside 1..%d", P, RC_MAX_P);
+    if (N < 8 || N % 8 || N > most_channels) return set_error(RC_ERR_INVALID, "N=%d is not a multiple of 8 up to %d", N, most_channels);
+    if (T < 0 || (long long)P * T >= (1ll << 31) - (1 << 20)) return set_error(RC_ERR_INVALID, "P=%d slots of T=%d rows: not 0 <= P*T < 2^31 - 2^20", P, T);
     return RC_OK;
 }
 
@@ -161,7 +190,7 @@ bool nested(const Operand &o)
 
 int check_apart(const Operand *results, int nres, const Operand *inputs, int nin, const unsigned *whole)
 {
-    constexpr int kMost = 12;
+    constexpr int kMost = 20;
     double ends[kMost];                    // of the results, then of the inputs
     for (int i = 0; i < nres + nin; ++i) ends[i] = end_of(i < nres ? results[i] : inputs[i - nres]);
     for (int i = 0; i < nres; ++i) {

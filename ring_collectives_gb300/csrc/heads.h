@@ -1,5 +1,5 @@
-// heads.h -- checks of head-strided operands, and whether two of them share
-// bytes (heads.cu; host code only).
+// heads.h -- checks of operands in strided heads or rows, and whether two of them
+// share bytes (heads.cu; host code only).
 #pragma once
 #include <stddef.h>
 #include <stdint.h>
@@ -28,6 +28,16 @@ struct Operand {
 inline Operand heads_at(const char *name, const rc_heads &h, int P, int T, int H, int D)
 {
     return Operand{name, h, P, T, H, (size_t)D * 2};
+}
+// Checks rows [P][T] of `bytes` bytes each, aligned to `align`, and gives the strides of
+// extents of 1 a valid value.  shared: a slot stride of 0 is one operand of all ranks.
+int check_rows(rc_rows &r, const char *name, int P, int T, size_t bytes, size_t align, bool shared = false);
+// The bytes of N channels and of their groups; and P, T, N of a call on rows.
+int check_act8(rc_act8 &a, const char *name, int P, int T, int N, bool shared = false);
+int check_row_sizes(int P, int T, int N, int most_channels);
+inline Operand rows_at(const char *name, const rc_rows &r, int P, int T, size_t bytes)
+{
+    return Operand{name, rc_heads{r.base, r.slot, r.row, 0}, P, T, 1, bytes};
 }
 inline Operand bytes_at(const char *name, const void *p, size_t bytes)
 {
