@@ -529,8 +529,8 @@ typedef struct {
  * (fewer at its end) are a group: element c is q[c] * 2^(e[i] - 127), with q
  * signed bytes in [-127, 127] (base and strides multiples of 8 bytes) and e
  * unsigned bytes (any alignment), one for each of the ceil(N / 32) groups of a
- * row.  e[i] = 255 makes a NaN of all its channels.  Every such value is a bf16
- * number.  base 0 in q: not given. */
+ * row, in [1, 248].  e[i] = 255, with q 0, makes NaNs of its channels.  Every such
+ * value is a bf16 number.  base 0 in q: not given. */
 typedef struct {
     rc_rows q, e;
 } rc_act8;
@@ -652,6 +652,44 @@ int glu(const rc_glu_args *args, void *stream);
  * db may each be a, b or dh, as wholes; results are apart otherwise.
  */
 int glu_bwd(const rc_glu_args *args, void *stream);
+
+/*
+ * Arguments of gemm_wgrad.  dy: bf16 [P][T][N]; x8: [P][T][K]; dw: [P][N][K], bf16
+ * (dw_type RC_BF16) or f32 (RC_F32), base and strides multiples of 16 bytes.  The
+ * slot strides of dy and of x8 may be 0: one operand of all ranks.
+ * workspace: null for the library's own, else DEVICE memory of ws_bytes bytes,
+ * 256-byte aligned, zeroed once before first use, under the rules of
+ * ring_all_gather_ex; it may be one that other calls use too, in stream order, as
+ * for attn_fwd.
+ */
+typedef struct {
+    rc_rows dy;
+    rc_act8 x8;
+    rc_rows dw;
+    void *workspace;
+    size_t ws_bytes;
+    int P, T, N, K;
+    int dw_type, accumulate;
+    int reserved[2]; /* 0 */
+} rc_wgrad_args;
+
+/*
+ * gemm_wgrad -- the weight gradient of either collective matmul from an
+ * activation held in 8 bits: for every rank dw = dy^T x (accumulate: dw += dy^T x),
+ * summed over the T tokens in binary32 on the tensor cores and rounded once.  For
+ * ag_gemm x is the gathered activation, one for all ranks; for gemm_rs dy is.  The
+ * products are those of bf16 numbers, exact; the result does not depend on timing.
+ * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, N and K multiples of
+ * 8 up to 2^20, 0 <= T < 2^31 - 2^20, layouts as above, at most 2^24 tiles of
+ * 256x256 over all ranks, reserved 0, dw apart from the operands.  T = 0 gives
+ * dw = 0 (accumulate: does nothing).
+ * The library's own space for partial results is that of attn_fwd, with its rules.
+ */
+int gemm_wgrad(const rc_wgrad_args *args, void *stream);
+
+/* Workspace bytes gemm_wgrad needs (pointers and strides are not read); 0 for
+ * invalid sizes or when no sm_103 device is current. */
+size_t gemm_wgrad_workspace_bytes(const rc_wgrad_args *args);
 
 /*
  * ring_status -- waits for `stream`, then returns and clears the device

@@ -35,7 +35,7 @@ __all__ = [
     "attn_fwd", "attn_fwd_workspace_bytes", "attn_bwd", "attn_bwd_workspace_bytes",
     "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_bytes", "RC_ROPE_HALF", "RC_ROPE_PAIRS",
     "act8_empty", "act8_pack", "act8_unpack", "block_norm", "block_norm_bwd", "block_norm_bwd_workspace_bytes",
-    "glu", "glu_bwd", "RC_GLU_SILU", "RC_GLU_GELU",
+    "glu", "glu_bwd", "RC_GLU_SILU", "RC_GLU_GELU", "gemm_wgrad", "gemm_wgrad_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -98,6 +98,8 @@ _SIGNATURES = {
     "block_norm_bwd_workspace_bytes": ([ctypes.c_char_p], _sz),
     "glu": ([ctypes.c_char_p, _vp], _i),
     "glu_bwd": ([ctypes.c_char_p, _vp], _i),
+    "gemm_wgrad": ([ctypes.c_char_p, _vp], _i),
+    "gemm_wgrad_workspace_bytes": ([ctypes.c_char_p], _sz),
 }
 
 _lib = None
@@ -695,10 +697,12 @@ def qk_norm_rope_bwd_workspace_bytes(P: int, T: int, Hq: int, Hkv: int, D: int) 
 
 
 # rc_act8_args of include/ringcoll.h: three rc_rows, four ints; rc_block_norm_args: fourteen rc_rows, eight pointers and
-# sizes, five ints, alpha, eps, reserved; rc_glu_args: twelve rc_rows, six ints
+# sizes, five ints, alpha, eps, reserved; rc_glu_args: twelve rc_rows, six ints; rc_wgrad_args: four rc_rows, workspace
+# and its size, eight ints
 _ACT8_ARGS = struct.Struct("@9Q4i")
 _BLOCK_NORM_ARGS = struct.Struct("@42Q8Q5iffi")
 _GLU_ARGS = struct.Struct("@36Q6i")
+_WGRAD_ARGS = struct.Struct("@14Q8i")
 _NO_ROWS, _NO_ACT8 = (0,) * 3, (0,) * 6
 _I8, _U8 = torch.int8, torch.uint8
 
@@ -885,3 +889,26 @@ def glu_bwd(a, b, dh: torch.Tensor, da: torch.Tensor, db: torch.Tensor, h: torch
         *_act8(h8, "h8", gpu, shape), P, T, N, act, 0, 0)
     _launch(load().glu_bwd, args, dh.device, stream)
     return da, db
+
+
+def gemm_wgrad(dy: torch.Tensor, x8, dw: torch.Tensor, accumulate: bool = False, workspace: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """The weight gradient of either collective matmul from an activation held in 8 bits:
+    dw[r] = dy[r].T @ x[r] for every rank, summed in binary32 (accumulate: added to dw).
+    dy [P, T, N] bf16, x8 the pair of an activation [P, T, K], dw [P, N, K] bf16 or float32.
+    What all ranks share (the gathered activation of ag_gemm, the gradient of gemm_rs's
+    result) is given with slot stride 0, as from ``expand``.  workspace: a zeroed CUDA tensor of
+    at least gemm_wgrad_workspace_bytes bytes, as for the ``_ex`` calls; None: the library's own."""
+    P, T, N = dy.shape
+    K = x8[0].shape[2]
+    gpu = dw.get_device()
+    f32 = dw.dtype is _F32
+    args = _WGRAD_ARGS.pack(*_rows(dy, "dy", gpu, (P, T, N)), *_act8(x8, "x8", gpu, (P, T, K)),
+                            *_rows(dw, "dw", gpu, (P, N, K), _F32 if f32 else _BF16, "bf16 or float32"), *_room(workspace, gpu),
+                            P, T, N, K, _DTYPE[dw.dtype], int(bool(accumulate)), 0, 0)
+    _launch(load().gemm_wgrad, args, dw.device, stream)
+    return dw
+
+
+def gemm_wgrad_workspace_bytes(P: int, T: int, N: int, K: int) -> int:
+    return int(load().gemm_wgrad_workspace_bytes(_WGRAD_ARGS.pack(*(0,) * 14, P, T, N, K, 1, 0, 0, 0)))

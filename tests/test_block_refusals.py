@@ -121,3 +121,24 @@ def test_nothing_to_do_is_no_error(lib):
     """T = 0 returns before any operand or device is looked at (the gradient still writes sums of 0)."""
     for fn, args in (("act8_pack", _act8), ("act8_unpack", _act8), ("block_norm", _norm), ("glu", _glu), ("glu_bwd", _glu)):
         assert getattr(lib, fn)(args(T=0), None) == rc.RC_OK
+
+
+def _wgrad(**change):
+    a = dict(dy=[0x100000000, *ROWS], x8=[0x200000000, 1 << 20, 72, 0x300000000, 1 << 20, 3], dw=[0x400000000, 1 << 20, 144], ws=0, ws_bytes=0,
+             P=2, T=8, N=64, K=72, dw_type=1, accumulate=0, reserved=[0, 0])
+    a.update(change)
+    return rc._WGRAD_ARGS.pack(*a["dy"], *a["x8"], *a["dw"], a["ws"], a["ws_bytes"], a["P"], a["T"], a["N"], a["K"], a["dw_type"],
+                               a["accumulate"], *a["reserved"])
+
+
+@pytest.mark.parametrize("change", [
+    dict(P=0), dict(P=65), dict(T=-1), dict(T=0x7FFFFFFF), dict(N=0), dict(N=60), dict(K=4), dict(K=76), dict(N=(1 << 20) + 8),
+    dict(N=1 << 20, K=1 << 20, dw=[0x400000000, 1 << 38, 1 << 21]), dict(dw_type=2), dict(accumulate=2), dict(reserved=[1, 0]),
+    dict(dy=[0, *ROWS]), dict(dy=[0x100000008, *ROWS]), dict(dy=[0x100000000, 64, 128]), dict(x8=[0] * 6),
+    dict(x8=[0x200000000, 1 << 20, 76, 0x300000000, 1 << 20, 3]), dict(x8=[0x200000000, 1 << 20, 72, 0x300000000, 1 << 20, 2]),
+    dict(dw=[0, 1 << 20, 144]), dict(dw=[0x400000008, 1 << 20, 144]), dict(dw=[0x400000000, 0, 144]), dict(dw=[0x400000000, 1 << 20, 128]),
+    dict(dw_type=0), dict(dw=[0x100000000, 1 << 20, 144]), dict(dw=[0x300000000, 1 << 20, 144]), dict(ws=0x1000080, ws_bytes=1 << 40)], ids=str)
+def test_wgrad_refuses(lib, change):
+    assert lib.gemm_wgrad(_wgrad(**change), None) == rc.RC_ERR_INVALID
+    assert rc.ring_last_error()
+    assert lib.gemm_wgrad(None, None) == rc.RC_ERR_INVALID and lib.gemm_wgrad_workspace_bytes(None) == 0
