@@ -11,7 +11,7 @@ namespace rc {
 namespace a8 {
 
 constexpr int THREADS = 256;
-constexpr int U = 4;                 // vectors of a thread, all loaded before the first is used
+constexpr int U = 2;                 // runs of 16 channels of a thread, all loaded before the first is used
 
 struct Params {
     Rows x;
@@ -19,34 +19,29 @@ struct Params {
     Flat f;
 };
 
-template <bool PACK>
+template <bool PACK, bool WIDE>
 __global__ void __launch_bounds__(THREADS) k_act8(const Params p)
 {
     const uint64_t first = (uint64_t)blockIdx.x * (THREADS * U);
     const uint32_t row0 = (uint32_t)(first / p.f.lanes.d), rem0 = (uint32_t)(first - (uint64_t)row0 * p.f.lanes.d);
-    uint4 w[U];
-    uint2 q[U];
+    uint4 w[U][2], q[U];
     uint32_t e[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const Spot s(p.f, row0, rem0, u * THREADS + threadIdx.x);
-        if (PACK) {
-            w[u] = make_uint4(0, 0, 0, 0);
-            if (s.on) w[u] = __ldcs((const uint4 *)(p.x.at(s.r, s.t) + s.v * 16));
-        } else if (s.on) {
-            q[u] = __ldcs((const uint2 *)(p.x8.q.at(s.r, s.t) + s.v * 8));
-            e[u] = *(const uint8_t *)(p.x8.e.at(s.r, s.t) + s.v / 4);
-        }
+        if (PACK) get16<WIDE>(p.x, s, w[u]);
+        else get16<WIDE>(p.x8, s, q[u], e[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const Spot s(p.f, row0, rem0, u * THREADS + threadIdx.x);
         if (PACK) {
-            put8(p.x8, s.r, s.t, s.v, s.on, w[u]);
-        } else if (s.on) {
-            f32x2 f[4];
-            held8(q[u], e[u], f);
-            __stcs((uint4 *)(p.x.at(s.r, s.t) + s.v * 16), narrow8(f));
+            set16<WIDE>(p.x8, s, w[u]);
+        } else {
+            f32x2 a[4], b[4];
+            held8(make_uint2(q[u].x, q[u].y), e[u], a);
+            held8(make_uint2(q[u].z, q[u].w), e[u], b);
+            set16<WIDE>(p.x, s, narrow8(a), narrow8(b));
         }
     }
 }
@@ -68,8 +63,9 @@ static int run(const rc_act8_args *args, bool pack, void *stream)
     const Params p{rows_of(a.x), act8_of(a.x8), Flat::of(a.P, a.T, a.N)};
     const uint64_t blocks = p.f.blocks(THREADS * U);
     if (blocks > 0x7FFFFFFFull) return set_error(RC_ERR_INVALID, "P*T rows of N=%d channels are too many", a.N);
-    if (pack) k_act8<true><<<(unsigned)blocks, THREADS, 0, (cudaStream_t)stream>>>(p);
-    else k_act8<false><<<(unsigned)blocks, THREADS, 0, (cudaStream_t)stream>>>(p);
+    const bool wide = a.N % 16 == 0 && wide_of(a.x, 32) && wide_of(a.x8.q, 16);
+    const auto kernel = pack ? (wide ? k_act8<true, true> : k_act8<true, false>) : (wide ? k_act8<false, true> : k_act8<false, false>);
+    kernel<<<(unsigned)blocks, THREADS, 0, (cudaStream_t)stream>>>(p);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return set_error(RC_ERR_CUDA, "act8 launch: %s", cudaGetErrorString(err));
     return RC_OK;

@@ -7,6 +7,7 @@
 #pragma once
 #include <stdint.h>
 
+#include "dev.cuh"
 #include "f32x2.cuh"
 #include "ringcoll.h"
 
@@ -42,27 +43,30 @@ struct FastDiv {
     }
 };
 
-// Elementwise work on [P][T][N]: all rows behind one another, four lanes a group of 32
-// channels, so that groups never leave a warp and narrow rows fill it too.
+// Elementwise work on [P][T][N]: all rows behind one another, 16 channels a lane and two
+// neighbouring lanes a group of 32, so that groups never leave a warp and narrow rows fill
+// it too.
 struct Flat {
-    FastDiv lanes, tokens;           // lanes of a row: 4 ceil(N / 32); rows of a slot
-    uint32_t rows, vecs;             // P * T; vectors of 8 channels of a row
+    FastDiv lanes, tokens;           // lanes of a row: 2 ceil(N / 32); rows of a slot
+    uint32_t rows, N;
     static Flat of(int P, int T, int N)
     {
-        return Flat{FastDiv::of(4u * (uint32_t)((N + 31) / 32)), FastDiv::of((uint32_t)T), (uint32_t)P * (uint32_t)T, (uint32_t)N / 8};
+        return Flat{FastDiv::of(2u * (uint32_t)((N + 31) / 32)), FastDiv::of((uint32_t)T), (uint32_t)P * (uint32_t)T, (uint32_t)N};
     }
-    // blocks of `lanes_a_block` lanes
+    // blocks of `lanes_a_block` lanes, an even number
     uint64_t blocks(uint32_t lanes_a_block) const { return ((uint64_t)rows * lanes.d + lanes_a_block - 1) / lanes_a_block; }
 };
-// Place of lane `off` behind the first lane (row0, rem0) of a block.
+// Place of lane `off` behind the first lane (row0, rem0) of a block: channels c.. of row t
+// of slot r, if `on`; the last 8 of the 16 exist if `all`.
 struct Spot {
-    uint32_t r, t, v;
-    bool on;
+    uint32_t r, t, c;
+    bool on, all;
     __device__ __forceinline__ Spot(const Flat &f, uint32_t row0, uint32_t rem0, uint32_t off)
     {
         const uint32_t d = f.lanes(rem0 + off), row = row0 + d;
-        v = rem0 + off - d * f.lanes.d;
-        on = row < f.rows && v < f.vecs;
+        c = (rem0 + off - d * f.lanes.d) * 16;
+        on = row < f.rows && c < f.N;
+        all = on && c + 8 < f.N;
         r = f.tokens(row);
         t = row - r * f.tokens.d;
     }
@@ -104,64 +108,156 @@ __device__ __forceinline__ uint4 narrow8(const f32x2 (&f)[4])
 }
 
 // ------------------------------------------------------------ 8 bits
-// The values of 8 bytes with their group's byte e.  A byte b + 128 as the low bits of
-// 2^23 gives an exact difference, and a power of two an exact product; e = 255 is an
-// infinity, which makes a NaN of a zero.
+// The values of 8 bytes with their group's byte e.  A byte b + 128 as the low bits of 2^23,
+// times the power of two, less 2^23 + 128 times it: exact, in one operation.  Where that
+// term is no number (above 2^104), the difference comes first; e = 255 is an infinity then,
+// which makes a NaN of a zero.
 __device__ __forceinline__ void held8(const uint2 &q, uint32_t e, f32x2 (&f)[4])
 {
-    const f32x2 scale = both(__uint_as_float(e << 23)), zero = both(-8388736.f);
+    const float s = __uint_as_float(e << 23);
+    const f32x2 scale = both(s), bias = both(s * -8388736.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t w = (i < 2 ? q.x : q.y) ^ 0x80808080u;
         const uint32_t a = __byte_perm(w, 0x4B000000u, i & 1 ? 0x7652 : 0x7650);
         const uint32_t b = __byte_perm(w, 0x4B000000u, i & 1 ? 0x7653 : 0x7651);
-        f[i] = mul2(add2(f2(__uint_as_float(a), __uint_as_float(b)), zero), scale);
+        f[i] = f2(__uint_as_float(a), __uint_as_float(b));
+    }
+    if (e > 230) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = mul2(add2(f[i], both(-8388736.f)), scale);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = fma2(f[i], scale, bias);
     }
 }
 
-// The 8-bit form of 8 bf16 channels; all 32 lanes call it, and the four lanes 4 i..4 i + 3
-// hold a group (zeros behind a row's end).  The sum x 2^-k + 1.5 * 2^23 rounds to the
-// nearest integer, ties to even, and leaves it in the low byte.
-__device__ __forceinline__ void pack8(const uint4 &w, uint2 &q, uint32_t &e)
+// The larger of each pair of halves, as unsigned numbers: for magnitudes of bf16 numbers
+// their order, infinities and NaNs above all.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
 {
-    uint32_t top = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-    top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The 8-bit form of V vectors of 8 bf16 channels; all 32 lanes call it, and 4 / V neighbouring
+// lanes hold a group (zeros behind a row's end).  The sum x 2^-k + 1.5 * 2^23 rounds to the
+// nearest integer, ties to even, and leaves it in the low byte.
+template <int V>
+__device__ __forceinline__ void pack8(const uint4 (&w)[V], uint2 (&q)[V], uint32_t &e)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        top = max2(max2(top, max2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu)), max2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu));
+#pragma unroll
+    for (int o = 1; o < 4 / V; o *= 2) top = max2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     top = max(top & 0xFFFFu, top >> 16);
-    const bool bad = top >= 0x7F80u;
     const int k = min(max((int)((top + 1u) >> 7) - 6, 1), 248);
     const f32x2 scale = both(__uint_as_float((uint32_t)(254 - k) << 23)), magic = both(12582912.f);
-    f32x2 f[4];
-    wide8(w, f);
-    uint32_t r[8];
+    e = top >= 0x7F80u ? 255u : (uint32_t)k;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[i] = fma2(f[i], scale, magic);
-        if (top == 0x7F7Fu)                    // the largest bf16 number is 127.5 * 2^121
-            f[i] = f2(fminf(fmaxf(lo(f[i]), 12582912.f - 127.f), 12582912.f + 127.f),
-                      fminf(fmaxf(hi(f[i]), 12582912.f - 127.f), 12582912.f + 127.f));
-        r[2 * i] = __float_as_uint(lo(f[i]));
-        r[2 * i + 1] = __float_as_uint(hi(f[i]));
+    for (int i = 0; i < V; ++i) {
+        f32x2 f[4];
+        wide8(w[i], f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = fma2(f[j], scale, magic);
+        if (top >= 0x7F7Fu) {                  // the largest bf16 number is 127.5 * 2^121; what is not finite is 0
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f[j] = top > 0x7F7Fu ? magic
+                                     : f2(fminf(fmaxf(lo(f[j]), 12582912.f - 127.f), 12582912.f + 127.f),
+                                          fminf(fmaxf(hi(f[j]), 12582912.f - 127.f), 12582912.f + 127.f));
+        }
+        uint32_t r[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[2 * j] = __float_as_uint(lo(f[j])), r[2 * j + 1] = __float_as_uint(hi(f[j]));
+        q[i].x = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
+        q[i].y = __byte_perm(__byte_perm(r[4], r[5], 0x0040), __byte_perm(r[6], r[7], 0x0040), 0x5410);
     }
-    q.x = __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040), 0x5410);
-    q.y = __byte_perm(__byte_perm(r[4], r[5], 0x0040), __byte_perm(r[6], r[7], 0x0040), 0x5410);
-    e = (uint32_t)k;
-    if (bad) q = make_uint2(0, 0), e = 255;
 }
 
-// Vector v (channels 8 v..) of a row to its place; lane 4 i writes the group's byte.
+// Vector v (channels 8 v..) of a row to its place, four lanes a group; lane 4 i writes the
+// group's byte.
 __device__ __forceinline__ void put8(const Act8 &o, uint32_t r, uint32_t t, uint32_t v, bool on, const uint4 &w)
 {
-    uint2 q;
+    const uint4 one[1] = {w};
+    uint2 q[1];
+    uint32_t e;
+    pack8(one, q, e);
+    if (!on) return;
+    __stcs((uint2 *)(o.q.at(r, t) + v * 8), q[0]);
+    if (v % 4 == 0) *(uint8_t *)(o.e.at(r, t) + v / 4) = (uint8_t)e;
+}
+
+// ------------------------------------------------------------ 16 channels of a Spot
+// WIDE: bf16 rows on 32-byte and bytes on 16-byte boundaries, N a multiple of 16.
+template <bool WIDE>
+__device__ __forceinline__ void get16(const Rows &o, const Spot &s, uint4 (&w)[2])
+{
+    w[0] = w[1] = make_uint4(0, 0, 0, 0);
+    if (!s.on) return;
+    const char *const p = o.at(s.r, s.t) + s.c * 2;
+    if (WIDE) {
+        ld8_ef(p, w[0], w[1]);
+    } else {
+        w[0] = __ldcs((const uint4 *)p);
+        if (s.all) w[1] = __ldcs((const uint4 *)p + 1);
+    }
+}
+template <bool WIDE>
+__device__ __forceinline__ void set16(const Rows &o, const Spot &s, const uint4 &a, const uint4 &b)
+{
+    if (!s.on) return;
+    char *const p = o.at(s.r, s.t) + s.c * 2;
+    if (WIDE) {
+        st8<kStEvictFirst>(p, a, b);
+    } else {
+        __stcs((uint4 *)p, a);
+        if (s.all) __stcs((uint4 *)p + 1, b);
+    }
+}
+template <bool WIDE>
+__device__ __forceinline__ void get16(const Act8 &o, const Spot &s, uint4 &q, uint32_t &e)
+{
+    q = make_uint4(0, 0, 0, 0);
+    e = 1;
+    if (!s.on) return;
+    const char *const p = o.q.at(s.r, s.t) + s.c;
+    e = __ldcs((const uint8_t *)o.e.at(s.r, s.t) + s.c / 32);
+    if (WIDE) {
+        q = __ldcs((const uint4 *)p);
+    } else {
+        const uint2 a = __ldcs((const uint2 *)p);
+        q.x = a.x;
+        q.y = a.y;
+        if (!s.all) return;
+        const uint2 b = __ldcs((const uint2 *)p + 1);
+        q.z = b.x;
+        q.w = b.y;
+    }
+}
+template <bool WIDE>
+__device__ __forceinline__ void set16(const Act8 &o, const Spot &s, const uint4 (&w)[2])
+{
+    uint2 q[2];
     uint32_t e;
     pack8(w, q, e);
-    if (!on) return;
-    __stcs((uint2 *)(o.q.at(r, t) + v * 8), q);
-    if (v % 4 == 0) *(uint8_t *)(o.e.at(r, t) + v / 4) = (uint8_t)e;
+    if (!s.on) return;
+    char *const p = o.q.at(s.r, s.t) + s.c;
+    if (WIDE) {
+        __stcs((uint4 *)p, make_uint4(q[0].x, q[0].y, q[1].x, q[1].y));
+    } else {
+        __stcs((uint2 *)p, q[0]);
+        if (s.all) __stcs((uint2 *)p + 1, q[1]);
+    }
+    if (s.c % 32 == 0) *(uint8_t *)(o.e.at(s.r, s.t) + s.c / 32) = (uint8_t)e;
 }
 
 // ------------------------------------------------------------ host
 inline Rows rows_of(const rc_rows &r) { return Rows{(char *)r.base, r.slot, r.row}; }
+inline bool wide_of(const rc_rows &r, size_t bytes) { return !(((uintptr_t)r.base | r.slot | r.row) & (bytes - 1)); }
 inline Act8 act8_of(const rc_act8 &a) { return Act8{rows_of(a.q), rows_of(a.e)}; }
 
 } // namespace rc

@@ -71,32 +71,58 @@ __device__ __forceinline__ uint2 lds8(uint32_t a)
     return v;
 }
 
-// Sums of K values over the block, the same in every thread: lanes in a fixed
-// pattern, then the warps in order.  Two areas take turns, so one barrier does.
+// Sums of K values over the block, the same in every thread, always added in the same
+// pattern.  In a warp the values are divided over the lanes while they are added (K values
+// cost 9 exchanges in the place of 5 K), each group of 32 / PAD lanes ending with one of
+// them; then every warp adds up all warps' sums alike.  Two areas take turns, so one
+// barrier does; the places of warps that do not exist hold zeros.
+constexpr int kAreaRow = 36;                            // floats of a value's row: 32 warps, and no bank twice
+constexpr int kAreaBytes = 2 * 8 * kAreaRow * 4;
+
 template <int K>
 __device__ __forceinline__ void block_sum(float (&v)[K], float *area, int &turn)
 {
-    constexpr int PAD = K == 1 ? 1 : K <= 2 ? 2 : K <= 4 ? 4 : 8;
+    constexpr int PAD = K == 1 ? 1 : K == 2 ? 2 : 8, GROUP = 32 / PAD;
+    const uint32_t lane = threadIdx.x & 31;
+    float s[PAD];
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < PAD; ++k) s[k] = k < K ? v[k] : 0.f;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return;
-    float *const red = area + turn * (32 * 8);
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0)
+    for (int n = PAD / 2, o = 16; n; n /= 2, o /= 2)
 #pragma unroll
-        for (int k = 0; k < K; ++k) red[(threadIdx.x >> 5) * PAD + k] = v[k];
-    __syncthreads();
-    float s[K] = {};
-    for (int w = 0; w < warps; ++w)
+        for (int k = 0; k < n; ++k) {
+            const bool upper = lane & o;
+            const float keep = upper ? s[k + n] : s[k], give = upper ? s[k] : s[k + n];
+            s[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+        }
 #pragma unroll
-        for (int k = 0; k < K; ++k) s[k] += red[w * PAD + k];
+    for (int o = GROUP / 2; o; o /= 2) s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], o);
+    if (blockDim.x > 32) {
+        float *const row = area + turn * (8 * kAreaRow) + lane / GROUP * kAreaRow;
+        turn ^= 1;
+        if (lane % GROUP == 0) row[threadIdx.x >> 5] = s[0];
+        __syncthreads();
+        if (PAD == 8) {
+            const float4 a = *(const float4 *)(row + lane % 4 * 8), b = *(const float4 *)(row + lane % 4 * 8 + 4);
+            s[0] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+        } else if (PAD == 2) {
+            const float2 a = *(const float2 *)(row + lane % 16 * 2);
+            s[0] = a.x + a.y;
+        } else {
+            s[0] = row[lane];
+        }
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = s[k];
+        for (int o = GROUP / 2; o; o /= 2) s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], o);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = PAD == 1 ? s[0] : __shfl_sync(0xFFFFFFFFu, s[0], k * GROUP);
 }
-constexpr int kAreaBytes = 2 * 32 * 8 * 4;
+
+__device__ __forceinline__ void clear_area(float *area)
+{
+    for (int i = threadIdx.x; i < kAreaBytes / 4; i += blockDim.x) area[i] = 0.f;
+    __syncthreads();
+}
 
 // The weights w and gamma_pre of vector v.  In shared memory the first and the last
 // four channels of the vectors lie in planes, 16 bytes a lane.
@@ -183,12 +209,14 @@ struct Scales {
     }
 };
 
-// Vector v of row `row` (t of slot r) of y or dy, whose slots hold `chunk` channels of all rows.
-__device__ __forceinline__ char *place(const Rows &o, uint32_t chunk, uint32_t row, uint32_t r, uint32_t t, uint32_t v)
+// y or dy, whose slots hold `chunk` channels of all rows (0: rows of all channels): the start
+// of row `row` (t of slot r), and behind it vector v.
+__device__ __forceinline__ char *row_of(const Rows &o, uint32_t chunk, uint32_t row, uint32_t r, uint32_t t) { return chunk ? o.at(0, row) : o.at(r, t); }
+__device__ __forceinline__ size_t behind(const Rows &o, uint32_t chunk, uint32_t v)
 {
-    if (!chunk) return o.at(r, t) + v * 16;
-    const uint32_t c = v * 8, s = c / chunk;
-    return o.at(s, row) + (c - s * chunk) * 2;
+    if (!chunk) return (size_t)v * 16;
+    const uint32_t s = v * 8 / chunk;
+    return s * o.slot + (v * 8 - s * chunk) * 2;
 }
 
 // ------------------------------------------------------------ forward
@@ -202,16 +230,21 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const Params p)
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(after + (WHERE == IN_SHARED ? 8 * p.N : 0)) + threadIdx.x * 16;
     Scales<VPT, WHERE, PRE> ws;
     ws.init(p, (float *)after);
+    clear_area(area);
     int turn = 0;
+    size_t yoff[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) yoff[i] = behind(p.y, p.y_chunk, i * threads + threadIdx.x);
     auto fetch = [&](uint32_t row, int stage) {
         if (row < p.rows) {
             const uint32_t r = p.tokens(row), t = row - r * p.T;
+            const char *const yrow = row_of(p.y, p.y_chunk, row, r, t), *const rrow = p.res.at(r, t);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const uint32_t v = i * threads + threadIdx.x;
                 if (v >= p.vecs) continue;
-                copy<16>(ring + stage * stage_bytes + i * 16 * threads, place(p.y, p.y_chunk, row, r, t, v));
-                copy<16>(ring + stage * stage_bytes + (VPT + i) * 16 * threads, p.res.at(r, t) + v * 16);
+                copy<16>(ring + stage * stage_bytes + i * 16 * threads, yrow + yoff[i]);
+                copy<16>(ring + stage * stage_bytes + (VPT + i) * 16 * threads, rrow + v * 16);
             }
         }
         copies_done();
@@ -302,8 +335,15 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(after + (WHERE == IN_SHARED ? 8 * p.N : 0));
     Scales<VPT, WHERE, PRE> ws;
     ws.init(p, (float *)after);
+    clear_area(area);
     const uint32_t r = blockIdx.x / p.per, first = blockIdx.x - r * p.per;
     int turn = 0;
+    size_t yoff[HELD ? 1 : VPT], dyoff[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        if (!HELD) yoff[i] = behind(p.y, p.y_chunk, i * threads + threadIdx.x);
+        dyoff[i] = behind(p.dy, p.dy_chunk, i * threads + threadIdx.x);
+    }
     auto fetch = [&](uint32_t t, int stage) {
         if (t < p.T) {
             const uint32_t at = ring + stage * stage_bytes + threadIdx.x * YB, dat = ring + stage * stage_bytes + 2 * in_bytes + threadIdx.x * 16;
@@ -315,7 +355,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
                     copy<8>(at + i * YB * threads, p.y8.q.at(r, t) + v * 8);
                     copy<8>(at + in_bytes + i * YB * threads, p.res8.q.at(r, t) + v * 8);
                 } else {
-                    copy<16>(at + i * YB * threads, place(p.y, p.y_chunk, r * p.T + t, r, t, v));
+                    copy<16>(at + i * YB * threads, row_of(p.y, p.y_chunk, r * p.T + t, r, t) + yoff[i]);
                     copy<16>(at + in_bytes + i * YB * threads, p.res.at(r, t) + v * 16);
                 }
                 if (p.dh.base) copy<16>(dat + i * 16 * threads, p.dh.at(r, t) + v * 16);
@@ -433,7 +473,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
                 if (POST) w[k] = mul2(fma2(y[i][k], both(-m), w[k]), both(rp));
             }
             __stcs((uint4 *)(p.dres.at(r, t) + v * 16), narrow8(d));
-            __stcs((uint4 *)place(p.dy, p.dy_chunk, r * p.T + t, r, t, v), narrow8(w));
+            __stcs((uint4 *)(row_of(p.dy, p.dy_chunk, r * p.T + t, r, t) + dyoff[i]), narrow8(w));
         }
     }
     if (!p.sums) return;
@@ -453,67 +493,80 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
     }
 }
 
-// Sum z of slot y over the blocks of the slot, for 32 channels: warp k adds parts k,
-// k + 32, ... and the warps' sums are added in order.  CLEAR: in a caller's workspace
+// Sum z of slot y over the blocks of the slot, four channels a lane: warp k adds parts k,
+// k + SUM_WARPS, ... and the warps' sums are added in order.  CLEAR: in a caller's workspace
 // the parts are zeroed once read, because other calls keep signal words there.
-constexpr int SUM_WARPS = 32;
-
-template <bool CLEAR>
+template <bool CLEAR, int SUM_WARPS>
 __global__ void __launch_bounds__(32 * SUM_WARPS) k_block_sums(const Params p)
 {
-    __shared__ float red[SUM_WARPS][33];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, slot = blockIdx.y, which = blockIdx.z;
+    __shared__ float4 red[SUM_WARPS][32];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = (blockIdx.x * 32 + lane) * 4, slot = blockIdx.y, which = blockIdx.z;
     asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written
     const size_t step = (size_t)p.sums * p.N;
     float *const part = p.part + (size_t)slot * p.per * step + (size_t)which * p.N + c;
-    float s = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < p.N)
-#pragma unroll 4
-        for (uint32_t b = warp; b < (uint32_t)p.per; b += SUM_WARPS) s += part[b * step];
-    if (CLEAR && c < p.N)
-        for (uint32_t b = warp; b < (uint32_t)p.per; b += SUM_WARPS) part[b * step] = 0.f;
+#pragma unroll 8
+        for (uint32_t b = warp; b < (uint32_t)p.per; b += SUM_WARPS) {
+            const float4 v = *(const float4 *)(part + b * step);
+            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+    if (CLEAR && c < p.N)                                  // in a loop of its own: stores would hold up the loads
+        for (uint32_t b = warp; b < (uint32_t)p.per; b += SUM_WARPS) *(float4 *)(part + b * step) = make_float4(0.f, 0.f, 0.f, 0.f);
     red[warp][lane] = s;
     __syncthreads();
     if (warp || c >= p.N) return;
-    s = 0.f;
 #pragma unroll
-    for (int k = 0; k < SUM_WARPS; ++k) s += red[k][lane];
-    const size_t at = (size_t)slot * p.N + c;
+    for (int k = 1; k < SUM_WARPS; ++k) {
+        const float4 v = red[k][lane];
+        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+    }
+    auto put = [&](float *to, float f, const float *g) {
+        const float4 w = g ? __ldg((const float4 *)(g + c)) : make_float4(1.f, 1.f, 1.f, 1.f);
+        to += (size_t)slot * p.N + c;                      // a caller's [P][N] floats, perhaps not on 16 bytes
+        to[0] = f * s.x * w.x;
+        to[1] = f * s.y * w.y;
+        to[2] = f * s.z * w.z;
+        to[3] = f * s.w * w.w;
+    };
     if (which == 0 && (p.gpost || p.gate)) {
-        s *= p.alpha;
-        if (p.gpost) p.dpost[at] = p.gate ? s * p.gate[c] : s;
-        if (p.gate) p.dgate[at] = p.gpost ? s * p.gpost[c] : s;
+        if (p.gpost) put(p.dpost, p.alpha, p.gate);
+        if (p.gate) put(p.dgate, p.alpha, p.gpost);
     } else {
-        p.dpre[at] = s;
+        put(p.dpre, 1.f, nullptr);
     }
 }
 
 // ------------------------------------------------------------ host
-// Vectors a thread: rows up to 8192 channels in one or two, wider ones in four.
+// Vectors of 8 channels a thread.  Two halve what a row costs besides its channels (the
+// sums over the block above all): 8192 x 4096 forward with checkpoints 58 us against 67
+// with one, the gradient 72 against 100.  Where no SM gets a second row only its latency
+// counts, and one is quicker (8 rows 4.1 us against 4.5).  Rows above 8192 channels take four.
 struct Shape {
-    int vpt, threads, stages;
+    int vpt, threads, stages, regs;
     size_t smem;
 };
 
-static Shape shape_of(const rc_block_norm_args &a, bool grad)
+static Shape shape_of(const rc_block_norm_args &a, bool grad, int sms)
 {
     const int vecs = a.N / 8;
     Shape s{};
-    s.vpt = vecs > 1024 ? 4 : 1;
+    s.vpt = vecs > 1024 ? 4 : (long long)a.P * a.T <= sms ? 1 : 2;
+    s.regs = s.vpt == 1 ? 64 : 128;                      // what the launch bounds leave a thread
     s.threads = ((vecs + s.vpt - 1) / s.vpt + 31) / 32 * 32;
     const bool held = grad && a.y8.q.base;
     const size_t lane = grad ? (held ? 16 : 32) + (a.gamma_pre ? 32 : 16) : 32;
     const size_t stage = lane * s.vpt * s.threads, fixed = kAreaBytes + (grad && s.vpt < 4 ? (size_t)8 * a.N : 0);
     s.stages = 3;
-    while (s.stages > 1 && fixed + s.stages * stage > (s.threads > 512 ? 220u : 110u) * 1024) --s.stages;
+    while (s.stages > 1 && fixed + s.stages * stage > (s.threads * s.regs > 32768 ? 220u : 110u) * 1024) --s.stages;
     s.smem = fixed + s.stages * stage;
     return s;
 }
 
 // Blocks that an SM holds: by threads, registers (the launch bounds' share) and shared memory.
-static int resident(const Shape &s, int regs)
+static int resident(const Shape &s)
 {
-    const int t = 2048 / s.threads, r = 65536 / (regs * s.threads), m = (int)(227 * 1024 / (s.smem + 1024));
+    const int t = 2048 / s.threads, r = 65536 / (s.regs * s.threads), m = (int)(227 * 1024 / (s.smem + 1024));
     int n = t < r ? t : r;
     n = n < m ? n : m;
     return n < 1 ? 1 : n > 32 ? 32 : n;
@@ -521,7 +574,7 @@ static int resident(const Shape &s, int regs)
 
 static int blocks_of_slot(const rc_block_norm_args &a, const Shape &s, int sms)
 {
-    const int most = (sms * resident(s, s.vpt == 4 ? 128 : 64) + a.P - 1) / a.P;
+    const int most = (sms * resident(s) + a.P - 1) / a.P;
     return a.T < most ? (a.T < 1 ? 1 : a.T) : most;
 }
 
@@ -540,13 +593,16 @@ static cudaError_t launch(bool grad, bool held, unsigned blocks, const Shape &s,
 {
     if (!grad) {
         if (s.vpt == 1) return start<k_block_norm<1, 1024, 1, IN_REGISTERS, POST, PRE>>(blocks, s, p, st);
+        if (s.vpt == 2) return start<k_block_norm<2, 512, 1, IN_REGISTERS, POST, PRE>>(blocks, s, p, st);
         return start<k_block_norm<4, 512, 1, IN_GLOBAL, POST, PRE>>(blocks, s, p, st);
     }
     if (held) {
         if (s.vpt == 1) return start<k_block_norm_bwd<1, 1024, 1, IN_SHARED, true, POST, PRE>>(blocks, s, p, st);
+        if (s.vpt == 2) return start<k_block_norm_bwd<2, 512, 1, IN_SHARED, true, POST, PRE>>(blocks, s, p, st);
         return start<k_block_norm_bwd<4, 512, 1, IN_GLOBAL, true, POST, PRE>>(blocks, s, p, st);
     }
     if (s.vpt == 1) return start<k_block_norm_bwd<1, 1024, 1, IN_SHARED, false, POST, PRE>>(blocks, s, p, st);
+    if (s.vpt == 2) return start<k_block_norm_bwd<2, 512, 1, IN_SHARED, false, POST, PRE>>(blocks, s, p, st);
     return start<k_block_norm_bwd<4, 512, 1, IN_GLOBAL, false, POST, PRE>>(blocks, s, p, st);
 }
 
@@ -560,15 +616,16 @@ static cudaError_t launch_sums(const Params &p, int P, cudaStream_t st)
 {
     // set up while the gradient runs; its blocks start when that has ended
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((p.N + 31) / 32, (unsigned)P, (unsigned)p.sums);
-    cfg.blockDim = dim3(32 * SUM_WARPS);
+    cfg.gridDim = dim3((p.N + 127) / 128, (unsigned)P, (unsigned)p.sums);
+    const bool few = cfg.gridDim.x * cfg.gridDim.y * cfg.gridDim.z < 128;      // blocks of 32 warps, if blocks are few
+    cfg.blockDim = dim3(few ? 1024 : 256);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return p.clear ? cudaLaunchKernelEx(&cfg, k_block_sums<true>, p) : cudaLaunchKernelEx(&cfg, k_block_sums<false>, p);
+    return cudaLaunchKernelEx(&cfg, p.clear ? (few ? k_block_sums<true, 32> : k_block_sums<true, 8>) : (few ? k_block_sums<false, 32> : k_block_sums<false, 8>), p);
 }
 
 static int sums_of(const rc_block_norm_args &a) { return (a.gamma_post || a.gate) + (a.gamma_pre ? 1 : 0); }
@@ -595,6 +652,8 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
     const bool held = grad && a.y8.q.base, some = a.T > 0;
     if (((uintptr_t)a.gamma_post | (uintptr_t)a.gate | (uintptr_t)a.gamma_pre) & 15u)
         return set_error(RC_ERR_INVALID, "gamma_post, gate and gamma_pre must be 16-byte aligned");
+    if (((uintptr_t)a.dgamma_post | (uintptr_t)a.dgate | (uintptr_t)a.dgamma_pre) & 3u)
+        return set_error(RC_ERR_INVALID, "dgamma_post, dgate and dgamma_pre must be 4-byte aligned");
     if (grad && ((uintptr_t)a.workspace & 255u)) return set_error(RC_ERR_INVALID, "workspace must be 256-byte aligned");
     auto rows = [&](rc_rows &x, const char *name, bool cols) {
         return cols ? check_rows(x, name, a.P, a.P * a.T, chunk, 16) : check_rows(x, name, a.P, a.T, bytes, 16);
@@ -645,7 +704,7 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
     if (rc_) return rc_;
     int sms = 0;
     if ((rc_ = device_sms(&sms))) return rc_;
-    const Shape s = shape_of(a, grad);
+    const Shape s = shape_of(a, grad, sms);
     Params p{};
     p.y = rows_of(a.y), p.res = rows_of(a.res), p.h = rows_of(a.h), p.z = rows_of(a.z);
     p.dh = rows_of(a.dh), p.dz = rows_of(a.dz), p.dy = rows_of(a.dy), p.dres = rows_of(a.dres);
@@ -665,7 +724,7 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
     p.inv_n = 1.f / (float)a.N;
     unsigned blocks;
     if (!grad) {
-        const uint32_t most = (uint32_t)(sms * resident(s, s.vpt == 4 ? 128 : 64));
+        const uint32_t most = (uint32_t)(sms * resident(s));
         blocks = p.rows < most ? p.rows : most;
     } else {
         p.per = blocks_of_slot(a, s, sms);
@@ -697,6 +756,6 @@ extern "C" size_t block_norm_bwd_workspace_bytes(const rc_block_norm_args *args)
     using namespace rc::bn;
     int sms = 0;
     if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
-    const Shape s = shape_of(*args, true);
+    const Shape s = shape_of(*args, true, sms);
     return rc::kWsHead + (size_t)blocks_of_slot(*args, s, sms) * args->P * sums_of(*args) * args->N * 4;
 }

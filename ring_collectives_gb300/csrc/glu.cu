@@ -3,8 +3,9 @@
 //
 // Both activations are x s(c(x)), s the logistic function: c(x) = x, or for the tanh
 // form of gelu 2 sqrt(2/pi) (x + 0.044715 x^3), because (1 + tanh y) / 2 = s(2 y).
-// So act'(x) = s + x c'(x) s (1 - s), with s and 1 - s = s(-c) each from an exponential
-// of its own sign: neither loses its small values by cancellation.
+// So act'(x) = s + x c'(x) s (1 - s).  With e = exp(-|c|) and g = 1 / (1 + e), s and 1 - s
+// are g and e g, in the order of c's sign: one exponential and one reciprocal for both, no
+// cancellation and no overflow.
 //
 // Bound by memory: 6 bytes an element forward and up to 5 more for checkpoints, 10
 // to 13 in the gradient.
@@ -24,16 +25,19 @@ struct Params {
     Flat f;
 };
 
-// rcp.approx keeps subnormal results, is exact to one unit in the last place, and takes
-// an infinity to 0.
-__device__ __forceinline__ float rcp(float x)
-{
-    float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 constexpr float kRoot = 1.5957691216057308f;     // 2 sqrt(2 / pi)
+
+// s(c), and 1 - s(c) in t.  Both approximations are within two units in the last place (of
+// the exponent's, 1.17 |c| more); an exponential below the normal numbers is 0.
+__device__ __forceinline__ float logistic(float c, float &t)
+{
+    float e, g;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(c) * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(g) : "f"(1.f + e));
+    const float l = e * g;
+    t = c < 0.f ? g : l;
+    return c < 0.f ? l : g;
+}
 
 template <int ACT>
 __device__ __forceinline__ float arg(float x)
@@ -44,116 +48,97 @@ __device__ __forceinline__ float arg(float x)
 template <int ACT>
 __device__ __forceinline__ float act(float x)
 {
-    return x * rcp(1.f + __expf(-arg<ACT>(x)));
+    float t;
+    return x * logistic(arg<ACT>(x), t);
 }
 
 // act(x), and act'(x) in d.
 template <int ACT>
 __device__ __forceinline__ float act_grad(float x, float &d)
 {
-    const float c = arg<ACT>(x), s = rcp(1.f + __expf(-c)), t = rcp(1.f + __expf(c));
+    float t;
+    const float s = logistic(arg<ACT>(x), t);
     const float slope = ACT == RC_GLU_SILU ? x : kRoot * x * fmaf(0.134145f * x, x, 1.f);
     d = s * fmaf(slope, t, 1.f);
     return x * s;
 }
 
-template <int ACT, int U>
+template <int ACT, bool WIDE>
 __global__ void __launch_bounds__(THREADS) k_glu(const Params p)
 {
-    const uint64_t first = (uint64_t)blockIdx.x * (THREADS * U);
+    const uint64_t first = (uint64_t)blockIdx.x * THREADS;
     const uint32_t row0 = (uint32_t)(first / p.f.lanes.d), rem0 = (uint32_t)(first - (uint64_t)row0 * p.f.lanes.d);
-    uint4 wa[U], wb[U];
+    const Spot s(p.f, row0, rem0, threadIdx.x);
+    uint4 wa[2], wb[2], wh[2];
+    get16<WIDE>(p.a, s, wa);
+    get16<WIDE>(p.b, s, wb);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const Spot s(p.f, row0, rem0, u * THREADS + threadIdx.x);
-        wa[u] = wb[u] = make_uint4(0, 0, 0, 0);
-        if (s.on) {
-            wa[u] = __ldcs((const uint4 *)(p.a.at(s.r, s.t) + s.v * 16));
-            wb[u] = __ldcs((const uint4 *)(p.b.at(s.r, s.t) + s.v * 16));
-        }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const Spot s(p.f, row0, rem0, u * THREADS + threadIdx.x);
+    for (int u = 0; u < 2; ++u) {
         f32x2 a[4], b[4];
         wide8(wa[u], a);
         wide8(wb[u], b);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = mul2(f2(act<ACT>(lo(a[i])), act<ACT>(hi(a[i]))), b[i]);
-        const uint4 h = narrow8(a);
-        if (s.on) __stcs((uint4 *)(p.h.at(s.r, s.t) + s.v * 16), h);
-        if (p.a8.q.base) put8(p.a8, s.r, s.t, s.v, s.on, wa[u]);
-        if (p.b8.q.base) put8(p.b8, s.r, s.t, s.v, s.on, wb[u]);
-        if (p.h8.q.base) put8(p.h8, s.r, s.t, s.v, s.on, h);
+        wh[u] = narrow8(a);
     }
+    set16<WIDE>(p.h, s, wh[0], wh[1]);
+    if (p.a8.q.base) set16<WIDE>(p.a8, s, wa);
+    if (p.b8.q.base) set16<WIDE>(p.b8, s, wb);
+    if (p.h8.q.base) set16<WIDE>(p.h8, s, wh);
 }
 
-template <int ACT, bool HELD, int U>
+template <int ACT, bool HELD, bool WIDE>
 __global__ void __launch_bounds__(THREADS) k_glu_bwd(const Params p)
 {
-    const uint64_t first = (uint64_t)blockIdx.x * (THREADS * U);
+    const uint64_t first = (uint64_t)blockIdx.x * THREADS;
     const uint32_t row0 = (uint32_t)(first / p.f.lanes.d), rem0 = (uint32_t)(first - (uint64_t)row0 * p.f.lanes.d);
-    uint4 wd[U], wa[U], wb[U];
-    uint2 qa[U], qb[U];
-    uint32_t ea[U], eb[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const Spot s(p.f, row0, rem0, u * THREADS + threadIdx.x);
-        wd[u] = wa[u] = wb[u] = make_uint4(0, 0, 0, 0);
-        qa[u] = qb[u] = make_uint2(0, 0);
-        ea[u] = eb[u] = 0;
-        if (!s.on) continue;
-        wd[u] = __ldcs((const uint4 *)(p.dh.at(s.r, s.t) + s.v * 16));
-        if (HELD) {
-            qa[u] = __ldcs((const uint2 *)(p.a8.q.at(s.r, s.t) + s.v * 8));
-            qb[u] = __ldcs((const uint2 *)(p.b8.q.at(s.r, s.t) + s.v * 8));
-            ea[u] = *(const uint8_t *)(p.a8.e.at(s.r, s.t) + s.v / 4);
-            eb[u] = *(const uint8_t *)(p.b8.e.at(s.r, s.t) + s.v / 4);
-        } else {
-            wa[u] = __ldcs((const uint4 *)(p.a.at(s.r, s.t) + s.v * 16));
-            wb[u] = __ldcs((const uint4 *)(p.b.at(s.r, s.t) + s.v * 16));
-        }
+    const Spot s(p.f, row0, rem0, threadIdx.x);
+    uint4 wd[2], wa[2], wb[2], wh[2], qa, qb;
+    uint32_t ea, eb;
+    if (HELD) {
+        get16<WIDE>(p.a8, s, qa, ea);
+        get16<WIDE>(p.b8, s, qb, eb);
+    } else {
+        get16<WIDE>(p.a, s, wa);
+        get16<WIDE>(p.b, s, wb);
     }
+    get16<WIDE>(p.dh, s, wd);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const Spot s(p.f, row0, rem0, u * THREADS + threadIdx.x);
-        f32x2 a[4], b[4], d[4];
+    for (int u = 0; u < 2; ++u) {
+        f32x2 a[4], b[4], d[4], h[4];
         if (HELD) {
-            held8(qa[u], ea[u], a);
-            held8(qb[u], eb[u], b);
+            held8(u ? make_uint2(qa.z, qa.w) : make_uint2(qa.x, qa.y), ea, a);
+            held8(u ? make_uint2(qb.z, qb.w) : make_uint2(qb.x, qb.y), eb, b);
         } else {
             wide8(wa[u], a);
             wide8(wb[u], b);
         }
         wide8(wd[u], d);
-        f32x2 da[4], db[4], h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float d0, d1;
             const float f0 = act_grad<ACT>(lo(a[i]), d0), f1 = act_grad<ACT>(hi(a[i]), d1);
             const f32x2 f = f2(f0, f1);
             h[i] = mul2(f, b[i]);
-            db[i] = mul2(d[i], f);
-            da[i] = mul2(mul2(d[i], b[i]), f2(d0, d1));
+            a[i] = mul2(mul2(d[i], b[i]), f2(d0, d1));
+            b[i] = mul2(d[i], f);
         }
-        const uint4 hw = narrow8(h);
-        if (s.on) {
-            __stcs((uint4 *)(p.da.at(s.r, s.t) + s.v * 16), narrow8(da));
-            __stcs((uint4 *)(p.db.at(s.r, s.t) + s.v * 16), narrow8(db));
-            if (p.h.base) __stcs((uint4 *)(p.h.at(s.r, s.t) + s.v * 16), hw);
-        }
-        if (p.h8.q.base) put8(p.h8, s.r, s.t, s.v, s.on, hw);
+        wa[u] = narrow8(a);
+        wb[u] = narrow8(b);
+        wh[u] = narrow8(h);
     }
+    set16<WIDE>(p.da, s, wa[0], wa[1]);
+    set16<WIDE>(p.db, s, wb[0], wb[1]);
+    if (p.h.base) set16<WIDE>(p.h, s, wh[0], wh[1]);
+    if (p.h8.q.base) set16<WIDE>(p.h8, s, wh);
 }
 
-template <int ACT>
-static void launch(const Params &p, bool grad, cudaStream_t st)
+template <int ACT, bool WIDE>
+static void launch(const Params &p, bool grad, unsigned blocks, cudaStream_t st)
 {
-    constexpr int U = 2;
-    const unsigned blocks = (unsigned)p.f.blocks(THREADS * U);
-    if (!grad) k_glu<ACT, U><<<blocks, THREADS, 0, st>>>(p);
-    else if (p.a8.q.base) k_glu_bwd<ACT, true, U><<<blocks, THREADS, 0, st>>>(p);
-    else k_glu_bwd<ACT, false, U><<<blocks, THREADS, 0, st>>>(p);
+    if (!grad) k_glu<ACT, WIDE><<<blocks, THREADS, 0, st>>>(p);
+    else if (p.a8.q.base) k_glu_bwd<ACT, true, WIDE><<<blocks, THREADS, 0, st>>>(p);
+    else k_glu_bwd<ACT, false, WIDE><<<blocks, THREADS, 0, st>>>(p);
 }
 
 static int run(const rc_glu_args *args, bool grad, void *stream)
@@ -195,8 +180,14 @@ static int run(const rc_glu_args *args, bool grad, void *stream)
     Params p{rows_of(g.a), rows_of(g.b), rows_of(g.h), rows_of(g.dh), rows_of(g.da), rows_of(g.db), act8_of(g.a8), act8_of(g.b8),
              act8_of(g.h8), Flat::of(g.P, g.T, g.N)};
     if (p.f.blocks(THREADS) > 0x7FFFFFFFull) return set_error(RC_ERR_INVALID, "P*T rows of N=%d channels are too many", g.N);
-    if (g.act == RC_GLU_SILU) launch<RC_GLU_SILU>(p, grad, (cudaStream_t)stream);
-    else launch<RC_GLU_GELU>(p, grad, (cudaStream_t)stream);
+    const unsigned blocks = (unsigned)p.f.blocks(THREADS);
+    // operands that are not given have null bases, and strides that a caller may leave as they are
+    auto wide_if = [](const rc_rows &r, size_t b) { return !r.base || wide_of(r, b); };
+    const bool wide = g.N % 16 == 0 && wide_if(g.a, 32) && wide_if(g.b, 32) && wide_if(g.h, 32) && (!grad || (wide_of(g.dh, 32) && wide_of(g.da, 32) && wide_of(g.db, 32))) &&
+                      wide_if(g.a8.q, 16) && wide_if(g.b8.q, 16) && wide_if(g.h8.q, 16);
+    const auto go = g.act == RC_GLU_SILU ? (wide ? launch<RC_GLU_SILU, true> : launch<RC_GLU_SILU, false>)
+                                         : (wide ? launch<RC_GLU_GELU, true> : launch<RC_GLU_GELU, false>);
+    go(p, grad, blocks, (cudaStream_t)stream);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return set_error(RC_ERR_CUDA, "glu launch: %s", cudaGetErrorString(err));
     return RC_OK;
