@@ -75,16 +75,7 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
 // it under one lane's branch, issuing took longer than executing: at 4096
 // tokens x 32 heads of 128 the forward pass spent 2300 clocks of issue on each
 // tile's 1024 clocks of MMA.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-    return e != 0;
-}
-
-// A value that is the same in every lane, in a form the compiler knows to be so.
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
-
+//
 // Descriptors (smem_desc_sw128, smem_desc_mn_sw128) as a varying low word -- the
 // address in 16-byte units, and the block step of an MN-major tile -- and this high word.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
@@ -138,52 +129,6 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, boo
 #pragma unroll
     for (int kk = 0; kk < KT / 16; ++kk)
         mma_ts(d, a + (kk >> 2) * half + (kk & 3) * 8, bd + 128 * kk, id, kk ? 1u : (first ? 0u : 1u));
-}
-
-// Every lane waits; the same answer in all.  (A wait by one lane, handed on by a
-// shuffle, costs the warp over 100 clocks more: the softmax warps waiting that way
-// made a 16384-token prompt 11 % slower.)
-__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Abort &ab, int where)
-{
-    uint64_t t0 = 0;
-    for (uint32_t it = 0; !__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)); ++it) {
-        if ((it & 63u) != 63u) continue;
-        bool over = *(volatile int *)ab.flag != 0;
-        const uint64_t now = global_timer_ns();
-        if (t0 == 0) t0 = now;
-        if (!over && now - t0 > ab.timeout_ns) {
-            record_timeout(ab, where);
-            over = true;
-        }
-        if (__any_sync(0xFFFFFFFFu, over)) return false;
-    }
-    return true;
-}
-
-// One arrival by a warp whose lanes are all here (no branch around it).
-__device__ __forceinline__ void arrive_warp(uint32_t bar, int lane)
-{
-    __syncwarp();
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"(lane) : "memory");
-}
-
-// The same for a warp in no hurry: asleep between polls, which would take issue
-// slots from the warps that share its scheduler.
-__device__ __forceinline__ bool wait_idle(uint32_t bar, uint32_t parity, const Abort &ab, int where)
-{
-    uint64_t t0 = 0;
-    while (!__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) {
-        __nanosleep(64);
-        bool over = *(volatile int *)ab.flag != 0;
-        const uint64_t now = global_timer_ns();
-        if (t0 == 0) t0 = now;
-        if (!over && now - t0 > ab.timeout_ns) {
-            record_timeout(ab, where);
-            over = true;
-        }
-        if (__any_sync(0xFFFFFFFFu, over)) return false;
-    }
-    return true;
 }
 
 // Stores 16 / 32 columns of this thread's TMEM lane; tmem_wait_st() ends them.

@@ -11,8 +11,10 @@
 // 128 rows n of it in TMEM, and steps over the tokens by 64:
 //   warp 0       copies its 128 n of dy by TMA (tokens and channels past the end
 //                arrive as zeros);
-//   warps 8-15   copy their pieces of 128 k of q ahead with cp.async, each thread into
-//                slots of its own, widen them and write the swizzled tile;
+//   warps 2, 3   copy 128 k of q ahead by cp.async, and the groups' bytes;
+//   warps 8..    widen them into the swizzled tile, groups of four warps taking steps in
+//                turn: from waiting for a stage to its announcement a step takes longer than
+//                its MMAs;
 //   warp 1       (even CTA) issues the MMAs of the pair, M = N = 256;
 //   warps 4-7    take finished tiles from TMEM, while the next one is summed.
 // Whole tiles are dealt out in rounds; the tokens of those that are left over are
@@ -36,12 +38,18 @@ constexpr int STEP = 64;                      // tokens a step
 constexpr int STAGES = 5;
 constexpr int BLOCK = 64 * STEP * 2;          // 64 channels x 64 tokens of bf16
 constexpr int OPERAND = 2 * BLOCK;            // a CTA's half of an operand's stage
-constexpr int DEEP = 5;                       // steps of q that a thread's slots hold
-constexpr int WIDEN = 256, EPILOGUE = 4;      // threads that widen; warps that store
-constexpr int THREADS = 256 + WIDEN;
-constexpr int SLOTS = DEEP * WIDEN * 32;      // 32 bytes of q a thread and step
+constexpr int GROUPS = 3, GROUP = 128;        // groups of threads that widen steps in turn
+constexpr int DEEP = 6;                       // steps of q on their way or waiting to be widened
+constexpr int TOKENS = GROUP / 8;             // a group takes 128 k of as many tokens at a time,
+constexpr int PIECES = STEP / TOKENS;         // so often in a step
+constexpr int STEP_BYTES = STEP * HALF;
+constexpr int EPILOGUE = 4;                   // warps that store
+constexpr int THREADS = 256 + GROUPS * GROUP;
+constexpr int SLOTS = DEEP * STEP_BYTES, ESLOTS = DEEP * STEP * 4;
 constexpr int TMEM_COLS = 512;                // two accumulators
-constexpr int SMEM = STAGES * 2 * OPERAND + SLOTS + 1024 + 256;
+constexpr int SMEM = STAGES * 2 * OPERAND + SLOTS + ESLOTS + 1024 + 512;
+static_assert(SMEM <= 227 * 1024 && TOKENS % 8 == 0, "the stages and slots fit; a thread's tokens share a swizzle");
+static_assert(GROUPS <= STAGES && GROUPS <= DEEP && DEEP % 2 == 0, "a group's next stage and slot are at most one round on; a slot has one loading warp");
 constexpr uint32_t kIdesc = idesc_bf16_f32(TILE, TILE) | (1u << 15) | kIdescBMnMajor;   // both MN-major
 
 struct Params {
@@ -50,16 +58,21 @@ struct Params {
     float *part;                              // [pair][2][256][256]
     WsHeader *hdr;
     int P, T, N, K;
-    int n_tiles, k_tiles, whole, left, pairs; // tiles dealt out whole; left over; pairs of the launch
+    int n_tiles, k_tiles, whole, left;        // tiles dealt out whole; left over
+    int pairs, sharers;                       // pairs of the launch; those that share the tiles left over
     uint32_t steps;
-    int dy_shared, wide, f32, accumulate, st32, clear;
+    int dy_shared, q_shared, wide, f32, accumulate, st32, clear;
     unsigned long long timeout_ns;
 };
 
-// A pair's share of the steps of the tiles left over: [first(i), first(i + 1)).
-__host__ __device__ __forceinline__ uint64_t first_step(const Params &p, int pair)
+// A pair's share of the steps of the tiles left over: [first(i), first(i + 1)), never empty
+// for i < sharers.
+__device__ __forceinline__ uint64_t first_step(const Params &p, int pair)
 {
-    return (uint64_t)p.left * p.steps * (uint32_t)pair / (uint32_t)p.pairs;
+    const uint64_t all = (uint64_t)p.left * p.steps;
+    if (pair >= p.sharers) return all;
+    if (all >> 25) return all * (uint32_t)pair / (uint32_t)p.sharers;
+    return (uint32_t)all * (uint32_t)pair / (uint32_t)p.sharers;      // fewer than 128 pairs: 32 bits do
 }
 
 // What a pair does one after the other: whole tiles, then parts of at most two.
@@ -115,17 +128,27 @@ struct Walk {
     }
 };
 
+// Descriptors of MN-major tiles in blocks of BLOCK bytes (smem_desc_mn_sw128): a varying low
+// word, and this high word.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) { return (addr >> 4) | ((uint32_t)(BLOCK >> 4) << 16); }
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(kIdesc), "r"(acc), "r"(kDescHi)
+                 : "memory");
+}
+
 __device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar_cluster)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
-// Copies of q into a thread's slot; nothing is read for `on` false, and the slot is zeroed.
-template <int B>
+// Copies 8 bytes of q; for `on` false nothing is read and zeros are written.
 __device__ __forceinline__ void copy(uint32_t dst, const void *src, bool on)
 {
-    if (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
 }
 
 // 32 columns of a row of dw from v, as far as they exist; k: the first of them.
@@ -172,18 +195,20 @@ __device__ __forceinline__ void store32(const Params &p, char *row, int k, uint3
         if (k + 8 * i < p.K) st_v4(o + i, w[i]);
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(const __grid_constant__ CUtensorMap map, const Params p)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
+                                                                            const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
     uint8_t *const gbase = smem_raw + (base - raw);
-    const uint32_t sA = base, sB = sA + STAGES * OPERAND, sQ = sB + STAGES * OPERAND, bars = sQ + SLOTS;
-    uint8_t *const bars_g = gbase + STAGES * 2 * OPERAND + SLOTS;
+    const uint32_t sA = base, sB = sA + STAGES * OPERAND, sQ = sB + STAGES * OPERAND, sE = sQ + SLOTS, bars = sE + ESLOTS;
+    uint8_t *const bars_g = gbase + STAGES * 2 * OPERAND + SLOTS + ESLOTS;
     const uint32_t full_a = bars, full_b = bars + 8 * STAGES, empty = bars + 16 * STAGES, tfull = bars + 24 * STAGES, tempty = tfull + 16,
-                   drained = tempty + 16;
-    uint32_t *const tmem_slot = (uint32_t *)(bars_g + 24 * STAGES + 40);
-    int *const abort_flag = (int *)(bars_g + 24 * STAGES + 44);
-    static_assert(24 * STAGES + 48 <= 256, "barriers fit behind the slots");
+                   drained = tempty + 16, qfull = drained + 16, qempty = qfull + 8 * DEEP;
+    constexpr int WORDS = 24 * STAGES + 48 + 16 * DEEP;
+    uint32_t *const tmem_slot = (uint32_t *)(bars_g + WORDS);
+    int *const abort_flag = (int *)(bars_g + WORDS + 4);
+    static_assert(WORDS + 8 <= 512, "barriers fit behind the slots");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t cta = cluster_ctarank();
@@ -192,8 +217,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_a + 8 * s, 1);                 // the even CTA's arm for the bytes of both
-            mbar_init(full_b + 8 * s, 2 * (WIDEN / 32));  // every widening warp of both CTAs
+            mbar_init(full_b + 8 * s, 2 * GROUP / 32);    // the group's warps of both CTAs
             mbar_init(empty + 8 * s, 1);                  // one commit of the pair's MMAs
+        }
+        for (int d = 0; d < DEEP; ++d) {
+            mbar_init(qfull + 8 * d, p.wide ? 2 : 33);    // the arm for TMA's bytes or a warp's own copies; the groups' bytes
+            mbar_init(qempty + 8 * d, GROUP / 32);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(tfull + 8 * a, 1);
@@ -204,6 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map) : "memory");
+        if (p.wide) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_q) : "memory");
     }
     __syncthreads();
     cluster_sync_all();
@@ -218,127 +248,186 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
     const uint32_t tmem = *tmem_slot;
     const Abort ab{abort_flag, p.hdr, p.timeout_ns, 0xACu, mapa_shared(smem_u32(abort_flag), cta ^ 1u)};
 
-    if (warp == 0 && lane == 0) {
+    const uint32_t full_even = mapa_shared(full_b, 0);
+    if (warp == 0) {
         // ---------------- dy by TMA (both CTAs; the bytes are counted on the even one's barrier)
-        const uint32_t full_even = mapa_shared(full_a, 0);
+        const uint32_t full_a_even = mapa_shared(full_a, 0);
         uint32_t stage = 0, phase = 0;
-        int issued[STAGES] = {};
+        int steps = 0;
         Walk w;
-        for (w.start(p, pair); w.tile >= 0; w.next(p, pair)) {
-            if (!wait_bar(empty + 8 * stage, phase ^ 1u, ab, 2)) break;
-            if (even) mbar_expect_tx(full_a + 8 * stage, 2 * OPERAND);
+        for (w.start(p, pair); w.tile >= 0; w.next(p, pair), ++steps) {
+            if (!wait_all(empty + 8 * stage, phase ^ 1u, ab, 2)) break;
+            if (elect_one()) {
+                if (even) mbar_expect_tx(full_a + 8 * stage, 2 * OPERAND);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                tma_load_3d_pair(sA + stage * OPERAND + i * BLOCK, &map, w.n + (int)cta * HALF + 64 * i, (int)(w.step * STEP),
-                                 p.dy_shared ? 0 : w.r, full_even + 8 * stage);
-            issued[stage]++;
+                for (int i = 0; i < 2; ++i)
+                    tma_load_3d_pair(sA + stage * OPERAND + i * BLOCK, &map, w.n + (int)cta * HALF + 64 * i, (int)(w.step * STEP),
+                                     p.dy_shared ? 0 : w.r, full_a_even + 8 * stage);
+            }
             if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
         if (even && *(volatile int *)abort_flag)          // no copy of either CTA stays in flight
-            for (int s = 0; s < STAGES; ++s)
-                if (issued[s] > 0) wait_bar(full_a + 8 * s, (uint32_t)((issued[s] - 1) & 1), ab, 9, true);
-    } else if (warp == 1 && lane == 0 && even) {
-        // ---------------- MMAs of the pair
+            for (int s = steps > STAGES ? steps - STAGES : 0; s < steps; ++s) wait_bar(full_a + 8 * (s % STAGES), (uint32_t)(s / STAGES & 1), ab, 9, true);
+    } else if (warp == 1 && even) {
+        // ---------------- MMAs of the pair (the whole warp, one elected lane issues)
         uint32_t stage = 0, phase = 0;
         int it = 0;
         bool ok = true;
         Walk w;
         for (w.start(p, pair); w.tile >= 0 && ok; ++it, w.next_tile(p, pair)) {
-            const uint32_t acc = it & 1;
-            if (!wait_bar<true>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1u, ab, 3)) break;
-            tc_fence_after();
-            const uint32_t d = tmem + acc * TILE;
+            const uint32_t acc = it & 1, d = tmem + acc * TILE;
+            if (!wait_all<true>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1u, ab, 3)) break;
+            uint32_t more = 0;                            // 0: the first MMA overwrites the accumulator
             for (uint32_t s = w.step; s < w.end; ++s) {
-                if (!wait_bar(full_a + 8 * stage, phase, ab, 4) || !wait_bar<true>(full_b + 8 * stage, phase, ab, 5)) {
+                if (!wait_all(full_a + 8 * stage, phase, ab, 4) || !wait_all<true>(full_b + 8 * stage, phase, ab, 5)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t ad = smem_desc_mn_sw128(sA + stage * OPERAND, BLOCK), bd = smem_desc_mn_sw128(sB + stage * OPERAND, BLOCK);
+                if (elect_one()) {
+                    const uint32_t ad = desc_mn(sA + stage * OPERAND), bd = desc_mn(sB + stage * OPERAND);
 #pragma unroll
-                for (int i = 0; i < STEP / 16; ++i)       // 16 tokens: 2048 bytes
-                    tc_mma_pair(d, ad + (uint64_t)(128 * i), bd + (uint64_t)(128 * i), kIdesc, s != w.step || i != 0);
-                tc_commit_pair_mc(empty + 8 * stage, 3);
+                    for (int i = 0; i < STEP / 16; ++i) mma_pair(d, ad + 128 * i, bd + 128 * i, i ? 1u : more);   // 16 tokens: 2048 bytes
+                    tc_commit_pair_mc(empty + 8 * stage, 3);
+                    if (s + 1 == w.end) tc_commit_pair_mc(tfull + 8 * acc, 3);
+                }
+                more = 1;
                 if (++stage == STAGES) stage = 0, phase ^= 1u;
             }
-            tc_commit_pair_mc(tfull + 8 * acc, 3);
         }
-        tc_commit_pair_mc(drained, 1);
+        if (elect_one()) tc_commit_pair_mc(drained, 1);
         wait_bar(drained, 0, ab, 10, true);
-    } else if (warp >= 8) {
-        // ---------------- q to bf16.  A thread takes 16 k of the tokens t and t + 32 of a step: eight
-        // lanes read the 128 bytes of a token.  Of a swizzled row of 128 bytes (64 k) a lane writes two
-        // 16-byte chunks; lanes 4-7 write the other block's, in the other order: no bank twice.
-        const int j = threadIdx.x - 256, c = j & 7, t0 = j >> 3;
-        const uint32_t slot = sQ + j * 16;                // pieces of 16 bytes, threads side by side
-        const uint32_t full_even = mapa_shared(full_b, 0);
-        const uint32_t out = sB + (c >> 2) * BLOCK;
-        Walk now, ahead;
-        now.start(p, pair);
-        ahead = now;
-        uint32_t e[DEEP][2];
-        auto fetch = [&](int d) {
-            if (ahead.tile >= 0) {
-                const int k = ahead.k + (int)cta * HALF + c * 16;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t t = ahead.step * STEP + t0 + 32 * i, dst = slot + (d * 2 + i) * (WIDEN * 16);
-                    const bool on = t < (uint32_t)p.T && k < p.K, more = on && k + 8 < p.K;
-                    const char *const src = on ? p.x8.q.at(ahead.r, t) + k : p.x8.q.base;
-                    if (p.wide) copy<16>(dst, src, on);
-                    else copy<8>(dst, src, on), copy<8>(dst + 8, more ? src + 8 : p.x8.q.base, more);
-                    e[d][i] = 1;
-                    if (on) e[d][i] = __ldg((const uint8_t *)p.x8.e.at(ahead.r, t) + (k >> 5));
-                }
-                ahead.next(p, pair);
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+    } else if (warp == 2 || warp == 3) {
+        // ---------------- q and e ahead, a warp every other step.  q by TMA where its rows allow (a copy of a lane's
+        // own takes some ten instructions a piece, and a warp issues one every ten clocks or so: 64 tokens x 128
+        // bytes by cp.async last longer than three steps' MMAs), else by cp.async, eight lanes a token's 128
+        // bytes.  The four groups' bytes of two tokens a lane are loaded two steps of the warp ahead, because
+        // a byte cannot be copied so.  Past the last token or channel: zeros.
+        const int c = lane & 7, t0 = lane >> 3, mine = warp - 2;
+        Walk w{}, far{};                                    // the step to copy, and the one whose groups' bytes to load
+        auto skip = [&](Walk &x, int n) {
+            for (; n && x.tile >= 0; --n) x.next(p, pair);
         };
+        uint32_t e[2][2][4] = {};                         // as loaded: nothing waits for them before they are stored
+        auto groups = [&](uint32_t (&b)[2][4]) {
+            if (far.tile < 0) return;
+            const int first = (far.k + (int)cta * HALF) >> 5, all = (p.K + 31) >> 5;
 #pragma unroll
-        for (int d = 0; d < DEEP; ++d) fetch(d);
-        uint32_t stage = 0, phase = 0;
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t t = far.step * STEP + lane + 32 * i;
+                const bool here = t < (uint32_t)p.T;
+                const uint8_t *const at = (const uint8_t *)p.x8.e.at(far.r, t) + first;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    b[i][g] = 1;
+                    if (here && first + g < all) b[i][g] = __ldg(at + g);
+                }
+            }
+            skip(far, 2);
+        };
+        w.start(p, pair);
+        skip(w, mine);
+        far = w;
+        groups(e[0]);
+        groups(e[1]);
+        uint32_t slot = (uint32_t)mine, phase = 0;
+        uint32_t n = (uint32_t)mine;                      // steps of the pair before w
         bool ok = true;
-        while (ok && now.tile >= 0) {
+        while (ok && w.tile >= 0) {
 #pragma unroll
-            for (int d = 0; d < DEEP; ++d) {
-                if (now.tile < 0) break;
-                asm volatile("cp.async.wait_group %0;" ::"n"(DEEP - 1) : "memory");
-                int got = lane == 0 ? (int)wait_bar(empty + 8 * stage, phase ^ 1u, ab, 7) : 0;
-                got = __shfl_sync(0xFFFFFFFFu, got, 0);
-                if (!got) {
-                    ok = false;
-                    break;
+            for (int turn = 0; turn < 2; ++turn) {
+                if (w.tile < 0) break;
+                if (!(ok = wait_all(qempty + 8 * slot, phase ^ 1u, ab, 8))) break;
+                if (p.wide) {
+                    if (elect_one()) {
+                        mbar_expect_tx(qfull + 8 * slot, STEP_BYTES);
+                        tma_load_3d(sQ + slot * STEP_BYTES, &map_q, w.k + (int)cta * HALF, (int)(w.step * STEP), p.q_shared ? 0 : w.r, qfull + 8 * slot);
+                    }
+                } else {
+                    const int k = w.k + (int)cta * HALF + c * 16;
+                    const bool on = k < p.K, more = k + 8 < p.K;
+                    const uint32_t dst = sQ + slot * STEP_BYTES + t0 * HALF + c * 16;
+                    const char *src = p.x8.q.at(w.r, w.step * STEP + t0) + k;
+#pragma unroll 4
+                    for (int i = 0; i < STEP; i += 4, src += 4 * p.x8.q.row) {
+                        const bool here = on && w.step * STEP + t0 + i < (uint32_t)p.T;
+                        copy(dst + i * HALF, here ? src : p.x8.q.base, here);
+                        copy(dst + i * HALF + 8, here && more ? src + 8 : p.x8.q.base, here && more);
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(qfull + 8 * slot) : "memory");
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint4 q;
-                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                                 : "r"(slot + (d * 2 + i) * (WIDEN * 16))
+                for (int i = 0; i < 2; ++i)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(sE + slot * (STEP * 4) + (lane + 32 * i) * 4),
+                                 "r"(e[turn][i][0] | e[turn][i][1] << 8 | e[turn][i][2] << 16 | e[turn][i][3] << 24)
                                  : "memory");
-                    f32x2 f[4], g[4];
-                    held8(make_uint2(q.x, q.y), e[d][i], f);
-                    held8(make_uint2(q.z, q.w), e[d][i], g);
-                    const uint4 a = narrow8(f), b = narrow8(g);
-                    const uint32_t t = t0 + 32 * i, row = out + stage * OPERAND + t * 128, ch = (c & 3) * 2;
-                    const bool flip = c >= 4;
-                    const uint4 u = flip ? b : a, v = flip ? a : b;
-                    const uint32_t cu = flip ? ch + 1 : ch, cv = flip ? ch : ch + 1;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((cu ^ (t & 7)) << 4)), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((cv ^ (t & 7)) << 4)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-                }
-                asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) {
-                    if (even) mbar_arrive(full_b + 8 * stage);
-                    else mbar_arrive_remote(full_even + 8 * stage);
-                }
-                fetch(d);
-                now.next(p, pair);
-                if (++stage == STAGES) stage = 0, phase ^= 1u;
+                arrive_warp(qfull + 8 * slot, lane);
+                skip(w, 2);
+                groups(e[turn]);
+                n += 2;
+                slot += 2;
+                if (slot >= DEEP) slot -= DEEP, phase ^= 1u;
             }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_all;" ::: "memory");  // no copy stays in flight, also after a wait that ran out
+        if (p.wide && *(volatile int *)abort_flag)
+            for (uint32_t i = n > DEEP ? n - DEEP : (uint32_t)mine; i < n; i += 2) wait_bar(qfull + 8 * (i % DEEP), i / DEEP & 1u, ab, 12, true);
+    } else if (warp >= 8) {
+        // ---------------- q to bf16.  The steps are dealt out to groups of warps in turn.  A thread takes 16 k
+        // of every 16th token of a step.  Of a swizzled row of 128 bytes (64 k) a lane writes two 16-byte
+        // chunks; lanes 4-7 write the other block's, in the other order: no bank twice.
+        const int group = (warp - 8) / (GROUP / 32), j = threadIdx.x & (GROUP - 1), c = j & 7, t0 = j >> 3;
+        const uint32_t in = sQ + t0 * HALF + c * 16, ein = sE + t0 * 4 + (c >> 1), out = sB + (c >> 2) * BLOCK + t0 * 128;
+        const uint32_t ch = ((c & 3) * 2 + (c >> 2)) ^ (t0 & 7);        // of the first chunk written; the other: ^ 1
+        const bool flip = c >= 4;
+        uint32_t total = 0;                               // steps of the pair; this group's: group, group + GROUPS, ...
+        {
+            Walk w;
+            for (w.start(p, pair); w.tile >= 0; w.next_tile(p, pair)) total += w.end - w.step;
+        }
+        uint32_t stage = (uint32_t)group, phase = 0, slot = (uint32_t)group, qphase = 0;
+        for (uint32_t n = (uint32_t)group; n < total; n += GROUPS) {
+            if (!wait_all(qfull + 8 * slot, qphase, ab, 7)) break;
+            uint4 x[PIECES][2];
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                uint4 q;
+                uint32_t e;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                             : "r"(in + slot * STEP_BYTES + i * (TOKENS * HALF))
+                             : "memory");
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(ein + slot * (STEP * 4) + i * (TOKENS * 4)) : "memory");
+                f32x2 f[4], g[4];
+                held8(flip ? make_uint2(q.z, q.w) : make_uint2(q.x, q.y), e, f);
+                held8(flip ? make_uint2(q.x, q.y) : make_uint2(q.z, q.w), e, g);
+                x[i][0] = narrow8(f);
+                x[i][1] = narrow8(g);
+            }
+            arrive_warp(qempty + 8 * slot, lane);
+            if (!wait_all(empty + 8 * stage, phase ^ 1u, ab, 11)) break;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(out + stage * OPERAND + i * (TOKENS * 128) + ((ch ^ k) << 4)),
+                                 "r"(x[i][k].x), "r"(x[i][k].y), "r"(x[i][k].z), "r"(x[i][k].w)
+                                 : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            // The odd CTA's halves are complete in its shared memory (the fence above), where its own tensor
+            // core reads them; the arrival publishes nothing else, so it is relaxed.  With a release at cluster
+            // scope the whole launch took 602 us in the place of 535.
+            if (even) {
+                arrive_warp(full_b + 8 * stage, lane);
+            } else {
+                __syncwarp();
+                if (lane == 0) arrive_remote_relaxed(full_even + 8 * stage);
+            }
+            stage += GROUPS;
+            if (stage >= STAGES) stage -= STAGES, phase ^= 1u;
+            slot += GROUPS;
+            if (slot >= DEEP) slot -= DEEP, qphase ^= 1u;
+        }
     } else if (warp >= 4) {
         // ---------------- finished tiles: this CTA's 128 rows, warp 4 + i the TMEM lanes 32 i..
         const int i = warp & 3;
@@ -347,9 +436,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
         Walk w;
         for (w.start(p, pair); w.tile >= 0; ++it, w.next_tile(p, pair)) {
             const uint32_t acc = it & 1;
-            int got = lane == 0 ? (int)wait_bar(tfull + 8 * acc, (it >> 1) & 1, ab, 6) : 0;
-            got = __shfl_sync(0xFFFFFFFFu, got, 0);
-            if (!got) break;
+            if (!wait_idle(tfull + 8 * acc, (it >> 1) & 1, ab, 6)) break;
             tc_fence_after();
             const int local = (int)cta * HALF + i * 32 + lane, n = w.n + local;
             const uint32_t from = tmem + ((uint32_t)(i * 32) << 16) + acc * TILE;
@@ -392,25 +479,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
 template <bool CLEAR>
 __global__ void __launch_bounds__(256) k_wgrad_join(const Params p)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int i = blockIdx.y, per = p.n_tiles * p.k_tiles, tile = p.whole + i, rest = tile % per;
     const int local = blockIdx.x * 4 + (threadIdx.x >> 6), col = (threadIdx.x & 63) * 4;
     const int n = rest / p.k_tiles * TILE + local, k = rest % p.k_tiles * TILE + col;
-    const uint64_t from = (uint64_t)i * p.steps, to = from + p.steps, all = (uint64_t)p.left * p.steps;
-    // the pairs whose share reaches into [from, to): the last that starts at or before `from`, and on
-    int pair = (int)(from * (uint32_t)p.pairs / all);
-    while (first_step(p, pair + 1) <= from) ++pair;
-    while (pair > 0 && first_step(p, pair) > from) --pair;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (; pair < p.pairs && first_step(p, pair) < to; ++pair) {
-        const uint64_t begin = first_step(p, pair);
-        if (first_step(p, pair + 1) == begin) continue;             // an empty share
-        const int second = begin / p.steps != (uint64_t)i;          // the pair's first part is of the tile before
-        float4 *const part = (float4 *)(p.part + ((size_t)(2 * pair + second) * TILE + local) * TILE + col);
-        const float4 v = *part;
+    // the sharers whose shares meet the tile's steps [from, to): the first may have begun in the tile
+    // before, which is then its part 0 and this tile its part 1
+    const uint64_t from = (uint64_t)i * p.steps, to = from + p.steps;
+    int first = (int)(from * (uint32_t)p.sharers / ((uint64_t)p.left * p.steps));
+    while (first_step(p, first + 1) <= from) ++first;
+    while (first_step(p, first) > from) --first;
+    int end = first + 1;
+    while (end < p.sharers && first_step(p, end) < to) ++end;
+    const bool second = first_step(p, first) < from;
+    const size_t step = (size_t)2 * TILE * TILE / 4;
+    float4 *part = (float4 *)(p.part + ((size_t)2 * first * TILE + local) * TILE + col);
+    asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written
+    float4 s = part[second ? step / 2 : 0];
+    if (CLEAR) part[second ? step / 2 : 0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    part += step;
+#pragma unroll 8
+    for (int j = 0; j < end - first - 1; ++j) {
+        const float4 v = part[j * step];
         s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-        if (CLEAR) *part = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    if (CLEAR)                                             // in a loop of its own: stores would hold up the loads
+        for (int j = 0; j < end - first - 1; ++j) part[j * step] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (n >= p.N || k >= p.K) return;
     char *const row = p.dw.at(tile / per, n);
     if (p.f32) {
@@ -445,17 +538,17 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// dy as [P][T][N] in boxes of 64 channels x 64 tokens, 128-byte swizzle.
-static int make_map(CUtensorMap *map, const rc_rows &dy, int P, int T, int N)
+// [P][T][channels] in boxes of `width` channels x 64 tokens.
+static int make_map(CUtensorMap *map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const rc_rows &o, int P, int T, int channels, uint32_t width)
 {
     auto fn = encode_fn();
     if (!fn) return set_error(RC_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available from the driver");
-    const bool one = P == 1 || dy.slot == 0;
-    const cuuint64_t dims[3] = {(cuuint64_t)N, (cuuint64_t)T, one ? 1u : (cuuint64_t)P};
-    const cuuint64_t strides[2] = {(cuuint64_t)dy.row, one ? (cuuint64_t)dy.row : (cuuint64_t)dy.slot};
-    const cuuint32_t box[3] = {64, STEP, 1}, estr[3] = {1, 1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, dy.base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const bool one = P == 1 || o.slot == 0;
+    const cuuint64_t dims[3] = {(cuuint64_t)channels, (cuuint64_t)T, one ? 1u : (cuuint64_t)P};
+    const cuuint64_t strides[2] = {(cuuint64_t)o.row, one ? (cuuint64_t)o.row : (cuuint64_t)o.slot};
+    const cuuint32_t box[3] = {width, STEP, 1}, estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, type, 3, o.base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return set_error(RC_ERR_INVALID, "tensor map encoding failed (CUresult %d)", (int)r);
     return RC_OK;
 }
@@ -463,7 +556,8 @@ static int make_map(CUtensorMap *map, const rc_rows &dy, int P, int T, int N)
 // Tiles that fill whole rounds of the pairs are dealt out whole.  The tokens of the rest are
 // divided over all pairs where that saves more steps than parts cost: they are written and
 // read again, and joined by a second launch.
-constexpr uint32_t kPartSteps = 24;
+constexpr uint32_t kPartSteps = 24;           // steps saved from which on tokens are divided
+constexpr uint32_t kShareSteps = 4;           // steps of a share, at least
 
 static void plan(const rc_wgrad_args &a, int sms, Params &p)
 {
@@ -480,9 +574,11 @@ static void plan(const rc_wgrad_args &a, int sms, Params &p)
     const uint64_t saved = (uint64_t)p.steps * (uint32_t)(p.pairs - p.left) / (uint32_t)p.pairs;
     if (p.left && saved < kPartSteps) p.left = 0;
     p.whole = tiles - p.left;
-    if (!p.left && p.whole < p.pairs) p.pairs = p.whole;
+    const uint64_t shares = (uint64_t)p.left * p.steps / kShareSteps;
+    p.sharers = p.left ? (int)(shares < (uint64_t)p.left ? (uint64_t)p.left : shares < (uint64_t)p.pairs ? shares : (uint64_t)p.pairs) : 0;
+    if (p.whole < p.pairs) p.pairs = p.whole > p.sharers ? p.whole : p.sharers;
 }
-static size_t part_bytes(const Params &p) { return p.left ? (size_t)p.pairs * 2 * TILE * TILE * 4 : 0; }
+static size_t part_bytes(const Params &p) { return (size_t)p.sharers * 2 * TILE * TILE * 4; }
 
 static int check_sizes(const rc_wgrad_args &a)
 {
@@ -527,7 +623,8 @@ static int run(const rc_wgrad_args *args, void *stream)
     p.x8 = act8_of(a.x8);
     p.dw = rows_of(a.dw);
     p.dy_shared = a.P == 1 || a.dy.slot == 0;
-    p.wide = !(((uintptr_t)a.x8.q.base | a.x8.q.slot | a.x8.q.row | (size_t)a.K) & 15u);
+    p.q_shared = a.P == 1 || a.x8.q.slot == 0;
+    p.wide = !(((uintptr_t)a.x8.q.base | (a.P > 1 ? a.x8.q.slot : 0) | a.x8.q.row) & 15u);
     p.f32 = a.dw_type == RC_F32;
     p.accumulate = a.accumulate;
     p.st32 = !(((uintptr_t)a.dw.base | a.dw.slot | a.dw.row) & 31u);
@@ -540,12 +637,14 @@ static int run(const rc_wgrad_args *args, void *stream)
     if (!a.workspace && bytes && (rc_ = prepare_scratch(bytes, &space))) return rc_;
     p.clear = a.workspace != nullptr;
     p.part = (float *)space;
-    CUtensorMap map;
-    if ((rc_ = make_map(&map, a.dy, a.P, a.T, a.N))) return rc_;
+    CUtensorMap map, map_q;
+    if ((rc_ = make_map(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.dy, a.P, a.T, a.N, 64))) return rc_;
+    if (!p.wide) map_q = map;                 // not used
+    else if ((rc_ = make_map(&map_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.x8.q, a.P, a.T, a.K, HALF))) return rc_;
     static OncePerDevice once;
     cudaError_t e = once([] { return cudaFuncSetAttribute(k_wgrad, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
     if (e == cudaSuccess) {
-        k_wgrad<<<2 * p.pairs, THREADS, SMEM, st>>>(map, p);
+        k_wgrad<<<2 * p.pairs, THREADS, SMEM, st>>>(map, map_q, p);
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && p.left) {
