@@ -13,7 +13,7 @@
 // it joins the sums for d in one round, so a row takes two rounds (of sum y^2, then
 // of the rest) instead of three.
 //
-// Bound by memory.  A block works on one row at a time and keeps it in registers;
+// Bound by memory.  A block (for wide rows a pair) works on one row at a time and keeps it in registers;
 // every thread copies its own share of the coming rows into its own shared-memory
 // slots (cp.async) and reads it back, so no barrier stands between loads and use.
 #include <cmath>
@@ -23,6 +23,7 @@
 #include "internal.h"
 #include "per_device.h"
 #include "ringcoll.h"
+#include "tc.cuh"
 
 namespace rc {
 namespace bn {
@@ -30,7 +31,7 @@ namespace bn {
 constexpr int kMostChannels = 16384;
 
 // Where a thread keeps the weights of its channels.
-enum Weights { IN_REGISTERS, IN_SHARED, IN_GLOBAL };
+enum Weights { IN_REGISTERS, IN_SHARED };
 
 struct Params {
     Rows y, res, h, z, dh, dz, dy, dres;
@@ -71,15 +72,16 @@ __device__ __forceinline__ uint2 lds8(uint32_t a)
     return v;
 }
 
-// Sums of K values over the block, the same in every thread, always added in the same
-// pattern.  In a warp the values are divided over the lanes while they are added (K values
-// cost 9 exchanges in the place of 5 K), each group of 32 / PAD lanes ending with one of
-// them; then every warp adds up all warps' sums alike.  Two areas take turns, so one
-// barrier does; the places of warps that do not exist hold zeros.
+// Sums of K values over a row's block, or pair of blocks (CL = 2), the same in every
+// thread, always added in the same pattern.  In a warp the values are divided over the lanes
+// while they are added (K values cost 9 exchanges in the place of 5 K), each group of
+// 32 / PAD lanes ending with one of them; every warp leaves its sums in both blocks of a
+// pair, and adds up all warps' sums alike.  Two areas take turns, so one barrier does; the
+// places of warps that do not exist hold zeros.
 constexpr int kAreaRow = 36;                            // floats of a value's row: 32 warps, and no bank twice
 constexpr int kAreaBytes = 2 * 8 * kAreaRow * 4;
 
-template <int K>
+template <int K, int CL>
 __device__ __forceinline__ void block_sum(float (&v)[K], float *area, int &turn)
 {
     constexpr int PAD = K == 1 ? 1 : K == 2 ? 2 : 8, GROUP = 32 / PAD;
@@ -97,11 +99,21 @@ __device__ __forceinline__ void block_sum(float (&v)[K], float *area, int &turn)
         }
 #pragma unroll
     for (int o = GROUP / 2; o; o /= 2) s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], o);
-    if (blockDim.x > 32) {
+    if (CL > 1 || blockDim.x > 32) {
         float *const row = area + turn * (8 * kAreaRow) + lane / GROUP * kAreaRow;
         turn ^= 1;
-        if (lane % GROUP == 0) row[threadIdx.x >> 5] = s[0];
-        __syncthreads();
+        if (CL == 1) {
+            if (lane % GROUP == 0) row[threadIdx.x >> 5] = s[0];
+            __syncthreads();
+        } else {
+            const uint32_t at = tc::smem_u32(row + tc::cluster_ctarank() * 16 + (threadIdx.x >> 5));
+            if (lane % GROUP == 0)
+#pragma unroll
+                for (int c = 0; c < CL; ++c)
+                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa_shared(at, c)), "f"(s[0]) : "memory");
+            __syncwarp();
+            tc::cluster_sync_all();
+        }
         if (PAD == 8) {
             const float4 a = *(const float4 *)(row + lane % 4 * 8), b = *(const float4 *)(row + lane % 4 * 8 + 4);
             s[0] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
@@ -118,10 +130,12 @@ __device__ __forceinline__ void block_sum(float (&v)[K], float *area, int &turn)
     for (int k = 0; k < K; ++k) v[k] = PAD == 1 ? s[0] : __shfl_sync(0xFFFFFFFFu, s[0], k * GROUP);
 }
 
+template <int CL>
 __device__ __forceinline__ void clear_area(float *area)
 {
     for (int i = threadIdx.x; i < kAreaBytes / 4; i += blockDim.x) area[i] = 0.f;
     __syncthreads();
+    if (CL > 1) tc::cluster_sync_all();
 }
 
 // The weights w and gamma_pre of vector v.  In shared memory the first and the last
@@ -150,62 +164,63 @@ __device__ __forceinline__ void scale_of(const Params &p, uint32_t v, f32x2 (&w)
         for (int i = 0; i < 4; ++i) w[i] = mul2(w[i], g[i]);
     }
 }
-__device__ __forceinline__ void sts_plane(float *plane, uint32_t v, uint32_t vecs, const f32x2 (&f)[4])
+__device__ __forceinline__ void sts_plane(float *plane, uint32_t at, uint32_t vecs, const f32x2 (&f)[4])
 {
-    *(float4 *)(plane + v * 4) = make_float4(lo(f[0]), hi(f[0]), lo(f[1]), hi(f[1]));
-    *(float4 *)(plane + (vecs + v) * 4) = make_float4(lo(f[2]), hi(f[2]), lo(f[3]), hi(f[3]));
+    *(float4 *)(plane + at * 4) = make_float4(lo(f[0]), hi(f[0]), lo(f[1]), hi(f[1]));
+    *(float4 *)(plane + (vecs + at) * 4) = make_float4(lo(f[2]), hi(f[2]), lo(f[3]), hi(f[3]));
 }
-__device__ __forceinline__ void lds_plane(const float *plane, uint32_t v, uint32_t vecs, f32x2 (&f)[4])
+__device__ __forceinline__ void lds_plane(const float *plane, uint32_t at, uint32_t vecs, f32x2 (&f)[4])
 {
-    const float4 a = *(const float4 *)(plane + v * 4), b = *(const float4 *)(plane + (vecs + v) * 4);
+    const float4 a = *(const float4 *)(plane + at * 4), b = *(const float4 *)(plane + (vecs + at) * 4);
     f[0] = f2(a.x, a.y);
     f[1] = f2(a.z, a.w);
     f[2] = f2(b.x, b.y);
     f[3] = f2(b.z, b.w);
 }
 
+// Bytes that Scales keeps of shared memory.
+__host__ __device__ __forceinline__ uint32_t scale_bytes(int vpt, uint32_t threads) { return 64u * vpt * threads; }
+
 template <int VPT, Weights WHERE, bool PRE>
 struct Scales {
     f32x2 w[WHERE == IN_REGISTERS ? VPT : 1][4], g[WHERE == IN_REGISTERS ? VPT : 1][4];
     float *plane;
 
-    // shared: 16 bytes aligned, 8 N floats' room (IN_SHARED)
-    __device__ __forceinline__ void init(const Params &p, float *shared)
+    // first: the block's first vector
+    __device__ __forceinline__ void init(const Params &p, float *shared, uint32_t first)
     {
         plane = shared;
-        if constexpr (WHERE != IN_GLOBAL)
+        const uint32_t vecs = VPT * blockDim.x;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = i * blockDim.x + threadIdx.x;
+            const uint32_t at = i * blockDim.x + threadIdx.x, v = first + at;
             f32x2 a[4] = {}, b[4] = {};
             if (v < p.vecs) {
                 scale_of(p, v, a);
                 if (PRE) ld8f(p.gpre + v * 8, b);
-                if (WHERE == IN_SHARED) {       // read back by the thread that wrote them
-                    sts_plane(plane, v, p.vecs, a);
-                    if (PRE) sts_plane(plane + p.N, v, p.vecs, b);
-                }
             }
-            if (WHERE == IN_REGISTERS)
+            if (WHERE == IN_SHARED) {               // read back by the thread that wrote them
+                sts_plane(plane, at, vecs, a);
+                if (PRE) sts_plane(plane + vecs * 8, at, vecs, b);
+            } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) w[i][k] = a[k], g[i][k] = b[k];
+            }
         }
     }
-    __device__ __forceinline__ void scale(const Params &p, int i, uint32_t v, f32x2 (&f)[4]) const
+    __device__ __forceinline__ void scale(int i, f32x2 (&f)[4]) const
     {
-        if (WHERE == IN_REGISTERS)
+        if (WHERE == IN_SHARED) lds_plane(plane, i * blockDim.x + threadIdx.x, VPT * blockDim.x, f);
+        else
 #pragma unroll
             for (int k = 0; k < 4; ++k) f[k] = w[i][k];
-        else if (WHERE == IN_SHARED) lds_plane(plane, v, p.vecs, f);
-        else scale_of(p, v, f);
     }
-    __device__ __forceinline__ void pre(const Params &p, int i, uint32_t v, f32x2 (&f)[4]) const
+    __device__ __forceinline__ void pre(int i, f32x2 (&f)[4]) const
     {
-        if (WHERE == IN_REGISTERS)
+        if (WHERE == IN_SHARED) lds_plane(plane + VPT * blockDim.x * 8, i * blockDim.x + threadIdx.x, VPT * blockDim.x, f);
+        else
 #pragma unroll
             for (int k = 0; k < 4; ++k) f[k] = g[i][k];
-        else if (WHERE == IN_SHARED) lds_plane(plane + p.N, v, p.vecs, f);
-        else ld8f(p.gpre + v * 8, f);
     }
 };
 
@@ -220,28 +235,29 @@ __device__ __forceinline__ size_t behind(const Rows &o, uint32_t chunk, uint32_t
 }
 
 // ------------------------------------------------------------ forward
-template <int VPT, int MAXT, int MINB, Weights WHERE, bool POST, bool PRE>
-__global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const Params p)
+template <int VPT, int MAXT, int CL, Weights WHERE, bool POST, bool PRE>
+__global__ void __launch_bounds__(MAXT, 1) k_block_norm(const Params p)
 {
     extern __shared__ __align__(16) uint8_t sm[];
     float *const area = (float *)sm;
     uint8_t *const after = sm + kAreaBytes;
     const uint32_t threads = blockDim.x, stage_bytes = 2 * VPT * 16 * threads;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(after + (WHERE == IN_SHARED ? 8 * p.N : 0)) + threadIdx.x * 16;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(after + (WHERE == IN_SHARED ? scale_bytes(VPT, threads) : 0)) + threadIdx.x * 16;
     Scales<VPT, WHERE, PRE> ws;
-    ws.init(p, (float *)after);
-    clear_area(area);
+    const uint32_t first_vec = CL > 1 ? tc::cluster_ctarank() * (VPT * threads) : 0, block = blockIdx.x / CL, blocks = gridDim.x / CL;
+    ws.init(p, (float *)after, first_vec);
+    clear_area<CL>(area);
     int turn = 0;
     size_t yoff[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) yoff[i] = behind(p.y, p.y_chunk, i * threads + threadIdx.x);
+    for (int i = 0; i < VPT; ++i) yoff[i] = behind(p.y, p.y_chunk, first_vec + i * threads + threadIdx.x);
     auto fetch = [&](uint32_t row, int stage) {
         if (row < p.rows) {
             const uint32_t r = p.tokens(row), t = row - r * p.T;
             const char *const yrow = row_of(p.y, p.y_chunk, row, r, t), *const rrow = p.res.at(r, t);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const uint32_t v = i * threads + threadIdx.x;
+                const uint32_t v = first_vec + i * threads + threadIdx.x;
                 if (v >= p.vecs) continue;
                 copy<16>(ring + stage * stage_bytes + i * 16 * threads, yrow + yoff[i]);
                 copy<16>(ring + stage * stage_bytes + (VPT + i) * 16 * threads, rrow + v * 16);
@@ -249,17 +265,17 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const Params p)
         }
         copies_done();
     };
-    uint32_t ahead = blockIdx.x;                        // rows stay below 2^31 - 2^20, and a grid below 2^16
-    for (int s = 0; s < p.stages; ++s, ahead += gridDim.x) fetch(ahead, s);
+    uint32_t ahead = block;                        // rows stay below 2^31 - 2^20, and a grid below 2^16
+    for (int s = 0; s < p.stages; ++s, ahead += blocks) fetch(ahead, s);
     int stage = 0;
-    for (uint32_t row = blockIdx.x; row < p.rows; row += gridDim.x, ahead += gridDim.x) {
+    for (uint32_t row = block; row < p.rows; row += blocks, ahead += blocks) {
         wait_oldest(p.stages);
         const uint32_t r = p.tokens(row), t = row - r * p.T;
         uint4 yw[VPT], rw[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             yw[i] = rw[i] = make_uint4(0, 0, 0, 0);
-            if (i * threads + threadIdx.x >= p.vecs) continue;
+            if (first_vec + i * threads + threadIdx.x >= p.vecs) continue;
             yw[i] = lds16(ring + stage * stage_bytes + i * 16 * threads);
             rw[i] = lds16(ring + stage * stage_bytes + (VPT + i) * 16 * threads);
         }
@@ -276,18 +292,18 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const Params p)
                 for (int k = 0; k < 4; ++k) ss = fma2(y[k], y[k], ss);
             }
             float sum[1] = {hsum(ss)};
-            block_sum(sum, area, turn);
+            block_sum<1, CL>(sum, area, turn);
             rp = rsqrtf(fmaf(sum[0], p.inv_n, p.eps));
         }
         f32x2 h[VPT][4], hh = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = i * threads + threadIdx.x;
+            const uint32_t v = first_vec + i * threads + threadIdx.x;
             const bool on = v < p.vecs;
             f32x2 y[4], w[4];
             wide8(yw[i], y);
             wide8(rw[i], h[i]);
-            if (on) ws.scale(p, i, v, w);
+            if (on) ws.scale(i, w);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (on) h[i][k] = fma2(w[k], mul2(y[k], both(rp)), h[i][k]);
@@ -299,16 +315,16 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const Params p)
         }
         if (!PRE) continue;
         float sum[1] = {hsum(hh)};
-        block_sum(sum, area, turn);
+        block_sum<1, CL>(sum, area, turn);
         const float q = rsqrtf(fmaf(sum[0], p.inv_n, p.eps));
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = i * threads + threadIdx.x;
+            const uint32_t v = first_vec + i * threads + threadIdx.x;
             const bool on = v < p.vecs;
             f32x2 g[4];
             uint4 zw = make_uint4(0, 0, 0, 0);
             if (on) {
-                ws.pre(p, i, v, g);
+                ws.pre(i, g);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) h[i][k] = mul2(mul2(h[i][k], both(q)), g[k]);
                 zw = narrow8(h[i]);
@@ -323,8 +339,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const Params p)
 // A block takes rows j, j + per, ... of one slot.  Its threads keep the sums of
 // their channels over all its rows, and leave them in the block's part, which
 // k_block_sums adds up in block order.
-template <int VPT, int MAXT, int MINB, Weights WHERE, bool HELD, bool POST, bool PRE>
-__global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
+template <int VPT, int MAXT, int CL, bool FULL, Weights WHERE, bool HELD, bool POST, bool PRE>
+__global__ void __launch_bounds__(MAXT, 1) k_block_norm_bwd(const Params p)
 {
     extern __shared__ __align__(16) uint8_t sm[];
     constexpr int YB = HELD ? 8 : 16;                   // staged bytes of 8 channels of y and of res
@@ -332,25 +348,26 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
     uint8_t *const after = sm + kAreaBytes;
     const uint32_t threads = blockDim.x, in_bytes = VPT * YB * threads, d_bytes = VPT * 16 * threads;
     const uint32_t stage_bytes = 2 * in_bytes + (PRE ? 2 : 1) * d_bytes;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(after + (WHERE == IN_SHARED ? 8 * p.N : 0));
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(after + (WHERE == IN_SHARED ? scale_bytes(VPT, threads) : 0));
     Scales<VPT, WHERE, PRE> ws;
-    ws.init(p, (float *)after);
-    clear_area(area);
-    const uint32_t r = blockIdx.x / p.per, first = blockIdx.x - r * p.per;
+    const uint32_t first_vec = CL > 1 ? tc::cluster_ctarank() * (VPT * threads) : 0, block = blockIdx.x / CL;
+    ws.init(p, (float *)after, first_vec);
+    clear_area<CL>(area);
+    const uint32_t r = block / p.per, first = block - r * p.per;
     int turn = 0;
     size_t yoff[HELD ? 1 : VPT], dyoff[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        if (!HELD) yoff[i] = behind(p.y, p.y_chunk, i * threads + threadIdx.x);
-        dyoff[i] = behind(p.dy, p.dy_chunk, i * threads + threadIdx.x);
+        if (!HELD) yoff[i] = behind(p.y, p.y_chunk, first_vec + i * threads + threadIdx.x);
+        dyoff[i] = behind(p.dy, p.dy_chunk, first_vec + i * threads + threadIdx.x);
     }
     auto fetch = [&](uint32_t t, int stage) {
         if (t < p.T) {
             const uint32_t at = ring + stage * stage_bytes + threadIdx.x * YB, dat = ring + stage * stage_bytes + 2 * in_bytes + threadIdx.x * 16;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const uint32_t v = i * threads + threadIdx.x;
-                if (v >= p.vecs) continue;
+                const uint32_t v = first_vec + i * threads + threadIdx.x;
+                if (!FULL && v >= p.vecs) continue;
                 if (HELD) {
                     copy<8>(at + i * YB * threads, p.y8.q.at(r, t) + v * 8);
                     copy<8>(at + in_bytes + i * YB * threads, p.res8.q.at(r, t) + v * 8);
@@ -369,8 +386,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
         if (HELD && t < p.T)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const uint32_t v = i * threads + threadIdx.x;
-                if (v >= p.vecs) continue;
+                const uint32_t v = first_vec + i * threads + threadIdx.x;
+                if (!FULL && v >= p.vecs) continue;
                 ey[i] = __ldcs((const uint8_t *)p.y8.e.at(r, t) + v / 4);
                 er[i] = __ldcs((const uint8_t *)p.res8.e.at(r, t) + v / 4);
             }
@@ -391,7 +408,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
             dh[i] = dz[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int k = 0; k < 4; ++k) y[i][k] = h[i][k] = 0;
-            if (i * threads + threadIdx.x >= p.vecs) continue;
+            if (!FULL && first_vec + i * threads + threadIdx.x >= p.vecs) continue;
             if (HELD) {
                 held8(lds8(at + i * YB * threads), ey[i], y[i]);
                 held8(lds8(at + in_bytes + i * YB * threads), er[i], h[i]);
@@ -410,17 +427,17 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
         float rp = 1.f;
         if (POST) {
             float sum[1] = {hsum(ss)};
-            block_sum(sum, area, turn);
+            block_sum<1, CL>(sum, area, turn);
             rp = rsqrtf(fmaf(sum[0], p.inv_n, p.eps));
         }
         f32x2 hh = 0, th = 0, vd = 0, vt = 0, vh = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = i * threads + threadIdx.x;
-            if (v >= p.vecs) continue;
+            const uint32_t v = first_vec + i * threads + threadIdx.x;
+            if (!FULL && v >= p.vecs) continue;
             f32x2 w[4], g[4], d[4], z[4];
-            ws.scale(p, i, v, w);
-            if (PRE) ws.pre(p, i, v, g), wide8(dz[i], z);
+            ws.scale(i, w);
+            if (PRE) ws.pre(i, g), wide8(dz[i], z);
             if (POST) wide8(dh[i], d);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -439,28 +456,28 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
         float q = 0.f, c = 0.f, m = 0.f;                // d = dh + q t - c h;  dy = rp (d w - yh m)
         if (PRE && POST) {
             float s[5] = {hsum(hh), hsum(th), hsum(vd), hsum(vt), hsum(vh)};
-            block_sum(s, area, turn);
+            block_sum<5, CL>(s, area, turn);
             q = rsqrtf(fmaf(s[0], p.inv_n, p.eps));
             c = q * q * q * (s[1] * p.inv_n);
             m = (s[2] + q * s[3] - c * s[4]) * p.inv_n;
         } else if (PRE) {
             float s[2] = {hsum(hh), hsum(th)};
-            block_sum(s, area, turn);
+            block_sum<2, CL>(s, area, turn);
             q = rsqrtf(fmaf(s[0], p.inv_n, p.eps));
             c = q * q * q * (s[1] * p.inv_n);
         } else if (POST) {
             float s[1] = {hsum(vd)};
-            block_sum(s, area, turn);
+            block_sum<1, CL>(s, area, turn);
             m = s[0] * p.inv_n;
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = i * threads + threadIdx.x;
-            if (v >= p.vecs) continue;
+            const uint32_t v = first_vec + i * threads + threadIdx.x;
+            if (!FULL && v >= p.vecs) continue;
             f32x2 w[4], g[4], d[4], z[4];
-            ws.scale(p, i, v, w);
+            ws.scale(i, w);
             wide8(dh[i], d);
-            if (PRE) ws.pre(p, i, v, g), wide8(dz[i], z);
+            if (PRE) ws.pre(i, g), wide8(dz[i], z);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (PRE) {
@@ -477,14 +494,14 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
         }
     }
     if (!p.sums) return;
-    float *part = p.part + (size_t)blockIdx.x * p.sums * p.N;
+    float *part = p.part + (size_t)block * p.sums * p.N;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         if (k == 0 ? !(p.gpost || p.gate) : !PRE) continue;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = i * threads + threadIdx.x;
-            if (v >= p.vecs) continue;
+            const uint32_t v = first_vec + i * threads + threadIdx.x;
+            if (!FULL && v >= p.vecs) continue;
             const f32x2(&f)[4] = k ? acc_z[i] : acc_d[i];
             ((float4 *)(part + v * 8))[0] = make_float4(lo(f[0]), hi(f[0]), lo(f[1]), hi(f[1]));
             ((float4 *)(part + v * 8))[1] = make_float4(lo(f[2]), hi(f[2]), lo(f[3]), hi(f[3]));
@@ -541,9 +558,11 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) k_block_sums(const Params p)
 // Vectors of 8 channels a thread.  Two halve what a row costs besides its channels (the
 // sums over the block above all): 8192 x 4096 forward with checkpoints 58 us against 67
 // with one, the gradient 72 against 100.  Where no SM gets a second row only its latency
-// counts, and one is quicker (8 rows 4.1 us against 4.5).  Rows above 8192 channels take four.
+// counts, and one is quicker (8 rows 4.1 us against 4.5).  Rows above 8192 channels are
+// divided over a pair of blocks, which leave their sums in one another's shared memory.
 struct Shape {
-    int vpt, threads, stages, regs;
+    int vpt, cl, threads, stages, regs;
+    bool full;                       // every thread has all its vectors
     size_t smem;
 };
 
@@ -551,30 +570,34 @@ static Shape shape_of(const rc_block_norm_args &a, bool grad, int sms)
 {
     const int vecs = a.N / 8;
     Shape s{};
-    s.vpt = vecs > 1024 ? 4 : (long long)a.P * a.T <= sms ? 1 : 2;
+    s.cl = vecs > 1024 ? 2 : 1;
+    s.vpt = s.cl == 1 && (long long)a.P * a.T <= sms ? 1 : 2;
     s.regs = s.vpt == 1 ? 64 : 128;                      // what the launch bounds leave a thread
-    s.threads = ((vecs + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+    s.threads = ((vecs + s.vpt * s.cl - 1) / (s.vpt * s.cl) + 31) / 32 * 32;
+    s.full = vecs == s.vpt * s.cl * s.threads;
     const bool held = grad && a.y8.q.base;
     const size_t lane = grad ? (held ? 16 : 32) + (a.gamma_pre ? 32 : 16) : 32;
-    const size_t stage = lane * s.vpt * s.threads, fixed = kAreaBytes + (grad && s.vpt < 4 ? (size_t)8 * a.N : 0);
+    const size_t stage = lane * s.vpt * s.threads, fixed = kAreaBytes + (grad ? scale_bytes(s.vpt, s.threads) : 0);
     s.stages = 3;
     while (s.stages > 1 && fixed + s.stages * stage > (s.threads * s.regs > 32768 ? 220u : 110u) * 1024) --s.stages;
     s.smem = fixed + s.stages * stage;
     return s;
 }
 
-// Blocks that an SM holds: by threads, registers (the launch bounds' share) and shared memory.
-static int resident(const Shape &s)
+// Rows at once (blocks or pairs of them) that the GPU holds: by threads, registers (the
+// launch bounds' share) and shared memory.
+static int resident(const Shape &s, int sms)
 {
     const int t = 2048 / s.threads, r = 65536 / (s.regs * s.threads), m = (int)(227 * 1024 / (s.smem + 1024));
     int n = t < r ? t : r;
     n = n < m ? n : m;
-    return n < 1 ? 1 : n > 32 ? 32 : n;
+    n = n < 1 ? 1 : n > 32 ? 32 : n;
+    return n * sms / s.cl;
 }
 
 static int blocks_of_slot(const rc_block_norm_args &a, const Shape &s, int sms)
 {
-    const int most = (sms * resident(s) + a.P - 1) / a.P;
+    const int most = (resident(s, sms) + a.P - 1) / a.P;
     return a.T < most ? (a.T < 1 ? 1 : a.T) : most;
 }
 
@@ -584,26 +607,40 @@ static cudaError_t start(unsigned blocks, const Shape &s, const Params &p, cudaS
     static OncePerDevice once;
     const cudaError_t e = once([] { return cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024); });
     if (e != cudaSuccess) return e;
-    KERNEL<<<blocks, s.threads, s.smem, st>>>(p);
-    return cudaGetLastError();
+    if (s.cl == 1) {
+        KERNEL<<<blocks, s.threads, s.smem, st>>>(p);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks * s.cl);
+    cfg.blockDim = dim3(s.threads);
+    cfg.dynamicSmemBytes = s.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = s.cl;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, KERNEL, p);
+}
+
+template <bool HELD, bool POST, bool PRE>
+static cudaError_t launch_grad(unsigned blocks, const Shape &s, const Params &p, cudaStream_t st)
+{
+    if (s.vpt == 1) return start<k_block_norm_bwd<1, 1024, 1, false, IN_SHARED, HELD, POST, PRE>>(blocks, s, p, st);
+    if (s.cl == 2) return start<k_block_norm_bwd<2, 512, 2, false, IN_SHARED, HELD, POST, PRE>>(blocks, s, p, st);
+    if (s.full) return start<k_block_norm_bwd<2, 512, 1, true, IN_SHARED, HELD, POST, PRE>>(blocks, s, p, st);
+    return start<k_block_norm_bwd<2, 512, 1, false, IN_SHARED, HELD, POST, PRE>>(blocks, s, p, st);
 }
 
 template <bool POST, bool PRE>
 static cudaError_t launch(bool grad, bool held, unsigned blocks, const Shape &s, const Params &p, cudaStream_t st)
 {
-    if (!grad) {
-        if (s.vpt == 1) return start<k_block_norm<1, 1024, 1, IN_REGISTERS, POST, PRE>>(blocks, s, p, st);
-        if (s.vpt == 2) return start<k_block_norm<2, 512, 1, IN_REGISTERS, POST, PRE>>(blocks, s, p, st);
-        return start<k_block_norm<4, 512, 1, IN_GLOBAL, POST, PRE>>(blocks, s, p, st);
-    }
-    if (held) {
-        if (s.vpt == 1) return start<k_block_norm_bwd<1, 1024, 1, IN_SHARED, true, POST, PRE>>(blocks, s, p, st);
-        if (s.vpt == 2) return start<k_block_norm_bwd<2, 512, 1, IN_SHARED, true, POST, PRE>>(blocks, s, p, st);
-        return start<k_block_norm_bwd<4, 512, 1, IN_GLOBAL, true, POST, PRE>>(blocks, s, p, st);
-    }
-    if (s.vpt == 1) return start<k_block_norm_bwd<1, 1024, 1, IN_SHARED, false, POST, PRE>>(blocks, s, p, st);
-    if (s.vpt == 2) return start<k_block_norm_bwd<2, 512, 1, IN_SHARED, false, POST, PRE>>(blocks, s, p, st);
-    return start<k_block_norm_bwd<4, 512, 1, IN_GLOBAL, false, POST, PRE>>(blocks, s, p, st);
+    if (grad) return held ? launch_grad<true, POST, PRE>(blocks, s, p, st) : launch_grad<false, POST, PRE>(blocks, s, p, st);
+    if (s.vpt == 1) return start<k_block_norm<1, 1024, 1, IN_REGISTERS, POST, PRE>>(blocks, s, p, st);
+    if (s.cl == 2) return start<k_block_norm<2, 512, 2, IN_REGISTERS, POST, PRE>>(blocks, s, p, st);
+    return start<k_block_norm<2, 512, 1, IN_REGISTERS, POST, PRE>>(blocks, s, p, st);
 }
 
 static cudaError_t launch_any(bool grad, bool held, unsigned blocks, const Shape &s, const Params &p, cudaStream_t st)
@@ -724,7 +761,7 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
     p.inv_n = 1.f / (float)a.N;
     unsigned blocks;
     if (!grad) {
-        const uint32_t most = (uint32_t)(sms * resident(s));
+        const uint32_t most = (uint32_t)resident(s, sms);
         blocks = p.rows < most ? p.rows : most;
     } else {
         p.per = blocks_of_slot(a, s, sms);

@@ -49,7 +49,10 @@ constexpr int SLOTS = DEEP * STEP_BYTES, ESLOTS = DEEP * STEP * 4;
 constexpr int TMEM_COLS = 512;                // two accumulators
 constexpr int SMEM = STAGES * 2 * OPERAND + SLOTS + ESLOTS + 1024 + 512;
 static_assert(SMEM <= 227 * 1024 && TOKENS % 8 == 0, "the stages and slots fit; a thread's tokens share a swizzle");
-static_assert(GROUPS <= STAGES && GROUPS <= DEEP && DEEP % 2 == 0, "a group's next stage and slot are at most one round on; a slot has one loading warp");
+// A group waits for a slot's or stage's next phase by its parity, so the phase before must be
+// known to be over: a slot's last step is the group's own (its copies may end in any order),
+// and a stage's last MMAs come before those that the group's last stage was freed by.
+static_assert(DEEP % GROUPS == 0 && DEEP % 2 == 0 && STAGES >= GROUPS, "a slot has one loading warp and one group");
 constexpr uint32_t kIdesc = idesc_bf16_f32(TILE, TILE) | (1u << 15) | kIdescBMnMajor;   // both MN-major
 
 struct Params {
@@ -279,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
             if (!wait_all<true>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1u, ab, 3)) break;
             uint32_t more = 0;                            // 0: the first MMA overwrites the accumulator
             for (uint32_t s = w.step; s < w.end; ++s) {
-                if (!wait_all(full_a + 8 * stage, phase, ab, 4) || !wait_all<true>(full_b + 8 * stage, phase, ab, 5)) {
+                if (!wait_all(full_a + 8 * stage, phase, ab, 4, full_b + 8 * stage)) {
                     ok = false;
                     break;
                 }
