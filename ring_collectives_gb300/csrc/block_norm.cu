@@ -13,9 +13,10 @@
 // it joins the sums for d in one round, so a row takes two rounds (of sum y^2, then
 // of the rest) instead of three.
 //
-// Bound by memory.  A block (for wide rows a pair) works on one row at a time and keeps it in registers;
+// Bound by memory.  A block (for wide rows four) works on one row at a time and keeps it in registers;
 // every thread copies its own share of the coming rows into its own shared-memory
-// slots (cp.async) and reads it back, so no barrier stands between loads and use.
+// slots (cp.async) and reads it back, so no barrier stands between loads and use.  Channels past
+// the end of a row arrive as zeros, with weights of zero, and only the stores leave them out.
 #include <cmath>
 
 #include "act8.cuh"
@@ -43,13 +44,16 @@ struct Params {
     uint32_t y_chunk, dy_chunk;      // channels of a slot of y, dy (0: rows of all N)
     int stages, per, sums, clear;    // gradient: blocks of a slot; sums of a block's part; 1: zero `part` once read
     float alpha, eps, inv_n;
+    WsHeader *hdr;                   // clusters: where a wait that ran out is recorded
+    unsigned long long timeout_ns;
 };
 
+// Copies B bytes; for `on` false nothing is read and zeros are written.
 template <int B>
-__device__ __forceinline__ void copy(uint32_t dst, const void *src)
+__device__ __forceinline__ void copy(uint32_t dst, const void *src, bool on)
 {
-    if (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+    if (B == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void wait_oldest(int stages)
@@ -72,71 +76,114 @@ __device__ __forceinline__ uint2 lds8(uint32_t a)
     return v;
 }
 
-// Sums of K values over a row's block, or pair of blocks (CL = 2), the same in every
-// thread, always added in the same pattern.  In a warp the values are divided over the lanes
-// while they are added (K values cost 9 exchanges in the place of 5 K), each group of
-// 32 / PAD lanes ending with one of them; every warp leaves its sums in both blocks of a
-// pair, and adds up all warps' sums alike.  Two areas take turns, so one barrier does; the
-// places of warps that do not exist hold zeros.
+// Sums of K values over the threads of a row, the same in every one, always added in the
+// same pattern.  In a warp the values are divided over the lanes while they are added
+// (K values cost 9 exchanges in the place of 5 K), each group of 32 / PAD lanes ending with
+// one of them.  GL > 0: a row has GL lanes, and that is all.  Else every warp leaves its
+// sums in shared memory (for a cluster of blocks in all of them) and adds up all warps' sums alike.
+// Two areas take turns, so one barrier does; the places of warps that do not exist hold zeros.
+//
+// Between a cluster's blocks sums travel with st.async, which counts their bytes on an
+// mbarrier of the block that they go to.  (A cluster barrier would have to release, and so
+// wait for the row's stores to memory: 2048 rows of 16384 took 200 us for the gradient.)
 constexpr int kAreaRow = 36;                            // floats of a value's row: 32 warps, and no bank twice
-constexpr int kAreaBytes = 2 * 8 * kAreaRow * 4;
+constexpr int kAreaBytes = 2 * 8 * kAreaRow * 4 + 32;   // two areas; two mbarriers, the abort flag
 
-template <int K, int CL>
-__device__ __forceinline__ void block_sum(float (&v)[K], float *area, int &turn)
-{
-    constexpr int PAD = K == 1 ? 1 : K == 2 ? 2 : 8, GROUP = 32 / PAD;
-    const uint32_t lane = threadIdx.x & 31;
-    float s[PAD];
-#pragma unroll
-    for (int k = 0; k < PAD; ++k) s[k] = k < K ? v[k] : 0.f;
-#pragma unroll
-    for (int n = PAD / 2, o = 16; n; n /= 2, o /= 2)
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-            const bool upper = lane & o;
-            const float keep = upper ? s[k + n] : s[k], give = upper ? s[k] : s[k + n];
-            s[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
-        }
-#pragma unroll
-    for (int o = GROUP / 2; o; o /= 2) s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], o);
-    if (CL > 1 || blockDim.x > 32) {
-        float *const row = area + turn * (8 * kAreaRow) + lane / GROUP * kAreaRow;
-        turn ^= 1;
-        if (CL == 1) {
-            if (lane % GROUP == 0) row[threadIdx.x >> 5] = s[0];
+template <int GL, int CL>
+struct Sums {
+    const Params &p;
+    float *const area;
+    uint32_t uses = 0;
+    bool ok = true;
+
+    __device__ __forceinline__ uint32_t bars() const { return tc::smem_u32(area + 2 * 8 * kAreaRow); }
+    __device__ __forceinline__ int *flag() const { return (int *)(area + 2 * 8 * kAreaRow + 4); }
+    __device__ __forceinline__ Sums(const Params &p_, uint8_t *at) : p(p_), area((float *)at)
+    {
+        if constexpr (GL == 0) {
+            for (int i = threadIdx.x; i < kAreaBytes / 4; i += blockDim.x) area[i] = 0.f;
             __syncthreads();
-        } else {
-            const uint32_t at = tc::smem_u32(row + tc::cluster_ctarank() * 16 + (threadIdx.x >> 5));
-            if (lane % GROUP == 0)
-#pragma unroll
-                for (int c = 0; c < CL; ++c)
-                    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa_shared(at, c)), "f"(s[0]) : "memory");
-            __syncwarp();
+        }
+        if constexpr (CL > 1) {
+            if (threadIdx.x == 0) {
+                tc::mbar_init(bars(), 1);
+                tc::mbar_init(bars() + 8, 1);
+                asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            }
+            __syncthreads();
             tc::cluster_sync_all();
         }
-        if (PAD == 8) {
-            const float4 a = *(const float4 *)(row + lane % 4 * 8), b = *(const float4 *)(row + lane % 4 * 8 + 4);
-            s[0] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
-        } else if (PAD == 2) {
-            const float2 a = *(const float2 *)(row + lane % 16 * 2);
-            s[0] = a.x + a.y;
-        } else {
-            s[0] = row[lane];
+    }
+
+    template <int K>
+    __device__ __forceinline__ void operator()(float (&v)[K])
+    {
+        if (GL && GL < 32) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int o = GL / 2; o; o /= 2) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+            return;
         }
+        constexpr int PAD = K == 1 ? 1 : K == 2 ? 2 : 8, GROUP = 32 / PAD;
+        const uint32_t lane = threadIdx.x & 31;
+        float s[PAD];
+#pragma unroll
+        for (int k = 0; k < PAD; ++k) s[k] = k < K ? v[k] : 0.f;
+#pragma unroll
+        for (int n = PAD / 2, o = 16; n; n /= 2, o /= 2)
+#pragma unroll
+            for (int k = 0; k < n; ++k) {
+                const bool upper = lane & o;
+                const float keep = upper ? s[k + n] : s[k], give = upper ? s[k] : s[k + n];
+                s[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+            }
 #pragma unroll
         for (int o = GROUP / 2; o; o /= 2) s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], o);
-    }
+        if (!GL) {
+            const uint32_t turn = uses & 1;
+            float *const row = area + turn * (8 * kAreaRow) + lane / GROUP * kAreaRow;
+            if (CL == 1) {
+                if (lane % GROUP == 0) row[threadIdx.x >> 5] = s[0];
+                __syncthreads();
+            } else {
+                const uint32_t at = tc::smem_u32(row + tc::cluster_ctarank() * (32 / CL) + (threadIdx.x >> 5)), bar = bars() + 8 * turn;
+                if (threadIdx.x == 0) tc::mbar_expect_tx(bar, CL * (blockDim.x >> 5) * PAD * 4);
+                if (lane % GROUP == 0)
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = PAD == 1 ? s[0] : __shfl_sync(0xFFFFFFFFu, s[0], k * GROUP);
-}
+                    for (int c = 0; c < CL; ++c)
+                        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(tc::mapa_shared(at, c)),
+                                     "r"(__float_as_uint(s[0])), "r"(tc::mapa_shared(bar, c))
+                                     : "memory");
+                __syncwarp();
+                const tc::Abort ab{flag(), p.hdr, p.timeout_ns, 0xD0u, tc::mapa_shared(tc::smem_u32(flag()), tc::cluster_ctarank() ^ 1u)};
+                if (ok) ok = tc::wait_all(bar, (uses >> 1) & 1, ab, 1);
+            }
+            ++uses;
+            if (PAD == 8) {
+                const float4 a = *(const float4 *)(row + lane % 4 * 8), b = *(const float4 *)(row + lane % 4 * 8 + 4);
+                s[0] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+            } else if (PAD == 2) {
+                const float2 a = *(const float2 *)(row + lane % 16 * 2);
+                s[0] = a.x + a.y;
+            } else {
+                s[0] = row[lane];
+            }
+#pragma unroll
+            for (int o = GROUP / 2; o; o /= 2) s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], o);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = PAD == 1 ? s[0] : __shfl_sync(0xFFFFFFFFu, s[0], k * GROUP);
+    }
 
-template <int CL>
-__device__ __forceinline__ void clear_area(float *area)
-{
-    for (int i = threadIdx.x; i < kAreaBytes / 4; i += blockDim.x) area[i] = 0.f;
-    __syncthreads();
-    if (CL > 1) tc::cluster_sync_all();
-}
+    // No block leaves while another may still write to it.
+    __device__ __forceinline__ void leave() const
+    {
+        if (CL == 1) return;
+        __syncthreads();
+        tc::cluster_sync_all();
+    }
+};
 
 // The weights w and gamma_pre of vector v.  In shared memory the first and the last
 // four channels of the vectors lie in planes, 16 bytes a lane.
@@ -178,30 +225,44 @@ __device__ __forceinline__ void lds_plane(const float *plane, uint32_t at, uint3
     f[3] = f2(b.z, b.w);
 }
 
-// Bytes that Scales keeps of shared memory.
-__host__ __device__ __forceinline__ uint32_t scale_bytes(int vpt, uint32_t threads) { return 64u * vpt * threads; }
+// What a thread takes of a row: vectors first + i * lanes + id, i < VPT.  GL > 0: blocks of
+// several rows, GL lanes each; else a row has the block's threads, or a cluster's (CL > 1).
+template <int VPT, int GL, int CL>
+struct Share {
+    uint32_t lanes, id, group, groups, first;
+    __device__ __forceinline__ Share()
+        : lanes(GL ? GL : blockDim.x), id(GL ? threadIdx.x % (GL ? GL : 1) : threadIdx.x), group(GL ? threadIdx.x / (GL ? GL : 1) : 0),
+          groups(GL ? blockDim.x / (GL ? GL : 1) : 1), first(CL > 1 ? tc::cluster_ctarank() * (VPT * blockDim.x) : 0)
+    {
+    }
+    __device__ __forceinline__ uint32_t vec(int i) const { return first + i * lanes + id; }
+};
 
-template <int VPT, Weights WHERE, bool PRE>
+// The weights of a thread's vectors.  In shared memory (scale_bytes) the first and the last
+// four channels of the vectors lie in planes, 16 bytes a lane.
+__host__ __device__ __forceinline__ uint32_t scale_bytes(int vpt, uint32_t lanes) { return 64u * vpt * lanes; }
+
+template <int VPT, int GL, int CL, Weights WHERE>
 struct Scales {
     f32x2 w[WHERE == IN_REGISTERS ? VPT : 1][4], g[WHERE == IN_REGISTERS ? VPT : 1][4];
     float *plane;
+    uint32_t lanes, id;
 
-    // first: the block's first vector
-    __device__ __forceinline__ void init(const Params &p, float *shared, uint32_t first)
+    // A barrier has to follow.
+    __device__ __forceinline__ Scales(const Params &p, float *shared, const Share<VPT, GL, CL> &me) : plane(shared), lanes(me.lanes), id(me.id)
     {
-        plane = shared;
-        const uint32_t vecs = VPT * blockDim.x;
+        if (WHERE == IN_SHARED && me.group) return;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t at = i * blockDim.x + threadIdx.x, v = first + at;
+            const uint32_t v = me.vec(i), at = i * lanes + id;
             f32x2 a[4] = {}, b[4] = {};
             if (v < p.vecs) {
                 scale_of(p, v, a);
-                if (PRE) ld8f(p.gpre + v * 8, b);
+                if (p.gpre) ld8f(p.gpre + v * 8, b);
             }
-            if (WHERE == IN_SHARED) {               // read back by the thread that wrote them
-                sts_plane(plane, at, vecs, a);
-                if (PRE) sts_plane(plane + vecs * 8, at, vecs, b);
+            if (WHERE == IN_SHARED) {
+                sts_plane(plane, at, VPT * lanes, a);
+                sts_plane(plane + VPT * lanes * 8, at, VPT * lanes, b);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) w[i][k] = a[k], g[i][k] = b[k];
@@ -210,14 +271,14 @@ struct Scales {
     }
     __device__ __forceinline__ void scale(int i, f32x2 (&f)[4]) const
     {
-        if (WHERE == IN_SHARED) lds_plane(plane, i * blockDim.x + threadIdx.x, VPT * blockDim.x, f);
+        if (WHERE == IN_SHARED) lds_plane(plane, i * lanes + id, VPT * lanes, f);
         else
 #pragma unroll
             for (int k = 0; k < 4; ++k) f[k] = w[i][k];
     }
     __device__ __forceinline__ void pre(int i, f32x2 (&f)[4]) const
     {
-        if (WHERE == IN_SHARED) lds_plane(plane + VPT * blockDim.x * 8, i * blockDim.x + threadIdx.x, VPT * blockDim.x, f);
+        if (WHERE == IN_SHARED) lds_plane(plane + VPT * lanes * 8, i * lanes + id, VPT * lanes, f);
         else
 #pragma unroll
             for (int k = 0; k < 4; ++k) f[k] = g[i][k];
@@ -235,54 +296,54 @@ __device__ __forceinline__ size_t behind(const Rows &o, uint32_t chunk, uint32_t
 }
 
 // ------------------------------------------------------------ forward
-template <int VPT, int MAXT, int CL, Weights WHERE, bool POST, bool PRE>
-__global__ void __launch_bounds__(MAXT, 1) k_block_norm(const Params p)
+// Which norms there are: known at compile time where the first is (in the usual blocks of
+// today's models none follows the block), else looked up.
+enum Kind { ANY, PRE, BOTH };
+
+template <int VPT, int GL, int MAXT, int MINB, int CL, Kind KIND>
+__global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const Params p)
 {
     extern __shared__ __align__(16) uint8_t sm[];
-    float *const area = (float *)sm;
-    uint8_t *const after = sm + kAreaBytes;
+    const bool post = KIND == BOTH || (KIND == ANY && p.gpost), pre = KIND != ANY || p.gpre;
+    const Share<VPT, GL, CL> me;
     const uint32_t threads = blockDim.x, stage_bytes = 2 * VPT * 16 * threads;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(after + (WHERE == IN_SHARED ? scale_bytes(VPT, threads) : 0)) + threadIdx.x * 16;
-    Scales<VPT, WHERE, PRE> ws;
-    const uint32_t first_vec = CL > 1 ? tc::cluster_ctarank() * (VPT * threads) : 0, block = blockIdx.x / CL, blocks = gridDim.x / CL;
-    ws.init(p, (float *)after, first_vec);
-    clear_area<CL>(area);
-    int turn = 0;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + (GL ? 0 : kAreaBytes)) + threadIdx.x * 16;
+    const Scales<VPT, GL, CL, IN_REGISTERS> ws(p, nullptr, me);
+    Sums<GL, CL> total(p, sm);
     size_t yoff[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) yoff[i] = behind(p.y, p.y_chunk, first_vec + i * threads + threadIdx.x);
+    for (int i = 0; i < VPT; ++i) yoff[i] = behind(p.y, p.y_chunk, me.vec(i));
     auto fetch = [&](uint32_t row, int stage) {
-        if (row < p.rows) {
+        if (GL || row < p.rows) {
             const uint32_t r = p.tokens(row), t = row - r * p.T;
             const char *const yrow = row_of(p.y, p.y_chunk, row, r, t), *const rrow = p.res.at(r, t);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const uint32_t v = first_vec + i * threads + threadIdx.x;
-                if (v >= p.vecs) continue;
-                copy<16>(ring + stage * stage_bytes + i * 16 * threads, yrow + yoff[i]);
-                copy<16>(ring + stage * stage_bytes + (VPT + i) * 16 * threads, rrow + v * 16);
+                const bool on = row < p.rows && me.vec(i) < p.vecs;
+                copy<16>(ring + stage * stage_bytes + i * 16 * threads, yrow + yoff[i], on);
+                copy<16>(ring + stage * stage_bytes + (VPT + i) * 16 * threads, rrow + me.vec(i) * 16, on);
             }
         }
         copies_done();
     };
-    uint32_t ahead = block;                        // rows stay below 2^31 - 2^20, and a grid below 2^16
-    for (int s = 0; s < p.stages; ++s, ahead += blocks) fetch(ahead, s);
-    int stage = 0;
-    for (uint32_t row = block; row < p.rows; row += blocks, ahead += blocks) {
+    const uint32_t step = gridDim.x / CL * me.groups;   // rows stay below 2^31 - 2^20, and a step below 2^18
+    uint32_t row = blockIdx.x / CL * me.groups + me.group, ahead = row;
+    for (int s = 0; s < p.stages; ++s, ahead += step) fetch(ahead, s);
+    // a warp's lanes take part in its sums as long as one of its rows exists
+    for (int stage = 0; row - (GL ? me.group % (32 / (GL ? GL : 32)) : 0) < p.rows; row += step, ahead += step) {
         wait_oldest(p.stages);
+        const bool live = !GL || row < p.rows;
         const uint32_t r = p.tokens(row), t = row - r * p.T;
         uint4 yw[VPT], rw[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            yw[i] = rw[i] = make_uint4(0, 0, 0, 0);
-            if (first_vec + i * threads + threadIdx.x >= p.vecs) continue;
             yw[i] = lds16(ring + stage * stage_bytes + i * 16 * threads);
             rw[i] = lds16(ring + stage * stage_bytes + (VPT + i) * 16 * threads);
         }
         fetch(ahead, stage);
         stage = stage + 1 == p.stages ? 0 : stage + 1;
         float rp = 1.f;
-        if (POST) {
+        if (post) {
             f32x2 ss = 0;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -292,91 +353,90 @@ __global__ void __launch_bounds__(MAXT, 1) k_block_norm(const Params p)
                 for (int k = 0; k < 4; ++k) ss = fma2(y[k], y[k], ss);
             }
             float sum[1] = {hsum(ss)};
-            block_sum<1, CL>(sum, area, turn);
+            total(sum);
             rp = rsqrtf(fmaf(sum[0], p.inv_n, p.eps));
         }
         f32x2 h[VPT][4], hh = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = first_vec + i * threads + threadIdx.x;
-            const bool on = v < p.vecs;
+            const uint32_t v = me.vec(i);
+            const bool on = live && v < p.vecs;
             f32x2 y[4], w[4];
             wide8(yw[i], y);
             wide8(rw[i], h[i]);
-            if (on) ws.scale(i, w);
+            ws.scale(i, w);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if (on) h[i][k] = fma2(w[k], mul2(y[k], both(rp)), h[i][k]);
+                h[i][k] = fma2(w[k], mul2(y[k], both(rp)), h[i][k]);
                 hh = fma2(h[i][k], h[i][k], hh);
             }
             if (on) __stcs((uint4 *)(p.h.at(r, t) + v * 16), narrow8(h[i]));
             if (p.y8.q.base) put8(p.y8, r, t, v, on, yw[i]);
             if (p.res8.q.base) put8(p.res8, r, t, v, on, rw[i]);
         }
-        if (!PRE) continue;
-        float sum[1] = {hsum(hh)};
-        block_sum<1, CL>(sum, area, turn);
-        const float q = rsqrtf(fmaf(sum[0], p.inv_n, p.eps));
+        if (pre) {
+            float sum[1] = {hsum(hh)};
+            total(sum);
+            const float q = rsqrtf(fmaf(sum[0], p.inv_n, p.eps));
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = first_vec + i * threads + threadIdx.x;
-            const bool on = v < p.vecs;
-            f32x2 g[4];
-            uint4 zw = make_uint4(0, 0, 0, 0);
-            if (on) {
+            for (int i = 0; i < VPT; ++i) {
+                const uint32_t v = me.vec(i);
+                const bool on = live && v < p.vecs;
+                f32x2 g[4];
                 ws.pre(i, g);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) h[i][k] = mul2(mul2(h[i][k], both(q)), g[k]);
-                zw = narrow8(h[i]);
-                __stcs((uint4 *)(p.z.at(r, t) + v * 16), zw);
+                const uint4 zw = narrow8(h[i]);
+                if (on) __stcs((uint4 *)(p.z.at(r, t) + v * 16), zw);
+                if (p.z8.q.base) put8(p.z8, r, t, v, on, on ? zw : make_uint4(0, 0, 0, 0));
             }
-            if (p.z8.q.base) put8(p.z8, r, t, v, on, zw);
         }
+        if (CL > 1 && !total.ok) break;
     }
+    total.leave();
 }
 
 // ------------------------------------------------------------ gradient
-// A block takes rows j, j + per, ... of one slot.  Its threads keep the sums of
-// their channels over all its rows, and leave them in the block's part, which
-// k_block_sums adds up in block order.
-template <int VPT, int MAXT, int CL, bool FULL, Weights WHERE, bool HELD, bool POST, bool PRE>
-__global__ void __launch_bounds__(MAXT, 1) k_block_norm_bwd(const Params p)
+// A block takes rows j, j + per, ... of one slot (with several rows at a time: runs of
+// them).  Its threads keep the sums of their channels over all their rows, and the block
+// leaves them in its part, which k_block_sums adds up in block order.
+template <int VPT, int GL, int MAXT, int MINB, int CL, bool FULL, bool HELD, Kind KIND>
+__global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
 {
     extern __shared__ __align__(16) uint8_t sm[];
     constexpr int YB = HELD ? 8 : 16;                   // staged bytes of 8 channels of y and of res
-    float *const area = (float *)sm;
-    uint8_t *const after = sm + kAreaBytes;
+    const bool post = KIND == BOTH || (KIND == ANY && p.gpost), pre = KIND != ANY || p.gpre;
+    const Share<VPT, GL, CL> me;
+    uint8_t *const after = sm + (GL ? 0 : kAreaBytes);
     const uint32_t threads = blockDim.x, in_bytes = VPT * YB * threads, d_bytes = VPT * 16 * threads;
-    const uint32_t stage_bytes = 2 * in_bytes + (PRE ? 2 : 1) * d_bytes;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(after + (WHERE == IN_SHARED ? scale_bytes(VPT, threads) : 0));
-    Scales<VPT, WHERE, PRE> ws;
-    const uint32_t first_vec = CL > 1 ? tc::cluster_ctarank() * (VPT * threads) : 0, block = blockIdx.x / CL;
-    ws.init(p, (float *)after, first_vec);
-    clear_area<CL>(area);
-    const uint32_t r = block / p.per, first = block - r * p.per;
-    int turn = 0;
+    const uint32_t stage_bytes = 2 * in_bytes + (pre ? 2 : 1) * d_bytes;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(after + scale_bytes(VPT, me.lanes));
+    const Scales<VPT, GL, CL, IN_SHARED> ws(p, (float *)after, me);
+    if (GL) __syncthreads();
+    Sums<GL, CL> total(p, sm);
+    const uint32_t block = blockIdx.x / CL, r = block / p.per, step = p.per * me.groups;
     size_t yoff[HELD ? 1 : VPT], dyoff[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        if (!HELD) yoff[i] = behind(p.y, p.y_chunk, first_vec + i * threads + threadIdx.x);
-        dyoff[i] = behind(p.dy, p.dy_chunk, first_vec + i * threads + threadIdx.x);
+        if (!HELD) yoff[i] = behind(p.y, p.y_chunk, me.vec(i));
+        dyoff[i] = behind(p.dy, p.dy_chunk, me.vec(i));
     }
     auto fetch = [&](uint32_t t, int stage) {
-        if (t < p.T) {
+        if (GL || t < p.T) {
             const uint32_t at = ring + stage * stage_bytes + threadIdx.x * YB, dat = ring + stage * stage_bytes + 2 * in_bytes + threadIdx.x * 16;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const uint32_t v = first_vec + i * threads + threadIdx.x;
-                if (!FULL && v >= p.vecs) continue;
+                const uint32_t v = me.vec(i);
+                const bool on = FULL || (t < p.T && v < p.vecs);
                 if (HELD) {
-                    copy<8>(at + i * YB * threads, p.y8.q.at(r, t) + v * 8);
-                    copy<8>(at + in_bytes + i * YB * threads, p.res8.q.at(r, t) + v * 8);
+                    copy<8>(at + i * YB * threads, p.y8.q.at(r, t) + v * 8, on);
+                    copy<8>(at + in_bytes + i * YB * threads, p.res8.q.at(r, t) + v * 8, on);
                 } else {
-                    copy<16>(at + i * YB * threads, row_of(p.y, p.y_chunk, r * p.T + t, r, t) + yoff[i]);
-                    copy<16>(at + in_bytes + i * YB * threads, p.res.at(r, t) + v * 16);
+                    copy<16>(at + i * YB * threads, row_of(p.y, p.y_chunk, r * p.T + t, r, t) + yoff[i], on);
+                    copy<16>(at + in_bytes + i * YB * threads, p.res.at(r, t) + v * 16, on);
                 }
-                if (p.dh.base) copy<16>(dat + i * 16 * threads, p.dh.at(r, t) + v * 16);
-                if (PRE) copy<16>(dat + d_bytes + i * 16 * threads, p.dz.at(r, t) + v * 16);
+                copy<16>(dat + i * 16 * threads, (p.dh.base ? p.dh : p.dres).at(r, t) + v * 16, on && p.dh.base);
+                if (pre) copy<16>(dat + d_bytes + i * 16 * threads, p.dz.at(r, t) + v * 16, on);
             }
         }
         copies_done();
@@ -386,29 +446,27 @@ __global__ void __launch_bounds__(MAXT, 1) k_block_norm_bwd(const Params p)
         if (HELD && t < p.T)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const uint32_t v = first_vec + i * threads + threadIdx.x;
+                const uint32_t v = me.vec(i);
+                ey[i] = er[i] = 1;
                 if (!FULL && v >= p.vecs) continue;
                 ey[i] = __ldcs((const uint8_t *)p.y8.e.at(r, t) + v / 4);
                 er[i] = __ldcs((const uint8_t *)p.res8.e.at(r, t) + v / 4);
             }
     };
     f32x2 acc_d[VPT][4] = {}, acc_z[VPT][4] = {};
-    uint32_t ahead = first;
-    fetch_groups(first);
-    for (int s = 0; s < p.stages; ++s, ahead += p.per) fetch(ahead, s);
-    int stage = 0;
-    for (uint32_t t = first; t < p.T; t += p.per, ahead += p.per) {
+    uint32_t t = (block - r * p.per) * me.groups + me.group, ahead = t;
+    fetch_groups(t);
+    for (int s = 0; s < p.stages; ++s, ahead += step) fetch(ahead, s);
+    // a warp's lanes take part in its sums as long as one of its rows exists
+    for (int stage = 0; t - (GL ? me.group % (32 / (GL ? GL : 32)) : 0) < p.T; t += step, ahead += step) {
         wait_oldest(p.stages);
+        const bool live = !GL || t < p.T;
         const uint32_t at = ring + stage * stage_bytes + threadIdx.x * YB, dat = ring + stage * stage_bytes + 2 * in_bytes + threadIdx.x * 16;
         f32x2 y[VPT][4], h[VPT][4];
         uint4 dh[VPT], dz[VPT];
         f32x2 ss = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            dh[i] = dz[i] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[i][k] = h[i][k] = 0;
-            if (!FULL && first_vec + i * threads + threadIdx.x >= p.vecs) continue;
             if (HELD) {
                 held8(lds8(at + i * YB * threads), ey[i], y[i]);
                 held8(lds8(at + in_bytes + i * YB * threads), er[i], h[i]);
@@ -416,95 +474,106 @@ __global__ void __launch_bounds__(MAXT, 1) k_block_norm_bwd(const Params p)
                 wide8(lds16(at + i * YB * threads), y[i]);
                 wide8(lds16(at + in_bytes + i * YB * threads), h[i]);
             }
-            if (p.dh.base) dh[i] = lds16(dat + i * 16 * threads);
-            if (PRE) dz[i] = lds16(dat + d_bytes + i * 16 * threads);
+            dh[i] = lds16(dat + i * 16 * threads);
+            if (pre) dz[i] = lds16(dat + d_bytes + i * 16 * threads);
 #pragma unroll
             for (int k = 0; k < 4; ++k) ss = fma2(y[i][k], y[i][k], ss);
         }
         fetch(ahead, stage);
-        fetch_groups(t + p.per);
+        fetch_groups(t + step);
         stage = stage + 1 == p.stages ? 0 : stage + 1;
         float rp = 1.f;
-        if (POST) {
+        if (post) {
             float sum[1] = {hsum(ss)};
-            block_sum<1, CL>(sum, area, turn);
-            rp = rsqrtf(fmaf(sum[0], p.inv_n, p.eps));
+            total(sum);
+            rp = live ? rsqrtf(fmaf(sum[0], p.inv_n, p.eps)) : 0.f;
         }
         f32x2 hh = 0, th = 0, vd = 0, vt = 0, vh = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = first_vec + i * threads + threadIdx.x;
-            if (!FULL && v >= p.vecs) continue;
             f32x2 w[4], g[4], d[4], z[4];
             ws.scale(i, w);
-            if (PRE) ws.pre(i, g), wide8(dz[i], z);
-            if (POST) wide8(dh[i], d);
+            if (pre) ws.pre(i, g), wide8(dz[i], z);
+            if (KIND != PRE) wide8(dh[i], d);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                y[i][k] = mul2(y[i][k], both(rp));
+                if (KIND != PRE) y[i][k] = mul2(y[i][k], both(rp));
                 const f32x2 x = mul2(w[k], y[i][k]);
                 h[i][k] = add2(h[i][k], x);
-                if (POST) vd = fma2(x, d[k], vd);
-                if (PRE) {
+                if (KIND != PRE) vd = fma2(x, d[k], vd);
+                if (pre) {
                     const f32x2 tt = mul2(z[k], g[k]);
                     hh = fma2(h[i][k], h[i][k], hh);
                     th = fma2(tt, h[i][k], th);
-                    if (POST) vt = fma2(x, tt, vt), vh = fma2(x, h[i][k], vh);
+                    if (KIND != PRE) vt = fma2(x, tt, vt), vh = fma2(x, h[i][k], vh);
                 }
             }
         }
         float q = 0.f, c = 0.f, m = 0.f;                // d = dh + q t - c h;  dy = rp (d w - yh m)
-        if (PRE && POST) {
-            float s[5] = {hsum(hh), hsum(th), hsum(vd), hsum(vt), hsum(vh)};
-            block_sum<5, CL>(s, area, turn);
-            q = rsqrtf(fmaf(s[0], p.inv_n, p.eps));
-            c = q * q * q * (s[1] * p.inv_n);
-            m = (s[2] + q * s[3] - c * s[4]) * p.inv_n;
-        } else if (PRE) {
+        if (KIND == PRE) {
             float s[2] = {hsum(hh), hsum(th)};
-            block_sum<2, CL>(s, area, turn);
-            q = rsqrtf(fmaf(s[0], p.inv_n, p.eps));
+            total(s);
+            q = live ? rsqrtf(fmaf(s[0], p.inv_n, p.eps)) : 0.f;         // a row that is not there adds zeros
             c = q * q * q * (s[1] * p.inv_n);
-        } else if (POST) {
-            float s[1] = {hsum(vd)};
-            block_sum<1, CL>(s, area, turn);
-            m = s[0] * p.inv_n;
+        } else if (post || pre) {
+            float s[5] = {hsum(hh), hsum(th), hsum(vd), hsum(vt), hsum(vh)};
+            total(s);
+            if (pre) {
+                q = live ? rsqrtf(fmaf(s[0], p.inv_n, p.eps)) : 0.f;
+                c = q * q * q * (s[1] * p.inv_n);
+            }
+            if (post) m = (s[2] + q * s[3] - c * s[4]) * p.inv_n;
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = first_vec + i * threads + threadIdx.x;
-            if (!FULL && v >= p.vecs) continue;
+            const uint32_t v = me.vec(i);
             f32x2 w[4], g[4], d[4], z[4];
             ws.scale(i, w);
             wide8(dh[i], d);
-            if (PRE) ws.pre(i, g), wide8(dz[i], z);
+            if (pre) ws.pre(i, g), wide8(dz[i], z);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if (PRE) {
+                if (pre) {
                     acc_z[i][k] = fma2(z[k], mul2(h[i][k], both(q)), acc_z[i][k]);
                     d[k] = fma2(mul2(z[k], g[k]), both(q), d[k]);
                     d[k] = fma2(h[i][k], both(-c), d[k]);
                 }
                 acc_d[i][k] = fma2(d[k], y[i][k], acc_d[i][k]);
                 w[k] = mul2(d[k], w[k]);
-                if (POST) w[k] = mul2(fma2(y[i][k], both(-m), w[k]), both(rp));
+                if (post) w[k] = mul2(fma2(y[i][k], both(-m), w[k]), both(rp));
             }
+            if (!FULL && (!live || v >= p.vecs)) continue;
             __stcs((uint4 *)(p.dres.at(r, t) + v * 16), narrow8(d));
             __stcs((uint4 *)(row_of(p.dy, p.dy_chunk, r * p.T + t, r, t) + dyoff[i]), narrow8(w));
         }
+        if (CL > 1 && !total.ok) break;
     }
+    total.leave();
     if (!p.sums) return;
+    // the sums that are wanted, one after the other; with several rows a block those of all its groups
     float *part = p.part + (size_t)block * p.sums * p.N;
+    float *const red = (float *)sm;                     // [group][N]
+    if (GL) __syncthreads();                            // the staging is done with, by every warp
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        if (k == 0 ? !(p.gpost || p.gate) : !PRE) continue;
+        if (k == 0 ? !(p.gpost || p.gate) : !pre) continue;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint32_t v = first_vec + i * threads + threadIdx.x;
-            if (!FULL && v >= p.vecs) continue;
+            const uint32_t v = me.vec(i);
+            if (v >= p.vecs) continue;
             const f32x2(&f)[4] = k ? acc_z[i] : acc_d[i];
-            ((float4 *)(part + v * 8))[0] = make_float4(lo(f[0]), hi(f[0]), lo(f[1]), hi(f[1]));
-            ((float4 *)(part + v * 8))[1] = make_float4(lo(f[2]), hi(f[2]), lo(f[3]), hi(f[3]));
+            float *const to = (GL ? red + me.group * p.N : part) + v * 8;
+            ((float4 *)to)[0] = make_float4(lo(f[0]), hi(f[0]), lo(f[1]), hi(f[1]));
+            ((float4 *)to)[1] = make_float4(lo(f[2]), hi(f[2]), lo(f[3]), hi(f[3]));
+        }
+        if (GL) {
+            __syncthreads();
+            for (uint32_t i = threadIdx.x; i < p.N; i += threads) {
+                float s = 0.f;
+                for (uint32_t g = 0; g < me.groups; ++g) s += red[g * p.N + i];
+                part[i] = s;
+            }
+            __syncthreads();
         }
         part += p.N;
     }
@@ -555,14 +624,17 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) k_block_sums(const Params p)
 }
 
 // ------------------------------------------------------------ host
-// Vectors of 8 channels a thread.  Two halve what a row costs besides its channels (the
-// sums over the block above all): 8192 x 4096 forward with checkpoints 58 us against 67
-// with one, the gradient 72 against 100.  Where no SM gets a second row only its latency
-// counts, and one is quicker (8 rows 4.1 us against 4.5).  Rows above 8192 channels are
-// divided over a pair of blocks, which leave their sums in one another's shared memory.
+// How rows are divided.  Up to 512 channels a row has 8, 16 or 32 lanes of a warp, and no
+// barrier (240000 rows of 64 took 96 us with a warp each).  Wider rows have a block with two
+// vectors of 8 channels a thread: two halve what a row costs besides its channels, the sums
+// above all (8192 x 4096 forward with checkpoints 58 us against 67 with one, the gradient 72
+// against 100).  Where no SM gets a second row only its latency counts, and one is quicker (8
+// rows of 4096 4.1 us against 4.5).  Rows above 8192 channels have four blocks, so that each SM
+// works on parts of two rows (2048 x 16384, gradient: 152 us with two blocks of twice the size).
 struct Shape {
-    int vpt, cl, threads, stages, regs;
-    bool full;                       // every thread has all its vectors
+    int vpt, gl, cl, threads, stages, rows;   // rows: at once, in the blocks that the GPU holds
+    int groups;                               // rows of a block at once
+    bool full;                                // every thread has all its vectors
     size_t smem;
 };
 
@@ -570,35 +642,31 @@ static Shape shape_of(const rc_block_norm_args &a, bool grad, int sms)
 {
     const int vecs = a.N / 8;
     Shape s{};
-    s.cl = vecs > 1024 ? 2 : 1;
-    s.vpt = s.cl == 1 && (long long)a.P * a.T <= sms ? 1 : 2;
-    s.regs = s.vpt == 1 ? 64 : 128;                      // what the launch bounds leave a thread
-    s.threads = ((vecs + s.vpt * s.cl - 1) / (s.vpt * s.cl) + 31) / 32 * 32;
-    s.full = vecs == s.vpt * s.cl * s.threads;
+    s.cl = vecs > 1024 ? (grad ? 4 : 2) : 1;
+    s.gl = vecs <= 16 ? 8 : vecs <= 32 ? 16 : vecs <= 64 ? 32 : 0;
+    s.vpt = s.gl ? (vecs > 8 ? 2 : 1) : s.cl == 1 && (long long)a.P * a.T <= sms ? 1 : 2;
+    s.threads = s.gl ? 128 : ((vecs + s.vpt * s.cl - 1) / (s.vpt * s.cl) + 31) / 32 * 32;
+    s.groups = s.gl ? s.threads / s.gl : 1;
+    s.full = !s.gl && vecs == s.vpt * s.cl * s.threads;
+    // registers: what the launch bounds leave a thread
+    const int regs = s.gl ? (grad && s.vpt == 2 ? 168 : 128) : s.vpt == 1 ? 64 : 128, by_regs = 65536 / (regs * s.threads);
     const bool held = grad && a.y8.q.base;
-    const size_t lane = grad ? (held ? 16 : 32) + (a.gamma_pre ? 32 : 16) : 32;
-    const size_t stage = lane * s.vpt * s.threads, fixed = kAreaBytes + (grad ? scale_bytes(s.vpt, s.threads) : 0);
+    const size_t lane = grad ? (held ? 16 : 32) + (a.gamma_pre ? 32 : 16) : 32, stage = lane * s.vpt * s.threads;
+    const size_t fixed = (s.gl ? 0 : kAreaBytes) + (grad ? scale_bytes(s.vpt, s.gl ? s.gl : s.threads) : 0);
+    const size_t room = (size_t)227 * 1024 / by_regs - 1024;
     s.stages = 3;
-    while (s.stages > 1 && fixed + s.stages * stage > (s.threads * s.regs > 32768 ? 220u : 110u) * 1024) --s.stages;
+    while (s.stages > 1 && fixed + s.stages * stage > room) --s.stages;
     s.smem = fixed + s.stages * stage;
+    if (grad && s.gl && s.smem < (size_t)s.groups * a.N * 4) s.smem = (size_t)s.groups * a.N * 4;   // the groups' sums
+    const int by_smem = (int)(227 * 1024 / (s.smem + 1024)), blocks = by_regs < by_smem ? by_regs : by_smem;
+    s.rows = (blocks < 1 ? 1 : blocks) * sms / s.cl * s.groups;
     return s;
 }
 
-// Rows at once (blocks or pairs of them) that the GPU holds: by threads, registers (the
-// launch bounds' share) and shared memory.
-static int resident(const Shape &s, int sms)
+static int blocks_of_slot(const rc_block_norm_args &a, const Shape &s)
 {
-    const int t = 2048 / s.threads, r = 65536 / (s.regs * s.threads), m = (int)(227 * 1024 / (s.smem + 1024));
-    int n = t < r ? t : r;
-    n = n < m ? n : m;
-    n = n < 1 ? 1 : n > 32 ? 32 : n;
-    return n * sms / s.cl;
-}
-
-static int blocks_of_slot(const rc_block_norm_args &a, const Shape &s, int sms)
-{
-    const int most = (resident(s, sms) + a.P - 1) / a.P;
-    return a.T < most ? (a.T < 1 ? 1 : a.T) : most;
+    const int most = (s.rows / s.groups + a.P - 1) / a.P, need = (a.T + s.groups - 1) / s.groups;
+    return need < most ? (need < 1 ? 1 : need) : most;
 }
 
 template <auto KERNEL>
@@ -625,28 +693,40 @@ static cudaError_t start(unsigned blocks, const Shape &s, const Params &p, cudaS
     return cudaLaunchKernelEx(&cfg, KERNEL, p);
 }
 
-template <bool HELD, bool POST, bool PRE>
-static cudaError_t launch_grad(unsigned blocks, const Shape &s, const Params &p, cudaStream_t st)
+template <Kind KIND>
+static cudaError_t launch_forward(unsigned n, const Shape &s, const Params &p, cudaStream_t st)
 {
-    if (s.vpt == 1) return start<k_block_norm_bwd<1, 1024, 1, false, IN_SHARED, HELD, POST, PRE>>(blocks, s, p, st);
-    if (s.cl == 2) return start<k_block_norm_bwd<2, 512, 2, false, IN_SHARED, HELD, POST, PRE>>(blocks, s, p, st);
-    if (s.full) return start<k_block_norm_bwd<2, 512, 1, true, IN_SHARED, HELD, POST, PRE>>(blocks, s, p, st);
-    return start<k_block_norm_bwd<2, 512, 1, false, IN_SHARED, HELD, POST, PRE>>(blocks, s, p, st);
+    if (s.gl == 8) return s.vpt == 1 ? start<k_block_norm<1, 8, 128, 4, 1, KIND>>(n, s, p, st) : start<k_block_norm<2, 8, 128, 4, 1, KIND>>(n, s, p, st);
+    if (s.gl == 16) return start<k_block_norm<2, 16, 128, 4, 1, KIND>>(n, s, p, st);
+    if (s.gl) return start<k_block_norm<2, 32, 128, 4, 1, KIND>>(n, s, p, st);
+    if (s.vpt == 1) return start<k_block_norm<1, 0, 1024, 1, 1, KIND>>(n, s, p, st);
+    return s.cl == 2 ? start<k_block_norm<2, 0, 512, 1, 2, KIND>>(n, s, p, st) : start<k_block_norm<2, 0, 512, 1, 1, KIND>>(n, s, p, st);
 }
 
-template <bool POST, bool PRE>
-static cudaError_t launch(bool grad, bool held, unsigned blocks, const Shape &s, const Params &p, cudaStream_t st)
+template <bool HELD, Kind KIND>
+static cudaError_t launch_gradient(unsigned n, const Shape &s, const Params &p, cudaStream_t st)
 {
-    if (grad) return held ? launch_grad<true, POST, PRE>(blocks, s, p, st) : launch_grad<false, POST, PRE>(blocks, s, p, st);
-    if (s.vpt == 1) return start<k_block_norm<1, 1024, 1, IN_REGISTERS, POST, PRE>>(blocks, s, p, st);
-    if (s.cl == 2) return start<k_block_norm<2, 512, 2, IN_REGISTERS, POST, PRE>>(blocks, s, p, st);
-    return start<k_block_norm<2, 512, 1, IN_REGISTERS, POST, PRE>>(blocks, s, p, st);
+    if (s.gl == 8 && s.vpt == 1) return start<k_block_norm_bwd<1, 8, 128, 4, 1, false, HELD, KIND>>(n, s, p, st);
+    if (s.gl == 8) return start<k_block_norm_bwd<2, 8, 128, 3, 1, false, HELD, KIND>>(n, s, p, st);
+    if (s.gl == 16) return start<k_block_norm_bwd<2, 16, 128, 3, 1, false, HELD, KIND>>(n, s, p, st);
+    if (s.gl) return start<k_block_norm_bwd<2, 32, 128, 3, 1, false, HELD, KIND>>(n, s, p, st);
+    if (s.vpt == 1) return start<k_block_norm_bwd<1, 0, 1024, 1, 1, false, HELD, KIND>>(n, s, p, st);
+    if (s.cl == 4) return start<k_block_norm_bwd<2, 0, 256, 2, 4, false, HELD, KIND>>(n, s, p, st);
+    if (s.full) return start<k_block_norm_bwd<2, 0, 512, 1, 1, true, HELD, KIND>>(n, s, p, st);
+    return start<k_block_norm_bwd<2, 0, 512, 1, 1, false, HELD, KIND>>(n, s, p, st);
 }
 
-static cudaError_t launch_any(bool grad, bool held, unsigned blocks, const Shape &s, const Params &p, cudaStream_t st)
+template <Kind KIND>
+static cudaError_t launch_kind(bool grad, bool held, unsigned n, const Shape &s, const Params &p, cudaStream_t st)
 {
-    if (p.gpost) return p.gpre ? launch<true, true>(grad, held, blocks, s, p, st) : launch<true, false>(grad, held, blocks, s, p, st);
-    return p.gpre ? launch<false, true>(grad, held, blocks, s, p, st) : launch<false, false>(grad, held, blocks, s, p, st);
+    if (!grad) return launch_forward<KIND>(n, s, p, st);
+    return held ? launch_gradient<true, KIND>(n, s, p, st) : launch_gradient<false, KIND>(n, s, p, st);
+}
+
+static cudaError_t launch(bool grad, bool held, unsigned n, const Shape &s, const Params &p, cudaStream_t st)
+{
+    const auto go = !p.gpre ? launch_kind<ANY> : p.gpost ? launch_kind<BOTH> : launch_kind<PRE>;
+    return go(grad, held, n, s, p, st);
 }
 
 static cudaError_t launch_sums(const Params &p, int P, cudaStream_t st)
@@ -743,6 +823,8 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
     if ((rc_ = device_sms(&sms))) return rc_;
     const Shape s = shape_of(a, grad, sms);
     Params p{};
+    uint32_t *unused = nullptr;
+    if (s.cl > 1 && (rc_ = prepare_workspace_ext(nullptr, 0, 0, &p.hdr, &unused, &sms, &p.timeout_ns))) return rc_;
     p.y = rows_of(a.y), p.res = rows_of(a.res), p.h = rows_of(a.h), p.z = rows_of(a.z);
     p.dh = rows_of(a.dh), p.dz = rows_of(a.dz), p.dy = rows_of(a.dy), p.dres = rows_of(a.dres);
     p.y8 = act8_of(a.y8), p.res8 = act8_of(a.res8), p.z8 = act8_of(a.z8);
@@ -761,10 +843,10 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
     p.inv_n = 1.f / (float)a.N;
     unsigned blocks;
     if (!grad) {
-        const uint32_t most = (uint32_t)resident(s, sms);
-        blocks = p.rows < most ? p.rows : most;
+        const uint32_t most = (uint32_t)s.rows, all = p.rows < most ? p.rows : most;
+        blocks = (all + s.groups - 1) / s.groups;
     } else {
-        p.per = blocks_of_slot(a, s, sms);
+        p.per = blocks_of_slot(a, s);
         p.sums = sums_of(a);
         blocks = (unsigned)(p.per * a.P);
         const size_t need = (size_t)blocks * p.sums * a.N * 4;
@@ -775,7 +857,7 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
         else if (need && (rc_ = prepare_scratch(need, &space))) return rc_;
         p.part = (float *)space;
     }
-    cudaError_t e = launch_any(grad, held, blocks, s, p, (cudaStream_t)stream);
+    cudaError_t e = launch(grad, held, blocks, s, p, (cudaStream_t)stream);
     if (e == cudaSuccess && grad && p.sums) e = launch_sums(p, a.P, (cudaStream_t)stream);
     if (e != cudaSuccess) return set_error(RC_ERR_CUDA, "block_norm launch: %s", cudaGetErrorString(e));
     return RC_OK;
@@ -794,5 +876,5 @@ extern "C" size_t block_norm_bwd_workspace_bytes(const rc_block_norm_args *args)
     int sms = 0;
     if (!args || check_sizes(*args) || rc::device_sms(&sms)) return 0;
     const Shape s = shape_of(*args, true, sms);
-    return rc::kWsHead + (size_t)blocks_of_slot(*args, s, sms) * args->P * sums_of(*args) * args->N * 4;
+    return rc::kWsHead + (size_t)blocks_of_slot(*args, s) * args->P * sums_of(*args) * args->N * 4;
 }

@@ -156,7 +156,7 @@ def check_gradient(p, in_cols=False, held=False, dh=True, alpha=0.7, eps=1e-6, w
     return dy, dres, dw
 
 
-WIDTHS = [8, 16, 40, 248, 256, 264, 1000, 1032, 2048, 4096, 4104, 8192, 8200, 12288, 16384]
+WIDTHS = [8, 16, 40, 64, 72, 128, 136, 248, 256, 264, 512, 520, 1000, 1032, 2048, 4096, 4104, 8192, 8200, 12288, 16384]
 
 
 @pytest.mark.parametrize("N", WIDTHS)
@@ -198,6 +198,24 @@ def test_block_norm_small_and_zero_rows():
     check_forward(p, eps=1e-2)
     check_gradient(p, eps=1e-2)
     check_gradient(p, eps=1e-2, held=True)
+
+
+@pytest.mark.parametrize("N", [24, 136, 328])
+@pytest.mark.parametrize("T", [1, 3, 13])
+def test_block_norm_few_rows_without_eps(N, T):
+    """Warps that hold several rows, some of them past the last: with eps = 0 nothing of those may reach a sum."""
+    p = problem(1, T, N, seed=T)
+    check_forward(p, eps=0.0)
+    check_gradient(p, eps=0.0)
+    check_gradient(p, eps=0.0, held=True)
+
+
+@pytest.mark.parametrize("N", [40, 264, 1000, 4104, 9000])
+def test_block_norm_many_rows(N):
+    """More rows than the GPU holds at once, so that blocks go round."""
+    p = problem(2, 2600 if N < 4000 else 700, N, seed=N)
+    check_forward(p)
+    check_gradient(p, held=True)
 
 
 def test_block_norm_without_rows():
