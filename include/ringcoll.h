@@ -564,8 +564,8 @@ int act8_unpack(const rc_act8_args *args, void *stream);
 /*
  * Arguments of block_norm and block_norm_bwd.  T rows (tokens) of N channels on
  * each of P ranks; bf16 [P][T][N] (the row shards that ag_gemm gathers), except
- * that y and dy may lie as gemm_rs leaves its result: y_cols, dy_cols = 1 for
- * [P][P*T][N/P], column chunk k of all P*T rows in slot k (N/P a multiple of 8).
+ * that y, dy and dz may lie as gemm_rs leaves its result: y_cols, dy_cols, dz_cols
+ * = 1 for [P][P*T][N/P], column chunk k of all P*T rows in slot k (N/P a multiple of 8).
  * gamma_post, gate, gamma_pre: f32 [N], 16-byte aligned, each may be null.
  * y8, res8, z8: block_norm writes those given; block_norm_bwd reads y8 and res8
  * in the place of y and res when y8.q.base is not null (then both).
@@ -584,7 +584,7 @@ typedef struct {
     size_t ws_bytes;
     int P, T, N, y_cols, dy_cols;
     float alpha, eps;
-    int reserved; /* 0 */
+    int dz_cols;
 } rc_block_norm_args;
 
 /*
@@ -598,7 +598,7 @@ typedef struct {
  * would make them.  h may be res (in place); results are apart otherwise.
  * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, N a multiple of 8 up
  * to 16384, P*T < 2^31 - 2^20, layouts as for rc_rows, alpha finite, eps finite
- * and not negative, z8 only with z, reserved 0.  T = 0 does nothing.
+ * and not negative, z8 only with z.  T = 0 does nothing.
  */
 int block_norm(const rc_block_norm_args *args, void *stream);
 
@@ -607,9 +607,9 @@ int block_norm(const rc_block_norm_args *args, void *stream);
  * (then at those values: the statistics are computed again, nothing else need be
  * kept).  Reads dh (null: zero) and dz (null where gamma_pre is), the gradients of
  * h and z; writes dy, dres, each rounded once, and the sums of the weights'
- * gradients in binary32, in an order that does not depend on timing.  dres may be
- * dh or dz, dy may be dh or dz where both are [P][T][N], as wholes; results are
- * apart otherwise.  T = 0 gives sums of 0.  The library's own space for partial sums
+ * gradients in binary32, in an order that does not depend on timing.  dres and
+ * dy may each be dh or dz, as wholes, where both lie alike; results are apart
+ * otherwise.  T = 0 gives sums of 0.  The library's own space for partial sums
  * is that of attn_fwd, with its rules.  h, z, z8 are not used.
  */
 int block_norm_bwd(const rc_block_norm_args *args, void *stream);

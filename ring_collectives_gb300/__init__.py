@@ -697,7 +697,7 @@ def qk_norm_rope_bwd_workspace_bytes(P: int, T: int, Hq: int, Hkv: int, D: int) 
 
 
 # rc_act8_args of include/ringcoll.h: three rc_rows, four ints; rc_block_norm_args: fourteen rc_rows, eight pointers and
-# sizes, five ints, alpha, eps, reserved; rc_glu_args: twelve rc_rows, six ints; rc_wgrad_args: four rc_rows, workspace
+# sizes, five ints, alpha, eps, an int; rc_glu_args: twelve rc_rows, six ints; rc_wgrad_args: four rc_rows, workspace
 # and its size, eight ints
 _ACT8_ARGS = struct.Struct("@9Q4i")
 _BLOCK_NORM_ARGS = struct.Struct("@42Q8Q5iffi")
@@ -828,9 +828,9 @@ def block_norm_bwd(y, res, dh: torch.Tensor | None, dz: torch.Tensor | None, dy:
                    eps: float = 1e-6, workspace: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """Gradient of :func:`block_norm`.  y and res are its inputs, or both are the pairs y8 and
     res8 that it left (the gradient is then that at their values).  dh (or None) and dz are the
-    gradients of h and z; writes dy (in either layout of y) and dres, and where the weight is
-    given each rank's own sums dgamma_post, dgate, dgamma_pre (float32 [P, N]).  dres may be dh
-    or dz.  workspace: a CUDA tensor of at least block_norm_bwd_workspace_bytes bytes, which
+    gradients of h and z (dz in either layout of y: gemm_rs may have left it); writes dy (likewise) and dres, and where the weight is
+    given each rank's own sums dgamma_post, dgate, dgamma_pre (float32 [P, N]).  dres and dy
+    may each be dh or dz.  workspace: a CUDA tensor of at least block_norm_bwd_workspace_bytes bytes, which
     other calls may use too in stream order; None takes the library's own."""
     P, T, N = shape = dres.shape
     gpu = dres.get_device()
@@ -839,14 +839,15 @@ def block_norm_bwd(y, res, dh: torch.Tensor | None, dz: torch.Tensor | None, dy:
         raise TypeError("y and res are both tensors or both 8-bit pairs")
     rows, cols = (_NO_ROWS, 0) if held else _side(y, "y", gpu, shape)
     drows, dcols = _side(dy, "dy", gpu, shape)
+    zrows, zcols = (_NO_ROWS, 0) if dz is None else _side(dz, "dz", gpu, shape)
     args = _BLOCK_NORM_ARGS.pack(
         *rows, *(_NO_ROWS if held else _rows(res, "res", gpu, shape)), *_NO_ROWS * 2,
-        *(_NO_ROWS if dh is None else _rows(dh, "dh", gpu, shape)), *(_NO_ROWS if dz is None else _rows(dz, "dz", gpu, shape)),
+        *(_NO_ROWS if dh is None else _rows(dh, "dh", gpu, shape)), *zrows,
         *drows, *_rows(dres, "dres", gpu, shape), *(_act8(y, "y", gpu, shape) if held else _NO_ACT8),
         *(_act8(res, "res", gpu, shape) if held else _NO_ACT8), *_NO_ACT8,
         _weights(gamma_post, "gamma_post", gpu, (N,)), _weights(gate, "gate", gpu, (N,)), _weights(gamma_pre, "gamma_pre", gpu, (N,)),
         _weights(dgamma_post, "dgamma_post", gpu, (P, N)), _weights(dgate, "dgate", gpu, (P, N)), _weights(dgamma_pre, "dgamma_pre", gpu, (P, N)),
-        *_room(workspace, gpu), P, T, N, cols, dcols, alpha, eps, 0)
+        *_room(workspace, gpu), P, T, N, cols, dcols, alpha, eps, zcols)
     _launch(load().block_norm_bwd, args, dres.device, stream)
     return dy, dres
 

@@ -34,6 +34,13 @@ constexpr int kMostChannels = 16384;
 // Where a thread keeps the weights of its channels.
 enum Weights { IN_REGISTERS, IN_SHARED };
 
+// An operand [P][T][N], or in column chunks: slot s holds channels [s chunk, (s + 1) chunk) of
+// all P * T rows, `skip` bytes further from one chunk to the next than in a row of all.
+struct Side {
+    bool cols;
+    size_t skip;                     // 0 for rows
+};
+
 struct Params {
     Rows y, res, h, z, dh, dz, dy, dres;
     Act8 y8, res8, z8;
@@ -41,7 +48,8 @@ struct Params {
     float *dpost, *dgate, *dpre, *part;
     FastDiv tokens;                  // rows of a slot
     uint32_t rows, T, N, vecs;
-    uint32_t y_chunk, dy_chunk;      // channels of a slot of y, dy (0: rows of all N)
+    Side ys, dys, dzs;               // how y, dy and dz lie
+    uint32_t chunk;                  // channels of a slot of those that lie in column chunks
     int stages, per, sums, clear;    // gradient: blocks of a slot; sums of a block's part; 1: zero `part` once read
     float alpha, eps, inv_n;
     WsHeader *hdr;                   // clusters: where a wait that ran out is recorded
@@ -285,14 +293,10 @@ struct Scales {
     }
 };
 
-// y or dy, whose slots hold `chunk` channels of all rows (0: rows of all channels): the start
-// of row `row` (t of slot r), and behind it vector v.
-__device__ __forceinline__ char *row_of(const Rows &o, uint32_t chunk, uint32_t row, uint32_t r, uint32_t t) { return chunk ? o.at(0, row) : o.at(r, t); }
-__device__ __forceinline__ size_t behind(const Rows &o, uint32_t chunk, uint32_t v)
+// Vector v, in column chunk s, of row `row` (t of slot r).
+__device__ __forceinline__ char *place(const Rows &o, const Side &d, uint32_t row, uint32_t r, uint32_t t, uint32_t v, uint32_t s)
 {
-    if (!chunk) return (size_t)v * 16;
-    const uint32_t s = v * 8 / chunk;
-    return s * o.slot + (v * 8 - s * chunk) * 2;
+    return (d.cols ? o.at(0, row) : o.at(r, t)) + (size_t)v * 16 + s * d.skip;
 }
 
 // ------------------------------------------------------------ forward
@@ -310,17 +314,17 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const Params p)
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + (GL ? 0 : kAreaBytes)) + threadIdx.x * 16;
     const Scales<VPT, GL, CL, IN_REGISTERS> ws(p, nullptr, me);
     Sums<GL, CL> total(p, sm);
-    size_t yoff[VPT];
+    uint32_t chunk[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) yoff[i] = behind(p.y, p.y_chunk, me.vec(i));
+    for (int i = 0; i < VPT; ++i) chunk[i] = me.vec(i) * 8 / p.chunk;
     auto fetch = [&](uint32_t row, int stage) {
         if (GL || row < p.rows) {
             const uint32_t r = p.tokens(row), t = row - r * p.T;
-            const char *const yrow = row_of(p.y, p.y_chunk, row, r, t), *const rrow = p.res.at(r, t);
+            const char *const rrow = p.res.at(r, t);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const bool on = row < p.rows && me.vec(i) < p.vecs;
-                copy<16>(ring + stage * stage_bytes + i * 16 * threads, yrow + yoff[i], on);
+                copy<16>(ring + stage * stage_bytes + i * 16 * threads, place(p.y, p.ys, row, r, t, me.vec(i), chunk[i]), on);
                 copy<16>(ring + stage * stage_bytes + (VPT + i) * 16 * threads, rrow + me.vec(i) * 16, on);
             }
         }
@@ -415,12 +419,9 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
     if (GL) __syncthreads();
     Sums<GL, CL> total(p, sm);
     const uint32_t block = blockIdx.x / CL, r = block / p.per, step = p.per * me.groups;
-    size_t yoff[HELD ? 1 : VPT], dyoff[VPT];
+    uint32_t chunk[VPT];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if (!HELD) yoff[i] = behind(p.y, p.y_chunk, me.vec(i));
-        dyoff[i] = behind(p.dy, p.dy_chunk, me.vec(i));
-    }
+    for (int i = 0; i < VPT; ++i) chunk[i] = me.vec(i) * 8 / p.chunk;
     auto fetch = [&](uint32_t t, int stage) {
         if (GL || t < p.T) {
             const uint32_t at = ring + stage * stage_bytes + threadIdx.x * YB, dat = ring + stage * stage_bytes + 2 * in_bytes + threadIdx.x * 16;
@@ -432,23 +433,23 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
                     copy<8>(at + i * YB * threads, p.y8.q.at(r, t) + v * 8, on);
                     copy<8>(at + in_bytes + i * YB * threads, p.res8.q.at(r, t) + v * 8, on);
                 } else {
-                    copy<16>(at + i * YB * threads, row_of(p.y, p.y_chunk, r * p.T + t, r, t) + yoff[i], on);
+                    copy<16>(at + i * YB * threads, place(p.y, p.ys, r * p.T + t, r, t, v, chunk[i]), on);
                     copy<16>(at + in_bytes + i * YB * threads, p.res.at(r, t) + v * 16, on);
                 }
                 copy<16>(dat + i * 16 * threads, (p.dh.base ? p.dh : p.dres).at(r, t) + v * 16, on && p.dh.base);
-                if (pre) copy<16>(dat + d_bytes + i * 16 * threads, p.dz.at(r, t) + v * 16, on);
+                if (pre) copy<16>(dat + d_bytes + i * 16 * threads, place(p.dz, p.dzs, r * p.T + t, r, t, v, chunk[i]), on);
             }
         }
         copies_done();
     };
     uint32_t ey[HELD ? VPT : 1], er[HELD ? VPT : 1];     // the groups' bytes of the next row
     auto fetch_groups = [&](uint32_t t) {
-        if (HELD && t < p.T)
+        if (HELD)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const uint32_t v = me.vec(i);
-                ey[i] = er[i] = 1;
-                if (!FULL && v >= p.vecs) continue;
+                ey[i] = er[i] = 1;                       // where nothing is: 0 times a number
+                if (t >= p.T || (!FULL && v >= p.vecs)) continue;
                 ey[i] = __ldcs((const uint8_t *)p.y8.e.at(r, t) + v / 4);
                 er[i] = __ldcs((const uint8_t *)p.res8.e.at(r, t) + v / 4);
             }
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
             }
             if (!FULL && (!live || v >= p.vecs)) continue;
             __stcs((uint4 *)(p.dres.at(r, t) + v * 16), narrow8(d));
-            __stcs((uint4 *)(row_of(p.dy, p.dy_chunk, r * p.T + t, r, t) + dyoff[i]), narrow8(w));
+            __stcs((uint4 *)place(p.dy, p.dys, r * p.T + t, r, t, v, chunk[i]), narrow8(w));
         }
         if (CL > 1 && !total.ok) break;
     }
@@ -751,11 +752,10 @@ static int check_sizes(const rc_block_norm_args &a)
 {
     const int rc_ = check_row_sizes(a.P, a.T, a.N, kMostChannels);
     if (rc_) return rc_;
-    if ((a.y_cols | a.dy_cols) & ~1) return set_error(RC_ERR_INVALID, "y_cols and dy_cols are 0 or 1");
-    if ((a.y_cols || a.dy_cols) && a.N % (8 * a.P)) return set_error(RC_ERR_INVALID, "N=%d channels in P=%d chunks: not multiples of 8", a.N, a.P);
+    if ((a.y_cols | a.dy_cols | a.dz_cols) & ~1) return set_error(RC_ERR_INVALID, "y_cols, dy_cols and dz_cols are 0 or 1");
+    if ((a.y_cols || a.dy_cols || a.dz_cols) && a.N % (8 * a.P)) return set_error(RC_ERR_INVALID, "N=%d channels in P=%d chunks: not multiples of 8", a.N, a.P);
     if (!std::isfinite(a.alpha)) return set_error(RC_ERR_INVALID, "alpha must be finite");
     if (!(a.eps >= 0.f) || !std::isfinite(a.eps)) return set_error(RC_ERR_INVALID, "eps must be finite and not negative");
-    if (a.reserved) return set_error(RC_ERR_INVALID, "reserved is not 0");
     return RC_OK;
 }
 
@@ -790,7 +790,7 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
         if (some) {
             if (!a.gamma_pre != !a.dz.base) return set_error(RC_ERR_INVALID, "dz goes with gamma_pre");
             if ((held && ((rc_ = packed(a.y8, "y8")) || (rc_ = packed(a.res8, "res8")))) || (a.dh.base && (rc_ = rows(a.dh, "dh", false))) ||
-                (a.dz.base && (rc_ = rows(a.dz, "dz", false))) || (rc_ = rows(a.dy, "dy", a.dy_cols)) || (rc_ = rows(a.dres, "dres", false)))
+                (a.dz.base && (rc_ = rows(a.dz, "dz", a.dz_cols))) || (rc_ = rows(a.dy, "dy", a.dy_cols)) || (rc_ = rows(a.dres, "dres", false)))
                 return rc_;
         }
     }
@@ -813,9 +813,9 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
         const size_t wb = (size_t)a.P * a.N * 4;
         const Operand out[] = {at("dy", a.dy, a.dy_cols), at("dres", a.dres), bytes_at("dgamma_post", a.dgamma_post, wb),
                                bytes_at("dgate", a.dgate, wb), bytes_at("dgamma_pre", a.dgamma_pre, wb)};
-        const Operand in[] = {at("dh", a.dh), at("dz", a.dz), y, res_, q8("y8.q", a.y8, held), e8("y8.e", a.y8, held), q8("res8.q", a.res8, held),
+        const Operand in[] = {at("dh", a.dh), at("dz", a.dz, a.dz_cols), y, res_, q8("y8.q", a.y8, held), e8("y8.e", a.y8, held), q8("res8.q", a.res8, held),
                               e8("res8.e", a.res8, held), w0, w1, w2};
-        const unsigned whole[] = {a.dy_cols ? 0u : 3u, 3, 0, 0, 0};
+        const unsigned whole[] = {(a.dy_cols ? 0u : 1u) | (a.dy_cols == a.dz_cols ? 2u : 0u), 1u | (a.dz_cols ? 0u : 2u), 0, 0, 0};
         rc_ = check_apart(out, 5, in, 11, whole);
     }
     if (rc_) return rc_;
@@ -835,8 +835,9 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
     p.T = a.T;
     p.N = a.N;
     p.vecs = a.N / 8;
-    p.y_chunk = a.y_cols ? a.N / a.P : 0;
-    p.dy_chunk = a.dy_cols ? a.N / a.P : 0;
+    p.chunk = a.y_cols || a.dy_cols || a.dz_cols ? a.N / a.P : a.N;
+    auto side = [&](int cols, const rc_rows &o) { return Side{cols != 0, cols ? o.slot - chunk : 0}; };
+    p.ys = side(a.y_cols, a.y), p.dys = side(a.dy_cols, a.dy), p.dzs = side(a.dz_cols, a.dz);
     p.stages = s.stages;
     p.alpha = a.alpha;
     p.eps = a.eps;

@@ -29,7 +29,7 @@ WEIGHTS = ("gamma_post", "gate", "gamma_pre", "dgamma_post", "dgate", "dgamma_pr
 
 
 def _norm(**change):
-    a = dict(P=2, T=8, N=64, y_cols=0, dy_cols=0, alpha=1.0, eps=1e-6, reserved=0, ws=0, ws_bytes=0, y8=[0] * 6, res8=[0] * 6, z8=[0] * 6)
+    a = dict(P=2, T=8, N=64, y_cols=0, dy_cols=0, dz_cols=0, alpha=1.0, eps=1e-6, ws=0, ws_bytes=0, y8=[0] * 6, res8=[0] * 6, z8=[0] * 6)
     for i, n in enumerate(NORM):
         a[n] = [0x100000000 * (i + 1), *ROWS]
     for i, n in enumerate(WEIGHTS):
@@ -37,7 +37,7 @@ def _norm(**change):
     a.update(change)
     return rc._BLOCK_NORM_ARGS.pack(*sum((list(a[n]) for n in NORM + ("y8", "res8", "z8")), []), *(a[n] for n in WEIGHTS),
                                     a["ws"], a["ws_bytes"], a["P"], a["T"], a["N"], a["y_cols"], a["dy_cols"], a["alpha"],
-                                    a["eps"], a["reserved"])
+                                    a["eps"], a["dz_cols"])
 
 
 GLU = ("a", "b", "h", "dh", "da", "db")
@@ -68,7 +68,7 @@ def test_act8_refuses(lib, fn, change):
 
 @pytest.mark.parametrize("fn", ["block_norm", "block_norm_bwd"])
 @pytest.mark.parametrize("change", SIZES + [
-    dict(N=16392), dict(reserved=1), dict(y_cols=2), dict(dy_cols=-1), dict(alpha=float("inf")), dict(alpha=float("nan")), dict(eps=-1.0),
+    dict(N=16392), dict(dz_cols=2), dict(y_cols=2), dict(dy_cols=-1), dict(alpha=float("inf")), dict(alpha=float("nan")), dict(eps=-1.0),
     dict(eps=float("inf")), dict(P=3, N=64, y_cols=1), dict(y=[0, *ROWS]), dict(res=[0x200000008, *ROWS]), dict(gate=0xB004),
     dict(y_cols=1, y=[0x100000000, 1 << 20, 48])], ids=str)
 def test_block_norm_refuses(lib, fn, change):
@@ -89,7 +89,8 @@ def test_block_norm_forward_refuses(lib, change):
     dict(dz=[0, 0, 0]), dict(gamma_pre=0), dict(dgamma_pre=0), dict(gate=0), dict(dgate=0), dict(gamma_post=0), dict(dgamma_post=0),
     dict(dy=[0, *ROWS]), dict(dres=[0, *ROWS]), dict(res8=_packed(0x2000000000)), dict(y8=_packed(0x2000000000)),
     dict(dy=[0x100000000, *ROWS]), dict(dy=[0x800000000, *ROWS]), dict(dres=[0x600000080, *ROWS]), dict(dgate=0xF000),
-    dict(dy_cols=1, dy=[0x500000000, 1 << 20, 64]), dict(ws=0x1000080, ws_bytes=1 << 40)], ids=str)
+    dict(dy_cols=1, dy=[0x500000000, 1 << 20, 64]), dict(dz_cols=1, dz=[0x600000000, 1 << 20, 48]),
+    dict(dz_cols=1, dz=[0x600000000, 1 << 20, 128], dres=[0x600000000, 1 << 20, 128]), dict(ws=0x1000080, ws_bytes=1 << 40)], ids=str)
 def test_block_norm_gradient_refuses(lib, change):
     assert lib.block_norm_bwd(_norm(**change), None) == rc.RC_ERR_INVALID
 

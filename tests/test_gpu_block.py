@@ -143,7 +143,8 @@ def check_gradient(p, in_cols=False, held=False, dh=True, alpha=0.7, eps=1e-6, w
     P, T, N = res.shape
     dy, dres, dw = grads(p, in_cols)
     y8, res8 = (rc.act8_pack(t, rc.act8_empty(t.shape, DEV)) for t in (y, res)) if held else (cols(y, in_cols), res)
-    rc.block_norm_bwd(y8, res8, p["dh"] if dh else None, p["dz"], dy, dres, **named(dw, "d"), **named(p["w"]), alpha=alpha, eps=eps,
+    dz = p["dz"] if p["dz"] is None else cols(p["dz"], in_cols)
+    rc.block_norm_bwd(y8, res8, p["dh"] if dh else None, dz, dy, dres, **named(dw, "d"), **named(p["w"]), alpha=alpha, eps=eps,
                       workspace=workspace)
     at = [ob.act8_values(*ob.act8_pack(f64(t))) if held else f64(t) for t in (y, res)]
     dz = np.zeros(res.shape) if p["dz"] is None else f64(p["dz"])
@@ -210,6 +211,21 @@ def test_block_norm_few_rows_without_eps(N, T):
     check_gradient(p, eps=0.0, held=True)
 
 
+@pytest.mark.parametrize("N", [24, 136, 328, 1000])
+def test_block_norm_rows_behind_a_marked_one(N):
+    """A last row whose groups are marked as holding no numbers reaches its own results only, not the sums of
+    rows that come after it in the same lanes and do not exist."""
+    p = problem(1, 700, N, seed=N)
+    clean = check_gradient(p, held=True)
+    y8, res8 = (rc.act8_pack(p[k], rc.act8_empty(p[k].shape, DEV)) for k in ("y", "res"))
+    dy, dres, dw = grads(p)
+    for q, e in (y8, res8):
+        q[0, 650:], e[0, 650:] = 0, 255
+    p["dh"][0, 650:], p["dz"][0, 650:] = 0, 0
+    rc.block_norm_bwd(y8, res8, p["dh"], p["dz"], dy, dres, **named(dw, "d"), **named(p["w"]), alpha=0.7)
+    assert torch.equal(dy[0, :650], clean[0][0, :650]) and torch.isnan(dy[0, 650:]).all() and all(torch.isnan(t).all() for t in dw)
+
+
 @pytest.mark.parametrize("N", [40, 264, 1000, 4104, 9000])
 def test_block_norm_many_rows(N):
     """More rows than the GPU holds at once, so that blocks go round."""
@@ -228,7 +244,7 @@ def test_block_norm_without_rows():
 
 
 def test_block_norm_strided_views_in_place_and_gaps():
-    P, T, N = 2, 33, 264
+    P, T, N = 2, 33, 272
     p = problem(P, T, N, seed=6)
     h, z, _, _ = check_forward(p, alpha=1.0)
     dy, dres, dw = check_gradient(p, alpha=1.0)
@@ -242,6 +258,9 @@ def test_block_norm_strided_views_in_place_and_gaps():
     rc.block_norm_bwd(p["y"], p["res"], a, b, b, a, **named(dw2, "d"), **named(p["w"]))  # dres over dh, dy over dz
     assert torch.equal(a, dres) and torch.equal(b, dy) and (room[..., 2 * N:] == 9).all()
     assert all(torch.equal(s, t) for s, t in zip(dw, dw2))
+    both = cols(p["dz"], True)
+    rc.block_norm_bwd(p["y"], p["res"], p["dh"], both, both, dres, **named(dw2, "d"), **named(p["w"]))   # dy over dz, in chunks
+    assert torch.equal(both, cols(dy, True)) and torch.equal(a, dres)
 
 
 def test_a_non_finite_row_stays_alone():
