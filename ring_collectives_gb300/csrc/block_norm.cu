@@ -712,6 +712,7 @@ static cudaError_t launch_gradient(unsigned n, const Shape &s, const Params &p, 
     if (s.gl == 16) return start<k_block_norm_bwd<2, 16, 128, 3, 1, false, HELD, KIND>>(n, s, p, st);
     if (s.gl) return start<k_block_norm_bwd<2, 32, 128, 3, 1, false, HELD, KIND>>(n, s, p, st);
     if (s.vpt == 1) return start<k_block_norm_bwd<1, 0, 1024, 1, 1, false, HELD, KIND>>(n, s, p, st);
+    if (s.cl == 4 && s.full) return start<k_block_norm_bwd<2, 0, 256, 2, 4, true, HELD, KIND>>(n, s, p, st);
     if (s.cl == 4) return start<k_block_norm_bwd<2, 0, 256, 2, 4, false, HELD, KIND>>(n, s, p, st);
     if (s.full) return start<k_block_norm_bwd<2, 0, 512, 1, 1, true, HELD, KIND>>(n, s, p, st);
     return start<k_block_norm_bwd<2, 0, 512, 1, 1, false, HELD, KIND>>(n, s, p, st);
