@@ -11,14 +11,23 @@
 // 128 rows n of it in TMEM, and steps over the tokens by 64:
 //   warp 0       copies its 128 n of dy by TMA (tokens and channels past the end
 //                arrive as zeros);
-//   warps 2, 3   copy 128 k of q ahead by cp.async, and the groups' bytes;
-//   warps 8..    widen them into the swizzled tile, groups of four warps taking steps in
-//                turn: from waiting for a stage to its announcement a step takes longer than
-//                its MMAs;
+//   warps 2, 3   copy 128 k of q ahead, and the groups' bytes;
+//   warps 8-19   widen them into the swizzled tile, groups of four warps taking steps in
+//                turn: from a step's q to its announcement takes some four times as long as
+//                its MMAs.  A group converts in registers before it waits for a stage, so
+//                the stage is held for the stores and the fence only;
 //   warp 1       (even CTA) issues the MMAs of the pair, M = N = 256;
 //   warps 4-7    take finished tiles from TMEM, while the next one is summed.
 // Whole tiles are dealt out in rounds; the tokens of those that are left over are
 // divided evenly over all pairs, and k_wgrad_join adds the parts in order.
+//
+// Bound by shared memory: a step's MMAs last 512 clocks, in which a CTA's shared memory
+// takes in 16 KB of dy, 8 KB of q and 16 KB of widened x, and gives out the q again and
+// 32 KB to the tensor cores, 80 KB or 640 clocks.  Measured: 8 ranks x 768x4096 over 8192
+// tokens 269 + 7 us (412 GFLOP, 1.49 PFLOP/s; the MMAs by themselves take 195 us, with dy's
+// copies 219), one rank's 4096x4096 190 + 9 us (1.38 PFLOP/s).  What it went through: waits and issue by
+// single lanes 1101 -> 450 us, by whole warps 274; two groups of widening warps 308,
+// four 284 in the place of 269.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -301,13 +310,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
         if (elect_one()) tc_commit_pair_mc(drained, 1);
         wait_bar(drained, 0, ab, 10, true);
     } else if (warp == 2 || warp == 3) {
-        // ---------------- q and e ahead, a warp every other step.  q by TMA where its rows allow (a copy of a lane's
-        // own takes some ten instructions a piece, and a warp issues one every ten clocks or so: 64 tokens x 128
-        // bytes by cp.async last longer than three steps' MMAs), else by cp.async, eight lanes a token's 128
-        // bytes.  The four groups' bytes of two tokens a lane are loaded two steps of the warp ahead, because
-        // a byte cannot be copied so.  Past the last token or channel: zeros.
+        // ---------------- q and e ahead, a warp every other step.  q by TMA where its rows start on 16 bytes, else
+        // by cp.async, eight lanes a token's 128 bytes (4096 x 4104 over 8192 tokens: 286 us against 190).  The
+        // four groups' bytes of two tokens a lane are loaded two steps of the warp ahead, because a byte
+        // cannot be copied so.  Past the last token or channel: zeros.
         const int c = lane & 7, t0 = lane >> 3, mine = warp - 2;
-        Walk w{}, far{};                                    // the step to copy, and the one whose groups' bytes to load
+        Walk w{}, far{};                                  // the step to copy, and the one whose groups' bytes to load
         auto skip = [&](Walk &x, int n) {
             for (; n && x.tile >= 0; --n) x.next(p, pair);
         };
@@ -451,9 +459,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
                 tmem_ld32(from + col, v);
                 if (part) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        *(float4 *)(part + col + 4 * x) = make_float4(__uint_as_float(v[4 * x]), __uint_as_float(v[4 * x + 1]),
-                                                                      __uint_as_float(v[4 * x + 2]), __uint_as_float(v[4 * x + 3]));
+                    for (int x = 0; x < 4; ++x)
+                        st8<kStNormal>(part + col + 8 * x, make_uint4(v[8 * x], v[8 * x + 1], v[8 * x + 2], v[8 * x + 3]),
+                                       make_uint4(v[8 * x + 4], v[8 * x + 5], v[8 * x + 6], v[8 * x + 7]));
                 } else if (n < p.N) {
                     if (p.f32) store32<true>(p, row, w.k + col, v);
                     else store32<false>(p, row, w.k + col, v);
