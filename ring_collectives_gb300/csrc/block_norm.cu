@@ -13,10 +13,16 @@
 // it joins the sums for d in one round, so a row takes two rounds (of sum y^2, then
 // of the rest) instead of three.
 //
-// Bound by memory.  A block (for wide rows four) works on one row at a time and keeps it in registers;
-// every thread copies its own share of the coming rows into its own shared-memory
-// slots (cp.async) and reads it back, so no barrier stands between loads and use.  Channels past
-// the end of a row arrive as zeros, with weights of zero, and only the stores leave them out.
+// Bound by memory forward.  A block (for wide rows several) works on one row at a time
+// and keeps it in registers; every thread copies its own share of the coming rows into its own
+// shared-memory slots (cp.async) and reads it back, so no barrier stands between loads and
+// use.  Channels past the end of a row arrive as zeros, with weights of zero, and only the
+// stores leave them out.  The gradient is bound by what a row costs in instructions at 16
+// warps an SM, which its sums of the weights' gradients (32 registers a thread) hold it to:
+// issue slots 57 % busy, the shared-memory pipe 51 % (the weights are read from there twice).
+//
+// Measured on 8192 x 4096 with all weights: forward 47 us (5.7 TB/s, 84 % of the copy rate), with
+// checkpoints of y and res 58 us (86 %); the gradient from the checkpoints 70 + 4 us (4.6 TB/s, 68 %).
 #include <cmath>
 
 #include "act8.cuh"
