@@ -598,7 +598,9 @@ typedef struct {
  * would make them.  h may be res (in place); results are apart otherwise.
  * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, N a multiple of 8 up
  * to 16384, P*T < 2^31 - 2^20, layouts as for rc_rows, alpha finite, eps finite
- * and not negative, z8 only with z.  T = 0 does nothing.
+ * and not negative, z8 only with z.  T = 0 does nothing.  (eps = 0 makes NaNs of a
+ * row of zeros.)  Where N is above 8192 several blocks work on a row, and a wait of
+ * theirs that runs out is reported by ring_status(), as for the collectives.
  */
 int block_norm(const rc_block_norm_args *args, void *stream);
 

@@ -834,8 +834,8 @@ def block_norm_bwd(y, res, dh: torch.Tensor | None, dz: torch.Tensor | None, dy:
     other calls may use too in stream order; None takes the library's own."""
     P, T, N = shape = dres.shape
     gpu = dres.get_device()
-    held = isinstance(y, tuple)
-    if held != isinstance(res, tuple):
+    held = isinstance(y, (tuple, list))
+    if held != isinstance(res, (tuple, list)):
         raise TypeError("y and res are both tensors or both 8-bit pairs")
     rows, cols = (_NO_ROWS, 0) if held else _side(y, "y", gpu, shape)
     drows, dcols = _side(dy, "dy", gpu, shape)
@@ -880,8 +880,8 @@ def glu_bwd(a, b, dh: torch.Tensor, da: torch.Tensor, db: torch.Tensor, h: torch
     h8.  da and db may each be a, b or dh."""
     P, T, N = shape = dh.shape
     gpu = dh.get_device()
-    held = isinstance(a, tuple)
-    if held != isinstance(b, tuple):
+    held = isinstance(a, (tuple, list))
+    if held != isinstance(b, (tuple, list)):
         raise TypeError("a and b are both tensors or both 8-bit pairs")
     args = _GLU_ARGS.pack(
         *(_NO_ROWS * 2 if held else _rows(a, "a", gpu, shape) + _rows(b, "b", gpu, shape)),

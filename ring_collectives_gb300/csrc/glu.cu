@@ -153,6 +153,7 @@ static int run(const rc_glu_args *args, bool grad, void *stream)
     if (rc_ || g.T == 0) return rc_;
     const size_t bytes = (size_t)g.N * 2, groups = (size_t)(g.N + 31) / 32;
     const bool held = grad && g.a8.q.base, a8 = g.a8.q.base, b8 = g.b8.q.base, h8 = g.h8.q.base;
+    if (grad && !held && b8) return set_error(RC_ERR_INVALID, "b8 goes with a8");
     auto rows = [&](rc_rows &x, const char *name) { return check_rows(x, name, g.P, g.T, bytes, 16); };
     auto packed = [&](rc_act8 &x, const char *name) { return check_act8(x, name, g.P, g.T, g.N); };
     if ((!held && ((rc_ = rows(g.a, "a")) || (rc_ = rows(g.b, "b")))) ||

@@ -107,7 +107,7 @@ def test_glu_refuses(lib, fn, change):
 @pytest.mark.parametrize("fn,change", [
     ("glu", dict(h=[0, *ROWS])), ("glu", dict(h=[0x100000080, *ROWS])), ("glu", dict(a8=_packed(0x300000000))),
     ("glu_bwd", dict(da=[0, *ROWS])), ("glu_bwd", dict(db=[0x500000000, *ROWS])), ("glu_bwd", dict(h=[0x400000000, *ROWS])),
-    ("glu_bwd", dict(a8=_packed(0x2000000000))), ("glu_bwd", dict(dh=[0, *ROWS])), ("glu_bwd", dict(da=[0x400000040, *ROWS]))], ids=str)
+    ("glu_bwd", dict(a8=_packed(0x2000000000))), ("glu_bwd", dict(b8=_packed(0x2000000000))), ("glu_bwd", dict(dh=[0, *ROWS])), ("glu_bwd", dict(da=[0x400000040, *ROWS]))], ids=str)
 def test_glu_places_refused(lib, fn, change):
     assert getattr(lib, fn)(_glu(**change), None) == rc.RC_ERR_INVALID
 
