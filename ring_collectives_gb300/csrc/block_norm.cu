@@ -306,19 +306,20 @@ __device__ __forceinline__ char *place(const Rows &o, const Side &d, uint32_t ro
 }
 
 // ------------------------------------------------------------ forward
-// Which norms there are: known at compile time where the first is (in the usual blocks of
-// today's models none follows the block), else looked up.
-enum Kind { ANY, PRE, BOTH };
+// Which norms there are.  Known at compile time: looked up, they cost the gradient spilled
+// registers (777 x 1544 without the first norm 12.3 us in the place of 8.6).
+enum Kind { NONE = 0, POST = 1, PRE = 2, BOTH = 3 };
 
-template <int VPT, int GL, int MAXT, int MINB, int CL, Kind KIND>
+template <int VPT, int GL, int MAXT, int MINB, int CL, Weights WHERE, Kind KIND>
 __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const Params p)
 {
     extern __shared__ __align__(16) uint8_t sm[];
-    const bool post = KIND == BOTH || (KIND == ANY && p.gpost), pre = KIND != ANY || p.gpre;
+    constexpr bool post = KIND & POST, pre = KIND & PRE;
     const Share<VPT, GL, CL> me;
     const uint32_t threads = blockDim.x, stage_bytes = 2 * VPT * 16 * threads;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm + (GL ? 0 : kAreaBytes)) + threadIdx.x * 16;
-    const Scales<VPT, GL, CL, IN_REGISTERS> ws(p, nullptr, me);
+    uint8_t *const after = sm + (GL ? 0 : kAreaBytes);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(after + (WHERE == IN_SHARED ? scale_bytes(VPT, me.lanes) : 0)) + threadIdx.x * 16;
+    const Scales<VPT, GL, CL, WHERE> ws(p, (float *)after, me);
     Sums<GL, CL> total(p, sm);
     uint32_t chunk[VPT];
 #pragma unroll
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
 {
     extern __shared__ __align__(16) uint8_t sm[];
     constexpr int YB = HELD ? 8 : 16;                   // staged bytes of 8 channels of y and of res
-    const bool post = KIND == BOTH || (KIND == ANY && p.gpost), pre = KIND != ANY || p.gpre;
+    constexpr bool post = KIND & POST, pre = KIND & PRE;
     const Share<VPT, GL, CL> me;
     uint8_t *const after = sm + (GL ? 0 : kAreaBytes);
     const uint32_t threads = blockDim.x, in_bytes = VPT * YB * threads, d_bytes = VPT * 16 * threads;
@@ -501,35 +502,37 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
             f32x2 w[4], g[4], d[4], z[4];
             ws.scale(i, w);
             if (pre) ws.pre(i, g), wide8(dz[i], z);
-            if (KIND != PRE) wide8(dh[i], d);
+            if (post) wide8(dh[i], d);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                if (KIND != PRE) y[i][k] = mul2(y[i][k], both(rp));
+                if (post) y[i][k] = mul2(y[i][k], both(rp));
                 const f32x2 x = mul2(w[k], y[i][k]);
                 h[i][k] = add2(h[i][k], x);
-                if (KIND != PRE) vd = fma2(x, d[k], vd);
+                if (post) vd = fma2(x, d[k], vd);
                 if (pre) {
                     const f32x2 tt = mul2(z[k], g[k]);
                     hh = fma2(h[i][k], h[i][k], hh);
                     th = fma2(tt, h[i][k], th);
-                    if (KIND != PRE) vt = fma2(x, tt, vt), vh = fma2(x, h[i][k], vh);
+                    if (post) vt = fma2(x, tt, vt), vh = fma2(x, h[i][k], vh);
                 }
             }
         }
         float q = 0.f, c = 0.f, m = 0.f;                // d = dh + q t - c h;  dy = rp (d w - yh m)
-        if (KIND == PRE) {
-            float s[2] = {hsum(hh), hsum(th)};
+        if (KIND == BOTH) {
+            float s[5] = {hsum(hh), hsum(th), hsum(vd), hsum(vt), hsum(vh)};
             total(s);
             q = live ? rsqrtf(fmaf(s[0], p.inv_n, p.eps)) : 0.f;         // a row that is not there adds zeros
             c = q * q * q * (s[1] * p.inv_n);
-        } else if (post || pre) {
-            float s[5] = {hsum(hh), hsum(th), hsum(vd), hsum(vt), hsum(vh)};
+            m = (s[2] + q * s[3] - c * s[4]) * p.inv_n;
+        } else if (KIND == PRE) {
+            float s[2] = {hsum(hh), hsum(th)};
             total(s);
-            if (pre) {
-                q = live ? rsqrtf(fmaf(s[0], p.inv_n, p.eps)) : 0.f;
-                c = q * q * q * (s[1] * p.inv_n);
-            }
-            if (post) m = (s[2] + q * s[3] - c * s[4]) * p.inv_n;
+            q = live ? rsqrtf(fmaf(s[0], p.inv_n, p.eps)) : 0.f;
+            c = q * q * q * (s[1] * p.inv_n);
+        } else if (KIND == POST) {
+            float s[1] = {hsum(vd)};
+            total(s);
+            m = s[0] * p.inv_n;
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -642,6 +645,8 @@ struct Shape {
     int vpt, gl, cl, threads, stages, rows;   // rows: at once, in the blocks that the GPU holds
     int groups;                               // rows of a block at once
     bool full;                                // every thread has all its vectors
+    bool lean;                                // forward: weights in shared memory, so that an SM holds two blocks
+                                              // of 257 to 384 threads (6211 x 5064 with checkpoints: 75 -> 62 us)
     size_t smem;
 };
 
@@ -656,10 +661,11 @@ static Shape shape_of(const rc_block_norm_args &a, bool grad, int sms)
     s.groups = s.gl ? s.threads / s.gl : 1;
     s.full = !s.gl && vecs == s.vpt * s.cl * s.threads;
     // registers: what the launch bounds leave a thread
-    const int regs = s.gl ? (grad && s.vpt == 2 ? 168 : 128) : s.vpt == 1 ? 64 : 128, by_regs = 65536 / (regs * s.threads);
+    s.lean = !grad && !s.gl && s.cl == 1 && s.vpt == 2 && s.threads > 256 && s.threads <= 384;
+    const int regs = s.gl ? (grad && s.vpt == 2 ? 168 : 128) : s.vpt == 1 ? 64 : s.lean ? 80 : 128, by_regs = 65536 / (regs * s.threads);
     const bool held = grad && a.y8.q.base;
     const size_t lane = grad ? (held ? 16 : 32) + (a.gamma_pre ? 32 : 16) : 32, stage = lane * s.vpt * s.threads;
-    const size_t fixed = (s.gl ? 0 : kAreaBytes) + (grad ? scale_bytes(s.vpt, s.gl ? s.gl : s.threads) : 0);
+    const size_t fixed = (s.gl ? 0 : kAreaBytes) + (grad || s.lean ? scale_bytes(s.vpt, s.gl ? s.gl : s.threads) : 0);
     const size_t room = (size_t)227 * 1024 / by_regs - 1024;
     s.stages = 3;
     while (s.stages > 1 && fixed + s.stages * stage > room) --s.stages;
@@ -703,11 +709,13 @@ static cudaError_t start(unsigned blocks, const Shape &s, const Params &p, cudaS
 template <Kind KIND>
 static cudaError_t launch_forward(unsigned n, const Shape &s, const Params &p, cudaStream_t st)
 {
-    if (s.gl == 8) return s.vpt == 1 ? start<k_block_norm<1, 8, 128, 4, 1, KIND>>(n, s, p, st) : start<k_block_norm<2, 8, 128, 4, 1, KIND>>(n, s, p, st);
-    if (s.gl == 16) return start<k_block_norm<2, 16, 128, 4, 1, KIND>>(n, s, p, st);
-    if (s.gl) return start<k_block_norm<2, 32, 128, 4, 1, KIND>>(n, s, p, st);
-    if (s.vpt == 1) return start<k_block_norm<1, 0, 1024, 1, 1, KIND>>(n, s, p, st);
-    return s.cl == 2 ? start<k_block_norm<2, 0, 512, 1, 2, KIND>>(n, s, p, st) : start<k_block_norm<2, 0, 512, 1, 1, KIND>>(n, s, p, st);
+    if (s.gl == 8) return s.vpt == 1 ? start<k_block_norm<1, 8, 128, 4, 1, IN_REGISTERS, KIND>>(n, s, p, st) : start<k_block_norm<2, 8, 128, 4, 1, IN_REGISTERS, KIND>>(n, s, p, st);
+    if (s.gl == 16) return start<k_block_norm<2, 16, 128, 4, 1, IN_REGISTERS, KIND>>(n, s, p, st);
+    if (s.gl) return start<k_block_norm<2, 32, 128, 4, 1, IN_REGISTERS, KIND>>(n, s, p, st);
+    if (s.vpt == 1) return start<k_block_norm<1, 0, 1024, 1, 1, IN_REGISTERS, KIND>>(n, s, p, st);
+    if (s.cl == 2) return start<k_block_norm<2, 0, 512, 1, 2, IN_REGISTERS, KIND>>(n, s, p, st);
+    if (s.lean) return start<k_block_norm<2, 0, 384, 2, 1, IN_SHARED, KIND>>(n, s, p, st);
+    return start<k_block_norm<2, 0, 512, 1, 1, IN_REGISTERS, KIND>>(n, s, p, st);
 }
 
 template <bool HELD, Kind KIND>
@@ -733,7 +741,7 @@ static cudaError_t launch_kind(bool grad, bool held, unsigned n, const Shape &s,
 
 static cudaError_t launch(bool grad, bool held, unsigned n, const Shape &s, const Params &p, cudaStream_t st)
 {
-    const auto go = !p.gpre ? launch_kind<ANY> : p.gpost ? launch_kind<BOTH> : launch_kind<PRE>;
+    const auto go = p.gpre ? (p.gpost ? launch_kind<BOTH> : launch_kind<PRE>) : p.gpost ? launch_kind<POST> : launch_kind<NONE>;
     return go(grad, held, n, s, p, st);
 }
 
