@@ -52,9 +52,15 @@ constexpr int DEEP = 6;                       // steps of q on their way or wait
 constexpr int TOKENS = GROUP / 8;             // a group takes 128 k of as many tokens at a time,
 constexpr int PIECES = STEP / TOKENS;         // so often in a step
 constexpr int STEP_BYTES = STEP * HALF;
+constexpr int ODD_ROW = HALF + 16;            // bytes of an odd row in the slot of a step (TWINS)
+constexpr int EVEN_BYTES = STEP / 2 * HALF, SLOT = EVEN_BYTES + STEP / 2 * ODD_ROW;
+// How rows of q come: by cp.async, by TMA, or the even and the odd ones each by TMA.  Looked up
+// at run time the choice cost 4 % of the whole launch: the widening warps are that busy.
+enum Mode { COPIES, ROWS, TWINS };
 constexpr int EPILOGUE = 4;                   // warps that store
 constexpr int THREADS = 256 + GROUPS * GROUP;
-constexpr int SLOTS = DEEP * STEP_BYTES, ESLOTS = DEEP * STEP * 4;
+constexpr int ESLOT = STEP * 4 + 16;          // a step's groups' bytes, and whether its first row is an odd one
+constexpr int SLOTS = DEEP * SLOT, ESLOTS = DEEP * ESLOT;
 constexpr int TMEM_COLS = 512;                // two accumulators
 constexpr int SMEM = STAGES * 2 * OPERAND + SLOTS + ESLOTS + 1024 + 512;
 static_assert(SMEM <= 227 * 1024 && TOKENS % 8 == 0, "the stages and slots fit; a thread's tokens share a swizzle");
@@ -67,13 +73,13 @@ constexpr uint32_t kIdesc = idesc_bf16_f32(TILE, TILE) | (1u << 15) | kIdescBMnM
 struct Params {
     Act8 x8;
     Rows dw;
-    float *part;                              // [pair][2][256][256]
+    float *part;                              // [pair][2][64 of four k][256 n][4]
     WsHeader *hdr;
     int P, T, N, K;
     int n_tiles, k_tiles, whole, left;        // tiles dealt out whole; left over
     int pairs, sharers;                       // pairs of the launch; those that share the tiles left over
     uint32_t steps;
-    int dy_shared, q_shared, wide, f32, accumulate, st32, clear;
+    int dy_shared, q_shared, f32, accumulate, st32, clear;
     unsigned long long timeout_ns;
 };
 
@@ -207,8 +213,9 @@ __device__ __forceinline__ void store32(const Params &p, char *row, int k, uint3
         if (k + 8 * i < p.K) st_v4(o + i, w[i]);
 }
 
+template <Mode MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap map_q,
-                                                                            const Params p)
+                                                                            const __grid_constant__ CUtensorMap map_o, const Params p)
 {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -233,7 +240,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
             mbar_init(empty + 8 * s, 1);                  // one commit of the pair's MMAs
         }
         for (int d = 0; d < DEEP; ++d) {
-            mbar_init(qfull + 8 * d, p.wide ? 2 : 33);    // the arm for TMA's bytes or a warp's own copies; the groups' bytes
+            mbar_init(qfull + 8 * d, MODE == COPIES ? 33 : 2);    // the arm for TMA's bytes or a warp's own copies; the groups' bytes
             mbar_init(qempty + 8 * d, GROUP / 32);
         }
         for (int a = 0; a < 2; ++a) {
@@ -245,7 +252,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map) : "memory");
-        if (p.wide) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_q) : "memory");
+        if (MODE != COPIES) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_q) : "memory");
+        if (MODE == TWINS) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_o) : "memory");
     }
     __syncthreads();
     cluster_sync_all();
@@ -310,8 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
         if (elect_one()) tc_commit_pair_mc(drained, 1);
         wait_bar(drained, 0, ab, 10, true);
     } else if (warp == 2 || warp == 3) {
-        // ---------------- q and e ahead, a warp every other step.  q by TMA where its rows start on 16 bytes, else
-        // by cp.async, eight lanes a token's 128 bytes (4096 x 4104 over 8192 tokens: 286 us against 190).  The
+        // ---------------- q and e ahead, a warp every other step.  q by TMA where its rows start on 16 bytes or
+        // every other one does; else by cp.async, eight lanes a token's 128 bytes.  The
         // four groups' bytes of two tokens a lane are loaded two steps of the warp ahead, because a byte
         // cannot be copied so.  Past the last token or channel: zeros.
         const int c = lane & 7, t0 = lane >> 3, mine = warp - 2;
@@ -349,15 +357,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
             for (int turn = 0; turn < 2; ++turn) {
                 if (w.tile < 0) break;
                 if (!(ok = wait_all(qempty + 8 * slot, phase ^ 1u, ab, 8))) break;
-                if (p.wide) {
+                const uint32_t row = (p.q_shared ? 0u : (uint32_t)w.r * (uint32_t)p.T) + w.step * STEP;   // of all ranks' (TWINS)
+                if (MODE != COPIES) {
                     if (elect_one()) {
-                        mbar_expect_tx(qfull + 8 * slot, STEP_BYTES);
-                        tma_load_3d(sQ + slot * STEP_BYTES, &map_q, w.k + (int)cta * HALF, (int)(w.step * STEP), p.q_shared ? 0 : w.r, qfull + 8 * slot);
+                        const uint32_t dst = sQ + slot * SLOT, bar = qfull + 8 * slot;
+                        const int k = w.k + (int)cta * HALF;
+                        if (MODE == ROWS) {
+                            mbar_expect_tx(bar, STEP_BYTES);
+                            tma_load_3d(dst, &map_q, k, (int)(w.step * STEP), p.q_shared ? 0 : w.r, bar);
+                        } else {
+                            mbar_expect_tx(bar, SLOT);
+                            tma_load_2d(dst, &map_q, k, (int)((row + 1) / 2), bar);
+                            tma_load_2d(dst + EVEN_BYTES, &map_o, k, (int)(row / 2), bar);
+                        }
                     }
                 } else {
                     const int k = w.k + (int)cta * HALF + c * 16;
                     const bool on = k < p.K, more = k + 8 < p.K;
-                    const uint32_t dst = sQ + slot * STEP_BYTES + t0 * HALF + c * 16;
+                    const uint32_t dst = sQ + slot * SLOT + t0 * HALF + c * 16;
                     const char *src = p.x8.q.at(w.r, w.step * STEP + t0) + k;
 #pragma unroll 4
                     for (int i = 0; i < STEP; i += 4, src += 4 * p.x8.q.row) {
@@ -369,9 +386,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
                 }
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(sE + slot * (STEP * 4) + (lane + 32 * i) * 4),
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(sE + slot * ESLOT + (lane + 32 * i) * 4),
                                  "r"(e[turn][i][0] | e[turn][i][1] << 8 | e[turn][i][2] << 16 | e[turn][i][3] << 24)
                                  : "memory");
+                if (MODE == TWINS && lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(sE + slot * ESLOT + STEP * 4), "r"(row & 1u) : "memory");
                 arrive_warp(qfull + 8 * slot, lane);
                 skip(w, 2);
                 groups(e[turn]);
@@ -381,7 +399,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");  // no copy stays in flight, also after a wait that ran out
-        if (p.wide && *(volatile int *)abort_flag)
+        if (MODE != COPIES && *(volatile int *)abort_flag)
             for (uint32_t i = n > DEEP ? n - DEEP : (uint32_t)mine; i < n; i += 2) wait_bar(qfull + 8 * (i % DEEP), i / DEEP & 1u, ab, 12, true);
     } else if (warp >= 8) {
         // ---------------- q to bf16.  The steps are dealt out to groups of warps in turn.  A thread takes 16 k
@@ -399,16 +417,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
         uint32_t stage = (uint32_t)group, phase = 0, slot = (uint32_t)group, qphase = 0;
         for (uint32_t n = (uint32_t)group; n < total; n += GROUPS) {
             if (!wait_all(qfull + 8 * slot, qphase, ab, 7)) break;
+            uint32_t odd = 0;                             // of this thread's rows: its tokens are all even or all odd
+            if (MODE == TWINS) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(odd) : "r"(sE + slot * ESLOT + STEP * 4) : "memory");
+            odd = (odd ^ t0) & 1u;
             uint4 x[PIECES][2];
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
                 uint4 q;
                 uint32_t e;
-                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                             : "r"(in + slot * STEP_BYTES + i * (TOKENS * HALF))
-                             : "memory");
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(ein + slot * (STEP * 4) + i * (TOKENS * 4)) : "memory");
+                if (MODE != TWINS) {
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                                 : "r"(in + slot * SLOT + i * (TOKENS * HALF))
+                                 : "memory");
+                } else {
+                    const uint32_t at = sQ + slot * SLOT + c * 16 + (odd ? EVEN_BYTES + 8 + ((t0 >> 1) + i * (TOKENS / 2)) * ODD_ROW : ((t0 >> 1) + i * (TOKENS / 2)) * HALF);
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "r"(at) : "memory");
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q.z), "=r"(q.w) : "r"(at + 8) : "memory");
+                }
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(ein + slot * ESLOT + i * (TOKENS * 4)) : "memory");
                 f32x2 f[4], g[4];
                 held8(flip ? make_uint2(q.z, q.w) : make_uint2(q.x, q.y), e, f);
                 held8(flip ? make_uint2(q.x, q.y) : make_uint2(q.z, q.w), e, g);
@@ -451,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
             tc_fence_after();
             const int local = (int)cta * HALF + i * 32 + lane, n = w.n + local;
             const uint32_t from = tmem + ((uint32_t)(i * 32) << 16) + acc * TILE;
-            float *const part = w.part < 0 ? nullptr : p.part + ((size_t)w.part * TILE + local) * TILE;
+            float *const part = w.part < 0 ? nullptr : p.part + ((size_t)w.part * TILE * TILE + local * 4);
             char *const row = p.dw.at(w.r, n);
 #pragma unroll 1
             for (int col = 0; col < TILE; col += 32) {
@@ -459,9 +486,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
                 tmem_ld32(from + col, v);
                 if (part) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        st8<kStNormal>(part + col + 8 * x, make_uint4(v[8 * x], v[8 * x + 1], v[8 * x + 2], v[8 * x + 3]),
-                                       make_uint4(v[8 * x + 4], v[8 * x + 5], v[8 * x + 6], v[8 * x + 7]));
+                    for (int x = 0; x < 8; ++x)           // four columns of 32 rows side by side
+                        st_v4(part + (col / 4 + x) * (TILE * 4), make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]));
                 } else if (n < p.N) {
                     if (p.f32) store32<true>(p, row, w.k + col, v);
                     else store32<false>(p, row, w.k + col, v);
@@ -484,15 +510,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
     if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
 }
 
-// Tile y of those left over, rows 4 x..: the sum of its parts in the order of their
-// tokens.  CLEAR: in a caller's workspace the parts are zeroed once read, because other
-// calls keep signal words there.
+// Tile y of those left over, 8 columns from 8 x: the sum of its parts in the order of
+// their tokens, a row a thread.  CLEAR: in a caller's workspace the parts are zeroed once
+// read, because other calls keep signal words there.
 template <bool CLEAR>
-__global__ void __launch_bounds__(256) k_wgrad_join(const Params p)
+__global__ void __launch_bounds__(TILE) k_wgrad_join(const Params p)
 {
     const int i = blockIdx.y, per = p.n_tiles * p.k_tiles, tile = p.whole + i, rest = tile % per;
-    const int local = blockIdx.x * 4 + (threadIdx.x >> 6), col = (threadIdx.x & 63) * 4;
-    const int n = rest / p.k_tiles * TILE + local, k = rest % p.k_tiles * TILE + col;
+    const int n = rest / p.k_tiles * TILE + (int)threadIdx.x, k = rest % p.k_tiles * TILE + (int)blockIdx.x * 8;
     // the sharers whose shares meet the tile's steps [from, to): the first may have begun in the tile
     // before, which is then its part 0 and this tile its part 1
     const uint64_t from = (uint64_t)i * p.steps, to = from + p.steps;
@@ -503,35 +528,43 @@ __global__ void __launch_bounds__(256) k_wgrad_join(const Params p)
     while (end < p.sharers && first_step(p, end) < to) ++end;
     const bool second = first_step(p, first) < from;
     const size_t step = (size_t)2 * TILE * TILE / 4;
-    float4 *part = (float4 *)(p.part + ((size_t)2 * first * TILE + local) * TILE + col);
+    float4 *part = (float4 *)p.part + first * step + (size_t)blockIdx.x * 2 * TILE + threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");     // the parts are written
-    float4 s = part[second ? step / 2 : 0];
-    if (CLEAR) part[second ? step / 2 : 0] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 *const own = part + (second ? step / 2 : 0);
+    float4 s[2] = {own[0], own[TILE]};
+    if (CLEAR) own[0] = own[TILE] = make_float4(0.f, 0.f, 0.f, 0.f);
     part += step;
 #pragma unroll 8
-    for (int j = 0; j < end - first - 1; ++j) {
-        const float4 v = part[j * step];
-        s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-    }
+    for (int j = 0; j < end - first - 1; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 v = part[j * step + h * TILE];
+            s[h] = make_float4(s[h].x + v.x, s[h].y + v.y, s[h].z + v.z, s[h].w + v.w);
+        }
     if (CLEAR)                                             // in a loop of its own: stores would hold up the loads
-        for (int j = 0; j < end - first - 1; ++j) part[j * step] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < end - first - 1; ++j) part[j * step] = part[j * step + TILE] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (n >= p.N || k >= p.K) return;
     char *const row = p.dw.at(tile / per, n);
     if (p.f32) {
         float4 *const o = (float4 *)(row + (size_t)k * 4);
-        if (p.accumulate) {
-            const float4 old = *o;
-            s = make_float4(old.x + s.x, old.y + s.y, old.z + s.z, old.w + s.w);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (p.accumulate) {
+                const float4 old = o[h];
+                s[h] = make_float4(old.x + s[h].x, old.y + s[h].y, old.z + s[h].z, old.w + s[h].w);
+            }
+            o[h] = s[h];
         }
-        *o = s;
     } else {
-        uint2 *const o = (uint2 *)(row + (size_t)k * 2);
+        uint4 *const o = (uint4 *)(row + (size_t)k * 2);
+        f32x2 f[4] = {f2(s[0].x, s[0].y), f2(s[0].z, s[0].w), f2(s[1].x, s[1].y), f2(s[1].z, s[1].w)};
         if (p.accumulate) {
-            const uint2 old = *o;
-            const f32x2 a = wide2(old.x), b = wide2(old.y);
-            s = make_float4(lo(a) + s.x, hi(a) + s.y, lo(b) + s.z, hi(b) + s.w);
+            f32x2 old[4];
+            wide8(*o, old);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = add2(old[j], f[j]);
         }
-        *o = make_uint2(narrow2(f2(s.x, s.y)), narrow2(f2(s.z, s.w)));
+        *o = narrow8(f);
     }
 }
 
@@ -549,19 +582,36 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// [P][T][channels] in boxes of `width` channels x 64 tokens.
-static int make_map(CUtensorMap *map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const rc_rows &o, int P, int T, int channels, uint32_t width)
+static int encode(CUtensorMap *map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, uint32_t rank, const void *base, const cuuint64_t *dims,
+                  const cuuint64_t *strides, const cuuint32_t *box)
 {
     auto fn = encode_fn();
     if (!fn) return set_error(RC_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled is not available from the driver");
-    const bool one = P == 1 || o.slot == 0;
-    const cuuint64_t dims[3] = {(cuuint64_t)channels, (cuuint64_t)T, one ? 1u : (cuuint64_t)P};
-    const cuuint64_t strides[2] = {(cuuint64_t)o.row, one ? (cuuint64_t)o.row : (cuuint64_t)o.slot};
-    const cuuint32_t box[3] = {width, STEP, 1}, estr[3] = {1, 1, 1};
-    const CUresult r = fn(map, type, 3, o.base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, type, rank, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return set_error(RC_ERR_INVALID, "tensor map encoding failed (CUresult %d)", (int)r);
     return RC_OK;
+}
+
+// [P][T][channels] in boxes of `width` channels x 64 tokens.
+static int make_map(CUtensorMap *map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const rc_rows &o, int P, int T, int channels, uint32_t width)
+{
+    const bool one = P == 1 || o.slot == 0;
+    const cuuint64_t dims[3] = {(cuuint64_t)channels, (cuuint64_t)T, one ? 1u : (cuuint64_t)P};
+    const cuuint64_t strides[2] = {(cuuint64_t)o.row, one ? (cuuint64_t)o.row : (cuuint64_t)o.slot};
+    const cuuint32_t box[3] = {width, STEP, 1};
+    return encode(map, type, swizzle, 3, o.base, dims, strides, box);
+}
+
+// Rows of an odd number of 8 bytes, every other of which starts 8 bytes off a boundary of 16:
+// the even rows by one map, and the odd ones by another that starts 8 bytes before the first.
+static int make_twins(CUtensorMap *even, CUtensorMap *odd, const rc_rows &q, uint64_t rows, int K)
+{
+    const cuuint64_t stride[1] = {2 * (cuuint64_t)q.row}, de[2] = {(cuuint64_t)K, (rows + 1) / 2}, dodd[2] = {(cuuint64_t)K + 8, rows / 2};
+    const cuuint32_t be[2] = {HALF, STEP / 2}, bo[2] = {ODD_ROW, STEP / 2};
+    const int rc_ = encode(even, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, 2, q.base, de, stride, be);
+    return rc_ ? rc_ : encode(odd, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, 2, (const char *)q.base + q.row - 8, dodd, stride, bo);
 }
 
 // Tiles that fill whole rounds of the pairs are dealt out whole.  The tokens of the rest are
@@ -590,6 +640,16 @@ static void plan(const rc_wgrad_args &a, int sms, Params &p)
     if (p.whole < p.pairs) p.pairs = p.whole > p.sharers ? p.whole : p.sharers;
 }
 static size_t part_bytes(const Params &p) { return (size_t)p.sharers * 2 * TILE * TILE * 4; }
+
+template <Mode MODE>
+static cudaError_t start(const CUtensorMap &map, const CUtensorMap &map_q, const CUtensorMap &map_o, const Params &p, cudaStream_t st)
+{
+    static OncePerDevice once;
+    const cudaError_t e = once([] { return cudaFuncSetAttribute(k_wgrad<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
+    if (e != cudaSuccess) return e;
+    k_wgrad<MODE><<<2 * p.pairs, THREADS, SMEM, st>>>(map, map_q, map_o, p);
+    return cudaGetLastError();
+}
 
 static int check_sizes(const rc_wgrad_args &a)
 {
@@ -635,7 +695,11 @@ static int run(const rc_wgrad_args *args, void *stream)
     p.dw = rows_of(a.dw);
     p.dy_shared = a.P == 1 || a.dy.slot == 0;
     p.q_shared = a.P == 1 || a.x8.q.slot == 0;
-    p.wide = !(((uintptr_t)a.x8.q.base | (a.P > 1 ? a.x8.q.slot : 0) | a.x8.q.row) & 15u);
+    const rc_rows &q = a.x8.q;
+    const uint64_t rows = p.q_shared ? (uint64_t)a.T : (uint64_t)a.P * a.T;
+    Mode mode = COPIES;
+    if (!(((uintptr_t)q.base | (a.P > 1 ? q.slot : 0) | q.row) & 15u)) mode = ROWS;
+    else if (!((uintptr_t)q.base & 15u) && q.row % 16 == 8 && rows > 1 && rows < 0x7FFFFFFFu && (p.q_shared || q.slot == q.row * (size_t)a.T)) mode = TWINS;
     p.f32 = a.dw_type == RC_F32;
     p.accumulate = a.accumulate;
     p.st32 = !(((uintptr_t)a.dw.base | a.dw.slot | a.dw.row) & 31u);
@@ -648,21 +712,19 @@ static int run(const rc_wgrad_args *args, void *stream)
     if (!a.workspace && bytes && (rc_ = prepare_scratch(bytes, &space))) return rc_;
     p.clear = a.workspace != nullptr;
     p.part = (float *)space;
-    CUtensorMap map, map_q;
+    CUtensorMap map, map_q, map_o;
     if ((rc_ = make_map(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, a.dy, a.P, a.T, a.N, 64))) return rc_;
-    if (!p.wide) map_q = map;                 // not used
-    else if ((rc_ = make_map(&map_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, a.x8.q, a.P, a.T, a.K, HALF))) return rc_;
-    static OncePerDevice once;
-    cudaError_t e = once([] { return cudaFuncSetAttribute(k_wgrad, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM); });
-    if (e == cudaSuccess) {
-        k_wgrad<<<2 * p.pairs, THREADS, SMEM, st>>>(map, map_q, p);
-        e = cudaGetLastError();
-    }
+    map_q = map_o = map;                      // where they are not used
+    if (mode == ROWS) rc_ = make_map(&map_q, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, q, a.P, a.T, a.K, HALF);
+    if (mode == TWINS) rc_ = make_twins(&map_q, &map_o, q, rows, a.K);
+    if (rc_) return rc_;
+    const auto go = mode == ROWS ? start<ROWS> : mode == TWINS ? start<TWINS> : start<COPIES>;
+    cudaError_t e = go(map, map_q, map_o, p, st);
     if (e == cudaSuccess && p.left) {
         // set up while the tiles are summed; its blocks start when that has ended
         cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3(TILE / 4, (unsigned)p.left);
-        cfg.blockDim = dim3(256);
+        cfg.gridDim = dim3(TILE / 8, (unsigned)p.left);
+        cfg.blockDim = dim3(TILE);
         cfg.stream = st;
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -131,6 +131,35 @@ def test_non_finite_values_reach_their_row_or_column_only():
     assert torch.isnan(dw[0, :, 96:128]).all() and not torch.isfinite(dw[0, 260]).any() and torch.equal(dw[~bad], want[~bad])
 
 
+@pytest.mark.parametrize("K", [200, 208])
+def test_a_rank_does_not_reach_another(K):
+    """Tokens come 64 at a time, the last of a rank with the next rank's first; marked groups there stay there."""
+    dy, (q, e) = problem(3, 129, 136, K, seed=8)
+    want = check(dy, (q, e))
+    q[1], e[1] = 0, 255
+    dy[2] = float("nan")
+    dw = torch.empty_like(want)
+    rc.gemm_wgrad(dy, (q, e), dw)
+    assert torch.equal(dw[0], want[0]) and torch.isnan(dw[1:]).all()
+
+
+@pytest.mark.parametrize("K,pad", [(72, 0), (72, 8), (80, 8), (256, 8), (264, 16), (1000, 0)])
+def test_rows_of_every_alignment(K, pad):
+    """Rows of bytes on 16-byte boundaries, every other on one, and neither; slots that follow one another or not."""
+    P, T, N = 2, 131, 72
+    dy, (q, e) = problem(P, T, N, K, seed=K)
+    want = check(dy, (q, e))
+    for gap in (0, 1):
+        room = torch.full((P, T + gap, K + pad), 99, dtype=torch.int8, device=DEV)
+        view = room[:, :T, :K]
+        view.copy_(q)
+        assert torch.equal(check(dy, (view, e)), want)
+        flat = torch.full((room.numel() + 16,), 99, dtype=torch.int8, device=DEV)
+        shifted = flat[8:].as_strided((P, T, K), room.stride())
+        shifted.copy_(q)
+        assert torch.equal(check(dy, (shifted, e)), want)
+
+
 def test_workspace_streams_and_graph():
     P, T, N, K = 1, 6000, 512, 768
     a, b = problem(P, T, N, K, seed=5), problem(P, T, N, K, seed=6)
