@@ -110,8 +110,7 @@ __device__ __forceinline__ uint4 narrow8(const f32x2 (&f)[4])
 // ------------------------------------------------------------ 8 bits
 // The values of 8 bytes with their group's byte e.  A byte b + 128 as the low bits of 2^23
 // gives an exact difference, and a power of two an exact product; e = 255 is an infinity,
-// which makes a NaN of a zero.  (One multiply-add in their place needs a second way for
-// groups above 2^104, and its choice cost more than it saved.)
+// which makes a NaN of a zero.
 __device__ __forceinline__ void held8(const uint2 &q, uint32_t e, f32x2 (&f)[4])
 {
     const f32x2 scale = both(__uint_as_float(e << 23)), zero = both(-8388736.f);
@@ -121,6 +120,21 @@ __device__ __forceinline__ void held8(const uint2 &q, uint32_t e, f32x2 (&f)[4])
         const uint32_t a = __byte_perm(w, 0x4B000000u, i & 1 ? 0x7652 : 0x7650);
         const uint32_t b = __byte_perm(w, 0x4B000000u, i & 1 ? 0x7653 : 0x7651);
         f[i] = mul2(add2(f2(__uint_as_float(a), __uint_as_float(b)), zero), scale);
+    }
+}
+
+// The same in one multiply-add, for e <= 230 (gemm_wgrad of 8 x 768x4096 over 8192 tokens: 260 -> 255
+// us): above, 2^23 + 128 times the power of two is no number.
+__device__ __forceinline__ void held8_low(const uint2 &q, uint32_t e, f32x2 (&f)[4])
+{
+    const float s = __uint_as_float(e << 23);
+    const f32x2 scale = both(s), bias = both(s * -8388736.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = (i < 2 ? q.x : q.y) ^ 0x80808080u;
+        const uint32_t a = __byte_perm(w, 0x4B000000u, i & 1 ? 0x7652 : 0x7650);
+        const uint32_t b = __byte_perm(w, 0x4B000000u, i & 1 ? 0x7653 : 0x7651);
+        f[i] = fma2(f2(__uint_as_float(a), __uint_as_float(b)), scale, bias);
     }
 }
 

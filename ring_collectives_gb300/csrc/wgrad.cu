@@ -11,7 +11,9 @@
 // 128 rows n of it in TMEM, and steps over the tokens by 64:
 //   warp 0       copies its 128 n of dy by TMA (tokens and channels past the end
 //                arrive as zeros);
-//   warps 2, 3   copy 128 k of q ahead, and the groups' bytes;
+//   warps 2, 3   copy 128 k of q ahead (rows on 16 bytes by TMA; rows of an odd number of 8
+//                bytes by TMA too, the even ones and the odd ones each; others by cp.async),
+//                and the groups' bytes;
 //   warps 8-19   widen them into the swizzled tile, groups of four warps taking steps in
 //                turn: from a step's q to its announcement takes some four times as long as
 //                its MMAs.  A group converts in registers before it waits for a stage, so
@@ -24,10 +26,11 @@
 // Bound by shared memory: a step's MMAs last 512 clocks, in which a CTA's shared memory
 // takes in 16 KB of dy, 8 KB of q and 16 KB of widened x, and gives out the q again and
 // 32 KB to the tensor cores, 80 KB or 640 clocks.  Measured: 8 ranks x 768x4096 over 8192
-// tokens 269 + 7 us (412 GFLOP, 1.49 PFLOP/s; the MMAs by themselves take 195 us, with dy's
-// copies 219), one rank's 4096x4096 190 + 9 us (1.38 PFLOP/s).  What it went through: waits and issue by
-// single lanes 1101 -> 450 us, by whole warps 274; two groups of widening warps 308,
-// four 284 in the place of 269.
+// tokens 255 + 7 us (412 GFLOP, 1.57 PFLOP/s; the MMAs by themselves take 195 us, with dy's
+// copies 219), one rank's 4096x4096 181 + 7 us (1.46 PFLOP/s), 4096x4104 184 + 9 us (rows of an
+// odd number of 8 bytes; by cp.async 286).  Two groups of widening warps in the place of three:
+// 263, 182 and 199 us.  Over a few tokens the tiles' stores bound it: 8 x 2736x3448 over 4
+// tokens 72 us, 2.1 TB/s.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -420,28 +423,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
             uint32_t odd = 0;                             // of this thread's rows: its tokens are all even or all odd
             if (MODE == TWINS) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(odd) : "r"(sE + slot * ESLOT + STEP * 4) : "memory");
             odd = (odd ^ t0) & 1u;
-            uint4 x[PIECES][2];
+            uint4 q[PIECES], x[PIECES][2];
+            uint32_t e[PIECES], high = 0;
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {
-                uint4 q;
-                uint32_t e;
                 if (MODE != TWINS) {
                     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                                 : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w)
                                  : "r"(in + slot * SLOT + i * (TOKENS * HALF))
                                  : "memory");
                 } else {
                     const uint32_t at = sQ + slot * SLOT + c * 16 + (odd ? EVEN_BYTES + 8 + ((t0 >> 1) + i * (TOKENS / 2)) * ODD_ROW : ((t0 >> 1) + i * (TOKENS / 2)) * HALF);
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "r"(at) : "memory");
-                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q.z), "=r"(q.w) : "r"(at + 8) : "memory");
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q[i].x), "=r"(q[i].y) : "r"(at) : "memory");
+                    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q[i].z), "=r"(q[i].w) : "r"(at + 8) : "memory");
                 }
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(ein + slot * ESLOT + i * (TOKENS * 4)) : "memory");
-                f32x2 f[4], g[4];
-                held8(flip ? make_uint2(q.z, q.w) : make_uint2(q.x, q.y), e, f);
-                held8(flip ? make_uint2(q.x, q.y) : make_uint2(q.z, q.w), e, g);
-                x[i][0] = narrow8(f);
-                x[i][1] = narrow8(g);
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e[i]) : "r"(ein + slot * ESLOT + i * (TOKENS * 4)) : "memory");
+                high = max(high, e[i]);
             }
+            auto widen = [&](auto held) {
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i) {
+                    f32x2 f[4], g[4];
+                    held(flip ? make_uint2(q[i].z, q[i].w) : make_uint2(q[i].x, q[i].y), e[i], f);
+                    held(flip ? make_uint2(q[i].x, q[i].y) : make_uint2(q[i].z, q[i].w), e[i], g);
+                    x[i][0] = narrow8(f);
+                    x[i][1] = narrow8(g);
+                }
+            };
+            if (__any_sync(0xFFFFFFFFu, high > 230)) widen([](const uint2 &w, uint32_t b, f32x2 (&f)[4]) { held8(w, b, f); });
+            else widen([](const uint2 &w, uint32_t b, f32x2 (&f)[4]) { held8_low(w, b, f); });
             arrive_warp(qempty + 8 * slot, lane);
             if (!wait_all(empty + 8 * stage, phase ^ 1u, ab, 11)) break;
 #pragma unroll
@@ -454,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             // The odd CTA's halves are complete in its shared memory (the fence above), where its own tensor
             // core reads them; the arrival publishes nothing else, so it is relaxed.  With a release at cluster
-            // scope the whole launch took 602 us in the place of 535.
+            // scope an early form of the whole launch took 602 us in the place of 535.
             if (even) {
                 arrive_warp(full_b + 8 * stage, lane);
             } else {

@@ -131,6 +131,16 @@ def test_non_finite_values_reach_their_row_or_column_only():
     assert torch.isnan(dw[0, :, 96:128]).all() and not torch.isfinite(dw[0, 260]).any() and torch.equal(dw[~bad], want[~bad])
 
 
+def test_huge_and_tiny_groups():
+    """Groups near both ends of the range: their values, products and sums are all numbers."""
+    dy, (q, e) = problem(1, 96, 72, 136, seed=9)
+    dy = (dy * 2.0 ** -20).contiguous()
+    e[0, 5], e[0, 70], e[0, 71] = 240, 228, 231
+    e[0, 30:40] = 2
+    dw = check(dy, (q, e), torch.float32)
+    assert torch.isfinite(dw).all() and dw.abs().max() > 1e30
+
+
 @pytest.mark.parametrize("K", [200, 208])
 def test_a_rank_does_not_reach_another(K):
     """Tokens come 64 at a time, the last of a rank with the next rank's first; marked groups there stay there."""
