@@ -23,6 +23,8 @@
 //
 // Measured on 8192 x 4096 with all weights: forward 47 us (5.7 TB/s, 84 % of the copy rate), with
 // checkpoints of y and res 58 us (86 %); the gradient from the checkpoints 70 + 4 us (4.6 TB/s, 68 %).
+// A row's sum y^2 taken with the sums of the row before, one round a row, changed nothing there (70 us)
+// and cost rows that do not fill their threads 7 %.
 #include <cmath>
 
 #include "act8.cuh"
@@ -640,7 +642,7 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) k_block_sums(const Params p)
 // above all (8192 x 4096 forward with checkpoints 58 us against 67 with one, the gradient 72
 // against 100).  Where no SM gets a second row only its latency counts, and one is quicker (8
 // rows of 4096 4.1 us against 4.5).  Rows above 8192 channels have four blocks, so that each SM
-// works on parts of two rows (2048 x 16384, gradient: 152 us with two blocks of twice the size).
+// works on parts of two rows (2048 x 16384, gradient: 89 us; 152 with two blocks of twice the size).
 struct Shape {
     int vpt, gl, cl, threads, stages, rows;   // rows: at once, in the blocks that the GPU holds
     int groups;                               // rows of a block at once
@@ -649,6 +651,44 @@ struct Shape {
                                               // of 257 to 384 threads (6211 x 5064 with checkpoints: 75 -> 62 us)
     size_t smem;
 };
+
+static void cluster_of(cudaLaunchConfig_t &cfg, cudaLaunchAttribute (&at)[1], const Shape &s, unsigned clusters)
+{
+    cfg.gridDim = dim3(clusters * s.cl);
+    cfg.blockDim = dim3(s.threads);
+    cfg.dynamicSmemBytes = s.smem;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = s.cl;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+}
+
+// How many clusters of the gradient's the current device holds at once: fewer than its SMs would,
+// because a cluster stays inside one of their groups, and these are not all multiples of it (74
+// clusters of four blocks, two an SM, on 152 SMs).  A launch of more would start the last ones when
+// the first have ended, and last longer for it (2048 x 16384: 76 clusters 128 us, 74 of them 89).
+// The blocks of several slots are rounded down to what the GPU holds for the same reason.
+static int clusters_held(const Shape &s, const rc_block_norm_args &a, int fallback)
+{
+    static std::atomic<int> known[64][8][2][2];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return fallback;
+    std::atomic<int> &n = known[dev][s.threads / 32 - 1][a.y8.q.base != nullptr][a.gamma_pre != nullptr];
+    int held = n.load(std::memory_order_relaxed);
+    if (held) return held;
+    const auto kernel = k_block_norm_bwd<2, 0, 256, 2, 4, false, true, BOTH>;      // as any of them
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[1];
+    cluster_of(cfg, at, s, (unsigned)fallback);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&held, kernel, &cfg) != cudaSuccess || held < 1) {
+        (void)cudaGetLastError();
+        return fallback;
+    }
+    n.store(held, std::memory_order_relaxed);
+    return held;
+}
 
 static Shape shape_of(const rc_block_norm_args &a, bool grad, int sms)
 {
@@ -673,13 +713,14 @@ static Shape shape_of(const rc_block_norm_args &a, bool grad, int sms)
     if (grad && s.gl && s.smem < (size_t)s.groups * a.N * 4) s.smem = (size_t)s.groups * a.N * 4;   // the groups' sums
     const int by_smem = (int)(227 * 1024 / (s.smem + 1024)), blocks = by_regs < by_smem ? by_regs : by_smem;
     s.rows = (blocks < 1 ? 1 : blocks) * sms / s.cl * s.groups;
+    if (grad && s.cl > 1) s.rows = clusters_held(s, a, s.rows);
     return s;
 }
 
 static int blocks_of_slot(const rc_block_norm_args &a, const Shape &s)
 {
-    const int most = (s.rows / s.groups + a.P - 1) / a.P, need = (a.T + s.groups - 1) / s.groups;
-    return need < most ? (need < 1 ? 1 : need) : most;
+    const int most = s.rows / s.groups / a.P, need = (a.T + s.groups - 1) / s.groups;
+    return need > most ? (most < 1 ? 1 : most) : (need < 1 ? 1 : need);
 }
 
 template <auto KERNEL>
@@ -693,16 +734,9 @@ static cudaError_t start(unsigned blocks, const Shape &s, const Params &p, cudaS
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks * s.cl);
-    cfg.blockDim = dim3(s.threads);
-    cfg.dynamicSmemBytes = s.smem;
-    cfg.stream = st;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = s.cl;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cluster_of(cfg, at, s, blocks);
+    cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, KERNEL, p);
 }
 
