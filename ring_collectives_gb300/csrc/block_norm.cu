@@ -646,6 +646,7 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) k_block_sums(const Params p)
 struct Shape {
     int vpt, gl, cl, threads, stages, rows;   // rows: at once, in the blocks that the GPU holds
     int groups;                               // rows of a block at once
+    int sms;
     bool full;                                // every thread has all its vectors
     bool lean;                                // forward: weights in shared memory, so that an SM holds two blocks
                                               // of 257 to 384 threads (6211 x 5064 with checkpoints: 75 -> 62 us)
@@ -694,6 +695,7 @@ static Shape shape_of(const rc_block_norm_args &a, bool grad, int sms)
 {
     const int vecs = a.N / 8;
     Shape s{};
+    s.sms = sms;
     s.cl = vecs > 1024 ? (grad ? 4 : 2) : 1;
     s.gl = vecs <= 16 ? 8 : vecs <= 32 ? 16 : vecs <= 64 ? 32 : 0;
     s.vpt = s.gl ? (vecs > 8 ? 2 : 1) : s.cl == 1 && (long long)a.P * a.T <= sms ? 1 : 2;
@@ -717,10 +719,17 @@ static Shape shape_of(const rc_block_norm_args &a, bool grad, int sms)
     return s;
 }
 
+// No more than the GPU holds at once, and no more than end in as many turns, because every block's
+// part is written and read again.  For the same reason a block has up to three rows before an SM
+// gets another block (777 x 1544 without the first norm: 9 + 6 us with a block for every row or two, 8.4 + 3.7;
+// 400 x 4096 10.8 + 4.6, 10.5 + 3.8); rows within a warp, of which a block has several anyway, do not.
 static int blocks_of_slot(const rc_block_norm_args &a, const Shape &s)
 {
-    const int most = s.rows / s.groups / a.P, need = (a.T + s.groups - 1) / s.groups;
-    return need > most ? (most < 1 ? 1 : most) : (need < 1 ? 1 : need);
+    const int held = s.rows / s.groups / a.P, most = held < 1 ? 1 : held, need = (a.T + s.groups - 1) / s.groups;
+    const long long rounds = ((long long)need * a.P * s.cl + s.sms - 1) / s.sms;
+    const int least = s.gl || s.vpt == 1 ? 1 : rounds < 3 ? (int)rounds : 3, balanced = (need + most - 1) / most;
+    const int turns = balanced > least ? balanced : least;
+    return need < 1 ? 1 : (need + turns - 1) / turns;
 }
 
 template <auto KERNEL>
