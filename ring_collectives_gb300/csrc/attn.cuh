@@ -14,7 +14,7 @@
 #include "f32x2.cuh"
 #include "internal.h"
 #include "ringcoll.h"
-#include "tc.cuh"
+#include "warp.cuh"
 
 namespace rc {
 namespace attn {

@@ -32,7 +32,7 @@
 #include "internal.h"
 #include "per_device.h"
 #include "ringcoll.h"
-#include "tc.cuh"
+#include "warp.cuh"
 
 namespace rc {
 namespace bn {

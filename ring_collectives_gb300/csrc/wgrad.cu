@@ -38,7 +38,7 @@
 #include "act8.cuh"
 #include "heads.h"
 #include "per_device.h"
-#include "tc.cuh"
+#include "warp.cuh"
 
 namespace rc {
 namespace wg {
