@@ -715,27 +715,24 @@ def _here(t, name: str, kind: str, gpu: int) -> None:
         raise ValueError(f"{name} must be on GPU {gpu} with the other tensors of the call, not on GPU {t.get_device()}")
 
 
-def _rows(t, name: str, gpu: int, shape, dtype=_BF16, kind="bf16"):
-    """Address and strides in bytes of rows [P, T, N]."""
+def _rows(t, name: str, gpu: int, shape, dtype=_BF16, kind="bf16", size=2):
+    """Address and strides in bytes of rows [P, T, N] of elements of `size` bytes."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be a {kind} CUDA tensor")
     if gpu < 0 or t.get_device() != gpu:
         _here(t, name, kind, gpu)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    st = t.stride()
-    if len(st) != 3 or (st[2] != 1 and shape[2] > 1):
+    slot, row, channel = t.stride()
+    if channel != 1 and shape[2] > 1:
         raise ValueError(f"{name} must be [P, T, N] with contiguous rows")
-    size = t.element_size()
-    return t.data_ptr(), size * st[0], size * st[1]
+    return t.data_ptr(), size * slot, size * row
 
 
 def _act8(x8, name: str, gpu: int, shape):
-    if x8 is None:
-        return _NO_ACT8
     q, e = x8
     P, T, N = shape
-    return (*_rows(q, name + "[0]", gpu, shape, _I8, "int8"), *_rows(e, name + "[1]", gpu, (P, T, -(-N // 32)), _U8, "uint8"))
+    return (*_rows(q, name + "[0]", gpu, shape, _I8, "int8", 1), *_rows(e, name + "[1]", gpu, (P, T, -(-N // 32)), _U8, "uint8", 1))
 
 
 def act8_empty(shape, device=None) -> tuple[torch.Tensor, torch.Tensor]:
@@ -750,7 +747,7 @@ def _act8_call(fn, x, x8, stream):
     gpu = x.get_device()
     if x8 is None:
         raise TypeError("x8 must be a pair of CUDA tensors")
-    _launch(fn, _ACT8_ARGS.pack(*_rows(x, "x", gpu, shape), *_act8(x8, "x8", gpu, shape), P, T, N, 0), x.device, stream)
+    _launch(fn, _ACT8_ARGS.pack(*_rows(x, "x", gpu, shape), *(_NO_ACT8 if x8 is None else _act8(x8, "x8", gpu, shape)), P, T, N, 0), x.device, stream)
 
 
 def act8_pack(x: torch.Tensor, x8, stream=None):
@@ -769,8 +766,6 @@ def act8_unpack(x8, x: torch.Tensor, stream=None) -> torch.Tensor:
 
 
 def _weights(t, name: str, gpu: int, shape) -> int:
-    if t is None:
-        return 0
     if t.get_device() != gpu:
         _here(t, name, "float32", gpu)
     return _f32(t, name, gpu, shape)
@@ -787,7 +782,7 @@ def _room(workspace, gpu: int):
 def _cols(t, shape) -> bool:
     """Whether a block's output or its gradient lies in column chunks [P, P * T, N / P]."""
     P, T, N = shape
-    return P > 1 and N % P == 0 and t.shape == (P, P * T, N // P) and t.shape != shape
+    return P > 1 and N % P == 0 and t.shape == (P, P * T, N // P)
 
 
 def _side(t, name: str, gpu: int, shape):
@@ -814,8 +809,10 @@ def block_norm(y: torch.Tensor, res: torch.Tensor, h: torch.Tensor, z: torch.Ten
     rows, cols = _side(y, "y", gpu, shape)
     args = _BLOCK_NORM_ARGS.pack(
         *rows, *_rows(res, "res", gpu, shape), *_rows(h, "h", gpu, shape), *(_NO_ROWS if z is None else _rows(z, "z", gpu, shape)),
-        *_NO_ROWS * 4, *_act8(y8, "y8", gpu, shape), *_act8(res8, "res8", gpu, shape), *_act8(z8, "z8", gpu, shape),
-        _weights(gamma_post, "gamma_post", gpu, (N,)), _weights(gate, "gate", gpu, (N,)), _weights(gamma_pre, "gamma_pre", gpu, (N,)),
+        *_NO_ROWS * 4, *(_NO_ACT8 if y8 is None else _act8(y8, "y8", gpu, shape)),
+        *(_NO_ACT8 if res8 is None else _act8(res8, "res8", gpu, shape)), *(_NO_ACT8 if z8 is None else _act8(z8, "z8", gpu, shape)),
+        0 if gamma_post is None else _weights(gamma_post, "gamma_post", gpu, (N,)),
+        0 if gate is None else _weights(gate, "gate", gpu, (N,)), 0 if gamma_pre is None else _weights(gamma_pre, "gamma_pre", gpu, (N,)),
         0, 0, 0, 0, 0, P, T, N, cols, 0, alpha, eps, 0)
     _launch(load().block_norm, args, res.device, stream)
     return h, z
@@ -845,8 +842,11 @@ def block_norm_bwd(y, res, dh: torch.Tensor | None, dz: torch.Tensor | None, dy:
         *(_NO_ROWS if dh is None else _rows(dh, "dh", gpu, shape)), *zrows,
         *drows, *_rows(dres, "dres", gpu, shape), *(_act8(y, "y", gpu, shape) if held else _NO_ACT8),
         *(_act8(res, "res", gpu, shape) if held else _NO_ACT8), *_NO_ACT8,
-        _weights(gamma_post, "gamma_post", gpu, (N,)), _weights(gate, "gate", gpu, (N,)), _weights(gamma_pre, "gamma_pre", gpu, (N,)),
-        _weights(dgamma_post, "dgamma_post", gpu, (P, N)), _weights(dgate, "dgate", gpu, (P, N)), _weights(dgamma_pre, "dgamma_pre", gpu, (P, N)),
+        0 if gamma_post is None else _weights(gamma_post, "gamma_post", gpu, (N,)),
+        0 if gate is None else _weights(gate, "gate", gpu, (N,)), 0 if gamma_pre is None else _weights(gamma_pre, "gamma_pre", gpu, (N,)),
+        0 if dgamma_post is None else _weights(dgamma_post, "dgamma_post", gpu, (P, N)),
+        0 if dgate is None else _weights(dgate, "dgate", gpu, (P, N)),
+        0 if dgamma_pre is None else _weights(dgamma_pre, "dgamma_pre", gpu, (P, N)),
         *_room(workspace, gpu), P, T, N, cols, dcols, alpha, eps, zcols)
     _launch(load().block_norm_bwd, args, dres.device, stream)
     return dy, dres
@@ -867,7 +867,8 @@ def glu(a: torch.Tensor, b: torch.Tensor, h: torch.Tensor, act: int = RC_GLU_SIL
     P, T, N = shape = a.shape
     gpu = a.get_device()
     args = _GLU_ARGS.pack(*_rows(a, "a", gpu, shape), *_rows(b, "b", gpu, shape), *_rows(h, "h", gpu, shape), *_NO_ROWS * 3,
-                          *_act8(a8, "a8", gpu, shape), *_act8(b8, "b8", gpu, shape), *_act8(h8, "h8", gpu, shape),
+                          *(_NO_ACT8 if a8 is None else _act8(a8, "a8", gpu, shape)), *(_NO_ACT8 if b8 is None else _act8(b8, "b8", gpu, shape)),
+                          *(_NO_ACT8 if h8 is None else _act8(h8, "h8", gpu, shape)),
                           P, T, N, act, 0, 0)
     _launch(load().glu, args, a.device, stream)
     return h
@@ -887,7 +888,7 @@ def glu_bwd(a, b, dh: torch.Tensor, da: torch.Tensor, db: torch.Tensor, h: torch
         *(_NO_ROWS * 2 if held else _rows(a, "a", gpu, shape) + _rows(b, "b", gpu, shape)),
         *(_NO_ROWS if h is None else _rows(h, "h", gpu, shape)), *_rows(dh, "dh", gpu, shape), *_rows(da, "da", gpu, shape),
         *_rows(db, "db", gpu, shape), *(_act8(a, "a", gpu, shape) + _act8(b, "b", gpu, shape) if held else _NO_ACT8 * 2),
-        *_act8(h8, "h8", gpu, shape), P, T, N, act, 0, 0)
+        *(_NO_ACT8 if h8 is None else _act8(h8, "h8", gpu, shape)), P, T, N, act, 0, 0)
     _launch(load().glu_bwd, args, dh.device, stream)
     return da, db
 
@@ -905,7 +906,7 @@ def gemm_wgrad(dy: torch.Tensor, x8, dw: torch.Tensor, accumulate: bool = False,
     gpu = dw.get_device()
     f32 = dw.dtype is _F32
     args = _WGRAD_ARGS.pack(*_rows(dy, "dy", gpu, (P, T, N)), *_act8(x8, "x8", gpu, (P, T, K)),
-                            *_rows(dw, "dw", gpu, (P, N, K), _F32 if f32 else _BF16, "bf16 or float32"), *_room(workspace, gpu),
+                            *_rows(dw, "dw", gpu, (P, N, K), _F32 if f32 else _BF16, "bf16 or float32", 4 if f32 else 2), *_room(workspace, gpu),
                             P, T, N, K, _DTYPE[dw.dtype], int(bool(accumulate)), 0, 0)
     _launch(load().gemm_wgrad, args, dw.device, stream)
     return dw
