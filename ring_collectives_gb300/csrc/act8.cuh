@@ -111,16 +111,23 @@ __device__ __forceinline__ uint4 narrow8(const f32x2 (&f)[4])
 // The values of 8 bytes with their group's byte e.  A byte b + 128 as the low bits of 2^23
 // gives an exact difference, and a power of two an exact product; e = 255 is an infinity,
 // which makes a NaN of a zero.
-__device__ __forceinline__ void held8(const uint2 &q, uint32_t e, f32x2 (&f)[4])
+__device__ __forceinline__ void bytes8(const uint2 &q, f32x2 (&f)[4])
 {
-    const f32x2 scale = both(__uint_as_float(e << 23)), zero = both(-8388736.f);
+    const f32x2 zero = both(-8388736.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t w = (i < 2 ? q.x : q.y) ^ 0x80808080u;
         const uint32_t a = __byte_perm(w, 0x4B000000u, i & 1 ? 0x7652 : 0x7650);
         const uint32_t b = __byte_perm(w, 0x4B000000u, i & 1 ? 0x7653 : 0x7651);
-        f[i] = mul2(add2(f2(__uint_as_float(a), __uint_as_float(b)), zero), scale);
+        f[i] = add2(f2(__uint_as_float(a), __uint_as_float(b)), zero);
     }
+}
+__device__ __forceinline__ void held8(const uint2 &q, uint32_t e, f32x2 (&f)[4])
+{
+    const f32x2 scale = both(__uint_as_float(e << 23));
+    bytes8(q, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], scale);
 }
 
 // The same in one multiply-add, for e <= 230 (gemm_wgrad of 8 x 768x4096 over 8192 tokens: 260 -> 255

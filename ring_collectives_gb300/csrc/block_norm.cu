@@ -22,9 +22,9 @@
 // issue slots 57 % busy, the shared-memory pipe 51 % (the weights are read from there twice).
 //
 // Measured on 8192 x 4096 with all weights: forward 47 us (5.7 TB/s, 84 % of the copy rate), with
-// checkpoints of y and res 58 us (86 %); the gradient from the checkpoints 70 + 4 us (4.6 TB/s, 68 %).
-// A row's sum y^2 taken with the sums of the row before, one round a row, changed nothing there (70 us)
-// and cost rows that do not fill their threads 7 %.
+// checkpoints of y and res 58 us (86 %); the gradient from the checkpoints 67 + 4 us (4.8 TB/s, 70 %).
+// A row's sum y^2 taken with the sums of the row before, one round a row, changed little there (70.8 to
+// 69.8 us) and cost rows that do not fill their threads 7 %.
 #include <cmath>
 
 #include "act8.cuh"
@@ -418,6 +418,9 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
 {
     extern __shared__ __align__(16) uint8_t sm[];
     constexpr int YB = HELD ? 8 : 16;                   // staged bytes of 8 channels of y and of res
+    // sum y^2 from the bytes' exact dot products: 69 -> 67 us (8192 x 4096); rows that do not fill their
+    // threads lose by it, for registers (4096 x 7000: 69 -> 75 us)
+    constexpr bool SQUARES = HELD && FULL && (KIND & POST);
     constexpr bool post = KIND & POST, pre = KIND & PRE;
     const Share<VPT, GL, CL> me;
     uint8_t *const after = sm + (GL ? 0 : kAreaBytes);
@@ -475,10 +478,16 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
         f32x2 y[VPT][4], h[VPT][4];
         uint4 dh[VPT], dz[VPT];
         f32x2 ss = 0;
+        float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (HELD) {
-                held8(lds8(at + i * YB * threads), ey[i], y[i]);
+                const uint2 b = lds8(at + i * YB * threads);
+                held8(b, ey[i], y[i]);
+                if (SQUARES) {
+                    const float s = __uint_as_float(ey[i] << 23);
+                    sq = fmaf((float)__dp4a((int)b.x, (int)b.x, __dp4a((int)b.y, (int)b.y, 0)) * s, s, sq);
+                }
                 held8(lds8(at + in_bytes + i * YB * threads), er[i], h[i]);
             } else {
                 wide8(lds16(at + i * YB * threads), y[i]);
@@ -486,15 +495,16 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
             }
             dh[i] = lds16(dat + i * 16 * threads);
             if (pre) dz[i] = lds16(dat + d_bytes + i * 16 * threads);
+            if (post && !SQUARES)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) ss = fma2(y[i][k], y[i][k], ss);
+                for (int k = 0; k < 4; ++k) ss = fma2(y[i][k], y[i][k], ss);
         }
         fetch(ahead, stage);
         fetch_groups(t + step);
         stage = stage + 1 == p.stages ? 0 : stage + 1;
         float rp = 1.f;
         if (post) {
-            float sum[1] = {hsum(ss)};
+            float sum[1] = {SQUARES ? sq : hsum(ss)};
             total(sum);
             rp = live ? rsqrtf(fmaf(sum[0], p.inv_n, p.eps)) : 0.f;
         }
@@ -546,8 +556,14 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (pre) {
-                    acc_z[i][k] = fma2(z[k], mul2(h[i][k], both(q)), acc_z[i][k]);
-                    d[k] = fma2(mul2(z[k], g[k]), both(q), d[k]);
+                    if (HELD) {                         // one product less: 71 -> 69 us (8192 x 4096); from bf16 72 -> 75
+                        z[k] = mul2(z[k], both(q));
+                        acc_z[i][k] = fma2(z[k], h[i][k], acc_z[i][k]);
+                        d[k] = fma2(z[k], g[k], d[k]);
+                    } else {
+                        acc_z[i][k] = fma2(z[k], mul2(h[i][k], both(q)), acc_z[i][k]);
+                        d[k] = fma2(mul2(z[k], g[k]), both(q), d[k]);
+                    }
                     d[k] = fma2(h[i][k], both(-c), d[k]);
                 }
                 acc_d[i][k] = fma2(d[k], y[i][k], acc_d[i][k]);

@@ -234,6 +234,24 @@ def test_block_norm_many_rows(N):
     check_gradient(p, held=True)
 
 
+@pytest.mark.parametrize("N", [1024, 12288])
+def test_block_norm_rows_that_fill_their_threads(N):
+    """Many rows of a width that needs no bounds, some of them zeros, tiny, or marked in one group."""
+    p = problem(1, 400, N, seed=N)
+    p["y"][0, 7], p["y"][0, 211] = 0, 0
+    p["y"][0, 30] *= 2.0 ** -30
+    p["y"][0, 31, 32:64] *= 2.0 ** -60
+    clean = check_gradient(p, held=True, eps=1e-2)
+    check_gradient(p, eps=1e-2)
+    (q, e), res8 = (rc.act8_pack(p[k], rc.act8_empty(p[k].shape, DEV)) for k in ("y", "res"))
+    q[0, 390, 64:96], e[0, 390, 2] = 0, 255
+    dy, dres, dw = grads(p)
+    rc.block_norm_bwd((q, e), res8, p["dh"], p["dz"], dy, dres, **named(dw, "d"), **named(p["w"]), alpha=0.7, eps=1e-2)
+    keep = [i for i in range(400) if i != 390]
+    assert torch.equal(dy[0, keep], clean[0][0, keep]) and torch.equal(dres[0, keep], clean[1][0, keep])
+    assert torch.isnan(dy[0, 390]).all() and torch.isnan(dres[0, 390]).all() and all(torch.isnan(t).all() for t in dw)
+
+
 def test_block_norm_without_rows():
     p = problem(3, 0, 64)
     _, _, dw = grads(p)
