@@ -172,48 +172,86 @@ __device__ __forceinline__ void copy(uint32_t dst, const void *src, bool on)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
 }
 
-// 32 columns of a row of dw from v, as far as they exist; k: the first of them.
-template <bool F32>
-__device__ __forceinline__ void store32(const Params &p, char *row, int k, uint32_t (&v)[32])
+// A row of a tile in units of 16 bytes, as far as it exists; ADD: what is there is added, 32 columns of it on
+// their way at once and with those from TMEM.  (Unit by unit 8 x 2816x3456 in binary32 over 4 tokens took
+// 432 us in the place of 184; the next 32 as well, while these are stored, 141 there but 337 instead of 132
+// us in bf16: a line's store waits for loads of its other half.)  Each way of storing has a loop of its own,
+// because few instructions matter: by one loop with all of them the same without ADD took 132 us
+// instead of 64, and in bf16 40 instead of 35.
+template <bool F32, bool ADD>
+__device__ __forceinline__ void store_row(const Params &p, uint32_t from, char *row, int k, bool mine)
 {
-    if (F32) {
-        float4 *const o = (float4 *)(row + (size_t)k * 4);
+    constexpr int UNITS = F32 ? 8 : 4, WIDTH = F32 ? 4 : 8;
+    uint4 *o = (uint4 *)row + k / WIDTH;
+    uint4 old[UNITS] = {};
+    auto load = [&](int k, const uint4 *o) {
+        if (p.st32 && k + 32 <= p.K) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (k + 4 * i >= p.K) break;
-            float4 f = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
-            if (p.accumulate) {
-                const float4 old = __ldcs(o + i);
-                f = make_float4(old.x + f.x, old.y + f.y, old.z + f.z, old.w + f.w);
-            }
-            __stcs(o + i, f);
+            for (int u = 0; u < UNITS; u += 2) ld8_ef_if(o + u, mine, old[u], old[u + 1]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u)
+                if (mine && k + u * WIDTH < p.K) old[u] = __ldcs(o + u);
         }
-        return;
+    };
+#pragma unroll 1
+    for (int col = 0; col < TILE; col += 32, k += 32, o += UNITS) {
+        uint32_t v[32];
+        if (ADD) load(k, o);
+        tmem_ld32(from + col, v);
+        uint4 x[UNITS];
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+            f32x2 f[WIDTH / 2];
+#pragma unroll
+            for (int j = 0; j < WIDTH / 2; ++j) f[j] = f2(__uint_as_float(v[u * WIDTH + 2 * j]), __uint_as_float(v[u * WIDTH + 2 * j + 1]));
+            if constexpr (F32) {
+                if (ADD) f[0] = add2(f2(__uint_as_float(old[u].x), __uint_as_float(old[u].y)), f[0]);
+                if (ADD) f[1] = add2(f2(__uint_as_float(old[u].z), __uint_as_float(old[u].w)), f[1]);
+                x[u] = make_uint4(__float_as_uint(lo(f[0])), __float_as_uint(hi(f[0])), __float_as_uint(lo(f[1])), __float_as_uint(hi(f[1])));
+            } else {
+                f32x2 b[4];
+                wide8(old[u], b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (ADD) f[j] = add2(b[j], f[j]);
+                x[u] = narrow8(f);
+            }
+        }
+        if (!mine) continue;
+        if (p.st32 && k + 32 <= p.K) {
+#pragma unroll
+            for (int u = 0; u < UNITS; u += 2) st8<kStEvictFirst>(o + u, x[u], x[u + 1]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u)
+                if (k + u * WIDTH < p.K) st_v4(o + u, x[u]);
+        }
     }
-    uint4 *const o = (uint4 *)(row + (size_t)k * 2);
+}
+
+// 32 columns of a row of a whole tile in bf16, by whole sectors of 32 bytes.  A row that lies off them (`off`;
+// every other one where K is an odd multiple of 8) keeps its last 16 bytes in `carry` for the next 32.
+__device__ __forceinline__ void store32_whole(const Params &p, uint4 *o, bool first, const uint32_t (&v)[32], bool off, uint4 &carry)
+{
     uint4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (p.accumulate && k + 8 * i < p.K) {
-            f32x2 old[4];
-            wide8(__ldcs(o + i), old);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[8 * i + 2 * j] = __float_as_uint(__uint_as_float(v[8 * i + 2 * j]) + lo(old[j]));
-                v[8 * i + 2 * j + 1] = __float_as_uint(__uint_as_float(v[8 * i + 2 * j + 1]) + hi(old[j]));
-            }
-        }
+    for (int i = 0; i < 4; ++i)
         w[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]), pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
                           pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-    }
-    if (p.st32 && k + 32 <= p.K) {
+    if (!p.st32) {
+        if (off) {
+            const uint4 last = w[3];
+            if (first) st_v4(o, w[0]);
+            w[3] = w[2], w[2] = w[1], w[1] = w[0], w[0] = carry;
+            carry = last;
+            --o;
+        }
+        if (!off || !first) st8<kStEvictFirst>(o, w[0], w[1]);
+    } else {
         st8<kStEvictFirst>(o, w[0], w[1]);
-        st8<kStEvictFirst>(o + 2, w[2], w[3]);
-        return;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (k + 8 * i < p.K) st_v4(o + i, w[i]);
+    st8<kStEvictFirst>(o + 2, w[2], w[3]);
 }
 
 template <Mode MODE>
@@ -484,24 +522,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
         Walk w;
         for (w.start(p, pair); w.tile >= 0; ++it, w.next_tile(p, pair)) {
             const uint32_t acc = it & 1;
+            const int local = (int)cta * HALF + i * 32 + lane, n = w.n + local;
             if (!wait_idle(tfull + 8 * acc, (it >> 1) & 1, ab, 6)) break;
             tc_fence_after();
-            const int local = (int)cta * HALF + i * 32 + lane, n = w.n + local;
             const uint32_t from = tmem + ((uint32_t)(i * 32) << 16) + acc * TILE;
             float *const part = w.part < 0 ? nullptr : p.part + ((size_t)w.part * TILE * TILE + local * 4);
             char *const row = p.dw.at(w.r, n);
+            if (!part && !p.f32 && !p.accumulate && w.k + TILE <= p.K) {
+                const bool off = (uintptr_t)row & 16;
+                uint4 *const o = (uint4 *)(row + (size_t)w.k * 2);
+                uint4 carry = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-            for (int col = 0; col < TILE; col += 32) {
-                uint32_t v[32];
-                tmem_ld32(from + col, v);
-                if (part) {
+                for (int col = 0; col < TILE; col += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(from + col, v);
+                    if (n < p.N) store32_whole(p, o + col / 8, col == 0, v, off, carry);
+                }
+                if (off && n < p.N) st_v4(o + TILE / 8 - 1, carry);
+            } else if (part) {
+#pragma unroll 1
+                for (int col = 0; col < TILE; col += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(from + col, v);
 #pragma unroll
                     for (int x = 0; x < 8; ++x)           // four columns of 32 rows side by side
                         st_v4(part + (col / 4 + x) * (TILE * 4), make_uint4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]));
-                } else if (n < p.N) {
-                    if (p.f32) store32<true>(p, row, w.k + col, v);
-                    else store32<false>(p, row, w.k + col, v);
                 }
+            } else if (p.f32) {
+                if (p.accumulate) store_row<true, true>(p, from, row, w.k, n < p.N);
+                else store_row<true, false>(p, from, row, w.k, n < p.N);
+            } else {
+                if (p.accumulate) store_row<false, true>(p, from, row, w.k, n < p.N);
+                else store_row<false, false>(p, from, row, w.k, n < p.N);
             }
             tc_fence_before();
             __syncwarp();

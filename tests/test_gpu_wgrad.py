@@ -102,6 +102,26 @@ def test_strided_views_leave_the_rest():
     assert (room == 7).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,K", [(264, 256), (136, 520), (256, 776)])
+def test_rows_of_dw_off_whole_sectors(N, K, dtype):
+    """Whole and partial tiles whose rows start 16 bytes off a multiple of 32: all of them, none, or every other
+    one; what lies between them stays as it was."""
+    dy, x8 = problem(2, 70, N, K, seed=K)
+    unit = 8 if dtype is BF else 4
+    want, bound = ob.gemm_wgrad(f64(dy), values(x8), 2.0 ** -8 if dtype is BF else 2.0 ** -24)
+    for shift, pad in ((0, unit), (unit, 2 * unit), (unit, unit), (0, 2 * unit)):
+        room = torch.full((2, N, shift + K + pad), 7.0, dtype=dtype, device=DEV)
+        dw = room[..., shift:shift + K]
+        for turn in (1, 2):
+            rc.gemm_wgrad(dy, x8, dw, accumulate=turn == 2)
+            # twice: the first result's error, this sum's, the addition's in binary32 and the last rounding
+            u = (2.0 ** -8 if dtype is BF else 2.0 ** -24) + 2.0 ** -24
+            inside(dw, turn * want, bound if turn == 1 else 2 * bound + u * (2 * np.abs(want) + 2 * bound))
+        room[..., shift:shift + K] = 7
+        assert (room == 7).all()
+
+
 def test_workspace_is_for_parts():
     assert rc.gemm_wgrad_workspace_bytes(1, 16384, 256, 512) > 256 and rc.gemm_wgrad_workspace_bytes(38, 16384, 256, 512) == 256
     assert rc.gemm_wgrad_workspace_bytes(1, 64, 256, 256) == 256 and rc.gemm_wgrad_workspace_bytes(1, 64, 257, 256) == 0
