@@ -29,8 +29,9 @@
 // tokens 255 + 7 us (412 GFLOP, 1.57 PFLOP/s; the MMAs by themselves take 195 us, with dy's
 // copies 219), one rank's 4096x4096 181 + 7 us (1.46 PFLOP/s), 4096x4104 184 + 9 us (rows of an
 // odd number of 8 bytes; by cp.async 286).  Two groups of widening warps in the place of three:
-// 263, 182 and 199 us.  Over a few tokens the tiles' stores bound it: 8 x 2736x3448 over 4
-// tokens 72 us, 2.1 TB/s.
+// 263, 182 and 199 us.  Over a few tokens the tiles' stores bound it, a row a lane: 8 x
+// 2816x3456 over 4 tokens 35 us (4.4 TB/s), 2736x3448 with every other row off whole sectors 43 us (73 with
+// 16-byte stores), in binary32 64 us, added to what is there 184.
 #include <cudaTypedefs.h>
 
 #include <mutex>
