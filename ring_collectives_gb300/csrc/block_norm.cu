@@ -19,7 +19,7 @@
 // use.  Channels past the end of a row arrive as zeros, with weights of zero, and only the
 // stores leave them out.  The gradient is bound by what a row costs in instructions at 16
 // warps an SM, which its sums of the weights' gradients (32 registers a thread) hold it to:
-// issue slots 57 % busy, the shared-memory pipe 51 % (the weights are read from there twice).
+// issue slots 56 % busy, the shared-memory pipe 57 % (the weights are read from there twice).
 //
 // Measured on 8192 x 4096 with all weights: forward 47 us (5.7 TB/s, 84 % of the copy rate), with
 // checkpoints of y and res 58 us (86 %); the gradient from the checkpoints 67 + 4 us (4.8 TB/s, 70 %).
