@@ -21,14 +21,16 @@ __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, 
 // Every lane waits; the same answer in all.  (A wait by one lane, handed on by a
 // shuffle, costs the warp over 100 clocks more: the softmax warps waiting that way
 // made a 16384-token prompt 11 % slower.)  With a second barrier of the same parity
-// both are asked for before either answer is looked at.
+// both are asked for before either answer is looked at.  CLUSTER: acquire at cluster
+// scope, of both (what they announce lies in another CTA, or was sent from there).
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, const Abort &ab, int where, uint32_t also = 0)
 {
     uint64_t t0 = 0;
+    auto one = [&](uint32_t b) { return CLUSTER ? mbar_try_wait_cluster(b, parity) : mbar_try_wait(b, parity); };
     auto passed = [&] {
-        const bool one = CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
-        return also ? one & mbar_try_wait(also, parity) : one;
+        const bool first = one(bar);
+        return also ? first & one(also) : first;
     };
     for (uint32_t it = 0; !__all_sync(0xFFFFFFFFu, passed()); ++it) {
         if ((it & 63u) != 63u) continue;

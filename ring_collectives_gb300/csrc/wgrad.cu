@@ -14,24 +14,25 @@
 //   warps 2, 3   copy 128 k of q ahead (rows on 16 bytes by TMA; rows of an odd number of 8
 //                bytes by TMA too, the even ones and the odd ones each; others by cp.async),
 //                and the groups' bytes;
-//   warps 8-19   widen them into the swizzled tile, groups of four warps taking steps in
-//                turn: from a step's q to its announcement takes some four times as long as
-//                its MMAs.  A group converts in registers before it waits for a stage, so
+//   warps 8-15   widen them into the swizzled tile, groups of four warps taking steps in
+//                turn.  A group converts in registers before it waits for a stage, so
 //                the stage is held for the stores and the fence only;
 //   warp 1       (even CTA) issues the MMAs of the pair, M = N = 256;
+//   warps 1, 16-19 (odd CTA) announce its widened steps to the even one;
 //   warps 4-7    take finished tiles from TMEM, while the next one is summed.
 // Whole tiles are dealt out in rounds; the tokens of those that are left over are
 // divided evenly over all pairs, and k_wgrad_join adds the parts in order.
 //
-// Bound by shared memory: a step's MMAs last 512 clocks, in which a CTA's shared memory
-// takes in 16 KB of dy, 8 KB of q and 16 KB of widened x, and gives out the q again and
-// 32 KB to the tensor cores, 80 KB or 640 clocks.  Measured: 8 ranks x 768x4096 over 8192
-// tokens 255 + 7 us (412 GFLOP, 1.57 PFLOP/s; the MMAs by themselves take 195 us, with dy's
-// copies 219), one rank's 4096x4096 181 + 7 us (1.46 PFLOP/s), 4096x4104 184 + 9 us (rows of an
-// odd number of 8 bytes; by cp.async 286).  Two groups of widening warps in the place of three:
-// 263, 182 and 199 us.  Over a few tokens the tiles' stores bound it, a row a lane: 8 x
-// 2816x3456 over 4 tokens 35 us (4.4 TB/s), 2736x3448 with every other row off whole sectors 43 us (73 with
-// 16-byte stores), in binary32 64 us, added to what is there 184.
+// Bound by shared memory, and by what a step's way to the tensor cores takes in all: a step's MMAs last 512
+// clocks, in which a CTA's shared memory takes in 16 KB of dy, 8 KB of q and 16 KB of widened x, and gives out
+// the q again and 32 KB to the tensor cores, 80 KB or 640 clocks; and of the five stages some three are
+// taken by steps that wait for their announcement.  Measured: 8 ranks x 768x4096 over 8192
+// tokens 270 + 7 us (412 GFLOP, 1.49 PFLOP/s; the MMAs by themselves take 195 us, with dy's
+// copies 219), one rank's 4096x4096 188 + 7 us (1.41 PFLOP/s), 4096x4104 198 + 8 us (rows of an
+// odd number of 8 bytes; by cp.async 286 before announcements were releases).  Three groups of widening warps in
+// the place of two: 271, 190 and 198 us, and registers spilled in the additions to dw.  Over a few tokens
+// the tiles' stores bound it, a row a lane: 8 x 2816x3456 over 4 tokens 37 us (4.2 TB/s), 2736x3448 with every
+// other row off whole sectors 43 us (73 with 16-byte stores), in binary32 64 us, added to what is there 186.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -51,7 +52,7 @@ constexpr int STEP = 64;                      // tokens a step
 constexpr int STAGES = 5;
 constexpr int BLOCK = 64 * STEP * 2;          // 64 channels x 64 tokens of bf16
 constexpr int OPERAND = 2 * BLOCK;            // a CTA's half of an operand's stage
-constexpr int GROUPS = 3, GROUP = 128;        // groups of threads that widen steps in turn
+constexpr int GROUPS = 2, GROUP = 128;        // groups of threads that widen steps in turn
 constexpr int DEEP = 6;                       // steps of q on their way or waiting to be widened
 constexpr int TOKENS = GROUP / 8;             // a group takes 128 k of as many tokens at a time,
 constexpr int PIECES = STEP / TOKENS;         // so often in a step
@@ -62,7 +63,13 @@ constexpr int EVEN_BYTES = STEP / 2 * HALF, SLOT = EVEN_BYTES + STEP / 2 * ODD_R
 // at run time the choice cost 4 % of the whole launch: the widening warps are that busy.
 enum Mode { COPIES, ROWS, TWINS };
 constexpr int EPILOGUE = 4;                   // warps that store
-constexpr int THREADS = 256 + GROUPS * GROUP;
+// Warps that announce the odd CTA's widened steps to the even one, a stage each: warp 1 and those from
+// FIRST_HERALD on.  A release at cluster scope takes about 2000 clocks while copies are on their way, so one warp for all
+// stages made the whole launch last 720 us in the place of 271, two 340, three 280.  One fence for all steps that are
+// ready, before relaxed arrivals, took 373 us with one warp.
+constexpr int HERALDS = STAGES;
+constexpr int FIRST_HERALD = (256 + GROUPS * GROUP) / 32;
+constexpr int THREADS = 256 + GROUPS * GROUP + (HERALDS - 1) * 32;
 constexpr int ESLOT = STEP * 4 + 16;          // a step's groups' bytes, and whether its first row is an odd one
 constexpr int SLOTS = DEEP * SLOT, ESLOTS = DEEP * ESLOT;
 constexpr int TMEM_COLS = 512;                // two accumulators
@@ -150,6 +157,15 @@ struct Walk {
     }
 };
 
+// Steps of a pair, of all its tiles and parts.
+__device__ __forceinline__ uint32_t steps_of(const Params &p, int pair)
+{
+    uint32_t n = 0;
+    Walk w;
+    for (w.start(p, pair); w.tile >= 0; w.next_tile(p, pair)) n += w.end - w.step;
+    return n;
+}
+
 // Descriptors of MN-major tiles in blocks of BLOCK bytes (smem_desc_mn_sw128): a varying low
 // word, and this high word.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
@@ -162,6 +178,8 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uin
                  : "memory");
 }
 
+// Hands back an accumulator: its TMEM loads have completed, and nothing is published.  What another
+// CTA reads is announced with mbar_arrive_remote, a release.
 __device__ __forceinline__ void arrive_remote_relaxed(uint32_t bar_cluster)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
@@ -278,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(full_a + 8 * s, 1);                 // the even CTA's arm for the bytes of both
-            mbar_init(full_b + 8 * s, 2 * GROUP / 32);    // the group's warps of both CTAs
+            mbar_init(full_b + 8 * s, GROUP / 32 + even);     // the group's warps; in the even CTA also the odd one's announcement
             mbar_init(empty + 8 * s, 1);                  // one commit of the pair's MMAs
         }
         for (int d = 0; d < DEEP; ++d) {
@@ -310,7 +328,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
     const uint32_t tmem = *tmem_slot;
     const Abort ab{abort_flag, p.hdr, p.timeout_ns, 0xACu, mapa_shared(smem_u32(abort_flag), cta ^ 1u)};
 
-    const uint32_t full_even = mapa_shared(full_b, 0);
     if (warp == 0) {
         // ---------------- dy by TMA (both CTAs; the bytes are counted on the even one's barrier)
         const uint32_t full_a_even = mapa_shared(full_a, 0);
@@ -341,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
             if (!wait_all<true>(tempty + 8 * acc, ((it >> 1) & 1) ^ 1u, ab, 3)) break;
             uint32_t more = 0;                            // 0: the first MMA overwrites the accumulator
             for (uint32_t s = w.step; s < w.end; ++s) {
-                if (!wait_all(full_a + 8 * stage, phase, ab, 4, full_b + 8 * stage)) {
+                if (!wait_all<true>(full_a + 8 * stage, phase, ab, 4, full_b + 8 * stage)) {
                     ok = false;
                     break;
                 }
@@ -359,6 +376,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
         }
         if (elect_one()) tc_commit_pair_mc(drained, 1);
         wait_bar(drained, 0, ab, 10, true);
+    } else if (warp == 1 || warp >= FIRST_HERALD) {
+        // ---------------- the odd CTA's widened steps, announced to the even one, whose MMAs read them: one release at
+        // cluster scope for the four warps that wrote, after their own arrivals here, so that they never wait for
+        // one.  A warp announces every step of its stage, so the stage's phase before is known to be over.
+        const uint32_t stage = warp == 1 ? 0u : (uint32_t)(warp - FIRST_HERALD + 1), full_even = mapa_shared(full_b + 8 * stage, 0);
+        const uint32_t total = even ? 0u : steps_of(p, pair);
+        uint32_t phase = 0;
+        for (uint32_t n = stage; n < total; n += STAGES, phase ^= 1u) {
+            if (!wait_all(full_b + 8 * stage, phase, ab, 13)) break;
+            if (elect_one()) mbar_arrive_remote(full_even);
+        }
     } else if (warp == 2 || warp == 3) {
         // ---------------- q and e ahead, a warp every other step.  q by TMA where its rows start on 16 bytes or
         // every other one does; else by cp.async, eight lanes a token's 128 bytes.  The
@@ -451,11 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
         const uint32_t in = sQ + t0 * HALF + c * 16, ein = sE + t0 * 4 + (c >> 1), out = sB + (c >> 2) * BLOCK + t0 * 128;
         const uint32_t ch = ((c & 3) * 2 + (c >> 2)) ^ (t0 & 7);        // of the first chunk written; the other: ^ 1
         const bool flip = c >= 4;
-        uint32_t total = 0;                               // steps of the pair; this group's: group, group + GROUPS, ...
-        {
-            Walk w;
-            for (w.start(p, pair); w.tile >= 0; w.next_tile(p, pair)) total += w.end - w.step;
-        }
+        const uint32_t total = steps_of(p, pair);         // this group's: group, group + GROUPS, ...
         uint32_t stage = (uint32_t)group, phase = 0, slot = (uint32_t)group, qphase = 0;
         for (uint32_t n = (uint32_t)group; n < total; n += GROUPS) {
             if (!wait_all(qfull + 8 * slot, qphase, ab, 7)) break;
@@ -501,15 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
                                  "r"(x[i][k].x), "r"(x[i][k].y), "r"(x[i][k].z), "r"(x[i][k].w)
                                  : "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            // The odd CTA's halves are complete in its shared memory (the fence above), where its own tensor
-            // core reads them; the arrival publishes nothing else, so it is relaxed.  With a release at cluster
-            // scope an early form of the whole launch took 602 us in the place of 535.
-            if (even) {
-                arrive_warp(full_b + 8 * stage, lane);
-            } else {
-                __syncwarp();
-                if (lane == 0) arrive_remote_relaxed(full_even + 8 * stage);
-            }
+            arrive_warp(full_b + 8 * stage, lane);
             stage += GROUPS;
             if (stage >= STAGES) stage -= STAGES, phase ^= 1u;
             slot += GROUPS;
