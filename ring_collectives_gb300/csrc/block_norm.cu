@@ -79,6 +79,8 @@ __device__ __forceinline__ void wait_oldest(int stages)
     else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
     else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
+// Every copy of this thread has landed, those of rows that do not exist (zeros) among them.
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ uint4 lds16(uint32_t a)
 {
     uint4 v;
@@ -406,6 +408,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const Params p)
         }
         if (CL > 1 && !total.ok) break;
     }
+    wait_copies();
     total.leave();
 }
 
@@ -576,12 +579,13 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
         }
         if (CL > 1 && !total.ok) break;
     }
+    wait_copies();                                      // before the staging is written otherwise or given up
     total.leave();
     if (!p.sums) return;
     // the sums that are wanted, one after the other; with several rows a block those of all its groups
     float *part = p.part + (size_t)block * p.sums * p.N;
     float *const red = (float *)sm;                     // [group][N]
-    if (GL) __syncthreads();                            // the staging is done with, by every warp
+    if (GL) __syncthreads();                            // the staging is done with, by every warp and every copy
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         if (k == 0 ? !(p.gpost || p.gate) : !pre) continue;

@@ -42,3 +42,17 @@ def test_the_mmas_wait_at_cluster_scope():
     wait = body(source("warp.cuh"), "bool wait_all(")
     asked = re.findall(r"mbar_try_wait(?:_cluster)?\((\w+), parity\)", wait)
     assert len(asked) == 2 and asked[0] == asked[1] and "CLUSTER ? mbar_try_wait_cluster(" in wait
+
+
+# ---------------------------------------------------------------- norm's gradient
+def test_copies_land_before_their_space_is_used_again():
+    """Past the last row copies still write zeros, and a barrier does not wait for them: every thread waits for its own
+    before the barrier after which the groups' sums lie where the rows were staged."""
+    text = source("block_norm.cu")
+    assert "cp.async.wait_all;" in body(text, "void wait_copies()")
+    kernel = body(text, "k_block_norm_bwd(const Params p)")
+    end = kernel.index("total.leave();")
+    assert kernel[:end].rstrip().endswith("wait_copies();")
+    assert end < kernel.index("__syncthreads();", end) < kernel.index("red + me.group * p.N")
+    kernel = body(text, "k_block_norm(const Params p)")
+    assert kernel[:kernel.index("total.leave();")].rstrip().endswith("wait_copies();")

@@ -1,0 +1,70 @@
+"""GPU block operators at few rows and at the ends of the number range, against 64 bits (needs a GB300)."""
+import numpy as np
+import pytest
+import torch
+
+import ring_collectives_gb300 as rc
+from oracle import block as ob
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+    torch.cuda.set_device(DEV)
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def inside(got, want, bound):
+    err = np.abs(f64(got) - want)
+    assert (err <= bound).all(), float((err / bound).max())
+
+
+def rand(seed, *shape):
+    return torch.randn(shape, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV).to(BF)
+
+
+def norm_problem(P, T, N, seed=0):
+    y, res, dh, dz = (rand(seed + i, P, T, N) for i in range(4))
+    w = [1 + 0.3 * torch.randn(N, generator=torch.Generator(device=DEV).manual_seed(seed + 4 + i), device=DEV) for i in range(3)]
+    return y, res, dh, dz, w
+
+
+def norm_gradient(y, res, dh, dz, w, held, alpha=0.7, eps=1e-6, workspace=None):
+    """{name: result} of block_norm_bwd with the weights that are given."""
+    P, T, N = dz.shape if dz is not None else dh.shape
+    out = {k: torch.full((P, T, N), float("nan"), dtype=BF, device=DEV) for k in ("dy", "dres")}
+    dw = [None if t is None else torch.full((P, N), float("nan"), device=DEV) for t in w]
+    if held:
+        y, res = (rc.act8_pack(t, rc.act8_empty(t.shape, DEV)) for t in (y, res))
+    names = ("gamma_post", "gate", "gamma_pre")
+    rc.block_norm_bwd(y, res, dh, dz, out["dy"], out["dres"], *dw, **dict(zip(names, w)), alpha=alpha, eps=eps, workspace=workspace)
+    return out | {"d" + n: t for n, t in zip(names, dw) if t is not None}
+
+
+def held_values(t):
+    return ob.act8_values(*ob.act8_pack(f64(t)))
+
+
+@pytest.mark.parametrize("held", [False, True], ids=["bf16", "8bit"])
+@pytest.mark.parametrize("N", [8, 64, 72, 128, 136, 256, 264, 512])
+def test_sums_of_few_narrow_rows(N, held):
+    """Rows within a warp, fewer of them than a block takes at once: some warps have none, and each block's sums follow
+    its last row at once.  The same bits every time."""
+    for T in (1, 2, 3, 4, 5, 7, 8, 15, 16, 17):
+        y, res, dh, dz, w = norm_problem(2, T, N, seed=T)
+        first = norm_gradient(y, res, dh, dz, w, held)
+        at = [held_values(t) if held else f64(t) for t in (y, res)]
+        want, bound = ob.block_norm_bwd(*at, f64(dh), f64(dz), *(f64(t) for t in w), alpha=0.7)
+        for name, t in first.items():
+            inside(t, want[name], bound[name])
+        for _ in range(20):
+            again = norm_gradient(y, res, dh, dz, w, held)
+            assert all(torch.equal(t, again[name]) for name, t in first.items())
