@@ -175,7 +175,7 @@ struct Sums {
                                      : "memory");
                 __syncwarp();
                 const tc::Abort ab{flag(), p.hdr, p.timeout_ns, 0xD0u, tc::mapa_shared(tc::smem_u32(flag()), tc::cluster_ctarank() ^ 1u)};
-                if (ok) ok = tc::wait_all(bar, (uses >> 1) & 1, ab, 1);
+                if (ok) ok = tc::wait_all<true>(bar, (uses >> 1) & 1, ab, 1);
             }
             ++uses;
             if (PAD == 8) {

@@ -56,3 +56,10 @@ def test_copies_land_before_their_space_is_used_again():
     assert end < kernel.index("__syncthreads();", end) < kernel.index("red + me.group * p.N")
     kernel = body(text, "k_block_norm(const Params p)")
     assert kernel[:kernel.index("total.leave();")].rstrip().endswith("wait_copies();")
+
+
+def test_sums_of_other_blocks_are_acquired_at_cluster_scope():
+    """They arrive by st.async, whose count on the mbarrier is a release at that scope."""
+    sums = body(source("block_norm.cu"), "struct Sums")
+    assert "st.async.shared::cluster" in sums
+    assert re.findall(r"wait_all(?:<\w+>)?\(", sums) == ["wait_all<true>("]
