@@ -612,7 +612,10 @@ int block_norm(const rc_block_norm_args *args, void *stream);
  * gradients in binary32, in an order that does not depend on timing.  dres and
  * dy may each be dh or dz, as wholes, where both lie alike; results are apart
  * otherwise.  T = 0 gives sums of 0.  The library's own space for partial sums
- * is that of attn_fwd, with its rules.  h, z, z8 are not used.
+ * is that of attn_fwd, with its rules.  h, z, z8 are not used.  Where N is above
+ * 8192 a wait that runs out is reported by ring_status(), as for block_norm and
+ * whether a workspace is given or not: a workspace's header, whose contents are
+ * arbitrary, is left alone, so ring_status_ex() has nothing of this call.
  */
 int block_norm_bwd(const rc_block_norm_args *args, void *stream);
 

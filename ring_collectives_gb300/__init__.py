@@ -828,7 +828,8 @@ def block_norm_bwd(y, res, dh: torch.Tensor | None, dz: torch.Tensor | None, dy:
     gradients of h and z (dz in either layout of y: gemm_rs may have left it); writes dy (likewise) and dres, and where the weight is
     given each rank's own sums dgamma_post, dgate, dgamma_pre (float32 [P, N]).  dres and dy
     may each be dh or dz.  workspace: a CUDA tensor of at least block_norm_bwd_workspace_bytes bytes, which
-    other calls may use too in stream order; None takes the library's own."""
+    other calls may use too in stream order; None takes the library's own.  Above 8192 channels a wait that
+    runs out is reported by ring_status(), with a workspace too."""
     P, T, N = shape = dres.shape
     gpu = dres.get_device()
     held = isinstance(y, (tuple, list))

@@ -902,6 +902,7 @@ static int run(const rc_block_norm_args *args, bool grad, void *stream)
     const Shape s = shape_of(a, grad, sms);
     Params p{};
     uint32_t *unused = nullptr;
+    // a caller's workspace has arbitrary contents here, so the library's own header takes what a wait reports
     if (s.cl > 1 && (rc_ = prepare_workspace_ext(nullptr, 0, 0, &p.hdr, &unused, &sms, &p.timeout_ns))) return rc_;
     p.y = rows_of(a.y), p.res = rows_of(a.res), p.h = rows_of(a.h), p.z = rows_of(a.z);
     p.dh = rows_of(a.dh), p.dz = rows_of(a.dz), p.dy = rows_of(a.dy), p.dres = rows_of(a.dres);
