@@ -68,3 +68,30 @@ def test_sums_of_few_narrow_rows(N, held):
         for _ in range(20):
             again = norm_gradient(y, res, dh, dz, w, held)
             assert all(torch.equal(t, again[name]) for name, t in first.items())
+
+
+# ---------------------------------------------------------------- gated activations
+KINDS = {"silu": rc.RC_GLU_SILU, "gelu": rc.RC_GLU_GELU}
+
+
+@pytest.mark.parametrize("held", [False, True], ids=["bf16", "8bit"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_glu_gradient_of_every_finite_gate(kind, held):
+    """With factors 3 and -1/2.  Beyond 100 the derivative is 1 or 0: the logistic function's distance from 1 or 0 is at
+    most 100 e^-100 < 4e-42 there, times 1.5, so da is -1.5 without an error, or nearly nothing."""
+    bits = torch.arange(65536, dtype=torch.int32, device=DEV).to(torch.int16).view(BF)
+    a = torch.zeros((1, 65280, 32), dtype=BF, device=DEV)                # a group for every gate, with zeros
+    a[0, :, 0] = bits[torch.isfinite(bits)]
+    dh, b = torch.full_like(a, 3.0), torch.full_like(a, -0.5)
+    da, db, h = (torch.full_like(a, float("nan")) for _ in range(3))
+    operands = [rc.act8_pack(t, rc.act8_empty(t.shape, DEV)) for t in (a, b)] if held else [a, b]
+    rc.glu_bwd(*operands, dh, da, db, h=h, act=KINDS[kind])
+    x = held_values(a) if held else f64(a)
+    (wa, wb, wh), (oa, obb, oh) = ob.glu_bwd(x, f64(b), f64(dh), kind)
+    near = np.abs(x) <= 1e9                                              # the bound for tiny results grows beyond
+    assert (np.abs(f64(da) - wa) <= oa)[near].all()
+    assert (np.abs(f64(da) - np.where(x > 0, -1.5, 0.0)) <= 1e-37)[np.abs(x) >= 100].all()
+    # db = 3 act(a) and h = -act(a) / 2: past the limit an infinity
+    for got, want, off in ((db, wb, obb), (h, wh, oh)):
+        fits = np.abs(want) <= 3.38e38
+        assert (np.abs(f64(got) - want) <= off)[fits].all() and np.isinf(f64(got)[np.abs(want) > 3.4e38]).all()
