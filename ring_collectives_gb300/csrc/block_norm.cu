@@ -537,13 +537,13 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm_bwd(const Params p)
             float s[5] = {hsum(hh), hsum(th), hsum(vd), hsum(vt), hsum(vh)};
             total(s);
             q = live ? rsqrtf(fmaf(s[0], p.inv_n, p.eps)) : 0.f;         // a row that is not there adds zeros
-            c = q * q * q * (s[1] * p.inv_n);
+            c = q * (q * (q * (s[1] * p.inv_n)));       // no cube of q by itself: it leaves the range where c does not
             m = (s[2] + q * s[3] - c * s[4]) * p.inv_n;
         } else if (KIND == PRE) {
             float s[2] = {hsum(hh), hsum(th)};
             total(s);
             q = live ? rsqrtf(fmaf(s[0], p.inv_n, p.eps)) : 0.f;
-            c = q * q * q * (s[1] * p.inv_n);
+            c = q * (q * (q * (s[1] * p.inv_n)));
         } else if (KIND == POST) {
             float s[1] = {hsum(vd)};
             total(s);

@@ -95,3 +95,41 @@ def test_glu_gradient_of_every_finite_gate(kind, held):
     for got, want, off in ((db, wb, obb), (h, wh, oh)):
         fits = np.abs(want) <= 3.38e38
         assert (np.abs(f64(got) - want) <= off)[fits].all() and np.isinf(f64(got)[np.abs(want) > 3.4e38]).all()
+
+
+# ---------------------------------------------------------------- norm's gradient: loud and quiet rows
+def check_gradient(y, res, dh, dz, w, held, alpha, eps):
+    got = norm_gradient(y, res, dh, dz, w, held, alpha, eps)
+    at = [held_values(t) if held else f64(t) for t in (y, res)]
+    at += [np.zeros(at[0].shape) if dh is None else f64(dh), f64(dz)]
+    want, bound = ob.block_norm_bwd(*at, *(None if t is None else f64(t) for t in w), alpha=alpha, eps=eps)
+    assert set(want) == set(got)
+    for name, t in got.items():
+        # the definition's bound counts 1e-37 for results below the normal numbers; those here are far above
+        assert (np.abs(want[name]) > 1e-34).mean() > 0.9
+        inside(t, want[name], bound[name])
+
+
+@pytest.mark.parametrize("held", [False, True], ids=["bf16", "8bit"])
+@pytest.mark.parametrize("N", [64, 1024, 1544, 12288])
+@pytest.mark.parametrize("power", [40, 44, 50, 55])
+def test_gradient_of_loud_rows(N, held, power):
+    """Rows of 2^power, whose squares' sum is a number: the part along the row counts as much as the rest, with the gradient
+    of the sum itself left out so that nothing hides it."""
+    y, res, _, dz, w = norm_problem(2, 3, N, seed=power)
+    loud = (res.float() * 2.0 ** power).to(BF)
+    dz = (dz.float() + res.float()).to(BF)                               # along the row too
+    check_gradient(y, loud, None, dz, w, held, 0.7, 1e-6)
+    check_gradient((y.float() * 2.0 ** power).to(BF), loud, None, dz, (None, w[1], w[2]), held, 0.7, 1e-6)
+
+
+@pytest.mark.parametrize("held", [False, True], ids=["bf16", "8bit"])
+@pytest.mark.parametrize("N", [64, 1024, 1544, 12288])
+@pytest.mark.parametrize("power", [20, 45, 50])
+def test_gradient_of_quiet_rows(N, held, power):
+    """Rows of 2^-power, without eps: only a row of zeros has no gradient."""
+    y, res, dh, dz, w = norm_problem(2, 3, N, seed=power)
+    quiet = (res.float() * 2.0 ** -power).to(BF)
+    dz = (dz.float() + res.float()).to(BF)
+    check_gradient(y, quiet, dh, dz, w, held, 0.7 * 2.0 ** -power, 0.0)
+    check_gradient((y.float() * 2.0 ** -power).to(BF), quiet, dh, dz, (None, w[1], w[2]), held, 0.7, 0.0)
