@@ -130,8 +130,9 @@ __device__ __forceinline__ void held8(const uint2 &q, uint32_t e, f32x2 (&f)[4])
     for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], scale);
 }
 
-// The same in one multiply-add, for e <= 230 (gemm_wgrad of 8 x 768x4096 over 8192 tokens: 260 -> 255
-// us): above, 2^23 + 128 times the power of two is no number.
+// The same in one multiply-add, for e <= kLowMost (gemm_wgrad of 8 x 768x4096 over 8192 tokens: 260 -> 255
+// us): above, 2^23 + 128 times the power of two, 2^104 there, is no number.
+constexpr uint32_t kLowMost = 231;
 __device__ __forceinline__ void held8_low(const uint2 &q, uint32_t e, f32x2 (&f)[4])
 {
     const float s = __uint_as_float(e << 23);

@@ -513,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wgrad(
                     x[i][1] = narrow8(g);
                 }
             };
-            if (__any_sync(0xFFFFFFFFu, high > 230)) widen([](const uint2 &w, uint32_t b, f32x2 (&f)[4]) { held8(w, b, f); });
+            if (__any_sync(0xFFFFFFFFu, high > kLowMost)) widen([](const uint2 &w, uint32_t b, f32x2 (&f)[4]) { held8(w, b, f); });
             else widen([](const uint2 &w, uint32_t b, f32x2 (&f)[4]) { held8_low(w, b, f); });
             arrive_warp(qempty + 8 * slot, lane);
             if (!wait_all(empty + 8 * stage, phase ^ 1u, ab, 11)) break;

@@ -133,3 +133,21 @@ def test_gradient_of_quiet_rows(N, held, power):
     dz = (dz.float() + res.float()).to(BF)
     check_gradient(y, quiet, dh, dz, w, held, 0.7 * 2.0 ** -power, 0.0)
     check_gradient((y.float() * 2.0 ** -power).to(BF), quiet, dh, dz, (None, w[1], w[2]), held, 0.7, 0.0)
+
+
+# ---------------------------------------------------------------- weight gradient: every power of two
+@pytest.mark.parametrize("K", [64, 72])
+def test_weight_gradient_of_every_exponent(K):
+    """A token for every exponent, with every byte, alone in its column of dy: products with 1 are the held values
+    themselves, among them those at the limit from which on they are widened in two steps (231 and 232)."""
+    T = 248
+    q = (torch.arange(T * K, device=DEV) % 255 - 127).to(torch.int8).view(1, T, K)
+    e = torch.arange(1, T + 1, device=DEV).to(torch.uint8).view(1, T, 1).expand(1, T, -(-K // 32)).contiguous()
+    dy = torch.eye(T, device=DEV).to(BF)[None]
+    for first in (0, 230, 231):                                          # with all others, and in launches of their own
+        some = slice(first, first + (T if first == 0 else 1))
+        dw = torch.full((1, T, K), float("nan"), device=DEV)
+        rc.gemm_wgrad(dy[:, some], (q[:, some].contiguous(), e[:, some].contiguous()), dw)
+        want = ob.act8_values(q.cpu().numpy(), e.cpu().numpy())
+        want[0, [t for t in range(T) if not some.start <= t < some.stop]] = 0
+        assert np.array_equal(f64(dw), want)
