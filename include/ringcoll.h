@@ -593,7 +593,8 @@ typedef struct {
  *     u = y (mean y^2 + eps)^(-1/2) gamma_post     (u = y where gamma_post is null),
  *     h = res + alpha * gate * u                   (gate 1 where null),
  *     z = h (mean h^2 + eps)^(-1/2) gamma_pre      (z is null where gamma_pre is),
- * in binary32, h and z rounded once to bf16 (z from h before its rounding).  y8 and
+ * in binary32, h and z rounded once to bf16 (z from h before its rounding); the sum of a
+ * row's squares has to be a binary32 number, and a normal one or eps above 0.  y8 and
  * res8 are the 8-bit forms of y and res, z8 that of the rounded z, as act8_pack
  * would make them.  h may be res (in place); results are apart otherwise.
  * Requirements (RC_ERR_INVALID otherwise): 1 <= P <= RC_MAX_P, N a multiple of 8 up
@@ -652,7 +653,7 @@ int glu(const rc_glu_args *args, void *stream);
 
 /*
  * glu_bwd -- its gradient, from a and b or from what a8 and b8 hold: da = dh b act'(a),
- * db = dh act(a), each rounded once; h, where given, is written again (the
+ * db = dh act(a), in binary32 from the left, each rounded once; h, where given, is written again (the
  * operand of the next matmul's weight gradient), and h8 its 8-bit form.  da and
  * db may each be a, b or dh, as wholes; results are apart otherwise.
  */

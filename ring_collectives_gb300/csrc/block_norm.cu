@@ -58,7 +58,8 @@ struct Params {
     uint32_t rows, T, N, vecs;
     Side ys, dys, dzs;               // how y, dy and dz lie
     uint32_t chunk;                  // channels of a slot of those that lie in column chunks
-    int stages, per, sums, clear;    // gradient: blocks of a slot; sums of a block's part; 1: zero `part` once read
+    int stages;                      // of rows on their way
+    int per, sums, clear;            // gradient: blocks of a slot; sums of a block's part; 1: zero `part` once read
     float alpha, eps, inv_n;
     WsHeader *hdr;                   // clusters: where a wait that ran out is recorded
     unsigned long long timeout_ns;
@@ -661,8 +662,9 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) k_block_sums(const Params p)
 // vectors of 8 channels a thread: two halve what a row costs besides its channels, the sums
 // above all (8192 x 4096 forward with checkpoints 58 us against 67 with one, the gradient 72
 // against 100).  Where no SM gets a second row only its latency counts, and one is quicker (8
-// rows of 4096 4.1 us against 4.5).  Rows above 8192 channels have four blocks, so that each SM
-// works on parts of two rows (2048 x 16384, gradient: 89 us; 152 with two blocks of twice the size).
+// rows of 4096 4.1 us against 4.5).  Rows above 8192 channels have a cluster: in the gradient of four blocks,
+// so that each SM works on parts of two rows (2048 x 16384: 89 us; 152 with two blocks of twice the
+// size); forward of two (68 us with checkpoints).
 struct Shape {
     int vpt, gl, cl, threads, stages, rows;   // rows: at once, in the blocks that the GPU holds
     int groups;                               // rows of a block at once
